@@ -66,6 +66,27 @@ class SlQkvoGrads(ctypes.Structure):
                 ("dAo", _vp), ("dBo", _vp)]
 
 
+class SlRotarySpec(ctypes.Structure):
+    _fields_ = [("rot_dim", _i32), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", _i64), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double)]
+
+
+class SlRotary(ctypes.Structure):
+    _fields_ = [("rot_dim", _i32), ("interleaved", _i32), ("amplitude", ctypes.c_float), ("turns", _vp),
+                ("pos", _vp)]
+
+
+class SlDiffAttn(ctypes.Structure):
+    _fields_ = [("heads", SlHeads), ("lambda_init", ctypes.c_float), ("scale", ctypes.c_float),
+                ("causal", _i32), ("lens", ctypes.POINTER(_i32)), ("lq1", _vp), ("lk1", _vp), ("lq2", _vp),
+                ("lk2", _vp)]
+
+
+class SlDiffAttnGrads(ctypes.Structure):
+    _fields_ = [("dlq1", _vp), ("dlk1", _vp), ("dlq2", _vp), ("dlk2", _vp)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "sl_abi_version": (ctypes.c_int, []),
@@ -113,6 +134,24 @@ SIGNATURES = {
                                    ctypes.POINTER(SlQkvoWeights), _vp, _vp, _i32, _vp, _i32, _vp,
                                    _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp,
                                    ctypes.POINTER(SlQkvoGrads), _vp, _sz, _vp]),
+    "sl_rotary_table": (ctypes.c_int, [ctypes.POINTER(SlRotarySpec), ctypes.POINTER(ctypes.c_uint64),
+                                       ctypes.POINTER(ctypes.c_float)]),
+    "sl_rotary_apply": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlHeads),
+                                       ctypes.POINTER(SlRotary), _vp, _vp, _vp, _vp, _i32, _vp]),
+    "sl_head_norm_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlHeads),
+                                        ctypes.POINTER(SlRotary), ctypes.c_float, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _vp]),
+    "sl_head_norm_workspace_bytes": (_sz, [ctypes.POINTER(SlLayout), ctypes.POINTER(SlHeads)]),
+    "sl_head_norm_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlHeads),
+                                        ctypes.POINTER(SlRotary), ctypes.c_float, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sl_diff_attn_saved_bytes": (_sz, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlHeads)]),
+    "sl_diff_attn_workspace_bytes": (_sz, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlHeads)]),
+    "sl_diff_attn_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlDiffAttn),
+                                        _vp, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp]),
+    "sl_diff_attn_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlDiffAttn),
+                                        _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp, _vp, _vp,
+                                        ctypes.POINTER(SlDiffAttnGrads), _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -483,4 +522,243 @@ def qkvo_bwd(w: QKVOWeights, X: Optional[torch.Tensor], a: Optional[torch.Tensor
                          _ptr(dv), _ptr(d_out), _ptr(out.get("dX")), _ptr(out.get("da")),
                          ctypes.byref(g), _ptr(buf.ws), buf.ws.numel(), _stream()),
            "sl_qkvo_bwd")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Between the q/k/v and the o projection: rotary positions, head norms,
+# differential attention.
+def _check_rows(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
+    """The pointer of a contiguous tensor of this shape and type on the current device."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise SparseLoraError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise SparseLoraError(f"{name}: tensors must be contiguous")
+    if t.device.type != "cuda":
+        raise SparseLoraError(f"{name}: tensors must be on the GPU, got {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise SparseLoraError(f"{name}: on {t.device}, but the current device is "
+                              f"cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3, "yarn": 4}
+
+
+class Rotary:
+    """The frequency table of rotary positions: pair i of a head's first
+    ``rot_dim`` values turns by ``position * base**(-2 i / rot_dim)``, pairs
+    being values i and i + rot_dim / 2, or 2 i and 2 i + 1 (``interleaved``).
+
+    ``scaling`` stretches the positions by ``factor`` for long contexts:
+    "linear" (every frequency), "base" (a larger base), "wavelength" (pairs
+    that turn fewer than ``low_turns`` times within ``original_len``, none
+    above ``high_turns``, linear between) or "yarn" (a ramp over the pair
+    index, with the amplitude 0.1 ln(factor) + 1)."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original_len: int = 4096, low_turns: float = 1.0,
+                 high_turns: Optional[float] = None, device="cuda"):
+        if scaling not in ROPE_SCALINGS:
+            raise SparseLoraError(f"unknown rotary scaling {scaling!r}: one of {sorted(ROPE_SCALINGS)}")
+        if high_turns is None:
+            high_turns = 32.0 if scaling == "yarn" else 4.0
+        spec = SlRotarySpec(int(rot_dim), ROPE_SCALINGS[scaling], float(base), float(factor), int(original_len),
+                            float(low_turns), float(high_turns))
+        table = (ctypes.c_uint64 * max(int(rot_dim) // 2, 1))()
+        amp = ctypes.c_float(0)
+        _check(lib().sl_rotary_table(ctypes.byref(spec), table, ctypes.byref(amp)), "sl_rotary_table")
+        self.rot_dim, self.interleaved, self.amplitude = int(rot_dim), bool(interleaved), amp.value
+        # torch holds the table's 64 bits as signed integers
+        self.turns = torch.tensor([ctypes.c_int64(x).value for x in table], dtype=torch.int64).to(device)
+
+    def _c(self, pos: Optional[torch.Tensor], T: int) -> SlRotary:
+        pp = None if pos is None else _check_rows("pos", pos, (T,), torch.int32)
+        tp = _check_rows("turns", self.turns, (self.rot_dim // 2,), torch.int64)
+        return SlRotary(self.rot_dim, int(self.interleaved), self.amplitude, tp, pp)
+
+
+def _check_scratch(name: str, ws: torch.Tensor, like: torch.Tensor) -> int:
+    if ws.device != like.device:
+        raise SparseLoraError(f"{name}: buffers on {ws.device}, tensors on {like.device}")
+    return _ptr(ws)
+
+
+def _pair_ptrs(names, q, k, layout, heads, dtype):
+    """Pointers of a q-shaped and an optional k-shaped tensor."""
+    T = layout.batch * layout.seq_len
+    qp = _check_rows(names[0], q, (T, heads[0] * heads[2]), dtype)
+    kp = None if k is None else _check_rows(names[1], k, (T, heads[1] * heads[2]), dtype)
+    return qp, kp
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], layout: Layout, heads: Sequence[int], rot: Rotary,
+           pos: Optional[torch.Tensor] = None, inverse: bool = False,
+           out: Optional[Sequence[Optional[torch.Tensor]]] = None):
+    """(q, k) [T, H * head_dim] with the position rotation applied to every
+    head; ``inverse`` turns back, which is the gradient.  ``pos`` [T] int32,
+    or None: the row's place in its sequence.  ``out`` may hold q and k
+    themselves.  k may be None."""
+    L = lib()
+    dt = _dtype_code(q)
+    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, heads, q.dtype)
+    qo, ko = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
+    if (k is None) != (ko is None):
+        raise SparseLoraError("out must hold a tensor for each input")
+    qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, layout, heads, q.dtype)
+    r = rot._c(pos, q.shape[0])
+    _check(L.sl_rotary_apply(dt, layout.ref, ctypes.byref(SlHeads(*heads)), ctypes.byref(r), qp, kp, qop, kop,
+                             int(inverse), _stream()), "sl_rotary_apply")
+    return qo, ko
+
+
+class HeadNormWorkspace:
+    """Reusable scratch of head_norm_bwd."""
+
+    def __init__(self, layout: Layout, heads: Sequence[int], device):
+        self.ws = _bytes_tensor(lib().sl_head_norm_workspace_bytes(layout.ref, ctypes.byref(SlHeads(*heads))),
+                                device)
+
+
+def head_norm_fwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, wk: Optional[torch.Tensor],
+                  layout: Layout, heads: Sequence[int], rot: Optional[Rotary] = None,
+                  pos: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  out: Optional[Sequence[Optional[torch.Tensor]]] = None):
+    """(q, k) with every head divided by its root mean square and multiplied
+    by wq / wk [head_dim] (fp32), then rotated (``rot`` None: not).  k and wk
+    may both be None."""
+    L = lib()
+    dt = _dtype_code(q)
+    hd = heads[2]
+    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, heads, q.dtype)
+    wqp = _check_rows("wq", wq, (hd,), torch.float32)
+    wkp = None if wk is None else _check_rows("wk", wk, (hd,), torch.float32)
+    qo, ko = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
+    qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, layout, heads, q.dtype)
+    r = rot._c(pos, q.shape[0]) if rot is not None else None
+    _check(L.sl_head_norm_fwd(dt, layout.ref, ctypes.byref(SlHeads(*heads)), ctypes.byref(r) if r else None,
+                              float(eps), qp, kp, wqp, wkp, qop, kop, _stream()), "sl_head_norm_fwd")
+    return qo, ko
+
+
+def head_norm_bwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, wk: Optional[torch.Tensor],
+                  layout: Layout, heads: Sequence[int], dq_out: torch.Tensor, dk_out: Optional[torch.Tensor],
+                  rot: Optional[Rotary] = None, pos: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  buf: Optional[HeadNormWorkspace] = None, out: Optional[Dict[str, torch.Tensor]] = None):
+    """Gradients dq, dk (call dtype) and dwq, dwk (fp32) of head_norm_fwd; q
+    and k are its inputs."""
+    L = lib()
+    dt = _dtype_code(q)
+    hd, dev = heads[2], q.device
+    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, heads, q.dtype)
+    gqp, gkp = _pair_ptrs(("dq_out", "dk_out"), dq_out, dk_out, layout, heads, q.dtype)
+    wqp = _check_rows("wq", wq, (hd,), torch.float32)
+    wkp = None if wk is None else _check_rows("wk", wk, (hd,), torch.float32)
+    buf = buf or HeadNormWorkspace(layout, heads, dev)
+    out = dict(out or {})
+    for n, x, w in (("q", q, wq), ("k", k, wk)):
+        if x is not None:
+            if "d" + n not in out:
+                out["d" + n] = torch.empty_like(x)
+            if "dw" + n not in out:
+                out["dw" + n] = torch.empty(hd, dtype=torch.float32, device=dev)
+    dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out.get("dk"), layout, heads, q.dtype)
+    dwq = _check_rows("dwq", out["dwq"], (hd,), torch.float32)
+    dwk = _check_rows("dwk", out["dwk"], (hd,), torch.float32) if "dwk" in out else None
+    r = rot._c(pos, q.shape[0]) if rot is not None else None
+    _check(L.sl_head_norm_bwd(dt, layout.ref, ctypes.byref(SlHeads(*heads)), ctypes.byref(r) if r else None,
+                              float(eps), qp, kp, wqp, wkp, gqp, gkp, dqp, dkp, dwq, dwk,
+                              _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()), "sl_head_norm_bwd")
+    return out
+
+
+class DiffAttnParams:
+    """Differential attention's learned vectors lq1, lk1, lq2, lk2 [head_dim]
+    (fp32 device tensors; lambda = exp(lq1.lk1) - exp(lq2.lk2) + lambda_init)
+    and its settings.  ``scale`` None: head_dim ** -0.5."""
+
+    NAMES = ("lq1", "lk1", "lq2", "lk2")
+
+    def __init__(self, t: Dict[str, torch.Tensor], heads: Sequence[int], lambda_init: float = 0.8,
+                 scale: Optional[float] = None, causal: bool = True):
+        self.t = t
+        self.heads = tuple(int(h) for h in heads)
+        self.lambda_init, self.causal = float(lambda_init), bool(causal)
+        self.scale = float(scale) if scale is not None else float(max(self.heads[2], 1)) ** -0.5
+
+    def _c(self, lens) -> SlDiffAttn:
+        ptrs = [_check_rows(n, self.t[n], (self.heads[2],), torch.float32) for n in self.NAMES]
+        return SlDiffAttn(SlHeads(*self.heads), self.lambda_init, self.scale, int(self.causal), lens, *ptrs)
+
+
+class DiffAttnWorkspace:
+    """Saved and scratch buffers of one differential attention call and its
+    backward, with the sequences' valid lengths (None: every row)."""
+
+    def __init__(self, p: DiffAttnParams, layout: Layout, dtype: torch.dtype, device,
+                 lens: Optional[Sequence[int]] = None):
+        L = lib()
+        code = {torch.bfloat16: SL_BF16, torch.float32: SL_F32}.get(dtype)
+        if code is None:
+            raise SparseLoraError(f"unsupported dtype {dtype}")
+        if lens is not None and len(lens) != layout.batch:
+            raise SparseLoraError(f"lens holds {len(lens)} lengths for {layout.batch} sequences")
+        self.lens = None if lens is None else (_i32 * len(lens))(*[int(n) for n in lens])
+        h = SlHeads(*p.heads)
+        self.saved = _bytes_tensor(L.sl_diff_attn_saved_bytes(code, layout.ref, ctypes.byref(h)), device)
+        self.ws = _bytes_tensor(L.sl_diff_attn_workspace_bytes(code, layout.ref, ctypes.byref(h)), device)
+
+
+def diff_attn_fwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, layout: Layout,
+                  lens: Optional[Sequence[int]] = None, buf: Optional[DiffAttnWorkspace] = None,
+                  out: Optional[torch.Tensor] = None):
+    """a [T, Hq * head_dim] and the buffers its backward reads.  ``lens``
+    [batch]: valid rows per sequence (a given ``buf`` holds its own)."""
+    L = lib()
+    dt = _dtype_code(q)
+    if k is None or v is None:
+        raise SparseLoraError("q, k and v are required")
+    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, p.heads, q.dtype)
+    vp = _check_rows("v", v, k.shape, q.dtype)
+    if buf is None:
+        buf = DiffAttnWorkspace(p, layout, q.dtype, q.device, lens)
+    elif lens is not None:
+        raise SparseLoraError("lens belongs to the buffers: give it to DiffAttnWorkspace")
+    a = out if out is not None else torch.empty_like(q)
+    ap = _check_rows("a", a, q.shape, q.dtype)
+    c = p._c(buf.lens)
+    _check(L.sl_diff_attn_fwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
+                              _check_scratch("saved", buf.saved, q), buf.saved.numel(),
+                              _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()), "sl_diff_attn_fwd")
+    return a, buf
+
+
+def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: torch.Tensor,
+                  layout: Layout, buf: DiffAttnWorkspace, da: torch.Tensor,
+                  out: Optional[Dict[str, torch.Tensor]] = None):
+    """Gradients dq, dk, dv (call dtype) and dlq1, dlk1, dlq2, dlk2 (fp32); a
+    and buf are diff_attn_fwd's."""
+    L = lib()
+    dt = _dtype_code(q)
+    if k is None or v is None:
+        raise SparseLoraError("q, k and v are required")
+    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, p.heads, q.dtype)
+    vp = _check_rows("v", v, k.shape, q.dtype)
+    ap = _check_rows("a", a, q.shape, q.dtype)
+    gp = _check_rows("da", da, q.shape, q.dtype)
+    out = dict(out or {})
+    for n, x in (("dq", q), ("dk", k), ("dv", v)):
+        if n not in out:
+            out[n] = torch.empty_like(x)
+    for n in p.NAMES:
+        if "d" + n not in out:
+            out["d" + n] = torch.empty_like(p.t[n])
+    dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out["dk"], layout, p.heads, q.dtype)
+    dvp = _check_rows("dv", out["dv"], v.shape, q.dtype)
+    g = SlDiffAttnGrads(*[_check_rows("d" + n, out["d" + n], (p.heads[2],), torch.float32) for n in p.NAMES])
+    c = p._c(buf.lens)
+    _check(L.sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
+                              _check_scratch("saved", buf.saved, q), buf.saved.numel(), gp, dqp, dkp, dvp,
+                              ctypes.byref(g), _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()),
+           "sl_diff_attn_bwd")
     return out

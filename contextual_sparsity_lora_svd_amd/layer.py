@@ -12,8 +12,8 @@ layers).
 Everything here is host-side bookkeeping: which k each call uses, the channel
 sets (all channels while dense, the estimator's per-sequence choice after), the
 buffers, and the routing of gradients.  Every arithmetic step runs in
-libsparselora.so; the attention core between the q/k/v and o projections is
-the caller's.
+libsparselora.so.  The attention core between the q/k/v and o projections is
+the caller's, or DiffAttention's.
 """
 import math
 from dataclasses import dataclass
@@ -23,7 +23,7 @@ import torch
 
 from . import api as sl
 
-__all__ = ["LayerRatios", "SparsitySchedule", "SparseLoRAFFN", "SparseLoRAQKVO"]
+__all__ = ["LayerRatios", "SparsitySchedule", "SparseLoRAFFN", "SparseLoRAQKVO", "DiffAttention"]
 
 
 @dataclass(frozen=True)
@@ -300,3 +300,102 @@ class SparseLoRAQKVO(torch.nn.Module):
         q, k, v = _QKVStep.apply(X, self.Aq, self.Bq, self.Ak, self.Bk, self.Av, self.Bv, st)
         a = attention(q, k, v)
         return _OStep.apply(a.contiguous(), self.Ao, self.Bo, st)
+
+
+class _RotaryStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, layout, heads, rot, pos):
+        ctx.args = (layout, heads, rot)
+        ctx.save_for_backward(pos)
+        return sl.rotary(q.detach().contiguous(), k.detach().contiguous(), layout, heads, rot, pos)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        layout, heads, rot = ctx.args
+        (pos,) = ctx.saved_tensors
+        dq, dk = sl.rotary(dq.contiguous(), dk.contiguous(), layout, heads, rot, pos, inverse=True)
+        return dq, dk, None, None, None, None
+
+
+class _HeadNormStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, layout, heads, rot, pos, eps):
+        q, k = q.detach().contiguous(), k.detach().contiguous()
+        ctx.args = (layout, heads, rot, eps)
+        ctx.save_for_backward(q, k, wq, wk, pos)
+        return sl.head_norm_fwd(q, k, wq.detach(), wk.detach(), layout, heads, rot, pos, eps)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        layout, heads, rot, eps = ctx.args
+        q, k, wq, wk, pos = ctx.saved_tensors
+        g = sl.head_norm_bwd(q, k, wq.detach(), wk.detach(), layout, heads, dq.contiguous(), dk.contiguous(), rot,
+                             pos, eps)
+        return g["dq"], g["dk"], g["dwq"], g["dwk"], None, None, None, None, None
+
+
+class _DiffAttnStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lq1, lk1, lq2, lk2, mod, layout, lens):
+        q, k, v = (x.detach().contiguous() for x in (q, k, v))
+        p = mod._params(lq1, lk1, lq2, lk2)
+        buf = sl.DiffAttnWorkspace(p, layout, q.dtype, q.device, lens)
+        a, _ = sl.diff_attn_fwd(p, q, k, v, layout, buf=buf)
+        ctx.args = (mod, layout, buf)
+        ctx.save_for_backward(q, k, v, a, lq1, lk1, lq2, lk2)
+        return a
+
+    @staticmethod
+    def backward(ctx, da):
+        mod, layout, buf = ctx.args
+        q, k, v, a, *lv = ctx.saved_tensors
+        g = sl.diff_attn_bwd(mod._params(*lv), q, k, v, a, layout, buf, da.contiguous())
+        return (g["dq"], g["dk"], g["dv"], g["dlq1"], g["dlk1"], g["dlq2"], g["dlk2"], None, None, None)
+
+
+class DiffAttention(torch.nn.Module):
+    """Differential attention between the q/k/v and the o projection:
+    optional norms of the q and k heads (``qk_norm``, weights ``wq, wk``) and
+    rotary positions (``rot``), one pass over q and k, then the difference of
+    the two softmax maps with the learned ``lq1, lk1, lq2, lk2`` (fp32
+    parameters).  q, k, v as the projections write them:
+
+        core = DiffAttention(heads, rot=Rotary(head_dim), qk_norm=True)
+        out = proj(X, layout, core.bind(layout), step)     # proj: SparseLoRAQKVO
+
+    ``lens`` (valid rows per sequence) and ``pos`` [T] int32 go with each call."""
+
+    def __init__(self, heads: Sequence[int], lambda_init: float = 0.8, causal: bool = True,
+                 scale: Optional[float] = None, rot: Optional[sl.Rotary] = None, qk_norm: bool = False,
+                 eps: float = 1e-6, init_std: float = 0.1, generator: Optional[torch.Generator] = None,
+                 device="cuda"):
+        super().__init__()
+        self.heads = tuple(int(h) for h in heads)
+        hd = self.heads[2]
+        self.lambda_init, self.causal, self.scale = float(lambda_init), bool(causal), scale
+        self.rot, self.qk_norm, self.eps = rot, bool(qk_norm), float(eps)
+
+        def p():
+            x = torch.randn(hd, generator=generator, dtype=torch.float32) * init_std
+            return torch.nn.Parameter(x.to(device))
+        self.lq1, self.lk1, self.lq2, self.lk2 = p(), p(), p(), p()
+        if self.qk_norm:
+            self.wq = torch.nn.Parameter(torch.ones(hd, device=device))
+            self.wk = torch.nn.Parameter(torch.ones(hd, device=device))
+
+    def _params(self, lq1, lk1, lq2, lk2):
+        t = {"lq1": lq1.detach(), "lk1": lk1.detach(), "lq2": lq2.detach(), "lk2": lk2.detach()}
+        return sl.DiffAttnParams(t, self.heads, self.lambda_init, self.scale, self.causal)
+
+    def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, layout: sl.Layout,
+                lens: Optional[Sequence[int]] = None, pos: Optional[torch.Tensor] = None):
+        if self.qk_norm:
+            q, k = _HeadNormStep.apply(q, k, self.wq, self.wk, layout, self.heads, self.rot, pos, self.eps)
+        elif self.rot is not None:
+            q, k = _RotaryStep.apply(q, k, layout, self.heads, self.rot, pos)
+        return _DiffAttnStep.apply(q, k, v, self.lq1, self.lk1, self.lq2, self.lk2, self, layout, lens)
+
+    def bind(self, layout: sl.Layout, lens: Optional[Sequence[int]] = None,
+             pos: Optional[torch.Tensor] = None) -> Callable:
+        """The ``attention(q, k, v) -> a`` that SparseLoRAQKVO calls."""
+        return lambda q, k, v: self(q, k, v, layout, lens, pos)

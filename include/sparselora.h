@@ -307,6 +307,112 @@ sl_status sl_qkvo_bwd(sl_dtype dt, const sl_layout* lay, const sl_qkvo_weights* 
                       void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Between the q/k/v and the o projection: rotary positions, norms of the q and
+ * k heads, differential attention.  q is [T, Hq*hd] and k, v [T, Hkv*hd], as
+ * sl_qkvo_fwd writes them (call dtype); of the layout, batch and seq_len are
+ * read (ctx_len is not).  Every call is stream-ordered on `stream` alone, never
+ * synchronises, launches nothing on error, and may be captured into a graph.
+ *
+ * Rotary positions.  The first rot_dim values of every head are pairs: value i
+ * with value i + rot_dim/2 (half layout) or 2i with 2i+1 (interleaved); pair i
+ * of the row at position p turns by p * f_i and is multiplied by amplitude.
+ * The rest of the head is copied.
+ *   turns [rot_dim/2] uint64: f_i / (2 pi) in units of 2^-64 turns (device),
+ *         as sl_rotary_table writes it on the host
+ *   pos   [T] int32 positions (any sign), or NULL: row % seq_len
+ * sl_rotary_table(spec): f_i = base^(-2i/rot_dim), stretched for long contexts:
+ *   LINEAR      f / factor
+ *   BASE        base * factor^(rot_dim/(rot_dim-2)) in place of base
+ *   WAVELENGTH  pairs that turn more than high_turns times within original_len
+ *               keep f, fewer than low_turns get f / factor, linear between
+ *   YARN        the same ends, the ramp linear in the pair index between the
+ *               indices (rounded outwards) that reach high_turns and low_turns;
+ *               amplitude 0.1 ln(factor) + 1
+ * base > 1, factor >= 1, 0 < low_turns < high_turns; rot_dim even, 2..256.
+ * turns and amplitude are host memory; the table is made once per model.
+ *
+ * sl_rotary_apply: q_out / k_out = the rotated rows; inverse != 0 turns the
+ * other way, which is the gradient.  q_out may be q, and k_out k.  k and k_out
+ * may both be NULL.  head_dim even, at most 256; rot_dim even, 0..head_dim.
+ * ------------------------------------------------------------------------- */
+typedef enum sl_rope_scaling {
+  SL_ROPE_NONE = 0, SL_ROPE_LINEAR = 1, SL_ROPE_BASE = 2, SL_ROPE_WAVELENGTH = 3, SL_ROPE_YARN = 4
+} sl_rope_scaling;
+typedef struct sl_rotary_spec {
+  int32_t rot_dim;
+  sl_rope_scaling scaling;
+  double base, factor;
+  int64_t original_len;             /* WAVELENGTH, YARN */
+  double low_turns, high_turns;     /* WAVELENGTH, YARN */
+} sl_rotary_spec;
+typedef struct sl_rotary {
+  int32_t rot_dim, interleaved;
+  float amplitude;
+  const uint64_t* turns;
+  const int32_t* pos;
+} sl_rotary;
+sl_status sl_rotary_table(const sl_rotary_spec* spec, uint64_t* turns, float* amplitude);
+sl_status sl_rotary_apply(sl_dtype dt, const sl_layout* lay, const sl_heads* heads, const sl_rotary* rot,
+                          const void* q, const void* k, void* q_out, void* k_out, int32_t inverse,
+                          void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms of the q and k heads, with the rotation in the same pass:
+ *   y = R(x r w),  r = (mean over the head of x^2 + eps)^(-1/2)
+ * wq, wk [hd] fp32 weights shared by the heads; rot NULL (or rot_dim 0): no
+ * rotation.  k, wk, k_out (and their gradients) may all be NULL.
+ *   fwd: q, k -> q_out, k_out (q_out may be q, k_out k; keep x for the backward)
+ *   bwd: x = q, k (the forward's inputs) and dq_out, dk_out -> dq, dk and the
+ *        fp32 weight gradients dwq, dwk [hd], overwritten, summed over rows and
+ *        heads in a fixed order.  dq may be dq_out, and dk dk_out.
+ * A row whose mean square and eps are both 0 has no norm: its outputs are NaN.
+ * ------------------------------------------------------------------------- */
+sl_status sl_head_norm_fwd(sl_dtype dt, const sl_layout* lay, const sl_heads* heads, const sl_rotary* rot,
+                           float eps, const void* q, const void* k, const float* wq, const float* wk,
+                           void* q_out, void* k_out, void* stream);
+size_t sl_head_norm_workspace_bytes(const sl_layout* lay, const sl_heads* heads);
+sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_heads* heads, const sl_rotary* rot,
+                           float eps, const void* q, const void* k, const float* wq, const float* wk,
+                           const void* dq_out, const void* dk_out, void* dq, void* dk,
+                           float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Differential attention: query heads 2h, 2h+1 are a pair that reads the kv
+ * heads 2g, 2g+1 of its group, g = h / (Hq / Hkv), and one value of 2 hd, v's
+ * columns [2g*hd, 2(g+1)*hd):
+ *   a[:, 2h*hd : 2(h+1)*hd] = softmax(s q_2h k_2g^T) V - lambda softmax(s q_2h+1 k_2g+1^T) V
+ *   lambda = exp(lq1 . lk1) - exp(lq2 . lk2) + lambda_init
+ *   lq1, lk1, lq2, lk2 [hd] fp32, 16-byte aligned: shared by the heads
+ *   scale   s (a positive number)
+ *   causal  != 0: row i of a sequence reads keys 0..i
+ *   lens    [host] batch valid lengths 0..seq_len, or NULL: every row.  Rows at
+ *           or past a sequence's length are padding: they are never read, and
+ *           their outputs and gradients are written as 0.
+ *   fwd: q, k, v -> a [T, Hq*hd]; writes `saved` for the backward.
+ *   bwd: q, k, v, a (the forward's) and da -> dq, dk, dv and the fp32 gradients
+ *        of the four vectors, overwritten.  Sums run in a fixed order.
+ * Hq and Hkv even, Hq a multiple of Hkv; hd a multiple of 8, at most 128; every
+ * tensor fewer than 2^31 elements.
+ * ------------------------------------------------------------------------- */
+typedef struct sl_diff_attn {
+  sl_heads heads;
+  float lambda_init, scale;
+  int32_t causal;
+  const int32_t* lens;
+  const float *lq1, *lk1, *lq2, *lk2;
+} sl_diff_attn;
+typedef struct sl_diff_attn_grads { float *dlq1, *dlk1, *dlq2, *dlk2; } sl_diff_attn_grads;
+size_t sl_diff_attn_saved_bytes(sl_dtype dt, const sl_layout* lay, const sl_heads* heads);
+size_t sl_diff_attn_workspace_bytes(sl_dtype dt, const sl_layout* lay, const sl_heads* heads);
+sl_status sl_diff_attn_fwd(sl_dtype dt, const sl_layout* lay, const sl_diff_attn* p, const void* q, const void* k,
+                           const void* v, void* a, void* saved, size_t saved_bytes, void* ws, size_t ws_bytes,
+                           void* stream);
+sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const sl_diff_attn* p, const void* q, const void* k,
+                           const void* v, const void* a, const void* saved, size_t saved_bytes, const void* da,
+                           void* dq, void* dk, void* dv, const sl_diff_attn_grads* g, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------
  * Offline quantization of a frozen weight to the 4-bit base of sl_ffn_weights
  * (SparseLoRA article §六: SparseLoRA over a QLoRA-style quantized base; the
  * pages name no format, this is the plainest 4-bit one).  W [rows, cols] in dt

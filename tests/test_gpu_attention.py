@@ -1,0 +1,366 @@
+"""GPU parity of rotary positions, head norms and differential attention with
+the fp64 oracle: element by element, within bounds derived from the number
+formats (half a step of the output's type, half a step of each matrix operand
+that is rounded, fp32 sums at their worst case)."""
+import numpy as np
+import pytest
+
+import oracle as O
+from workloads import round_to_bf16
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+U32 = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}          # half a step, relative
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _sl():
+    import contextual_sparsity_lora_svd_amd as sl
+    return sl
+
+
+def _draw(rng, shape, dt, scale=1.0):
+    x = (rng.standard_normal(shape) * scale).astype(np.float32)
+    return round_to_bf16(x) if dt == "bf16" else x
+
+
+def _dev(x, dt):
+    return torch.from_numpy(np.array(x, dtype=np.float32)).cuda().to(DT[dt])
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _within(got, ref, bound, what):
+    got = _np(got)
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    over = np.abs(got - ref) - bound
+    assert over.max() <= 0, (f"{what}: off by {np.abs(got - ref).ravel()[over.argmax()]:.3e}, "
+                             f"bound {np.broadcast_to(bound, over.shape).ravel()[over.argmax()]:.3e}")
+
+
+# ---- rotary and head norms --------------------------------------------------
+ROT = [  # batch, seq, hq, hkv, hd, rot, interleaved, scaling, factor
+    (1, 1, 1, 1, 2, 2, False, "none", 1.0),
+    (2, 3, 4, 2, 16, 16, True, "linear", 4.0),
+    (1, 37, 32, 8, 128, 128, False, "wavelength", 8.0),
+    (3, 5, 5, 1, 80, 40, True, "none", 1.0),
+    (1, 9, 3, 3, 80, 80, False, "yarn", 16.0),
+    (2, 7, 2, 1, 256, 64, False, "base", 4.0),
+    (1, 4, 2, 2, 6, 4, True, "none", 1.0),
+    (1, 5, 2, 1, 250, 250, False, "none", 1.0),       # single pairs, two units to a lane
+    (1, 3, 7, 2, 96, 24, False, "none", 1.0),
+    (1, 2500, 2, 1, 64, 64, False, "none", 1.0),      # more tokens than blocks
+]
+
+
+def _positions(rng, T, kind):
+    if kind == "row":
+        return None, None
+    p = rng.integers(-5 if kind == "near" else 0, 50 if kind == "near" else 2 ** 31 - 1, T)
+    return p, torch.from_numpy(p.astype(np.int32)).cuda()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", ROT, ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("where", ["row", "near", "far"])
+def test_rotary_and_head_norm(case, dt, where):
+    sl = _sl()
+    B, Ls, hq, hkv, hd, rot, inter, scaling, factor = case
+    rng = np.random.default_rng(hash((B, Ls, hd)) % 1000)
+    T, heads = B * Ls, (hq, hkv, hd)
+    lay = sl.Layout([Ls] * B, Ls)
+    pos_np, pos = _positions(rng, T, where)
+    pos_np = np.arange(T) % Ls if pos_np is None else pos_np
+    r = sl.Rotary(rot, interleaved=inter, scaling=scaling, factor=factor, original_len=2048)
+    f, amp = O.rotary_frequencies(rot, scaling=scaling, factor=factor, original_len=2048)
+    # the oracle's angles at far positions are off by p f 2^-53, the table's by p 2^-64 turns
+    ang = 2.0 ** 31 * 2.0 ** -50 if where == "far" else 0.0
+    x = {n: _draw(rng, (T, h * hd), dt) for n, h in (("q", hq), ("k", hkv))}
+    g = {n: _draw(rng, (T, h * hd), dt) for n, h in (("q", hq), ("k", hkv))}
+    w = {n: (1 + 0.3 * rng.standard_normal(hd)).astype(np.float32) for n in "qk"}
+    d = {n: _dev(t, dt) for n, t in x.items()}
+    dg = {n: _dev(t, dt) for n, t in g.items()}
+    dw = {n: torch.from_numpy(t).cuda() for n, t in w.items()}
+
+    def check(got, xin, inverse, what):
+        ref = O.rotate(xin, pos_np, f, amp, hd, inter, inverse)
+        mag = O.rotate(xin, pos_np, f, amp, hd, inter, absolute=True)
+        # cosine, amplitude, two products and their sum: below 8 half steps of fp32
+        _within(got, ref, HALF[dt] * np.abs(ref) + (8 * U32 + ang) * mag, what)
+
+    for inverse in (False, True):
+        q, k = sl.rotary(d["q"], d["k"], lay, heads, r, pos, inverse=inverse)
+        check(q, x["q"], inverse, "q")
+        check(k, x["k"], inverse, "k")
+    q1, none = sl.rotary(d["q"], None, lay, heads, r, pos)
+    assert none is None
+    check(q1, x["q"], False, "q alone")
+    c = d["q"].clone(), d["k"].clone()
+    sl.rotary(*c, lay, heads, r, pos, out=c)                 # in place
+    check(c[0], x["q"], False, "q in place")
+    check(c[1], x["k"], False, "k in place")
+
+    for use_rot in (True, False):
+        rr, ff = (r, f) if use_rot else (None, np.zeros(0))
+        y = dict(zip("qk", sl.head_norm_fwd(d["q"], d["k"], dw["q"], dw["k"], lay, heads, rr, pos, 1e-5)))
+        gr = sl.head_norm_bwd(d["q"], d["k"], dw["q"], dw["k"], lay, heads, dg["q"], dg["k"], rr, pos, 1e-5)
+        for n in "qk":
+            u = O.head_norm(x[n], w[n], hd, 1e-5)
+            ref = O.rotate(u, pos_np, ff, amp, hd, inter)
+            mag = O.rotate(u, pos_np, ff, amp, hd, inter, absolute=True)
+            # mean square: hd terms in fp32, halved by the root; then the rotation
+            _within(y[n], ref, HALF[dt] * np.abs(ref) + ((hd / 2 + 16) * U32 + ang) * mag, "norm " + n)
+            gb = O.rotate(g[n], pos_np, ff, amp, hd, inter, inverse=True)
+            gm = O.rotate(g[n], pos_np, ff, amp, hd, inter, absolute=True)
+            dx, dwn, _, _ = O.head_norm_backward(x[n], w[n], gb, hd, 1e-5)
+            _, _, mx, mw = O.head_norm_backward(x[n], w[n], gm, hd, 1e-5)
+            _within(gr["d" + n], dx, HALF[dt] * np.abs(dx) + ((2 * hd + 32) * U32 + 2 * ang) * mx, "d" + n)
+            chain = hd / 2 + 64 + T * max(hq, hkv) / 256        # longest run of additions in one sum
+            _within(gr["dw" + n], dwn, (chain * U32 + 2 * ang) * mw, "dw" + n)
+
+
+def test_norm_of_zero_rows_and_alone():
+    """Zero rows stay zero, their gradient is g w / sqrt(eps); k left out."""
+    sl = _sl()
+    lay, heads = sl.Layout([3], 3), (2, 1, 32)
+    x = torch.zeros(3, 64, device="cuda")
+    w = torch.full((32,), 2.0, device="cuda")
+    y, k = sl.head_norm_fwd(x, None, w, None, lay, heads, eps=0.25)
+    assert k is None and not y.any()
+    g = sl.head_norm_bwd(x, None, w, None, lay, heads, torch.ones_like(x), None, eps=0.25)
+    assert torch.equal(g["dq"], torch.full_like(x, 4.0)) and not g["dwq"].any() and "dk" not in g
+
+
+# ---- differential attention --------------------------------------------------
+DIFF = [  # batch, seq, hq, hkv, hd, causal, lens
+    (1, 1, 2, 2, 8, True, None),
+    (1, 2, 4, 2, 16, False, None),
+    (2, 33, 4, 2, 16, False, [33, 0]),
+    (1, 64, 4, 4, 32, True, None),
+    (3, 65, 8, 2, 64, True, [65, 1, 31]),
+    (2, 130, 4, 2, 80, True, [130, 77]),
+    (2, 96, 6, 2, 96, False, None),
+    (1, 257, 4, 4, 128, True, None),
+    (2, 200, 8, 2, 128, False, [200, 129]),
+    (3, 32, 2, 2, 40, True, [0, 32, 16]),
+    (1, 515, 2, 2, 64, True, None),
+    (1, 140, 2, 2, 128, True, [128]),
+]
+
+
+def _diff_inputs(case, dt, seed=0, spread=1.0):
+    B, Ls, hq, hkv, hd, causal, lens = case
+    rng = np.random.default_rng(seed + Ls)
+    T = B * Ls
+    x = {"q": _draw(rng, (T, hq * hd), dt, spread), "k": _draw(rng, (T, hkv * hd), dt, spread),
+         "v": _draw(rng, (T, hkv * hd), dt), "da": _draw(rng, (T, hq * hd), dt)}
+    lv = [(0.3 * rng.standard_normal(hd) / np.sqrt(hd / 8)).astype(np.float32) for _ in range(4)]
+    return x, lv
+
+
+def _run_diff(sl, case, dt, x, lv, lam0=0.6, pad=float("nan")):
+    B, Ls, hq, hkv, hd, causal, lens = case
+    lay = sl.Layout([Ls] * B, Ls)
+    d = {n: _dev(t, dt) for n, t in x.items()}
+    if lens is not None:
+        for b, n in enumerate(lens):                        # padding may hold anything
+            for t in d.values():
+                t[b * Ls + n:(b + 1) * Ls] = pad
+    p = sl.DiffAttnParams(dict(zip(sl.DiffAttnParams.NAMES, (torch.from_numpy(t).cuda() for t in lv))), (hq, hkv, hd),
+                          lambda_init=lam0, causal=causal)
+    a, buf = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], lay, lens=lens)
+    g = sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a, lay, buf, d["da"])
+    return p, d, lay, a, g, buf
+
+
+def _check_diff(case, dt, x, lv, a, g, lam0=0.6):
+    B, Ls, hq, hkv, hd, causal, lens = case
+    ref = O.diff_attention(x["q"], x["k"], x["v"], lv, lam0, B, (hq, hkv, hd), float(np.float32(hd ** -0.5)), causal,
+                           lens, x["da"], rnd=HALF["bf16"] if dt == "bf16" else 0.0)
+    for n, got in [("a", a)] + sorted(g.items()):
+        half = U32 if n.startswith("dl") else HALF[dt]
+        _within(got, ref[n], half * np.abs(ref[n]) + ref["bound"][n] * (1 + half) + 1e-30, n)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", DIFF, ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
+def test_diff_attention(case, dt):
+    sl = _sl()
+    x, lv = _diff_inputs(case, dt)
+    _, _, _, a, g, _ = _run_diff(sl, case, dt, x, lv)
+    _check_diff(case, dt, x, lv, a, g)
+    B, Ls, lens = case[0], case[1], case[6]
+    if lens is not None:                                     # padding: outputs and gradients are 0
+        for b, n in enumerate(lens):
+            for t in (a, g["dq"], g["dk"], g["dv"]):
+                assert not t[b * Ls + n:(b + 1) * Ls].any()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["peaked", "flat", "late", "negative"])
+def test_diff_attention_distributions(dt, kind):
+    """One key takes all the weight; all weights equal; the maximum arrives with
+    the last keys, far above the rest; lambda below zero."""
+    sl = _sl()
+    case = (1, 150, 4, 2, 64, kind != "flat", None)
+    x, lv = _diff_inputs(case, dt, seed=5)
+    if kind == "peaked":
+        x["q"] = _draw(np.random.default_rng(1), x["q"].shape, dt, 3.0)
+        x["k"] = _draw(np.random.default_rng(2), x["k"].shape, dt, 3.0)
+    if kind == "flat":
+        x["k"][:] = 0
+    if kind == "late":
+        x["q"][:] = 0.5
+        x["k"][:] = 0.25 * (np.arange(150)[:, None] // 40) ** 2
+    lam0 = -0.9 if kind == "negative" else 0.6
+    _, _, _, a, g, _ = _run_diff(sl, case, dt, x, lv, lam0)
+    _check_diff(case, dt, x, lv, a, g, lam0)
+
+
+def test_diff_attention_gradient_against_differences():
+    """Central differences of the fp32 kernel's own forward along random
+    directions.  With step e the difference is off by O(e^2) times the third
+    derivative and by the forward's rounding over e: at e = 2^-6 both stay
+    below a hundredth of the gradient's size here."""
+    sl = _sl()
+    case = (1, 40, 4, 2, 16, True, None)
+    x, lv = _diff_inputs(case, "f32", seed=9)
+    p, d, lay, a, g, _ = _run_diff(sl, case, "f32", x, lv)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def loss(q, k, v, t):
+        pp = sl.DiffAttnParams(t, p.heads, p.lambda_init, causal=True)
+        return (sl.diff_attn_fwd(pp, q, k, v, lay)[0].double() * d["da"].double()).sum().item()
+
+    base = {"q": d["q"], "k": d["k"], "v": d["v"], **p.t}
+    e = 2.0 ** -6
+    for n in base:
+        v = torch.randn(base[n].shape, generator=gen, device="cuda")
+        v /= v.norm()
+        f = []
+        for s in (e, -e):
+            y = dict(base)
+            y[n] = (base[n] + s * v).contiguous()
+            f.append(loss(y["q"], y["k"], y["v"], {m: y[m] for m in p.NAMES}))
+        num = (f[0] - f[1]) / (2 * e)
+        size = g["d" + n].double().norm().item()
+        assert abs(num - (g["d" + n].double() * v).sum().item()) <= 0.01 * size, n
+
+
+def test_calls_are_repeatable_and_independent():
+    """The same call gives the same bits; two calls on two streams with their
+    own buffers give what each gives alone; the inputs are left as they were."""
+    sl = _sl()
+    cases = [(2, 130, 8, 2, 64, True, [130, 100]), (1, 200, 4, 4, 128, False, None)]
+    runs = []
+    for c in cases:
+        x, lv = _diff_inputs(c, "bf16", seed=3)
+        runs.append((c, x, lv, _run_diff(sl, c, "bf16", x, lv, pad=0.0)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for s, (c, x, lv, (p, d, lay, a, g, _)) in zip(streams, runs):
+        before = {n: t.clone() for n, t in d.items()}
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            a2, buf = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], lay, lens=c[6])
+            g2 = sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a2, lay, buf, d["da"])
+        outs.append((a, g, a2, g2, d, before))
+    torch.cuda.synchronize()
+    for a, g, a2, g2, d, before in outs:
+        assert torch.equal(a, a2)
+        for n in g:
+            assert torch.equal(g[n], g2[n]), n
+        for n in d:
+            assert torch.equal(d[n], before[n]), n
+
+
+def test_results_do_not_depend_on_what_the_buffers_held():
+    sl = _sl()
+    case = (2, 97, 4, 2, 64, True, [97, 40])
+    x, lv = _diff_inputs(case, "bf16", seed=4)
+    p, d, lay, a, g, buf = _run_diff(sl, case, "bf16", x, lv, pad=0.0)
+    buf2 = sl.DiffAttnWorkspace(p, lay, torch.bfloat16, "cuda", lens=case[6])
+    out = {n: torch.full_like(t, float("nan")) for n, t in g.items()}
+    for t in (buf2.saved, buf2.ws):
+        t.fill_(0xFF)
+    a2, _ = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], lay, buf=buf2, out=torch.full_like(a, float("nan")))
+    buf2.ws.fill_(0xFF)
+    g2 = sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a2, lay, buf2, d["da"], out=out)
+    assert torch.equal(a, a2)
+    for n in g:
+        assert torch.equal(g[n], g2[n]), n
+    nbuf = sl.HeadNormWorkspace(lay, p.heads, "cuda")
+    w = torch.ones(64, device="cuda")
+    ref = sl.head_norm_bwd(d["q"], d["k"], w, w, lay, p.heads, d["da"], d["v"], buf=nbuf)
+    nbuf.ws.fill_(0xFF)
+    again = sl.head_norm_bwd(d["q"], d["k"], w, w, lay, p.heads, d["da"], d["v"], buf=nbuf)
+    for n in ref:
+        assert torch.equal(ref[n], again[n]), n
+
+
+def test_graph_replays_match_eager():
+    """The three operators, forward and backward, captured once and replayed
+    on changing inputs, with the program's own eager work in between."""
+    sl = _sl()
+    case = (2, 70, 4, 2, 64, True, [70, 50])
+    x, lv = _diff_inputs(case, "bf16", seed=6)
+    lay, heads = sl.Layout([70, 70], 70), (4, 2, 64)
+    rot, w = sl.Rotary(64), torch.ones(64, device="cuda")
+    d = {n: _dev(t, "bf16") for n, t in x.items()}
+    p = sl.DiffAttnParams(dict(zip(sl.DiffAttnParams.NAMES, (torch.from_numpy(t).cuda() for t in lv))), heads)
+    buf, nbuf = sl.DiffAttnWorkspace(p, lay, torch.bfloat16, "cuda", lens=case[6]), sl.HeadNormWorkspace(lay, heads, "cuda")
+
+    def step():
+        q, k = sl.head_norm_fwd(d["q"], d["k"], w, w, lay, heads, rot)
+        a, _ = sl.diff_attn_fwd(p, q, k, d["v"], lay, buf=buf)
+        g = sl.diff_attn_bwd(p, q, k, d["v"], a, lay, buf, d["da"])
+        n = sl.head_norm_bwd(d["q"], d["k"], w, w, lay, heads, g["dq"], g["dk"], rot, buf=nbuf)
+        r = sl.rotary(n["dq"], n["dk"], lay, heads, rot, inverse=True)
+        return [a, g["dv"], g["dlq1"], n["dq"], n["dk"], n["dwq"], n["dwk"], *r]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        d["q"].copy_(torch.roll(d["q"], 1, 0))
+        d["da"].mul_(0.5 if i % 2 else 2.0)
+        graph.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        for u, v in zip(got, step()):
+            assert torch.equal(u, v)
+
+
+def test_long_sequence_last_rows():
+    """Past one tile and one workgroup: a 2100-row causal sequence, its last
+    rows against the oracle's formula."""
+    sl = _sl()
+    L, heads = 2100, (2, 2, 128)
+    rng = np.random.default_rng(8)
+    x = {n: _draw(rng, (L, 256), "bf16") for n in ("q", "k", "v")}
+    lv = [(0.05 * rng.standard_normal(128)).astype(np.float32) for _ in range(4)]
+    p = sl.DiffAttnParams(dict(zip(sl.DiffAttnParams.NAMES, (torch.from_numpy(t).cuda() for t in lv))), heads, 0.5)
+    d = {n: _dev(t, "bf16") for n, t in x.items()}
+    a, _ = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], sl.Layout([L], L))
+    lam = O.diff_lambda(lv, 0.5)[0]
+    rows = np.array([0, 1, 127, 128, 1023, 2047, 2048, L - 1])
+    k, v = x["k"].astype(np.float64), x["v"].astype(np.float64)
+    for r in rows:
+        maps = []
+        for m in (0, 1):
+            s = x["q"][r, 128 * m:128 * (m + 1)].astype(np.float64) @ k[:r + 1, 128 * m:128 * (m + 1)].T * 128 ** -0.5
+            w = np.exp(s - s.max())
+            maps.append(w / w.sum())
+        ref = (maps[0] - lam * maps[1]) @ v[:r + 1]
+        mag = (maps[0] + abs(lam) * maps[1]) @ np.abs(v[:r + 1])
+        _within(a[r], ref, HALF["bf16"] * np.abs(ref) + (HALF["bf16"] + U32 * (r + 2000)) * mag, f"row {r}")
