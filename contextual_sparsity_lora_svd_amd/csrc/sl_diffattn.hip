@@ -1,262 +1,12 @@
-// Differential attention, forward and backward.
-//
-// Per head pair, with S_m = s q_m k_m^T (causal or within the sequence's length):
-//   P_m = softmax(S_m),  O = P_1 V - lambda P_2 V
-//   dP = dO V^T,  D_m = rowsum(P_m dP) = dO . (P_m V)
-//   dS_1 = P_1 (dP - D_1),  dS_2 = -lambda P_2 (dP - D_2)
-//   dQ_m = s dS_m K_m,  dK_m = s dS_m^T Q_m,  dV = (P_1 - lambda P_2)^T dO
-//   dlambda = -sum D_2
-// The two maps share V, dP and dV's product.  The forward keeps the running
-// maximum and sum of each map (one pass over the keys) and saves each row's
-// log2-sum-exp and O_2 = P_2 V; the backward forms the weights again from them.
-#include <cmath>
-
-#include "sl_common.hpp"
-#include "sl_host.hpp"
+#include "sl_diffattn.hpp"
+#include "sl_diffattn_direct.hpp"
+#include "sl_diffattn_lds.hpp"
 
 namespace sl {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-struct DiffArgs {
-  const void *q, *k, *v, *a, *da;
-  void *o, *o2;              // forward: output and P_2 V (also read by the backward)
-  float* lse;                // [batch][pairs][2][L], log2 units
-  float* dsum;               // [batch][pairs][2][L] row sums D_1, D_2
-  void *dq, *dk, *dv;
-  float* dlam_part;          // one partial sum of D_2 per wave of the dQ kernel
-  float *dlq1, *dlk1, *dlq2, *dlk2;
-  const float *lq1, *lk1, *lq2, *lk2;
-  float lambda_init, scale;
-  int B, L, hp, gp, hd;      // hp query pairs, gp kv pairs
-  int causal, npart;
-  int lens[SL_MAX_SEQS];
-};
-
-template <typename T> struct Frag;          // 8 consecutive k values of one row
-template <> struct Frag<bf16> { bf16x8 v; };
-template <> struct Frag<float> { float v[8]; };
-
-template <typename T> __device__ inline Frag<T> load_row(const T* p, bool ok);
-template <> __device__ inline Frag<bf16> load_row<bf16>(const bf16* p, bool ok) {
-  const uint4 z = make_uint4(0, 0, 0, 0);
-  return Frag<bf16>{__builtin_bit_cast(bf16x8, ok ? *reinterpret_cast<const uint4*>(p) : z)};
-}
-template <> __device__ inline Frag<float> load_row<float>(const float* p, bool ok) {
-  Frag<float> f;
-  float4 x = make_float4(0, 0, 0, 0), y = x;
-  if (ok) {
-    x = *reinterpret_cast<const float4*>(p);
-    y = *reinterpret_cast<const float4*>(p + 4);
-  }
-  f.v[0] = x.x; f.v[1] = x.y; f.v[2] = x.z; f.v[3] = x.w;
-  f.v[4] = y.x; f.v[5] = y.y; f.v[6] = y.z; f.v[7] = y.w;
-  return f;
-}
-
-// acc (32 x 32) += A (32 x 16) B (16 x 32).  Lane l holds row l % 32 of A and
-// column l % 32 of B, 8 k values of half l / 32; any order of k serves as long
-// as both operands use it.  acc[i] is row 8 (i / 4) + 4 (l / 32) + i % 4 of
-// column l % 32.
-__device__ inline void mma(f32x16& acc, const Frag<bf16>& a, const Frag<bf16>& b) {
-  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
-}
-__device__ inline void mma(f32x16& acc, const Frag<float>& a, const Frag<float>& b) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], acc, 0, 0, 0);
-}
-
-// Accumulator values 8 c .. 8 c + 7 as the k values of an operand: k position j
-// of half h is row 16 c + 8 (j / 4) + 4 h + j % 4.
-template <typename T> __device__ inline Frag<T> acc_frag(const f32x16& x, int c);
-template <> __device__ inline Frag<bf16> acc_frag<bf16>(const f32x16& x, int c) {
-  Frag<bf16> f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f.v[j] = (__bf16)x[8 * c + j];
-  return f;
-}
-template <> __device__ inline Frag<float> acc_frag<float>(const f32x16& x, int c) {
-  Frag<float> f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f.v[j] = x[8 * c + j];
-  return f;
-}
-
-// The matching operand from memory: column `col` of rows row0 + 16 c + 8 (j / 4)
-// + 4 h + j % 4, rows at or past `rows` as 0.
-template <typename T> __device__ inline Frag<T> load_col(const T* base, long long ld, int row0, int rows, int h, bool ok) {
-  Frag<T> f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = row0 + 8 * (j >> 2) + 4 * h + (j & 3);
-    if constexpr (sizeof(T) == 2) {
-      const uint16_t x = ok && r < rows ? base[r * ld].v : (uint16_t)0;
-      f.v[j] = __builtin_bit_cast(__bf16, x);
-    } else {
-      f.v[j] = ok && r < rows ? base[r * ld] : 0.f;
-    }
-  }
-  return f;
-}
-
-// four consecutive values of a row
-template <typename T> __device__ inline void store4(T* p, float a, float b, float c, float d);
-template <> __device__ inline void store4<bf16>(bf16* p, float a, float b, float c, float d) {
-  uint2 w;
-  w.x = (uint32_t)f2bf(a) | ((uint32_t)f2bf(b) << 16);
-  w.y = (uint32_t)f2bf(c) | ((uint32_t)f2bf(d) << 16);
-  *reinterpret_cast<uint2*>(p) = w;
-}
-template <> __device__ inline void store4<float>(float* p, float a, float b, float c, float d) {
-  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
-}
-
-__device__ inline float wave_sum(float x) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
-  return x;
-}
-
-// lambda, and the two exponentials it is made of; every lane gets them
-__device__ inline float lambda_of(const DiffArgs& a, float& e1, float& e2) {
-  const int lane = threadIdx.x & 63;
-  float s1 = 0.f, s2 = 0.f;
-  for (int i = lane; i < a.hd; i += 64) {
-    s1 = fmaf(a.lq1[i], a.lk1[i], s1);
-    s2 = fmaf(a.lq2[i], a.lk2[i], s2);
-  }
-  e1 = expf(wave_sum(s1));
-  e2 = expf(wave_sum(s2));
-  return e1 - e2 + a.lambda_init;
-}
-
-constexpr float kLog2e = 1.44269504088896341f;
-
-__device__ inline void zero16(f32x16& x) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-}
-
-// Keep a loop from hoisting (and then spilling) the loads behind an offset.
-__device__ inline int opaque(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
-
-// ---------------------------------------------------------------------------
-// Operands straight from memory.  One wave per 32 rows; the transposed score
-// tile (keys x queries) leaves a query in a lane pair, so the softmax needs one
-// exchange per tile and its weights feed the second product from registers.
-template <typename T, int D>
-__global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
-  constexpr int NT = D / 16;   // 32-value tiles of the 2 D wide output
-  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int nqb = (a.L + 31) / 32;
-  if (wave >= nqb * a.hp * a.B) return;
-  const int qb = nqb - 1 - wave / (a.hp * a.B);       // the longest rows first
-  const int pair = (wave / a.B) % a.hp, b = wave % a.B;
-  const int g = pair / (a.hp / a.gp), len = a.lens[b];
-  float e1, e2;
-  const float lam = lambda_of(a, e1, e2);
-  const int row = qb * 32 + c;
-  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
-  const T* qp = reinterpret_cast<const T*>(a.q) + (tok0 + row) * ldq + pair * 2 * a.hd;
-  const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * ldk + g * 2 * a.hd;
-  const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * ldk + g * 2 * a.hd;
-  const bool rok = row < len;
-  f32x16 o[2][NT];
-  float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) zero16(o[m][t]);
-  const float sc = a.scale * kLog2e;
-  int kend = len;
-  if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
-  if (qb * 32 >= len) kend = 0;
-  for (int k0 = 0; k0 < kend; k0 += 32) {
-    const int kz = opaque(0);
-    f32x16 s[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      zero16(s[m]);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int col = ks * 16 + h * 8;
-        const bool cok = col < a.hd;
-        const Frag<T> kf = load_row<T>(kp + (long long)(k0 + c) * ldk + m * a.hd + col, cok && k0 + c < len);
-        const Frag<T> qf = load_row<T>(qp + m * a.hd + col + kz, cok && rok);
-        mma(s[m], kf, qf);
-      }
-      float tm = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
-        if (key >= len || (a.causal && key > row)) s[m][i] = -INFINITY;
-        tm = fmaxf(tm, s[m][i]);
-      }
-      tm = fmaxf(tm, __shfl_xor(tm, 32));
-      const float nm = fmaxf(mx[m], tm);
-      const float ms = nm == -INFINITY ? 0.f : nm * sc;   // nothing seen yet: weights 0
-      const float f = exp2f(mx[m] * sc - ms);
-      float ts = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[m][i] = exp2f(fmaf(s[m][i], sc, -ms));
-        ts += s[m][i];
-      }
-      sum[m] = sum[m] * f + ts;
-      mx[m] = nm;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
-    }
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      const Frag<T> p0 = acc_frag<T>(s[0], cc), p1 = acc_frag<T>(s[1], cc);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int dv = 32 * t + c;
-        const Frag<T> vf = load_col<T>(vp + dv, ldk, k0 + 16 * cc, len, h, dv < 2 * a.hd);
-        mma(o[0][t], vf, p0);
-        mma(o[1][t], vf, p1);
-      }
-    }
-  }
-  if (row >= a.L) return;
-  float inv[2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float l = sum[m] + __shfl_xor(sum[m], 32);
-    inv[m] = rok ? 1.f / l : 0.f;
-    if (h == 0) a.lse[((long long)(b * a.hp + pair) * 2 + m) * a.L + row] = rok ? mx[m] * sc + log2f(l) : INFINITY;
-  }
-  const long long orow = (tok0 + row) * ldq + pair * 2 * a.hd;
-  T* op = reinterpret_cast<T*>(a.o) + orow;
-  T* o2p = reinterpret_cast<T*>(a.o2) + orow;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int dv = 32 * t + 2 * i + 4 * h;
-      if (dv >= 2 * a.hd) continue;
-      float x[4], y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = rok ? o[1][t][i + e] * inv[1] : 0.f;
-        x[e] = rok ? o[0][t][i + e] * inv[0] - lam * y[e] : 0.f;
-      }
-      store4<T>(op + dv, x[0], x[1], x[2], x[3]);
-      store4<T>(o2p + dv, y[0], y[1], y[2], y[3]);
-    }
-}
-
-// D_1 = dO . (O + lambda O_2), D_2 = dO . O_2, one wave per row and head pair.
-template <typename T>
+// fp32: D_1 = dO . (O + lambda O_2), D_2 = dO . O_2, one wave per row and head pair.
 __global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
+  using T = float;
   const int lane = threadIdx.x & 63;
   const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
   const long long rows = (long long)a.B * a.L;
@@ -264,8 +14,7 @@ __global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
   const int pair = (int)(w % a.hp);
   const long long tok = w / a.hp;
   const int b = (int)(tok / a.L), row = (int)(tok % a.L);
-  float e1, e2;
-  const float lam = lambda_of(a, e1, e2);
+  const float lam = a.lam[0];
   float d1 = 0.f, d2 = 0.f;
   if (row < a.lens[b]) {
     const long long at = (tok * a.hp + pair) * 2 * a.hd;
@@ -283,236 +32,20 @@ __global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
   if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.L + row] = lane ? d2 : d1;
 }
 
-// dQ: one wave per 32 queries, keys in order.  It also sums P_2 dP, whose total
-// is -dlambda, in fp32 (D_2 of the saved, rounded O_2 would not be exact enough).
-template <typename T, int D>
-__global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
-  constexpr int DT = D / 32;
-  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int nqb = (a.L + 31) / 32;
-  if (wave >= nqb * a.hp * a.B) return;
-  const int qb = nqb - 1 - wave / (a.hp * a.B);
-  const int pair = (wave / a.B) % a.hp, b = wave % a.B;
-  const int g = pair / (a.hp / a.gp), len = a.lens[b];
-  float e1, e2;
-  const float lam = lambda_of(a, e1, e2);
-  const int row = qb * 32 + c;
-  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
-  const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd, koff = tok0 * ldk + g * 2 * a.hd;
-  const T* qp = reinterpret_cast<const T*>(a.q) + qoff;
-  const T* dop = reinterpret_cast<const T*>(a.da) + qoff;
-  const T* kp = reinterpret_cast<const T*>(a.k) + koff;
-  const T* vp = reinterpret_cast<const T*>(a.v) + koff;
-  const bool rok = row < len;
-  float lse[2], ds[2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.L + row;
-    lse[m] = rok ? a.lse[at] : INFINITY;
-    ds[m] = rok ? a.dsum[at] : 0.f;
-  }
-  f32x16 dq[2][DT];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int t = 0; t < DT; ++t) zero16(dq[m][t]);
-  const float sc = a.scale * kLog2e;
-  float dlam = 0.f;
-  int kend = len;
-  if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
-  if (qb * 32 >= len) kend = 0;
-  for (int k0 = 0; k0 < kend; k0 += 32) {
-    const int kz = opaque(0);
-    f32x16 dp, s[2];
-    zero16(dp);
-#pragma unroll
-    for (int ks = 0; ks < D / 8; ++ks) {
-      const int col = ks * 16 + h * 8;
-      const bool cok = col < 2 * a.hd;
-      const Frag<T> vf = load_row<T>(vp + (long long)(k0 + c) * ldk + col, cok && k0 + c < len);
-      const Frag<T> gf = load_row<T>(dop + col + kz, cok && rok);
-      mma(dp, vf, gf);
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      zero16(s[m]);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int col = ks * 16 + h * 8;
-        const bool cok = col < a.hd;
-        const Frag<T> kf = load_row<T>(kp + (long long)(k0 + c) * ldk + m * a.hd + col, cok && k0 + c < len);
-        const Frag<T> qf = load_row<T>(qp + m * a.hd + col + kz, cok && rok);
-        mma(s[m], kf, qf);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
-        const bool hidden = key >= len || (a.causal && key > row) || !rok;
-        const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m]));
-        if (m == 1) dlam = fmaf(p, dp[i], dlam);
-        s[m][i] = p * (dp[i] - ds[m]);
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const Frag<T> sf = acc_frag<T>(s[m], cc);
-#pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          const int d = 32 * t + c;
-          const Frag<T> kf = load_col<T>(kp + m * a.hd + d, ldk, k0 + 16 * cc, len, h, d < a.hd);
-          mma(dq[m][t], kf, sf);
-        }
-      }
-  }
-  dlam = wave_sum(dlam);
-  if (lane == 0) a.dlam_part[wave] = dlam;
-  if (row >= a.L) return;
-  T* out = reinterpret_cast<T*>(a.dq) + qoff;
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float f = m ? -lam * a.scale : a.scale;
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int d = 32 * t + 2 * i + 4 * h;
-        if (d >= a.hd) continue;
-        store4<T>(out + m * a.hd + d, dq[m][t][i] * f, dq[m][t][i + 1] * f, dq[m][t][i + 2] * f, dq[m][t][i + 3] * f);
-      }
-  }
-}
-
-// dK and dV: one wave per 32 keys; the query pairs of the group in order, their
-// queries in order.
-template <typename T, int D>
-__global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
-  constexpr int DT = D / 32, NT = D / 16;
-  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int nkb = (a.L + 31) / 32;
-  if (wave >= nkb * a.gp * a.B) return;
-  const int kb = wave / (a.gp * a.B);                 // causal: the first keys have the most queries
-  const int g = (wave / a.B) % a.gp, b = wave % a.B;
-  const int grp = a.hp / a.gp, len = a.lens[b];
-  float e1, e2;
-  const float lam = lambda_of(a, e1, e2);
-  const int key = kb * 32 + c;
-  const bool kok = key < len;
-  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
-  const long long koff = (tok0 + key) * ldk + g * 2 * a.hd;
-  const T* kp = reinterpret_cast<const T*>(a.k) + koff;
-  const T* vp = reinterpret_cast<const T*>(a.v) + koff;
-  f32x16 dk[2][DT], dv[NT];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int t = 0; t < DT; ++t) zero16(dk[m][t]);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) zero16(dv[t]);
-  const float sc = a.scale * kLog2e;
-  const int qbeg = a.causal ? kb * 32 : 0;
-  for (int pr = g * grp; pr < (g + 1) * grp; ++pr) {
-    const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * ldq + pr * 2 * a.hd;
-    const T* dop = reinterpret_cast<const T*>(a.da) + tok0 * ldq + pr * 2 * a.hd;
-    const float* lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.L;
-    const float* dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.L;
-    for (int q0 = kb * 32 < len ? qbeg : len; q0 < len; q0 += 32) {
-      const int kz = opaque(0);
-      f32x16 dp, s[2], w;
-      zero16(dp);
-#pragma unroll
-      for (int ks = 0; ks < D / 8; ++ks) {
-        const int col = ks * 16 + h * 8;
-        const bool cok = col < 2 * a.hd;
-        const Frag<T> gf = load_row<T>(dop + (long long)(q0 + c) * ldq + col, cok && q0 + c < len);
-        const Frag<T> vf = load_row<T>(vp + col + kz, cok && kok);
-        mma(dp, gf, vf);
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        zero16(s[m]);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const int col = ks * 16 + h * 8;
-          const bool cok = col < a.hd;
-          const Frag<T> qf = load_row<T>(qp + (long long)(q0 + c) * ldq + m * a.hd + col, cok && q0 + c < len);
-          const Frag<T> kf = load_row<T>(kp + m * a.hd + col + kz, cok && kok);
-          mma(s[m], qf, kf);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3);
-          const bool hidden = q >= len || (a.causal && key > q) || !kok;
-          const int qq = q < len ? q : 0;
-          const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m * a.L + qq]));
-          w[i] = m ? w[i] - lam * p : p;
-          s[m][i] = p * (dp[i] - dsm[m * a.L + qq]);
-        }
-      }
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const Frag<T> wf = acc_frag<T>(w, cc);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int d = 32 * t + c;
-          const Frag<T> gf = load_col<T>(dop + d, ldq, q0 + 16 * cc, len, h, d < 2 * a.hd);
-          mma(dv[t], gf, wf);
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const Frag<T> sf = acc_frag<T>(s[m], cc);
-#pragma unroll
-          for (int t = 0; t < DT; ++t) {
-            const int d = 32 * t + c;
-            const Frag<T> qf = load_col<T>(qp + m * a.hd + d, ldq, q0 + 16 * cc, len, h, d < a.hd);
-            mma(dk[m][t], qf, sf);
-          }
-        }
-      }
-    }
-  }
-  if (key >= a.L) return;
-  T* dkp = reinterpret_cast<T*>(a.dk) + koff;
-  T* dvp = reinterpret_cast<T*>(a.dv) + koff;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int d = 32 * t + 2 * i + 4 * h;
-      if (d < 2 * a.hd) store4<T>(dvp + d, dv[t][i], dv[t][i + 1], dv[t][i + 2], dv[t][i + 3]);
-    }
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float f = m ? -lam * a.scale : a.scale;
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int d = 32 * t + 2 * i + 4 * h;
-        if (d < a.hd)
-          store4<T>(dkp + m * a.hd + d, dk[m][t][i] * f, dk[m][t][i + 1] * f, dk[m][t][i + 2] * f, dk[m][t][i + 3] * f);
-      }
-  }
-}
-
 // dlambda = -(sum of the partial sums, in a fixed order); the four vectors' gradients.
 __global__ void __launch_bounds__(1024) diff_dlambda(const DiffArgs a) {
-  __shared__ float sm[16];
-  float e1, e2;
-  lambda_of(a, e1, e2);
-  float s = 0.f;
+  __shared__ double sm[16];
+  double s = 0.0;
   for (int i = threadIdx.x; i < a.npart; i += 1024) s += a.dlam_part[i];
-  s = wave_sum(s);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
   __syncthreads();
-  s = 0.f;
+  s = 0.0;
   for (int i = 0; i < 16; ++i) s += sm[i];
   const int i = threadIdx.x;
   if (i < a.hd) {
-    const float g1 = -s * e1, g2 = s * e2;
+    const float g1 = -(float)s * a.lam[1], g2 = (float)s * a.lam[2];
     const float q1 = a.lq1[i], k1 = a.lk1[i], q2 = a.lq2[i], k2 = a.lk2[i];
     a.dlq1[i] = g1 * k1;
     a.dlk1[i] = g1 * q1;
@@ -524,10 +57,24 @@ __global__ void __launch_bounds__(1024) diff_dlambda(const DiffArgs a) {
 // ---------------------------------------------------------------------------
 // host side
 struct DiffPlan {
-  size_t lse, o2, saved;           // offsets and size of the saved buffer
-  size_t dsum, dlam, ws;           // of the workspace
-  int npart;
+  size_t lse, lam, rsc, o2, res, saved;    // offsets and size of the saved buffer
+  size_t dsum, dlam, part, ws;             // of the workspace
+  int npart, split;
+  long long part_elems;                    // of one part of dK or dV
 };
+
+// Parts that a kv group's heads are cut into for dK and dV: one workgroup per
+// 128 keys leaves CUs idle (or waiting for the longest) below two rounds of
+// 256; short loops are not worth the second launch.
+static int dkv_split(long long blocks, int grp, int tiles) {
+  int s = 1;
+  if (grp * tiles <= 16) return s;
+  while (s < grp && blocks * s < 512) {
+    ++s;
+    while (grp % s) ++s;
+  }
+  return s;
+}
 
 static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs, DiffPlan& pl) {
   if (dt != SL_BF16 && dt != SL_F32) SL_FAIL(SL_ERR_DTYPE, "dtype must be SL_F32 or SL_BF16");
@@ -546,13 +93,18 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   const long long stats = T * hq;   // two rows of statistics per head pair
   Bump s, w;
   pl.lse = s.take(stats * 4);
+  pl.lam = s.take(16);
+  pl.rsc = s.take(dt == SL_BF16 ? stats * 4 : 0);
   pl.o2 = s.take(T * hq * hd * (dt == SL_BF16 ? 2 : 4));
+  pl.res = s.take(dt == SL_BF16 ? T * hq * hd : 0);
   pl.saved = s.off;
-  const long long nqb = (lay->seq_len + 31) / 32;
-  if (nqb * (hq / 2) * lay->batch > 0x7fffffffLL / 4) SL_FAIL(SL_ERR_RANGE, "too many rows");
-  pl.npart = (int)(nqb * (hq / 2) * lay->batch);
+  const long long blocks = (long long)((lay->seq_len + 127) / 128) * lay->batch;   // of 4 waves
+  pl.npart = (int)(4 * blocks * (hq / 2));
   pl.dsum = w.take(stats * 4);
-  pl.dlam = w.take((size_t)pl.npart * 4);
+  pl.dlam = w.take((size_t)pl.npart * 8);
+  pl.split = dt == SL_BF16 ? dkv_split(blocks * (hkv / 2), hq / hkv, (lay->seq_len + 31) / 32) : 1;
+  pl.part_elems = T * hkv * hd;
+  pl.part = w.take(pl.split > 1 ? 2 * (size_t)pl.split * pl.part_elems * 4 : 0);
   pl.ws = w.off;
   return SL_OK;
 }
@@ -580,6 +132,15 @@ static sl_status diff_args(DiffArgs& a, const sl_layout* lay, const sl_diff_attn
   return SL_OK;
 }
 
+static void saved_args(DiffArgs& a, const DiffPlan& pl, void* saved) {
+  char* p = reinterpret_cast<char*>(saved);
+  a.lse = reinterpret_cast<float*>(p + pl.lse);
+  a.lam = reinterpret_cast<float*>(p + pl.lam);
+  a.rsc = reinterpret_cast<float*>(p + pl.rsc);
+  a.o2 = p + pl.o2;
+  a.res = reinterpret_cast<signed char*>(p + pl.res);
+}
+
 template <typename F> static void by_width(int hd, F f) {
   if (hd <= 32) f(std::integral_constant<int, 32>{});
   else if (hd <= 64) f(std::integral_constant<int, 64>{});
@@ -587,20 +148,41 @@ template <typename F> static void by_width(int hd, F f) {
   else f(std::integral_constant<int, 128>{});
 }
 
-template <typename T> static void launch_fwd(const DiffArgs& a, int waves, hipStream_t s) {
+static void launch_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.L + 127) / 128 * a.hp * a.B));
   by_width(a.hd, [&](auto d) {
-    hipLaunchKernelGGL((diff_fwd_direct<T, decltype(d)::value>), dim3((waves + 3) / 4), dim3(256), 0, s, a);
+    constexpr int D = decltype(d)::value;
+    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(diff_fwd_direct<D>, grid, dim3(256), 0, s, a);
   });
 }
 
-template <typename T> static void launch_bwd(const DiffArgs& a, int waves, hipStream_t s) {
+static void launch_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
   const long long rows = (long long)a.B * a.L * a.hp;
-  hipLaunchKernelGGL(diff_dsum<T>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
-  const int kwaves = (a.L + 31) / 32 * a.gp * a.B;
+  const int blocks = (a.L + 127) / 128 * a.B;
+  if (dt == SL_BF16) {
+    int lg = 0;
+    while ((8 << lg) < 2 * a.hd) ++lg;
+    const long long per = 256 >> lg;
+    hipLaunchKernelGGL(diff_dsum_q, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a, lg);
+  } else {
+    hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
+  }
   by_width(a.hd, [&](auto d) {
-    hipLaunchKernelGGL((diff_dq_direct<T, decltype(d)::value>), dim3((waves + 3) / 4), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((diff_dkv_direct<T, decltype(d)::value>), dim3((kwaves + 3) / 4), dim3(256), 0, s, a);
+    constexpr int D = decltype(d)::value;
+    const dim3 gq((unsigned)(blocks * a.hp)), gk((unsigned)(blocks * a.gp * a.split));
+    if (dt == SL_BF16) {
+      hipLaunchKernelGGL(diff_dq_lds<D>, gq, dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_lds<D>, gk, dim3(256), 0, s, a);
+    } else {
+      hipLaunchKernelGGL(diff_dq_direct<D>, gq, dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_direct<D>, gk, dim3(256), 0, s, a);
+    }
   });
+  if (a.split > 1) {
+    const long long n = 2 * ((long long)a.B * a.L * a.gp * 2 * a.hd / 4);
+    hipLaunchKernelGGL(diff_dkv_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+  }
   hipLaunchKernelGGL(diff_dlambda, dim3(1), dim3(1024), 0, s, a);
 }
 
@@ -636,11 +218,9 @@ extern "C" sl_status sl_diff_attn_fwd(sl_dtype dt, const sl_layout* lay, const s
   st = check_arch();
   if (st != SL_OK) return st;
   a.q = q; a.k = k; a.v = v; a.o = o;
-  a.lse = reinterpret_cast<float*>(reinterpret_cast<char*>(saved) + pl.lse);
-  a.o2 = reinterpret_cast<char*>(saved) + pl.o2;
+  saved_args(a, pl, saved);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dt == SL_BF16) launch_fwd<bf16>(a, pl.npart, s);
-  else launch_fwd<float>(a, pl.npart, s);
+  launch_fwd(dt, a, s);
   SL_HIP(hipGetLastError());
   return SL_OK;
 }
@@ -667,15 +247,16 @@ extern "C" sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const s
   st = check_arch();
   if (st != SL_OK) return st;
   a.q = q; a.k = k; a.v = v; a.a = o; a.da = da; a.dq = dq; a.dk = dk; a.dv = dv;
-  a.lse = reinterpret_cast<float*>(reinterpret_cast<char*>(const_cast<void*>(saved)) + pl.lse);
-  a.o2 = reinterpret_cast<char*>(const_cast<void*>(saved)) + pl.o2;
+  saved_args(a, pl, const_cast<void*>(saved));
   a.dsum = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.dsum);
-  a.dlam_part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.dlam);
+  a.dlam_part = reinterpret_cast<double*>(reinterpret_cast<char*>(ws) + pl.dlam);
   a.npart = pl.npart;
+  a.split = pl.split;
+  a.dk_part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.part);
+  a.dv_part = a.dk_part + pl.split * pl.part_elems;
   a.dlq1 = g->dlq1; a.dlk1 = g->dlk1; a.dlq2 = g->dlq2; a.dlk2 = g->dlk2;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dt == SL_BF16) launch_bwd<bf16>(a, pl.npart, s);
-  else launch_bwd<float>(a, pl.npart, s);
+  launch_bwd(dt, a, s);
   SL_HIP(hipGetLastError());
   return SL_OK;
 }

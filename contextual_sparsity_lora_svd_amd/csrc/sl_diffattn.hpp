@@ -1,0 +1,150 @@
+// Differential attention, forward and backward.
+//
+// Per head pair, with S_m = s q_m k_m^T (causal or within the sequence's length):
+//   P_m = softmax(S_m),  O = P_1 V - lambda P_2 V
+//   dP = dO V^T,  D_m = rowsum(P_m dP) = dO . (P_m V)
+//   dS_1 = P_1 (dP - D_1),  dS_2 = -lambda P_2 (dP - D_2)
+//   dQ_m = s dS_m K_m,  dK_m = s dS_m^T Q_m,  dV = (P_1 - lambda P_2)^T dO
+//   dlambda = -sum D_2
+// The two maps share V, dP and dV's product.  The forward keeps the running
+// maximum and sum of each map (one pass over the keys) and saves each row's
+// log2-sum-exp and O_2 = P_2 V; the backward forms the weights again from them.
+#pragma once
+
+#include <cmath>
+
+#include "sl_common.hpp"
+#include "sl_host.hpp"
+
+namespace sl {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+struct DiffArgs {
+  const void *q, *k, *v, *a, *da;
+  void *o, *o2;              // forward: output and O_2 = P_2 V (also read by the backward): fp32, or
+                             // 16-bit integers times the row's rsc[1]
+  signed char* res;          // bf16 calls: what rounding O to bf16 dropped, times the row's rsc[0]
+  float* rsc;                // [batch][pairs][2][L]
+  float* lam;                // lambda and its two exponentials, written by the forward
+  float* lse;                // [batch][pairs][2][L], log2 units
+  float* dsum;               // [batch][pairs][2][L] row sums D_1, D_2
+  void *dq, *dk, *dv;
+  float *dk_part, *dv_part;  // [split][tokens][kv columns] sums of the heads' parts, split > 1
+  double* dlam_part;         // one partial sum of D_2 per wave of the dQ kernel
+  float *dlq1, *dlk1, *dlq2, *dlk2;
+  const float *lq1, *lk1, *lq2, *lk2;
+  float lambda_init, scale;
+  int B, L, hp, gp, hd;      // hp query pairs, gp kv pairs
+  int causal, npart, split;
+  int lens[SL_MAX_SEQS];
+};
+
+template <typename T> struct Frag;          // 8 consecutive k values of one row
+template <> struct Frag<bf16> { bf16x8 v; };
+template <> struct Frag<float> { float v[8]; };
+
+template <typename T> __device__ inline Frag<T> load_row(const T* p, bool ok);
+template <> __device__ inline Frag<bf16> load_row<bf16>(const bf16* p, bool ok) {
+  uint4 x = make_uint4(0, 0, 0, 0);
+  if (ok) x = *reinterpret_cast<const uint4*>(p);
+  return Frag<bf16>{__builtin_bit_cast(bf16x8, x)};
+}
+template <> __device__ inline Frag<float> load_row<float>(const float* p, bool ok) {
+  Frag<float> f;
+  float4 x = make_float4(0, 0, 0, 0), y = x;
+  if (ok) {
+    x = *reinterpret_cast<const float4*>(p);
+    y = *reinterpret_cast<const float4*>(p + 4);
+  }
+  f.v[0] = x.x; f.v[1] = x.y; f.v[2] = x.z; f.v[3] = x.w;
+  f.v[4] = y.x; f.v[5] = y.y; f.v[6] = y.z; f.v[7] = y.w;
+  return f;
+}
+
+// acc (32 x 32) += A (32 x 16) B (16 x 32).  Lane l holds row l % 32 of A and
+// column l % 32 of B, 8 k values of half l / 32; any order of k serves as long
+// as both operands use it.  acc[i] is row 8 (i / 4) + 4 (l / 32) + i % 4 of
+// column l % 32.
+__device__ inline void mma(f32x16& acc, const Frag<bf16>& a, const Frag<bf16>& b) {
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
+}
+__device__ inline void mma(f32x16& acc, const Frag<float>& a, const Frag<float>& b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], acc, 0, 0, 0);
+}
+
+// Accumulator values 8 c .. 8 c + 7 as the k values of an operand: k position j
+// of half h is row 16 c + 8 (j / 4) + 4 h + j % 4.
+template <typename T> __device__ inline Frag<T> acc_frag(const f32x16& x, int c);
+template <> __device__ inline Frag<bf16> acc_frag<bf16>(const f32x16& x, int c) {
+  Frag<bf16> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j] = (__bf16)x[8 * c + j];
+  return f;
+}
+template <> __device__ inline Frag<float> acc_frag<float>(const f32x16& x, int c) {
+  Frag<float> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j] = x[8 * c + j];
+  return f;
+}
+
+// The matching operand from memory: column `col` of rows row0 + 8 (j / 4)
+// + 4 h + j % 4, rows at or past `rows` as 0.
+__device__ inline Frag<float> load_col(const float* base, long long ld, int row0, int rows, int h, bool ok) {
+  Frag<float> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = row0 + 8 * (j >> 2) + 4 * h + (j & 3);
+    f.v[j] = ok && r < rows ? base[r * ld] : 0.f;
+  }
+  return f;
+}
+
+// four consecutive values of a row
+template <typename T> __device__ inline void store4(T* p, float a, float b, float c, float d);
+template <> __device__ inline void store4<bf16>(bf16* p, float a, float b, float c, float d) {
+  uint2 w;
+  w.x = (uint32_t)f2bf(a) | ((uint32_t)f2bf(b) << 16);
+  w.y = (uint32_t)f2bf(c) | ((uint32_t)f2bf(d) << 16);
+  *reinterpret_cast<uint2*>(p) = w;
+}
+template <> __device__ inline void store4<float>(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+
+__device__ inline float wave_sum(float x) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
+// lambda, and the two exponentials it is made of; every lane gets them
+__device__ inline float lambda_of(const DiffArgs& a, float& e1, float& e2) {
+  const int lane = threadIdx.x & 63;
+  float s1 = 0.f, s2 = 0.f;
+  for (int i = lane; i < a.hd; i += 64) {
+    s1 = fmaf(a.lq1[i], a.lk1[i], s1);
+    s2 = fmaf(a.lq2[i], a.lk2[i], s2);
+  }
+  e1 = expf(wave_sum(s1));
+  e2 = expf(wave_sum(s2));
+  return e1 - e2 + a.lambda_init;
+}
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+__device__ inline void zero16(f32x16& x) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.f;
+}
+
+// Keep a loop from hoisting (and then spilling) the loads behind an offset.
+__device__ inline int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+}  // namespace sl
