@@ -17,7 +17,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparselora.so")
 
 SOURCES = ["sl_host.hip", "sl_estimate.hip", "sl_ffn.hip", "sl_qkvo.hip", "sl_svd.hip", "sl_quant.hip",
-           "sl_rotary.hip", "sl_diffattn.hip"]
+           "sl_rotary.hip", "sl_diffattn.hip", "sl_diffattn_fwd.hip", "sl_diffattn_bwd.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",
@@ -26,9 +26,11 @@ FLAGS = [
     "-I" + os.path.join(ROOT, "include"),
 ]
 
-# Per-source additions.  The estimator's kernels feed MFMA results straight to
-# VALU work, so their accumulators are kept in VGPRs (no AGPR round trip).
-EXTRA = {"sl_estimate.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# Per-source additions.  The estimator's kernels and the attention's forward feed
+# MFMA results straight to VALU work, so their accumulators are kept in VGPRs
+# (no AGPR round trip).
+EXTRA = {"sl_estimate.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "sl_diffattn_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _hipcc() -> str:

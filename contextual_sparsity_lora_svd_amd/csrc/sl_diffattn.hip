@@ -1,58 +1,7 @@
+// Differential attention: checks of arguments, buffers, entry points.
 #include "sl_diffattn.hpp"
-#include "sl_diffattn_direct.hpp"
-#include "sl_diffattn_lds.hpp"
 
 namespace sl {
-
-// fp32: D_1 = dO . (O + lambda O_2), D_2 = dO . O_2, one wave per row and head pair.
-__global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
-  using T = float;
-  const int lane = threadIdx.x & 63;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const long long rows = (long long)a.B * a.L;
-  if (w >= rows * a.hp) return;
-  const int pair = (int)(w % a.hp);
-  const long long tok = w / a.hp;
-  const int b = (int)(tok / a.L), row = (int)(tok % a.L);
-  const float lam = a.lam[0];
-  float d1 = 0.f, d2 = 0.f;
-  if (row < a.lens[b]) {
-    const long long at = (tok * a.hp + pair) * 2 * a.hd;
-    const T* dop = reinterpret_cast<const T*>(a.da) + at;
-    const T* op = reinterpret_cast<const T*>(a.a) + at;
-    const T* o2p = reinterpret_cast<const T*>(a.o2) + at;
-    for (int i = lane; i < 2 * a.hd; i += 64) {
-      const float g = ldv(dop, i), y = ldv(o2p, i);
-      d1 = fmaf(g, ldv(op, i) + lam * y, d1);
-      d2 = fmaf(g, y, d2);
-    }
-  }
-  d1 = wave_sum(d1);
-  d2 = wave_sum(d2);
-  if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.L + row] = lane ? d2 : d1;
-}
-
-// dlambda = -(sum of the partial sums, in a fixed order); the four vectors' gradients.
-__global__ void __launch_bounds__(1024) diff_dlambda(const DiffArgs a) {
-  __shared__ double sm[16];
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.npart; i += 1024) s += a.dlam_part[i];
-#pragma unroll
-  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
-  __syncthreads();
-  s = 0.0;
-  for (int i = 0; i < 16; ++i) s += sm[i];
-  const int i = threadIdx.x;
-  if (i < a.hd) {
-    const float g1 = -(float)s * a.lam[1], g2 = (float)s * a.lam[2];
-    const float q1 = a.lq1[i], k1 = a.lk1[i], q2 = a.lq2[i], k2 = a.lk2[i];
-    a.dlq1[i] = g1 * k1;
-    a.dlk1[i] = g1 * q1;
-    a.dlq2[i] = g2 * k2;
-    a.dlk2[i] = g2 * q2;
-  }
-}
 
 // ---------------------------------------------------------------------------
 // host side
@@ -141,51 +90,6 @@ static void saved_args(DiffArgs& a, const DiffPlan& pl, void* saved) {
   a.res = reinterpret_cast<signed char*>(p + pl.res);
 }
 
-template <typename F> static void by_width(int hd, F f) {
-  if (hd <= 32) f(std::integral_constant<int, 32>{});
-  else if (hd <= 64) f(std::integral_constant<int, 64>{});
-  else if (hd <= 96) f(std::integral_constant<int, 96>{});
-  else f(std::integral_constant<int, 128>{});
-}
-
-static void launch_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.L + 127) / 128 * a.hp * a.B));
-  by_width(a.hd, [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(diff_fwd_direct<D>, grid, dim3(256), 0, s, a);
-  });
-}
-
-static void launch_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
-  const long long rows = (long long)a.B * a.L * a.hp;
-  const int blocks = (a.L + 127) / 128 * a.B;
-  if (dt == SL_BF16) {
-    int lg = 0;
-    while ((8 << lg) < 2 * a.hd) ++lg;
-    const long long per = 256 >> lg;
-    hipLaunchKernelGGL(diff_dsum_q, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a, lg);
-  } else {
-    hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
-  }
-  by_width(a.hd, [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    const dim3 gq((unsigned)(blocks * a.hp)), gk((unsigned)(blocks * a.gp * a.split));
-    if (dt == SL_BF16) {
-      hipLaunchKernelGGL(diff_dq_lds<D>, gq, dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_lds<D>, gk, dim3(256), 0, s, a);
-    } else {
-      hipLaunchKernelGGL(diff_dq_direct<D>, gq, dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_direct<D>, gk, dim3(256), 0, s, a);
-    }
-  });
-  if (a.split > 1) {
-    const long long n = 2 * ((long long)a.B * a.L * a.gp * 2 * a.hd / 4);
-    hipLaunchKernelGGL(diff_dkv_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
-  }
-  hipLaunchKernelGGL(diff_dlambda, dim3(1), dim3(1024), 0, s, a);
-}
-
 }  // namespace sl
 
 using namespace sl;
@@ -220,7 +124,7 @@ extern "C" sl_status sl_diff_attn_fwd(sl_dtype dt, const sl_layout* lay, const s
   a.q = q; a.k = k; a.v = v; a.o = o;
   saved_args(a, pl, saved);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  launch_fwd(dt, a, s);
+  launch_diff_fwd(dt, a, s);
   SL_HIP(hipGetLastError());
   return SL_OK;
 }
@@ -256,7 +160,7 @@ extern "C" sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const s
   a.dv_part = a.dk_part + pl.split * pl.part_elems;
   a.dlq1 = g->dlq1; a.dlk1 = g->dlk1; a.dlq2 = g->dlq2; a.dlk2 = g->dlk2;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  launch_bwd(dt, a, s);
+  launch_diff_bwd(dt, a, s);
   SL_HIP(hipGetLastError());
   return SL_OK;
 }

@@ -147,4 +147,16 @@ __device__ inline int opaque(int x) {
   return x;
 }
 
+// Run f with the row width D that serves head_dim hd.
+template <typename F> inline void by_width(int hd, F f) {
+  if (hd <= 32) f(std::integral_constant<int, 32>{});
+  else if (hd <= 64) f(std::integral_constant<int, 64>{});
+  else if (hd <= 96) f(std::integral_constant<int, 96>{});
+  else f(std::integral_constant<int, 128>{});
+}
+
+// Enqueue the forward, and the backward, on s.
+void launch_diff_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s);
+void launch_diff_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s);
+
 }  // namespace sl

@@ -1,0 +1,752 @@
+// Differential attention: backward kernels.
+#include "sl_diffattn_lds.hpp"
+
+namespace sl {
+
+// ---------------------------------------------------------------------------
+// dQ.  As the forward: a wave owns 32 queries (their rows of Q and dO are held
+// in registers) and walks the key tiles, scores and dP = V dO^T transposed, so
+// that P and dS stay where they are formed.  K's tile is read twice, by rows
+// for the scores and by columns for dQ^T += K^T dS^T.
+template <int D>
+__global__ void __launch_bounds__(256, D > 64 ? 1 : 2) diff_dq_lds(const DiffArgs a) {
+  using R = RowTile<D>;
+  constexpr int DT = D / 32, KS = D / 16, NST = 4, PW = R::PER_WAVE;
+  constexpr bool PIPE = D > 64;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * NST * R::BYTES];
+  unsigned char* const sk = smem;
+  unsigned char* const sv = smem + NST * R::BYTES;
+  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nqb = (a.L + 127) / 128;
+  int blk, pair, b;
+  locate(blockIdx.x, a.hp * a.B, a.hp, blk, pair, b);
+  const int q0 = (nqb - 1 - blk) * 128, len = a.lens[b], g = pair / (a.hp / a.gp);
+  const int row = q0 + wave * 32 + c;
+  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
+  const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd;
+  const bf16* kbase = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.k) + tok0 * ldk + g * 2 * a.hd));
+  const bf16* vbase = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.v) + tok0 * ldk + g * 2 * a.hd));
+  const bool rok = row < len;
+  int kend = q0 < len ? len : 0, wend = q0 + wave * 32 < len ? len : 0;
+  if (a.causal) {
+    kend = kend < q0 + 128 ? kend : q0 + 128;
+    wend = wend < q0 + wave * 32 + 32 ? wend : q0 + wave * 32 + 32;
+  }
+  const int nt = (kend + 31) / 32, wt = (wend + 31) / 32;
+  const int wfull = a.causal ? ((q0 + wave * 32 + 1 < len ? q0 + wave * 32 + 1 : len) / 32) : len / 32;
+  const float lam = a.lam[0];
+
+  Frag<bf16> q[2][KS], go[2 * KS];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int col = s * 16 + h * 8;
+      const bool ok = rok && col < a.hd;
+      q[m][s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.q) + qoff + m * a.hd + col, ok);
+      // dO's columns follow the tile's: D per half, hd of them in use
+      go[m * KS + s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.da) + qoff + m * a.hd + col, ok);
+    }
+  float lse[2], ds[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.L + row;
+    lse[m] = rok ? a.lse[at] : INFINITY;      // weights of rows past the end: 0
+    ds[m] = rok ? a.dsum[at] : 0.f;
+  }
+  int srow[PW];
+  unsigned scol[PW];
+#pragma unroll
+  for (int i = 0; i < PW; ++i) R::source(wave * PW + i, lane, a.hd, srow[i], scol[i]);
+  const unsigned ldb = (unsigned)ldk * 2u;
+  const int last = len - 1;
+  auto issue_tile = [&](int tile) __attribute__((always_inline)) {
+    const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((tile & (NST - 1)) * R::BYTES + wave * PW * 1024));
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      int r = tile * 32 + srow[i];
+      r = r < last ? r : last;
+      const unsigned off = (unsigned)r * ldb + scol[i];
+      dma16(kbase, off, lds_addr(sk) + d0 + i * 1024);
+      dma16(vbase, off, lds_addr(sv) + d0 + i * 1024);
+    }
+  };
+
+  TileAddr<D> ad;
+  ad.init(lane, true, true);
+  f32x16 dq[2][DT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < DT; ++t) zero16(dq[m][t]);
+  const float sc = a.scale * kLog2e;
+  double dlam = 0.0;
+
+  auto scores = [&](f32x16 (&s)[2], f32x16& dp, int tile) __attribute__((always_inline)) {
+    const unsigned char* kt = sk + (tile & (NST - 1)) * R::BYTES;
+    const unsigned char* vt = sv + (tile & (NST - 1)) * R::BYTES;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      zero16(s[m]);
+#pragma unroll
+      for (int x = 0; x < KS; ++x) mma(s[m], ad.row(kt, m * (D / 8) + 2 * x), q[m][x]);
+    }
+    zero16(dp);
+#pragma unroll
+    for (int x = 0; x < 2 * KS; ++x) mma(dp, ad.row(vt, 2 * x), go[x]);
+  };
+  auto mask = [&](f32x16 (&s)[2], int tile) __attribute__((always_inline)) {
+    const int lim = a.causal && row + 1 < len ? row + 1 : len;
+    const int k0 = tile * 32 + 4 * h;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool hidden = k0 + 8 * (i >> 2) + (i & 3) >= lim;
+      s[0][i] = hidden ? -INFINITY : s[0][i];
+      s[1][i] = hidden ? -INFINITY : s[1][i];
+    }
+  };
+  // S and dP of a tile -> dS of both maps
+  auto grads = [&](f32x16 (&s)[2], const f32x16& dp) __attribute__((always_inline)) {
+    float part = 0.f;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float p = fast_exp2(fmaf(s[m][i], sc, -lse[m]));
+        if (m == 1) part = fmaf(p, dp[i], part);
+        s[m][i] = p * (dp[i] - ds[m]);
+      }
+    dlam += (double)part;
+  };
+  auto accumulate = [&](const f32x16 (&s)[2], int tile) __attribute__((always_inline)) {
+    const unsigned char* kt = sk + (tile & (NST - 1)) * R::BYTES;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const Frag<bf16> sf = acc_frag<bf16>(s[m], cc);
+#pragma unroll
+        for (int t = 0; t < DT; ++t) mma(dq[m][t], ad.col(kt, m * DT + t, cc), sf);
+      }
+  };
+
+  if (nt > 0) {
+    // PIPE: tile i + 1's products run in iteration i, which still needs K of tile i
+    constexpr int AHEAD = PIPE ? 1 : 0;
+    f32x16 s[2], dp;
+    if constexpr (PIPE) issue_tile(0);
+    issue_tile(AHEAD);
+    issue_tile(AHEAD + 1);
+    if constexpr (PIPE) {
+      wait_vm<4 * PW>();
+      lds_barrier();
+      scores(s, dp, 0);
+      if (wfull <= 0) mask(s, 0);
+    }
+    auto advance = [&](int i) __attribute__((always_inline)) {
+      wait_vm<2 * PW>();          // tile i + AHEAD has landed
+      lds_barrier();
+      issue_tile(i + AHEAD + 2);  // into the slot of tile i - 1 or i - 2
+    };
+    for (int i = 0; i < wt; ++i) {
+      advance(i);
+      f32x16 nx[2], ndp;
+      if constexpr (PIPE) {
+        scores(nx, ndp, i + 1);
+      } else {
+        scores(s, dp, i);
+        if (i >= wfull) mask(s, i);
+      }
+      grads(s, dp);
+      accumulate(s, i);
+      if constexpr (PIPE) {
+        if (i + 1 >= wfull) mask(nx, i + 1);
+        s[0] = nx[0];
+        s[1] = nx[1];
+        dp = ndp;
+      }
+    }
+    for (int i = wt; i < nt; ++i) advance(i);
+    wait_vm<0>();
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) dlam += __shfl_xor(dlam, o);
+  if (lane == 0) a.dlam_part[blockIdx.x * 4 + wave] = dlam;
+  if (row >= a.L) return;
+  bf16* out = reinterpret_cast<bf16*>(a.dq) + qoff;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float f = m ? -lam * a.scale : a.scale;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int d = 32 * t + 2 * i + 4 * h;
+        if (d >= a.hd) continue;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = rok ? dq[m][t][i + e] * f : 0.f;
+        store4<bf16>(out + m * a.hd + d, x[0], x[1], x[2], x[3]);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dK and dV.  A wave owns 32 keys (K's rows in registers; V's rows in registers
+// up to D = 64, else in LDS) and walks the query tiles of its group's heads:
+// scores and dP = dO V^T with a key per lane, then dV^T += dO^T (P_1 - lambda P_2)
+// and dK_m^T += Q_m^T dS_m with the tile's rows read by columns.  A key's column
+// never meets another's, so keys past the end need no mask: their results are
+// written as 0.  The heads of a group are cut into `split` parts where one
+// workgroup per key block would leave CUs idle; the parts' sums are then fp32
+// and diff_dkv_sum adds them in order.
+template <int D>
+__global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
+  using R = RowTile<D>;
+  constexpr int DT = D / 32, NT = D / 16, KS = D / 16, NST = 2, PW = R::PER_WAVE;
+  constexpr bool VREG = D <= 64;
+  constexpr int STAT = 4 * 64 * 4;      // lse and D of both maps for 64 rows (32 in use)
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * NST * R::BYTES + (VREG ? 0 : 4 * R::BYTES) + NST * STAT];
+  unsigned char* const sq = smem;
+  unsigned char* const sg = smem + NST * R::BYTES;
+  unsigned char* const sv = smem + 2 * NST * R::BYTES;
+  unsigned char* const ss = sv + (VREG ? 0 : 4 * R::BYTES);
+  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int blk, gs, b;
+  locate(blockIdx.x, a.gp * a.split * a.B, a.gp * a.split, blk, gs, b);
+  const int g = gs / a.split, part = gs % a.split;
+  const int grp = a.hp / a.gp, nh = grp / a.split, len = a.lens[b];
+  const int k0 = blk * 128, key = k0 + wave * 32 + c;           // causal: the first keys have the most queries
+  const bool kok = key < len;
+  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
+  const long long koff = (tok0 + key) * ldk + g * 2 * a.hd;
+  const float lam = a.lam[0];
+  const int pr0 = g * grp + part * nh;
+  const int t0 = a.causal ? k0 / 32 : 0;                        // first query tile
+  const int ntile = k0 < len ? (len + 31) / 32 - t0 : 0, total = ntile * nh;
+
+  int srow[PW];
+  unsigned scol[PW];
+#pragma unroll
+  for (int i = 0; i < PW; ++i) R::source(wave * PW + i, lane, a.hd, srow[i], scol[i]);
+  const int last = len - 1;
+  Frag<bf16> kf[2][KS], vf[VREG ? 2 * KS : 1];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int col = s * 16 + h * 8;
+      const bool ok = kok && col < a.hd;
+      kf[m][s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.k) + koff + m * a.hd + col, ok);
+      if constexpr (VREG) vf[m * KS + s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.v) + koff + m * a.hd + col, ok);
+    }
+  if constexpr (!VREG) {
+    // the workgroup's 128 rows of V, zeros where dO's tile repeats columns
+    for (int i = threadIdx.x; i < 128 * R::CH; i += 256) {
+      const int r = i / R::CH, p = i % R::CH, cl = p ^ (int)swz<D>((unsigned)r & 31);
+      const int m = cl / (D / 8), d = (cl % (D / 8)) * 8;
+      const bool ok = k0 + r < len && d < a.hd;
+      const Frag<bf16> x = load_row<bf16>(reinterpret_cast<const bf16*>(a.v) + (tok0 + k0 + r) * ldk + g * 2 * a.hd + m * a.hd + d, ok);
+      *reinterpret_cast<bf16x8*>(sv + r * R::PITCH + p * 16) = x.v;
+    }
+  }
+  const unsigned ldb = (unsigned)ldq * 2u;
+  int it_pr = pr0, it_t = t0;                                   // the next tile to load
+  // statistics: wave w loads lse (w < 2) or D of map w % 2, 64 rows
+  const float* const sbase = (wave < 2 ? a.lse : a.dsum) + (long long)b * a.hp * 2 * a.L + (wave & 1) * a.L;
+  auto issue_next = [&](int it) __attribute__((always_inline)) {
+    const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((it & 1) * R::BYTES + wave * PW * 1024));
+    const bf16* qb = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.q) + tok0 * ldq + it_pr * 2 * a.hd));
+    const bf16* gb = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.da) + tok0 * ldq + it_pr * 2 * a.hd));
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      int r = it_t * 32 + srow[i];
+      r = r < last ? r : last;
+      const unsigned off = (unsigned)r * ldb + scol[i];
+      dma16(qb, off, lds_addr(sq) + d0 + i * 1024);
+      dma16(gb, off, lds_addr(sg) + d0 + i * 1024);
+    }
+    int r = it_t * 32 + lane;
+    r = r < last ? r : last;
+    const float* sb = reinterpret_cast<const float*>(uniform(sbase + (long long)it_pr * 2 * a.L));
+    const unsigned sd = __builtin_amdgcn_readfirstlane(lds_addr(ss) + (unsigned)((it & 1) * STAT + wave * 256));
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, %2"
+                 :: "v"((unsigned)r * 4u), "s"(sd), "s"(sb) : "memory", "m0");
+    if (++it_t == t0 + ntile) {
+      it_t = t0;
+      if (it_pr + 1 < pr0 + nh) ++it_pr;                        // past the last: read again, used by none
+    }
+  };
+
+  TileAddr<D> ad;
+  ad.init(lane, true, true);
+  f32x16 dk[2][DT], dv[NT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < DT; ++t) zero16(dk[m][t]);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) zero16(dv[t]);
+  const float sc = a.scale * kLog2e;
+
+  if (total > 0) {
+    issue_next(0);
+    int it = 0;
+    auto advance = [&]() __attribute__((always_inline)) {
+      wait_vm<0>();               // tile `it` has landed
+      lds_barrier();              // ... for every wave, and the other slot is read by none
+      issue_next(it + 1);
+    };
+    const int skip = a.causal ? (wave < ntile ? wave : ntile) : 0;   // tiles before this wave's keys
+    for (int n = 0; n < nh; ++n) {
+      for (int j = 0; j < skip; ++j, ++it) advance();
+      for (int j = skip; j < ntile; ++j, ++it) {
+        advance();
+        const int q0 = (t0 + j) * 32;
+        const unsigned char* qt = sq + (it & 1) * R::BYTES;
+        const unsigned char* gt = sg + (it & 1) * R::BYTES;
+        const float* st = reinterpret_cast<const float*>(ss + (it & 1) * STAT);
+        f32x16 dp, s, w;
+        zero16(dp);
+#pragma unroll
+        for (int x = 0; x < 2 * KS; ++x) {
+          if constexpr (VREG) mma(dp, ad.row(gt, 2 * x), vf[x]);
+          else mma(dp, ad.row(gt, 2 * x), ad.row(sv + wave * R::BYTES, 2 * x));
+        }
+        const bool masked = q0 + 32 > len || (a.causal && q0 < k0 + wave * 32 + 31);
+        const int first = a.causal ? key : 0;                   // queries that read this key: first .. len - 1
+        Frag<bf16> df[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          zero16(s);
+#pragma unroll
+          for (int x = 0; x < KS; ++x) mma(s, ad.row(qt, m * (D / 8) + 2 * x), kf[m][x]);
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(st + m * 64 + 2 * i + 4 * h);
+            const float4 d4 = *reinterpret_cast<const float4*>(st + (2 + m) * 64 + 2 * i + 4 * h);
+            const float le[4] = {l4.x, l4.y, l4.z, l4.w}, de[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float p = fast_exp2(fmaf(s[i + e], sc, -le[e]));
+              if (masked) {
+                const int qr = q0 + 2 * i + 4 * h + e;
+                p = qr < first || qr >= len ? 0.f : p;
+              }
+              w[i + e] = m ? fmaf(-lam, p, w[i + e]) : p;
+              s[i + e] = p * (dp[i + e] - de[e]);
+            }
+          }
+          df[m][0] = acc_frag<bf16>(s, 0);
+          df[m][1] = acc_frag<bf16>(s, 1);
+        }
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const Frag<bf16> wf = acc_frag<bf16>(w, cc);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma(dv[t], ad.col(gt, t, cc), wf);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int t = 0; t < DT; ++t) mma(dk[m][t], ad.col(qt, m * DT + t, cc), df[m][cc]);
+        }
+      }
+    }
+    wait_vm<0>();
+  }
+  if (key >= a.L) return;
+  const long long pofs = (long long)part * a.B * a.L * ldk + koff;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int e = (32 * t) % D + 2 * i + 4 * h, m = 32 * t / D;
+      if (e >= a.hd) continue;
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = kok ? dv[t][i + j] : 0.f;
+      if (a.split > 1) store4<float>(a.dv_part + pofs + m * a.hd + e, x[0], x[1], x[2], x[3]);
+      else store4<bf16>(reinterpret_cast<bf16*>(a.dv) + koff + m * a.hd + e, x[0], x[1], x[2], x[3]);
+    }
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float f = m ? -lam * a.scale : a.scale;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int d = 32 * t + 2 * i + 4 * h;
+        if (d >= a.hd) continue;
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = kok ? dk[m][t][i + j] * f : 0.f;
+        if (a.split > 1) store4<float>(a.dk_part + pofs + m * a.hd + d, x[0], x[1], x[2], x[3]);
+        else store4<bf16>(reinterpret_cast<bf16*>(a.dk) + koff + m * a.hd + d, x[0], x[1], x[2], x[3]);
+      }
+  }
+}
+
+// dK and dV from the parts' sums, in order; 4 values per thread.
+__global__ void __launch_bounds__(256) diff_dkv_sum(const DiffArgs a) {
+  const long long n = (long long)a.B * a.L * a.gp * 2 * a.hd / 4;
+  long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const bool v = i >= n;
+  if (v) i -= n;
+  if (i >= n) return;
+  const float4* src = reinterpret_cast<const float4*>(v ? a.dv_part : a.dk_part) + i;
+  float4 x = src[0];
+  for (int p = 1; p < a.split; ++p) {
+    const float4 y = src[p * n];
+    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+  }
+  store4<bf16>(reinterpret_cast<bf16*>(v ? a.dv : a.dk) + 4 * i, x.x, x.y, x.z, x.w);
+}
+
+// D_1 = dO . (O + lambda O_2) and D_2 = dO . O_2 from the saved integers.  LP
+// lanes (a power of two) per row and head pair, 8 values each.
+__global__ void __launch_bounds__(256) diff_dsum_q(const DiffArgs a, int lp_log2) {
+  const int lp = 1 << lp_log2, sub = threadIdx.x & (lp - 1);
+  const long long n = (long long)a.B * a.L * a.hp;
+  const float lam = a.lam[0];
+  const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> lp_log2;
+  const bool on = w < n;
+  const int pair = on ? (int)(w % a.hp) : 0;
+  const long long tok = on ? w / a.hp : 0;
+  const int b = (int)(tok / a.L), row = (int)(tok % a.L);
+  const long long st = (long long)(b * a.hp + pair) * 2 * a.L + row;
+  float d1 = 0.f, d2 = 0.f, r1 = 0.f;
+  if (on && row < a.lens[b] && 8 * sub < 2 * a.hd) {
+    const long long at = (tok * a.hp + pair) * 2 * a.hd + 8 * sub;
+    const uint4 gv = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.da) + at);
+    const uint4 ov = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.a) + at);
+    const uint4 yv = *reinterpret_cast<const uint4*>(reinterpret_cast<const short*>(a.o2) + at);
+    const uint2 rv = *reinterpret_cast<const uint2*>(a.res + at);
+    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, ow[4] = {ov.x, ov.y, ov.z, ov.w}, yw[4] = {yv.x, yv.y, yv.z, yv.w};
+    const uint32_t rw[2] = {rv.x, rv.y};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float gx = bf2f((uint16_t)(gw[j >> 1] >> (16 * (j & 1)))), ox = bf2f((uint16_t)(ow[j >> 1] >> (16 * (j & 1))));
+      const float y = (float)(short)(yw[j >> 1] >> (16 * (j & 1)));
+      const float r = (float)(signed char)(rw[j >> 2] >> (8 * (j & 3)));
+      d1 = fmaf(gx, ox, d1);
+      r1 = fmaf(gx, r, r1);
+      d2 = fmaf(gx, y, d2);
+    }
+    d2 *= a.rsc[st + a.L];
+    d1 = fmaf(r1, a.rsc[st], d1);
+    d1 = fmaf(lam, d2, d1);
+  }
+  for (int o = lp >> 1; o; o >>= 1) {
+    d1 += __shfl_xor(d1, o);
+    d2 += __shfl_xor(d2, o);
+  }
+  if (on && sub == 0) {
+    a.dsum[st] = d1;
+    a.dsum[st + a.L] = d2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32: D_1 = dO . (O + lambda O_2), D_2 = dO . O_2, one wave per row and head pair.
+__global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
+  using T = float;
+  const int lane = threadIdx.x & 63;
+  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const long long rows = (long long)a.B * a.L;
+  if (w >= rows * a.hp) return;
+  const int pair = (int)(w % a.hp);
+  const long long tok = w / a.hp;
+  const int b = (int)(tok / a.L), row = (int)(tok % a.L);
+  const float lam = a.lam[0];
+  float d1 = 0.f, d2 = 0.f;
+  if (row < a.lens[b]) {
+    const long long at = (tok * a.hp + pair) * 2 * a.hd;
+    const T* dop = reinterpret_cast<const T*>(a.da) + at;
+    const T* op = reinterpret_cast<const T*>(a.a) + at;
+    const T* o2p = reinterpret_cast<const T*>(a.o2) + at;
+    for (int i = lane; i < 2 * a.hd; i += 64) {
+      const float g = ldv(dop, i), y = ldv(o2p, i);
+      d1 = fmaf(g, ldv(op, i) + lam * y, d1);
+      d2 = fmaf(g, y, d2);
+    }
+  }
+  d1 = wave_sum(d1);
+  d2 = wave_sum(d2);
+  if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.L + row] = lane ? d2 : d1;
+}
+
+// dQ: one wave per 32 queries, keys in order.  It also sums P_2 dP, whose total
+// is -dlambda, in fp32 (D_2 of the saved, rounded O_2 would not be exact enough).
+template <int D>
+__global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
+  using T = float;
+  constexpr int DT = D / 32;
+  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
+  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int nqb = (a.L + 31) / 32;
+  if (wave >= nqb * a.hp * a.B) {
+    if (lane == 0) a.dlam_part[wave] = 0.0;
+    return;
+  }
+  const int qb = nqb - 1 - wave / (a.hp * a.B);
+  const int pair = (wave / a.B) % a.hp, b = wave % a.B;
+  const int g = pair / (a.hp / a.gp), len = a.lens[b];
+  const float lam = a.lam[0];
+  const int row = qb * 32 + c;
+  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
+  const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd, koff = tok0 * ldk + g * 2 * a.hd;
+  const T* qp = reinterpret_cast<const T*>(a.q) + qoff;
+  const T* dop = reinterpret_cast<const T*>(a.da) + qoff;
+  const T* kp = reinterpret_cast<const T*>(a.k) + koff;
+  const T* vp = reinterpret_cast<const T*>(a.v) + koff;
+  const bool rok = row < len;
+  float lse[2], ds[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.L + row;
+    lse[m] = rok ? a.lse[at] : INFINITY;
+    ds[m] = rok ? a.dsum[at] : 0.f;
+  }
+  f32x16 dq[2][DT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < DT; ++t) zero16(dq[m][t]);
+  const float sc = a.scale * kLog2e;
+  double dlam = 0.0;
+  int kend = len;
+  if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
+  if (qb * 32 >= len) kend = 0;
+  for (int k0 = 0; k0 < kend; k0 += 32) {
+    const int kz = opaque(0);
+    f32x16 dp, s[2];
+    float part = 0.f;
+    zero16(dp);
+#pragma unroll
+    for (int ks = 0; ks < D / 8; ++ks) {
+      const int col = ks * 16 + h * 8;
+      const bool cok = col < 2 * a.hd;
+      const Frag<T> vf = load_row<T>(vp + (long long)(k0 + c) * ldk + col, cok && k0 + c < len);
+      const Frag<T> gf = load_row<T>(dop + col + kz, cok && rok);
+      mma(dp, vf, gf);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      zero16(s[m]);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int col = ks * 16 + h * 8;
+        const bool cok = col < a.hd;
+        const Frag<T> kf = load_row<T>(kp + (long long)(k0 + c) * ldk + m * a.hd + col, cok && k0 + c < len);
+        const Frag<T> qf = load_row<T>(qp + m * a.hd + col + kz, cok && rok);
+        mma(s[m], kf, qf);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
+        const bool hidden = key >= len || (a.causal && key > row) || !rok;
+        const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m]));
+        if (m == 1) part = fmaf(p, dp[i], part);
+        s[m][i] = p * (dp[i] - ds[m]);
+      }
+    }
+    dlam += (double)part;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const Frag<T> sf = acc_frag<T>(s[m], cc);
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          const int d = 32 * t + c;
+          const Frag<T> kf = load_col(kp + m * a.hd + d, ldk, k0 + 16 * cc, len, h, d < a.hd);
+          mma(dq[m][t], kf, sf);
+        }
+      }
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) dlam += __shfl_xor(dlam, o);
+  if (lane == 0) a.dlam_part[wave] = dlam;
+  if (row >= a.L) return;
+  T* out = reinterpret_cast<T*>(a.dq) + qoff;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float f = m ? -lam * a.scale : a.scale;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int d = 32 * t + 2 * i + 4 * h;
+        if (d >= a.hd) continue;
+        store4<T>(out + m * a.hd + d, dq[m][t][i] * f, dq[m][t][i + 1] * f, dq[m][t][i + 2] * f, dq[m][t][i + 3] * f);
+      }
+  }
+}
+
+// dK and dV: one wave per 32 keys; the query pairs of the group in order, their
+// queries in order.
+template <int D>
+__global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
+  using T = float;
+  constexpr int DT = D / 32, NT = D / 16;
+  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
+  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int nkb = (a.L + 31) / 32;
+  if (wave >= nkb * a.gp * a.B) return;
+  const int kb = wave / (a.gp * a.B);                 // causal: the first keys have the most queries
+  const int g = (wave / a.B) % a.gp, b = wave % a.B;
+  const int grp = a.hp / a.gp, len = a.lens[b];
+  const float lam = a.lam[0];
+  const int key = kb * 32 + c;
+  const bool kok = key < len;
+  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
+  const long long koff = (tok0 + key) * ldk + g * 2 * a.hd;
+  const T* kp = reinterpret_cast<const T*>(a.k) + koff;
+  const T* vp = reinterpret_cast<const T*>(a.v) + koff;
+  f32x16 dk[2][DT], dv[NT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < DT; ++t) zero16(dk[m][t]);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) zero16(dv[t]);
+  const float sc = a.scale * kLog2e;
+  const int qbeg = a.causal ? kb * 32 : 0;
+  for (int pr = g * grp; pr < (g + 1) * grp; ++pr) {
+    const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * ldq + pr * 2 * a.hd;
+    const T* dop = reinterpret_cast<const T*>(a.da) + tok0 * ldq + pr * 2 * a.hd;
+    const float* lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.L;
+    const float* dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.L;
+    for (int q0 = kb * 32 < len ? qbeg : len; q0 < len; q0 += 32) {
+      const int kz = opaque(0);
+      f32x16 dp, s[2], w;
+      zero16(dp);
+#pragma unroll
+      for (int ks = 0; ks < D / 8; ++ks) {
+        const int col = ks * 16 + h * 8;
+        const bool cok = col < 2 * a.hd;
+        const Frag<T> gf = load_row<T>(dop + (long long)(q0 + c) * ldq + col, cok && q0 + c < len);
+        const Frag<T> vf = load_row<T>(vp + col + kz, cok && kok);
+        mma(dp, gf, vf);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        zero16(s[m]);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int col = ks * 16 + h * 8;
+          const bool cok = col < a.hd;
+          const Frag<T> qf = load_row<T>(qp + (long long)(q0 + c) * ldq + m * a.hd + col, cok && q0 + c < len);
+          const Frag<T> kf = load_row<T>(kp + m * a.hd + col + kz, cok && kok);
+          mma(s[m], qf, kf);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3);
+          const bool hidden = q >= len || (a.causal && key > q) || !kok;
+          const int qq = q < len ? q : 0;
+          const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m * a.L + qq]));
+          w[i] = m ? w[i] - lam * p : p;
+          s[m][i] = p * (dp[i] - dsm[m * a.L + qq]);
+        }
+      }
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const Frag<T> wf = acc_frag<T>(w, cc);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int d = 32 * t + c;
+          const Frag<T> gf = load_col(dop + d, ldq, q0 + 16 * cc, len, h, d < 2 * a.hd);
+          mma(dv[t], gf, wf);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const Frag<T> sf = acc_frag<T>(s[m], cc);
+#pragma unroll
+          for (int t = 0; t < DT; ++t) {
+            const int d = 32 * t + c;
+            const Frag<T> qf = load_col(qp + m * a.hd + d, ldq, q0 + 16 * cc, len, h, d < a.hd);
+            mma(dk[m][t], qf, sf);
+          }
+        }
+      }
+    }
+  }
+  if (key >= a.L) return;
+  T* dkp = reinterpret_cast<T*>(a.dk) + koff;
+  T* dvp = reinterpret_cast<T*>(a.dv) + koff;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int d = 32 * t + 2 * i + 4 * h;
+      if (d < 2 * a.hd) store4<T>(dvp + d, dv[t][i], dv[t][i + 1], dv[t][i + 2], dv[t][i + 3]);
+    }
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float f = m ? -lam * a.scale : a.scale;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int d = 32 * t + 2 * i + 4 * h;
+        if (d < a.hd)
+          store4<T>(dkp + m * a.hd + d, dk[m][t][i] * f, dk[m][t][i + 1] * f, dk[m][t][i + 2] * f, dk[m][t][i + 3] * f);
+      }
+  }
+}
+
+// dlambda = -(sum of the partial sums, in a fixed order); the four vectors' gradients.
+__global__ void __launch_bounds__(1024) diff_dlambda(const DiffArgs a) {
+  __shared__ double sm[16];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < a.npart; i += 1024) s += a.dlam_part[i];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int i = 0; i < 16; ++i) s += sm[i];
+  const int i = threadIdx.x;
+  if (i < a.hd) {
+    const float g1 = -(float)s * a.lam[1], g2 = (float)s * a.lam[2];
+    const float q1 = a.lq1[i], k1 = a.lk1[i], q2 = a.lq2[i], k2 = a.lk2[i];
+    a.dlq1[i] = g1 * k1;
+    a.dlk1[i] = g1 * q1;
+    a.dlq2[i] = g2 * k2;
+    a.dlk2[i] = g2 * q2;
+  }
+}
+
+void launch_diff_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
+  const long long rows = (long long)a.B * a.L * a.hp;
+  const int blocks = (a.L + 127) / 128 * a.B;
+  if (dt == SL_BF16) {
+    int lg = 0;
+    while ((8 << lg) < 2 * a.hd) ++lg;
+    const long long per = 256 >> lg;
+    hipLaunchKernelGGL(diff_dsum_q, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a, lg);
+  } else {
+    hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
+  }
+  by_width(a.hd, [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    const dim3 gq((unsigned)(blocks * a.hp)), gk((unsigned)(blocks * a.gp * a.split));
+    if (dt == SL_BF16) {
+      hipLaunchKernelGGL(diff_dq_lds<D>, gq, dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_lds<D>, gk, dim3(256), 0, s, a);
+    } else {
+      hipLaunchKernelGGL(diff_dq_direct<D>, gq, dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_direct<D>, gk, dim3(256), 0, s, a);
+    }
+  });
+  if (a.split > 1) {
+    const long long n = 2 * ((long long)a.B * a.L * a.gp * 2 * a.hd / 4);
+    hipLaunchKernelGGL(diff_dkv_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+  }
+  hipLaunchKernelGGL(diff_dlambda, dim3(1), dim3(1024), 0, s, a);
+}
+
+}  // namespace sl

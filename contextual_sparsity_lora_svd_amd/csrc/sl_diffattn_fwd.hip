@@ -1,0 +1,486 @@
+// Differential attention: forward kernels.
+#include "sl_diffattn_lds.hpp"
+
+namespace sl {
+
+// ---------------------------------------------------------------------------
+// Forward.  A wave owns 32 queries of both maps (D <= 64) or of one (D > 64: two
+// maps' accumulators of 2 D columns would leave no register for a second wave
+// on the SIMD).  The score tiles are formed transposed (keys x queries), so a
+// lane holds 16 keys of one query: the weights are the next product's operand
+// as they stand and nothing is exchanged between lanes.
+//
+// The weights are taken relative to the maximum of the row's first tile and the
+// accumulators never rescaled (fp32 and bf16 reach 2^127 alike, and a sum of at
+// least 1 loses nothing to small weights).  A row whose sum passes 2^64 makes
+// the workgroup go again, after a pass that finds every row's maximum.
+//
+// Two waves of a SIMD cover each other's exponentials and LDS reads.  One barrier
+// per tile keeps a workgroup's waves in step; where both waves of a SIMD belong
+// to one workgroup (D > 64) the second map's waves pass it half a tile later, so
+// that one does its exponentials while the other feeds the matrix cores.  The
+// weights are rounded to bf16 for the matrix cores (half a step, 2^-8); their
+// sum is not.
+template <int D> struct FwdShape {
+  static constexpr int MAPS = D > 64 ? 1 : 2;            // maps per wave
+  static constexpr int WAVES = 8 / MAPS;
+  static constexpr int NDMA = RowTile<D>::NDMA;
+  static constexpr int PW = (NDMA + WAVES - 1) / WAVES;  // the last instruction may be issued twice
+};
+
+template <int D>
+__global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const DiffArgs a) {
+  using R = RowTile<D>;
+  using S = FwdShape<D>;
+  constexpr int NT = D / 16, KS = D / 16, NST = 4, PW = S::PW, M = S::MAPS;
+  constexpr int P2 = 4 * D + 16, P1 = 2 * D + 16;         // staged result rows: 2-byte and 1-byte values
+  constexpr int STAGED = S::WAVES * 32 * P2;
+  constexpr int RING = 2 * NST * R::BYTES > STAGED ? 2 * NST * R::BYTES : STAGED;
+  static_assert(M == 2 || 4 * NT * 4096 <= RING, "four waves' P_2 V fit the ring");
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[RING + 64];
+  unsigned char* const sk = smem;
+  unsigned char* const sv = smem + NST * R::BYTES;
+  float* const slam = reinterpret_cast<float*>(smem + RING);
+  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m0 = M == 1 ? wave >> 2 : 0, rb = wave & 3;   // first (or only) map, block of 32 rows
+  const bool late = M == 1 && m0 == 1;
+  const int nqb = (a.L + 127) / 128;
+  int blk, pair, b;
+  locate(blockIdx.x, a.hp * a.B, a.hp, blk, pair, b);
+  const int q0 = (nqb - 1 - blk) * 128, len = a.lens[b], g = pair / (a.hp / a.gp);
+  const int row0 = q0 + rb * 32, row = row0 + c;
+  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
+  const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd;
+  const bf16* kbase = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.k) + tok0 * ldk + g * 2 * a.hd));
+  const bf16* vbase = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.v) + tok0 * ldk + g * 2 * a.hd));
+  const bool rok = row < len;
+
+  int kend = q0 < len ? len : 0, wend = row0 < len ? len : 0;
+  if (a.causal) {
+    kend = kend < q0 + 128 ? kend : q0 + 128;
+    wend = wend < row0 + 32 ? wend : row0 + 32;
+  }
+  const int nt = (kend + 31) / 32, wt = (wend + 31) / 32;      // key tiles of the workgroup, of this wave
+  // tiles from here on hold keys that some query of the wave does not read
+  const int wfull = (a.causal && row0 + 1 < len ? row0 + 1 : len) / 32;
+
+  Frag<bf16> q[M][KS];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int col = s * 16 + h * 8;
+      q[m][s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.q) + qoff + (m0 + m) * a.hd + col, rok && col < a.hd);
+    }
+  int srow[PW], sins[PW];
+  unsigned scol[PW];
+#pragma unroll
+  for (int i = 0; i < PW; ++i) {
+    sins[i] = wave * PW + i < R::NDMA ? wave * PW + i : R::NDMA - 1;
+    R::source(sins[i], lane, a.hd, srow[i], scol[i]);
+  }
+  const unsigned ldb = (unsigned)ldk * 2u;
+  const int last = len - 1;
+  auto issue = [&](const bf16* base, unsigned char* ring, int tile) __attribute__((always_inline)) {
+    const unsigned dst = lds_addr(ring) + (unsigned)((tile & (NST - 1)) * R::BYTES);
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {
+      int r = tile * 32 + srow[i];
+      r = r < last ? r : last;
+      dma16(base, (unsigned)r * ldb + scol[i], __builtin_amdgcn_readfirstlane(dst + sins[i] * 1024));
+    }
+  };
+  // group j: V of tile j, K of the tile after it
+  auto issue_group = [&](int j) __attribute__((always_inline)) {
+    issue(kbase, sk, j + 1);
+    issue(vbase, sv, j);
+  };
+
+  TileAddr<D> ad;
+  ad.init(lane, M == 2, true);
+  unsigned kx[KS];                // M = 1: addresses of this wave's map in a row of K
+#pragma unroll
+  for (int x = 0; x < KS; ++x)
+    kx[x] = (unsigned)c * R::PITCH + 16 * (((unsigned)(m0 * (D / 8) + 2 * x) + h) ^ swz<D>((unsigned)c));
+  f32x16 o[M][NT];
+  float mx[M], sum[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    mx[m] = sum[m] = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) zero16(o[m][t]);
+  }
+  const float sc = a.scale * kLog2e;
+
+  auto scores = [&](f32x16 (&s)[M], int tile) __attribute__((always_inline)) {
+    const unsigned char* kt = sk + (tile & (NST - 1)) * R::BYTES;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      zero16(s[m]);
+#pragma unroll
+      for (int x = 0; x < KS; ++x) mma(s[m], M == 1 ? lds_row(kt + kx[x]) : ad.row(kt, m * (D / 8) + 2 * x), q[m][x]);
+    }
+  };
+  auto mask = [&](f32x16 (&s)[M], int tile) __attribute__((always_inline)) {
+    const int lim = a.causal && row + 1 < len ? row + 1 : len;   // keys this query reads
+    const int k0 = tile * 32 + 4 * h;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool hidden = k0 + 8 * (i >> 2) + (i & 3) >= lim;
+#pragma unroll
+      for (int m = 0; m < M; ++m) s[m][i] = hidden ? -INFINITY : s[m][i];
+    }
+  };
+  auto tile_max = [&](const f32x16& s) __attribute__((always_inline)) {
+    float t = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t = fmaxf(t, s[i]);
+    return pair_max(t);
+  };
+
+  if (wave == 0) {
+    float e1, e2;
+    const float lam = lambda_of(a, e1, e2);
+    if (lane == 0) {
+      slam[0] = lam;
+      if (blockIdx.x == 0) {
+        a.lam[0] = lam;
+        a.lam[1] = e1;
+        a.lam[2] = e2;
+      }
+    }
+  }
+  for (bool exact = false;; exact = true) {
+    float big = 0.f;
+    if (nt > 0) {
+      f32x16 s[M];
+      if (exact) {
+        for (int i = 0; i < nt; ++i) {
+          issue(kbase, sk, i);
+          wait_vm<0>();
+          lds_barrier();
+          if (i < wt) {
+            scores(s, i);
+            if (i >= wfull) mask(s, i);
+#pragma unroll
+            for (int m = 0; m < M; ++m) mx[m] = i == 0 ? tile_max(s[m]) : fmaxf(mx[m], tile_max(s[m]));
+          }
+        }
+        lds_barrier();
+      }
+      issue(kbase, sk, 0);
+      issue_group(0);
+      issue_group(1);
+      wait_vm<4 * PW>();
+      lds_barrier();
+      scores(s, 0);
+      if (wfull <= 0) mask(s, 0);
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        if (!exact) mx[m] = tile_max(s[m]);
+        sum[m] = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) zero16(o[m][t]);
+      }
+      auto sync = [&](int n) __attribute__((always_inline)) {
+        wait_vm<2 * PW>();        // group n has landed, n + 1 may be in flight
+        lds_barrier();            // ... for every wave, and all are done with group n - 2
+        issue_group(n + 2);       // past the last tile: rows of the end again, read by none
+      };
+      if (late) sync(0);
+      for (int i = 0; i < wt; ++i) {
+        if (!late) sync(i);
+        Frag<bf16> p[M][2];
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const float ms = mx[m] * sc;
+          float ts = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            s[m][e] = fast_exp2(fmaf(s[m][e], sc, -ms));
+            ts += s[m][e];
+          }
+          sum[m] += ts;
+          p[m][0] = acc_frag<bf16>(s[m], 0);
+          p[m][1] = acc_frag<bf16>(s[m], 1);
+        }
+        if (late) sync(i + 1);
+        const unsigned char* vt = sv + (i & (NST - 1)) * R::BYTES;
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const Frag<bf16> vf = ad.col(vt, t, cc);
+#pragma unroll
+            for (int m = 0; m < M; ++m) mma(o[m][t], vf, p[m][cc]);
+          }
+        scores(s, i + 1);         // past the last tile: unused
+        if (i + 1 >= wfull) mask(s, i + 1);
+      }
+      for (int i = wt; i < nt; ++i) sync(late ? i + 1 : i);
+      if (!late) sync(nt);
+      wait_vm<0>();               // no DMA outlives the sweep
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const float l = pair_sum(sum[m]);
+        if (rok && !(l < 0x1p64f)) big = 1.f;
+      }
+    }
+    lds_barrier();
+    if (exact) break;
+    const bool again = __any(big != 0.f);
+    if (lane == 0) reinterpret_cast<int*>(smem)[wave] = again;
+    lds_barrier();
+    int any = 0;
+#pragma unroll
+    for (int w = 0; w < S::WAVES; ++w) any |= reinterpret_cast<const int*>(smem)[w];
+    lds_barrier();
+    if (!any) break;
+  }
+
+  // The sweep's last barrier is behind every wave: the ring is free, and lambda
+  // is there.  The second map's waves hand P_2 V over in fp32.  For the backward
+  // O_2 is kept as 16-bit integers of its row's largest value, and what O's
+  // rounding to bf16 drops in 8 bits: D_m = dO . (P_m V) is then exact to 2^-16,
+  // where an error of D would add up over the whole row of keys.
+  const float lam = slam[0];
+  const long long stat = (long long)(b * a.hp + pair) * 2 * a.L + row;
+  const long long goff = (tok0 + row0) * ldq + pair * 2 * a.hd;   // the wave's first row
+  const int rows = a.L - row0 < 32 ? a.L - row0 : 32;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const float l = pair_sum(sum[m]);
+    const float inv = rok ? 1.f / l : 0.f;
+    if (h == 0 && row < a.L) a.lse[stat + (m0 + m) * a.L] = rok ? mx[m] * sc + __log2f(l) : INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[m][t][i] = rok ? o[m][t][i] * inv : 0.f;
+  }
+  // column of accumulator value (t, i): V's tile has D per half, hd of them in
+  // use, and 4 neighbours are in or out together
+  auto column = [&](int t, int i, bool& in) __attribute__((always_inline)) {
+    const int e0 = (32 * t) % D + 2 * i + 4 * h;
+    in = e0 < a.hd;
+    return 32 * t / D * a.hd + e0;
+  };
+  if constexpr (M == 1) {
+    unsigned char* const xch = smem + rb * NT * 4096 + lane * 16;
+    if (m0 == 1) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(xch + (t * 4 + (i >> 2)) * 1024) =
+              make_float4(o[0][t][i], o[0][t][i + 1], o[0][t][i + 2], o[0][t][i + 3]);
+    }
+    lds_barrier();
+    if (m0 == 0) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(xch + (t * 4 + (i >> 2)) * 1024);
+          o[0][t][i] = fmaf(-lam, y.x, o[0][t][i]);
+          o[0][t][i + 1] = fmaf(-lam, y.y, o[0][t][i + 1]);
+          o[0][t][i + 2] = fmaf(-lam, y.z, o[0][t][i + 2]);
+          o[0][t][i + 3] = fmaf(-lam, y.w, o[0][t][i + 3]);
+        }
+    }
+    lds_barrier();
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[0][t][i] = fmaf(-lam, o[1][t][i], o[0][t][i]);
+  }
+  unsigned char* const st = smem + wave * 32 * P2;
+  if (M == 2 || m0 == 1) {
+    constexpr int m = M - 1;
+    float top = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((32 * t) % D + 8 * (i >> 2) + 4 * h < a.hd) top = fmaxf(top, fabsf(o[m][t][i]));
+    top = pair_max(top);
+    const float f = top > 0.f ? 32767.f / top : 0.f;
+    if (h == 0 && row < a.L) a.rsc[stat + a.L] = top / 32767.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        bool in;
+        const int dv = column(t, i, in);
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = (uint32_t)__float2int_rn(o[m][t][i + e] * f) & 0xFFFFu;
+        if (in) *reinterpret_cast<uint2*>(st + c * P2 + 2 * dv) = make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
+      }
+    store_rows(st, P2, reinterpret_cast<short*>(a.o2) + goff, ldq * 2, 4 * a.hd, rows, lane);
+  }
+  if (M == 2 || m0 == 0) {
+    float top = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        bool in;
+        const int dv = column(t, i, in);
+        if (in)
+          store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + dv, o[0][t][i], o[0][t][i + 1], o[0][t][i + 2], o[0][t][i + 3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[0][t][i + e] -= bf2f(f2bf(o[0][t][i + e]));
+          top = fmaxf(top, in ? fabsf(o[0][t][i + e]) : 0.f);
+        }
+      }
+    top = pair_max(top);
+    if (h == 0 && row < a.L) a.rsc[stat] = top / 127.f;
+    const float f = top > 0.f ? 127.f / top : 0.f;
+    store_rows(st, P2, reinterpret_cast<bf16*>(a.o) + goff, ldq * 2, 4 * a.hd, rows, lane);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        bool in;
+        const int dv = column(t, i, in);
+        uint32_t r4 = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r4 |= ((uint32_t)__float2int_rn(o[0][t][i + e] * f) & 0xFFu) << (8 * e);
+        if (in) *reinterpret_cast<uint32_t*>(st + c * P1 + dv) = r4;
+      }
+    store_rows(st, P1, a.res + goff, ldq, 2 * a.hd, rows, lane);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32: operands straight from memory: the fp32
+// matrix instructions run at a sixteenth of the bf16 rate, so L1 and L2 feed
+// them (2 bytes per cycle and wave at full rate) and LDS would only add waits.
+// One wave per 32 rows; the transposed score
+// tile (keys x queries) leaves a query in a lane pair, so the softmax needs one
+// exchange per tile and its weights feed the second product from registers.
+template <int D>
+__global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
+  using T = float;
+  constexpr int NT = D / 16;   // 32-value tiles of the 2 D wide output
+  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
+  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int nqb = (a.L + 31) / 32;
+  if (wave >= nqb * a.hp * a.B) return;
+  const int qb = nqb - 1 - wave / (a.hp * a.B);       // the longest rows first
+  const int pair = (wave / a.B) % a.hp, b = wave % a.B;
+  const int g = pair / (a.hp / a.gp), len = a.lens[b];
+  float e1, e2;
+  const float lam = lambda_of(a, e1, e2);
+  if (wave == 0 && lane == 0) {
+    a.lam[0] = lam;
+    a.lam[1] = e1;
+    a.lam[2] = e2;
+  }
+  const int row = qb * 32 + c;
+  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
+  const T* qp = reinterpret_cast<const T*>(a.q) + (tok0 + row) * ldq + pair * 2 * a.hd;
+  const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * ldk + g * 2 * a.hd;
+  const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * ldk + g * 2 * a.hd;
+  const bool rok = row < len;
+  f32x16 o[2][NT];
+  float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) zero16(o[m][t]);
+  const float sc = a.scale * kLog2e;
+  int kend = len;
+  if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
+  if (qb * 32 >= len) kend = 0;
+  for (int k0 = 0; k0 < kend; k0 += 32) {
+    const int kz = opaque(0);
+    f32x16 s[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      zero16(s[m]);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int col = ks * 16 + h * 8;
+        const bool cok = col < a.hd;
+        const Frag<T> kf = load_row<T>(kp + (long long)(k0 + c) * ldk + m * a.hd + col, cok && k0 + c < len);
+        const Frag<T> qf = load_row<T>(qp + m * a.hd + col + kz, cok && rok);
+        mma(s[m], kf, qf);
+      }
+      float tm = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
+        if (key >= len || (a.causal && key > row)) s[m][i] = -INFINITY;
+        tm = fmaxf(tm, s[m][i]);
+      }
+      tm = fmaxf(tm, __shfl_xor(tm, 32));
+      const float nm = fmaxf(mx[m], tm);
+      const float ms = nm == -INFINITY ? 0.f : nm * sc;   // nothing seen yet: weights 0
+      const float f = exp2f(mx[m] * sc - ms);
+      float ts = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[m][i] = exp2f(fmaf(s[m][i], sc, -ms));
+        ts += s[m][i];
+      }
+      sum[m] = sum[m] * f + ts;
+      mx[m] = nm;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
+    }
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+      const Frag<T> p0 = acc_frag<T>(s[0], cc), p1 = acc_frag<T>(s[1], cc);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int dv = 32 * t + c;
+        const Frag<T> vf = load_col(vp + dv, ldk, k0 + 16 * cc, len, h, dv < 2 * a.hd);
+        mma(o[0][t], vf, p0);
+        mma(o[1][t], vf, p1);
+      }
+    }
+  }
+  if (row >= a.L) return;
+  float inv[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float l = sum[m] + __shfl_xor(sum[m], 32);
+    inv[m] = rok ? 1.f / l : 0.f;
+    if (h == 0) a.lse[((long long)(b * a.hp + pair) * 2 + m) * a.L + row] = rok ? mx[m] * sc + log2f(l) : INFINITY;
+  }
+  const long long orow = (tok0 + row) * ldq + pair * 2 * a.hd;
+  T* op = reinterpret_cast<T*>(a.o) + orow;
+  T* o2p = reinterpret_cast<T*>(a.o2) + orow;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int dv = 32 * t + 2 * i + 4 * h;
+      if (dv >= 2 * a.hd) continue;
+      float x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] = rok ? o[1][t][i + e] * inv[1] : 0.f;
+        x[e] = rok ? o[0][t][i + e] * inv[0] - lam * y[e] : 0.f;
+      }
+      store4<T>(op + dv, x[0], x[1], x[2], x[3]);
+      store4<T>(o2p + dv, y[0], y[1], y[2], y[3]);
+    }
+}
+
+void launch_diff_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.L + 127) / 128 * a.hp * a.B));
+  by_width(a.hd, [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, grid, dim3(FwdShape<D>::WAVES * 64), 0, s, a);
+    else hipLaunchKernelGGL(diff_fwd_direct<D>, grid, dim3(256), 0, s, a);
+  });
+}
+
+}  // namespace sl
