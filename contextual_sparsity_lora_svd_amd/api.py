@@ -8,6 +8,7 @@ back to any other implementation: if the library is missing it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional, Sequence
 
@@ -201,7 +202,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # torch.cuda.current_stream().cuda_stream without the Stream object (2.5 us)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 class Layout:
@@ -528,18 +530,24 @@ def qkvo_bwd(w: QKVOWeights, X: Optional[torch.Tensor], a: Optional[torch.Tensor
 # ---------------------------------------------------------------------------
 # Between the q/k/v and the o projection: rotary positions, head norms,
 # differential attention.
-def _check_rows(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
-    """The pointer of a contiguous tensor of this shape and type on the current device."""
+def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: Optional[int] = None) -> int:
+    """The pointer of a contiguous tensor of this shape and type on the current
+    device (``dev``, where the caller has it at hand)."""
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
+        if t.get_device() == (torch.cuda.current_device() if dev is None else dev):
+            return t.data_ptr()
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise SparseLoraError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if not t.is_contiguous():
         raise SparseLoraError(f"{name}: tensors must be contiguous")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise SparseLoraError(f"{name}: tensors must be on the GPU, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise SparseLoraError(f"{name}: on {t.device}, but the current device is "
-                              f"cuda:{torch.cuda.current_device()}")
-    return t.data_ptr()
+    raise SparseLoraError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _current(t: torch.Tensor) -> Optional[int]:
+    """The current device, where there is one to ask for."""
+    return torch.cuda.current_device() if t.is_cuda else None
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3, "yarn": 4}
@@ -572,23 +580,30 @@ class Rotary:
         # torch holds the table's 64 bits as signed integers
         self.turns = torch.tensor([ctypes.c_int64(x).value for x in table], dtype=torch.int64).to(device)
 
-    def _c(self, pos: Optional[torch.Tensor], T: int) -> SlRotary:
-        pp = None if pos is None else _check_rows("pos", pos, (T,), torch.int32)
-        tp = _check_rows("turns", self.turns, (self.rot_dim // 2,), torch.int64)
-        return SlRotary(self.rot_dim, int(self.interleaved), self.amplitude, tp, pp)
+    def _c(self, pos: Optional[torch.Tensor], T: int, dev: Optional[int]) -> SlRotary:
+        pp = None if pos is None else _check_rows("pos", pos, (T,), torch.int32, dev)
+        tp = _check_rows("turns", self.turns, (self.rot_dim // 2,), torch.int64, dev)
+        return SlRotary(self.rot_dim, self.interleaved, self.amplitude, tp, pp)
 
 
 def _check_scratch(name: str, ws: torch.Tensor, like: torch.Tensor) -> int:
-    if ws.device != like.device:
+    if ws.get_device() != like.get_device():
         raise SparseLoraError(f"{name}: buffers on {ws.device}, tensors on {like.device}")
     return _ptr(ws)
 
 
-def _pair_ptrs(names, q, k, layout, heads, dtype):
+@functools.lru_cache(maxsize=64)
+def _heads_ref(heads: tuple):
+    """The C struct of (n_q_heads, n_kv_heads, head_dim); calls only read it."""
+    h = SlHeads(*heads)
+    return h, ctypes.byref(h)
+
+
+def _pair_ptrs(names, q, k, T, heads, dtype, dev):
     """Pointers of a q-shaped and an optional k-shaped tensor."""
-    T = layout.batch * layout.seq_len
-    qp = _check_rows(names[0], q, (T, heads[0] * heads[2]), dtype)
-    kp = None if k is None else _check_rows(names[1], k, (T, heads[1] * heads[2]), dtype)
+    hd = heads[2]
+    qp = _check_rows(names[0], q, (T, heads[0] * hd), dtype, dev)
+    kp = None if k is None else _check_rows(names[1], k, (T, heads[1] * hd), dtype, dev)
     return qp, kp
 
 
@@ -599,16 +614,19 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], layout: Layout, heads: Se
     head; ``inverse`` turns back, which is the gradient.  ``pos`` [T] int32,
     or None: the row's place in its sequence.  ``out`` may hold q and k
     themselves.  k may be None."""
-    L = lib()
-    dt = _dtype_code(q)
-    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, heads, q.dtype)
-    qo, ko = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
-    if (k is None) != (ko is None):
-        raise SparseLoraError("out must hold a tensor for each input")
-    qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, layout, heads, q.dtype)
-    r = rot._c(pos, q.shape[0])
-    _check(L.sl_rotary_apply(dt, layout.ref, ctypes.byref(SlHeads(*heads)), ctypes.byref(r), qp, kp, qop, kop,
-                             int(inverse), _stream()), "sl_rotary_apply")
+    dt, T, dev = _dtype_code(q), layout.batch * layout.seq_len, _current(q)
+    qp, kp = _pair_ptrs(("q", "k"), q, k, T, heads, q.dtype, dev)
+    if out is None:
+        qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
+        qop, kop = qo.data_ptr(), None if k is None else ko.data_ptr()
+    else:
+        qo, ko = out
+        if (k is None) != (ko is None):
+            raise SparseLoraError("out must hold a tensor for each input")
+        qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, T, heads, q.dtype, dev)
+    r = rot._c(pos, T, dev)
+    _check(lib().sl_rotary_apply(dt, layout.ref, _heads_ref(tuple(heads))[1], ctypes.byref(r), qp, kp, qop, kop,
+                                 int(inverse), _stream()), "sl_rotary_apply")
     return qo, ko
 
 
@@ -627,17 +645,19 @@ def head_norm_fwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, 
     """(q, k) with every head divided by its root mean square and multiplied
     by wq / wk [head_dim] (fp32), then rotated (``rot`` None: not).  k and wk
     may both be None."""
-    L = lib()
-    dt = _dtype_code(q)
-    hd = heads[2]
-    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, heads, q.dtype)
-    wqp = _check_rows("wq", wq, (hd,), torch.float32)
-    wkp = None if wk is None else _check_rows("wk", wk, (hd,), torch.float32)
-    qo, ko = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
-    qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, layout, heads, q.dtype)
-    r = rot._c(pos, q.shape[0]) if rot is not None else None
-    _check(L.sl_head_norm_fwd(dt, layout.ref, ctypes.byref(SlHeads(*heads)), ctypes.byref(r) if r else None,
-                              float(eps), qp, kp, wqp, wkp, qop, kop, _stream()), "sl_head_norm_fwd")
+    dt, T, dev, hd = _dtype_code(q), layout.batch * layout.seq_len, _current(q), heads[2]
+    qp, kp = _pair_ptrs(("q", "k"), q, k, T, heads, q.dtype, dev)
+    wqp = _check_rows("wq", wq, (hd,), torch.float32, dev)
+    wkp = None if wk is None else _check_rows("wk", wk, (hd,), torch.float32, dev)
+    if out is None:
+        qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
+        qop, kop = qo.data_ptr(), None if k is None else ko.data_ptr()
+    else:
+        qo, ko = out
+        qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, T, heads, q.dtype, dev)
+    r = ctypes.byref(rot._c(pos, T, dev)) if rot is not None else None
+    _check(lib().sl_head_norm_fwd(dt, layout.ref, _heads_ref(tuple(heads))[1], r, eps, qp, kp, wqp, wkp, qop, kop,
+                                  _stream()), "sl_head_norm_fwd")
     return qo, ko
 
 
@@ -647,28 +667,26 @@ def head_norm_bwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, 
                   buf: Optional[HeadNormWorkspace] = None, out: Optional[Dict[str, torch.Tensor]] = None):
     """Gradients dq, dk (call dtype) and dwq, dwk (fp32) of head_norm_fwd; q
     and k are its inputs."""
-    L = lib()
-    dt = _dtype_code(q)
-    hd, dev = heads[2], q.device
-    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, heads, q.dtype)
-    gqp, gkp = _pair_ptrs(("dq_out", "dk_out"), dq_out, dk_out, layout, heads, q.dtype)
-    wqp = _check_rows("wq", wq, (hd,), torch.float32)
-    wkp = None if wk is None else _check_rows("wk", wk, (hd,), torch.float32)
-    buf = buf or HeadNormWorkspace(layout, heads, dev)
+    dt, T, dev, hd = _dtype_code(q), layout.batch * layout.seq_len, _current(q), heads[2]
+    qp, kp = _pair_ptrs(("q", "k"), q, k, T, heads, q.dtype, dev)
+    gqp, gkp = _pair_ptrs(("dq_out", "dk_out"), dq_out, dk_out, T, heads, q.dtype, dev)
+    wqp = _check_rows("wq", wq, (hd,), torch.float32, dev)
+    wkp = None if wk is None else _check_rows("wk", wk, (hd,), torch.float32, dev)
+    buf = buf or HeadNormWorkspace(layout, heads, q.device)
     out = dict(out or {})
     for n, x, w in (("q", q, wq), ("k", k, wk)):
         if x is not None:
             if "d" + n not in out:
                 out["d" + n] = torch.empty_like(x)
             if "dw" + n not in out:
-                out["dw" + n] = torch.empty(hd, dtype=torch.float32, device=dev)
-    dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out.get("dk"), layout, heads, q.dtype)
-    dwq = _check_rows("dwq", out["dwq"], (hd,), torch.float32)
-    dwk = _check_rows("dwk", out["dwk"], (hd,), torch.float32) if "dwk" in out else None
-    r = rot._c(pos, q.shape[0]) if rot is not None else None
-    _check(L.sl_head_norm_bwd(dt, layout.ref, ctypes.byref(SlHeads(*heads)), ctypes.byref(r) if r else None,
-                              float(eps), qp, kp, wqp, wkp, gqp, gkp, dqp, dkp, dwq, dwk,
-                              _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()), "sl_head_norm_bwd")
+                out["dw" + n] = torch.empty_like(w)
+    dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out.get("dk"), T, heads, q.dtype, dev)
+    dwq = _check_rows("dwq", out["dwq"], (hd,), torch.float32, dev)
+    dwk = _check_rows("dwk", out["dwk"], (hd,), torch.float32, dev) if "dwk" in out else None
+    r = ctypes.byref(rot._c(pos, T, dev)) if rot is not None else None
+    _check(lib().sl_head_norm_bwd(dt, layout.ref, _heads_ref(tuple(heads))[1], r, eps, qp, kp, wqp, wkp, gqp, gkp,
+                                  dqp, dkp, dwq, dwk, _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()),
+           "sl_head_norm_bwd")
     return out
 
 
@@ -686,8 +704,9 @@ class DiffAttnParams:
         self.lambda_init, self.causal = float(lambda_init), bool(causal)
         self.scale = float(scale) if scale is not None else float(max(self.heads[2], 1)) ** -0.5
 
-    def _c(self, lens) -> SlDiffAttn:
-        ptrs = [_check_rows(n, self.t[n], (self.heads[2],), torch.float32) for n in self.NAMES]
+    def _c(self, lens, dev: Optional[int]) -> SlDiffAttn:
+        shape = (self.heads[2],)
+        ptrs = [_check_rows(n, self.t[n], shape, torch.float32, dev) for n in self.NAMES]
         return SlDiffAttn(SlHeads(*self.heads), self.lambda_init, self.scale, int(self.causal), lens, *ptrs)
 
 
@@ -714,22 +733,21 @@ def diff_attn_fwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
                   out: Optional[torch.Tensor] = None):
     """a [T, Hq * head_dim] and the buffers its backward reads.  ``lens``
     [batch]: valid rows per sequence (a given ``buf`` holds its own)."""
-    L = lib()
-    dt = _dtype_code(q)
     if k is None or v is None:
         raise SparseLoraError("q, k and v are required")
-    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, p.heads, q.dtype)
-    vp = _check_rows("v", v, k.shape, q.dtype)
+    dt, T, dev = _dtype_code(q), layout.batch * layout.seq_len, _current(q)
+    qp, kp = _pair_ptrs(("q", "k"), q, k, T, p.heads, q.dtype, dev)
+    vp = _check_rows("v", v, k.shape, q.dtype, dev)
     if buf is None:
         buf = DiffAttnWorkspace(p, layout, q.dtype, q.device, lens)
     elif lens is not None:
         raise SparseLoraError("lens belongs to the buffers: give it to DiffAttnWorkspace")
     a = out if out is not None else torch.empty_like(q)
-    ap = _check_rows("a", a, q.shape, q.dtype)
-    c = p._c(buf.lens)
-    _check(L.sl_diff_attn_fwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
-                              _check_scratch("saved", buf.saved, q), buf.saved.numel(),
-                              _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()), "sl_diff_attn_fwd")
+    ap = _check_rows("a", a, q.shape, q.dtype, dev)
+    c = p._c(buf.lens, dev)
+    _check(lib().sl_diff_attn_fwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
+                                  _check_scratch("saved", buf.saved, q), buf.saved.numel(),
+                                  _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()), "sl_diff_attn_fwd")
     return a, buf
 
 
@@ -738,14 +756,13 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
                   out: Optional[Dict[str, torch.Tensor]] = None):
     """Gradients dq, dk, dv (call dtype) and dlq1, dlk1, dlq2, dlk2 (fp32); a
     and buf are diff_attn_fwd's."""
-    L = lib()
-    dt = _dtype_code(q)
     if k is None or v is None:
         raise SparseLoraError("q, k and v are required")
-    qp, kp = _pair_ptrs(("q", "k"), q, k, layout, p.heads, q.dtype)
-    vp = _check_rows("v", v, k.shape, q.dtype)
-    ap = _check_rows("a", a, q.shape, q.dtype)
-    gp = _check_rows("da", da, q.shape, q.dtype)
+    dt, T, dev = _dtype_code(q), layout.batch * layout.seq_len, _current(q)
+    qp, kp = _pair_ptrs(("q", "k"), q, k, T, p.heads, q.dtype, dev)
+    vp = _check_rows("v", v, k.shape, q.dtype, dev)
+    ap = _check_rows("a", a, q.shape, q.dtype, dev)
+    gp = _check_rows("da", da, q.shape, q.dtype, dev)
     out = dict(out or {})
     for n, x in (("dq", q), ("dk", k), ("dv", v)):
         if n not in out:
@@ -753,12 +770,13 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
     for n in p.NAMES:
         if "d" + n not in out:
             out["d" + n] = torch.empty_like(p.t[n])
-    dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out["dk"], layout, p.heads, q.dtype)
-    dvp = _check_rows("dv", out["dv"], v.shape, q.dtype)
-    g = SlDiffAttnGrads(*[_check_rows("d" + n, out["d" + n], (p.heads[2],), torch.float32) for n in p.NAMES])
-    c = p._c(buf.lens)
-    _check(L.sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
-                              _check_scratch("saved", buf.saved, q), buf.saved.numel(), gp, dqp, dkp, dvp,
-                              ctypes.byref(g), _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()),
+    dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out["dk"], T, p.heads, q.dtype, dev)
+    dvp = _check_rows("dv", out["dv"], v.shape, q.dtype, dev)
+    shape = (p.heads[2],)
+    g = SlDiffAttnGrads(*[_check_rows("d" + n, out["d" + n], shape, torch.float32, dev) for n in p.NAMES])
+    c = p._c(buf.lens, dev)
+    _check(lib().sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
+                                  _check_scratch("saved", buf.saved, q), buf.saved.numel(), gp, dqp, dkp, dvp,
+                                  ctypes.byref(g), _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()),
            "sl_diff_attn_bwd")
     return out

@@ -15,11 +15,13 @@
 // cosine are their Taylor polynomials on [-pi/4, pi/4] (the first dropped terms
 // are below 2e-9, under half a step of fp32) and a quarter-turn swap.
 //
-// What bounds it: HBM (each row read once and written once).  A thread owns one
-// "unit" of a head, two vectors of V values: V pairs, or 2 V values behind the
-// rotated part.  It keeps its V sines and cosines for every head it visits, and
-// the lanes of one head stand next to each other, so a norm's sums are shuffles
-// and nothing is staged in LDS.
+// What bounds it: HBM (each row read once and written once), as long as the
+// vector work stays below it.  A block forms the sines and cosines of its tokens
+// once, in LDS, and walks its rows (the tokens' heads, one behind the other).  A
+// thread owns one "unit" of a head, two vectors of V values: V pairs, or 2 V
+// values behind the rotated part; the lanes of one head stand next to each
+// other, so a norm's sums are shuffles.  The next row is loaded before this one
+// is worked on.
 #include <cmath>
 
 #include "sl_common.hpp"
@@ -39,12 +41,14 @@ struct RotArgs {
   const int* pos;
   int nh[2];            // heads of q and of k
   int hd, rot, L, T;
-  int nchunk;           // head chunks per token (rotate, norm forward)
+  int tokens;           // tokens a block takes at a time
   int lph_log2;         // lanes per head, log2
-  float amp, sign, eps;
+  float amp, sign, eps, inv_hd;
 };
 
-// V values in the element type, moved as one (or, fp32 with V = 8, never used)
+constexpr int kTokens = 4;   // most tokens a block takes at a time
+
+// V values, moved as one
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
 
 template <typename T> __device__ inline float el2f(T x);
@@ -52,7 +56,7 @@ template <> __device__ inline float el2f<float>(float x) { return x; }
 template <> __device__ inline float el2f<bf16>(bf16 x) { return bf2f(x.v); }
 template <typename T> __device__ inline T f2el(float x);
 template <> __device__ inline float f2el<float>(float x) { return x; }
-template <> __device__ inline bf16 f2el<bf16>(float x) { return bf16{f2bf(x)}; }
+template <> __device__ inline bf16 f2el<bf16>(float x) { return __builtin_bit_cast(bf16, (__bf16)x); }   // to nearest even
 
 // cos and sin of 2 pi * phase / 2^32
 __device__ inline void cos_sin_turn(uint32_t phase, float& c, float& s) {
@@ -77,212 +81,228 @@ __device__ inline void cos_sin_turn(uint32_t phase, float& c, float& s) {
 template <typename T, int V, bool INTER, int MODE>
 __global__ void __launch_bounds__(256) rotary_kernel(const RotArgs a) {
   constexpr int NU = V == 1 ? 2 : 1;   // units per lane (256-wide heads of single pairs need two)
+  constexpr int W = 2 * V;             // values of a unit
+  constexpr bool NORM = MODE != RM_ROTATE, BWD = MODE == RM_NORM_BWD;
   using VT = Vec<T, V>;
+  __shared__ __attribute__((aligned(32))) float trig[2][kTokens * 128];   // cosines, sines of the block's tokens
+  __shared__ __attribute__((aligned(16))) float red[BWD ? 256 * NU * W : 4];
   const int lph = 1 << a.lph_log2;
   const int ul = threadIdx.x & (lph - 1);          // unit (and ul + lph)
   const int slot = threadIdx.x >> a.lph_log2, nslot = 256 >> a.lph_log2;
-  const int nunit = a.hd / (2 * V), npair = a.rot / (2 * V);
-  const int H = a.nh[0] + a.nh[1];
+  const int nunit = a.hd / W, npair = a.rot / W, np2 = a.rot / 2;
 
   int off[NU][2];
   bool live[NU], pair[NU];
-  float w[2][NU][2 * V];
-  float acc[2][NU][2 * V];
+  float acc[2][NU][W];
 #pragma unroll
   for (int n = 0; n < NU; ++n) {
     const int u = ul + n * lph;
     live[n] = u < nunit;
     pair[n] = u < npair;
     if (pair[n]) {
-      off[n][0] = INTER ? 2 * V * u : V * u;
-      off[n][1] = INTER ? 2 * V * u + V : a.rot / 2 + V * u;
+      off[n][0] = INTER ? W * u : V * u;
+      off[n][1] = INTER ? W * u + V : a.rot / 2 + V * u;
     } else {
-      off[n][0] = live[n] ? 2 * V * u : 0;   // behind the pairs: units tile the head in order
-      off[n][1] = live[n] ? 2 * V * u + V : 0;
+      off[n][0] = live[n] ? W * u : 0;             // behind the pairs: units tile the head in order
+      off[n][1] = live[n] ? W * u + V : 0;
     }
-    if constexpr (MODE != RM_ROTATE) {
+    if constexpr (BWD) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int j = 0; j < 2 * V; ++j)
-          w[p][n][j] = live[n] && a.w[p] ? a.w[p][off[n][j / V] + j % V] : 0.f;
-    }
-    if constexpr (MODE == RM_NORM_BWD) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int j = 0; j < 2 * V; ++j) acc[p][n][j] = 0.f;
+      for (int j = 0; j < W; ++j) acc[0][n][j] = acc[1][n][j] = 0.f;
     }
   }
 
-  // rotate and norm forward: block = (token, chunk of heads), walking on only
-  // past the grid's limit; norm backward: a block walks tokens and keeps its
-  // weight-gradient sums in registers
-  const int t_step = MODE == RM_NORM_BWD ? (int)gridDim.x : (int)(gridDim.x / (unsigned)a.nchunk);
-  const int t0 = MODE == RM_NORM_BWD ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)a.nchunk);
-  const int chunk = MODE == RM_NORM_BWD ? 0 : (int)(blockIdx.x % (unsigned)a.nchunk);
-  const int h_step = nslot * (MODE == RM_NORM_BWD ? 1 : a.nchunk);
-  for (int t = t0; t < a.T; t += t_step) {
-    const int pos = a.pos ? a.pos[t] : t % a.L;
-    float cs[NU][V], sn[NU][V];
+  for (int tok0 = blockIdx.x * a.tokens; tok0 < a.T; tok0 += gridDim.x * a.tokens) {
+    const int ntok = a.T - tok0 < a.tokens ? a.T - tok0 : a.tokens;
+    if (tok0 != (int)blockIdx.x * a.tokens) __syncthreads();   // the last tokens' angles are still read
+    for (int i = threadIdx.x; i < ntok * np2; i += 256) {
+      const int t = i / np2, j = i - t * np2;
+      const int pos = a.pos ? a.pos[tok0 + t] : (tok0 + t) % a.L;
+      const unsigned long long f = a.turns[j];
+      const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), ps = (uint32_t)pos;
+      float c, sn;
+      // upper word of f * pos (pos signed)
+      cos_sin_turn(__umulhi(lo, ps) + hi * ps - (pos < 0 ? lo : 0u), c, sn);
+      trig[0][t * np2 + j] = c * a.amp;
+      trig[1][t * np2 + j] = sn * a.amp * a.sign;
+    }
+    __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NU; ++n)
+    for (int p = 0; p < 2; ++p) {
+      const int nh = a.nh[p], items = ntok * nh;   // rows of hd values, one behind the other
+      if (slot - (slot & (64 / lph - 1)) >= items) continue;   // none for this wave
+      float w[NU][W];
+      if constexpr (NORM) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        cs[n][j] = 1.f;
-        sn[n][j] = 0.f;
-        if (pair[n]) {
-          const unsigned long long f = a.turns[(ul + n * lph) * V + j];
-          const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), p = (uint32_t)pos;
-          // upper word of f * pos (pos signed)
-          const uint32_t ph = __umulhi(lo, p) + hi * p - (pos < 0 ? lo : 0u);
-          cos_sin_turn(ph, cs[n][j], sn[n][j]);
-          cs[n][j] *= a.amp;
-          sn[n][j] *= a.amp * a.sign;
-        }
+        for (int n = 0; n < NU; ++n)
+#pragma unroll
+          for (int j = 0; j < W; ++j) w[n][j] = live[n] ? a.w[p][off[n][j / V] + j % V] : 0.f;
       }
-    for (int h0 = chunk * nslot; h0 < H; h0 += h_step) {
-      const int hh = h0 + slot;
-      const bool on = hh < H;
-      const int p = hh >= a.nh[0];
-      const int h = p ? hh - a.nh[0] : hh;
-      const long long row = ((long long)t * a.nh[p] + (on ? h : 0)) * a.hd;
-      const T* src = reinterpret_cast<const T*>(MODE == RM_NORM_BWD ? a.dy[p] : a.x[p]) + row;
-      T* dst = reinterpret_cast<T*>(a.y[p]) + row;
-      float v[NU][2 * V], x[NU][2 * V];
+      const long long base = (long long)tok0 * nh * a.hd;
+      const T* src = reinterpret_cast<const T*>(BWD ? a.dy[p] : a.x[p]) + base;
+      const T* xin = reinterpret_cast<const T*>(a.x[p]) + base;
+      T* dst = reinterpret_cast<T*>(a.y[p]) + base;
+      VT rv[NU][2], rx[NU][2];
+      auto load = [&](int it) __attribute__((always_inline)) {
 #pragma unroll
-      for (int n = 0; n < NU; ++n)
-        if (on && live[n]) {
+        for (int n = 0; n < NU; ++n)
+          if (it < items && live[n]) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const VT r = *reinterpret_cast<const VT*>(src + off[n][e]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[n][e * V + j] = el2f<T>(r.v[j]);
-            if constexpr (MODE == RM_NORM_BWD) {
-              const VT q = *reinterpret_cast<const VT*>(reinterpret_cast<const T*>(a.x[p]) + row + off[n][e]);
-#pragma unroll
-              for (int j = 0; j < V; ++j) x[n][e * V + j] = el2f<T>(q.v[j]);
+            for (int e = 0; e < 2; ++e) {
+              rv[n][e] = *reinterpret_cast<const VT*>(src + (long long)it * a.hd + off[n][e]);
+              if constexpr (BWD) rx[n][e] = *reinterpret_cast<const VT*>(xin + (long long)it * a.hd + off[n][e]);
             }
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2 * V; ++j) v[n][j] = x[n][j] = 0.f;
-        }
-      if constexpr (MODE == RM_NORM_FWD) {
-        float ss = 0.f;
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-#pragma unroll
-          for (int j = 0; j < 2 * V; ++j) ss = fmaf(v[n][j], v[n][j], ss);
-        for (int o = lph >> 1; o; o >>= 1) ss += __shfl_xor(ss, o);
-        const float r = rsqrtf(ss / (float)a.hd + a.eps);
+      };
+      int t = slot / nh, h = slot - t * nh;
+      const int dt = nslot / nh, dh = nslot - dt * nh;
+      load(slot);
+      // (the lanes of a wave leave together, so that the shuffles are whole)
+      for (int it = slot; it - (slot & (64 / lph - 1)) < items; it += nslot) {
+        const bool on = it < items;
+        float v[NU][W], x[NU][W];
 #pragma unroll
         for (int n = 0; n < NU; ++n)
 #pragma unroll
-          for (int j = 0; j < 2 * V; ++j) v[n][j] = v[n][j] * r * w[p][n][j];
-      }
-      // the pairs of a unit: value j of both vectors, or neighbours across them
-#pragma unroll
-      for (int n = 0; n < NU; ++n)
-        if (pair[n]) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : V + j;
-            const float va = v[n][ia], vb = v[n][ib];
-            v[n][ia] = va * cs[n][j] - vb * sn[n][j];
-            v[n][ib] = vb * cs[n][j] + va * sn[n][j];
+          for (int j = 0; j < W; ++j) {
+            v[n][j] = on && live[n] ? el2f<T>(rv[n][j / V].v[j % V]) : 0.f;
+            if constexpr (BWD) x[n][j] = on && live[n] ? el2f<T>(rx[n][j / V].v[j % V]) : 0.f;
           }
+        load(it + nslot);
+        if constexpr (MODE == RM_NORM_FWD) {
+          float ss = 0.f;
+#pragma unroll
+          for (int n = 0; n < NU; ++n)
+#pragma unroll
+            for (int j = 0; j < W; ++j) ss = fmaf(v[n][j], v[n][j], ss);
+          for (int o = lph >> 1; o; o >>= 1) ss += __shfl_xor(ss, o);
+          const float r = rsqrtf(fmaf(ss, a.inv_hd, a.eps));
+#pragma unroll
+          for (int n = 0; n < NU; ++n)
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[n][j] = v[n][j] * r * w[n][j];
         }
-      if constexpr (MODE == RM_NORM_BWD) {
-        float ss = 0.f, hx = 0.f;
+        // the pairs of a unit: value j of both vectors, or neighbours across them
 #pragma unroll
         for (int n = 0; n < NU; ++n)
+          if (pair[n]) {
+            const float* const tc = &trig[0][(on ? t : 0) * np2 + (ul + n * lph) * V];
+            const float* const ts = &trig[1][(on ? t : 0) * np2 + (ul + n * lph) * V];
+            const Vec<float, V> cs = *reinterpret_cast<const Vec<float, V>*>(tc);
+            const Vec<float, V> sn = *reinterpret_cast<const Vec<float, V>*>(ts);
 #pragma unroll
-          for (int j = 0; j < 2 * V; ++j) {
-            ss = fmaf(x[n][j], x[n][j], ss);
-            hx = fmaf(v[n][j] * w[p][n][j], x[n][j], hx);
-          }
-        for (int o = lph >> 1; o; o >>= 1) {
-          ss += __shfl_xor(ss, o);
-          hx += __shfl_xor(hx, o);
-        }
-        const float r = rsqrtf(ss / (float)a.hd + a.eps);
-        const float m = hx / (float)a.hd * r * r;
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-#pragma unroll
-          for (int j = 0; j < 2 * V; ++j) {
-            const float g = v[n][j];
-            if (on) {   // a lane without a head holds zeros, and r may be infinite
-              if (p) acc[1][n][j] = fmaf(g, x[n][j] * r, acc[1][n][j]);
-              else acc[0][n][j] = fmaf(g, x[n][j] * r, acc[0][n][j]);
+            for (int j = 0; j < V; ++j) {
+              const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : V + j;
+              const float va = v[n][ia], vb = v[n][ib];
+              v[n][ia] = va * cs.v[j] - vb * sn.v[j];
+              v[n][ib] = vb * cs.v[j] + va * sn.v[j];
             }
-            v[n][j] = r * (g * w[p][n][j] - x[n][j] * m);
           }
-      }
+        if constexpr (BWD) {
+          float ss = 0.f, hx = 0.f;
 #pragma unroll
-      for (int n = 0; n < NU; ++n)
-        if (on && live[n]) {
+          for (int n = 0; n < NU; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            VT r;
-#pragma unroll
-            for (int j = 0; j < V; ++j) r.v[j] = f2el<T>(v[n][e * V + j]);
-            *reinterpret_cast<VT*>(dst + off[n][e]) = r;
+            for (int j = 0; j < W; ++j) {
+              ss = fmaf(x[n][j], x[n][j], ss);
+              hx = fmaf(v[n][j] * w[n][j], x[n][j], hx);
+            }
+          for (int o = lph >> 1; o; o >>= 1) {
+            ss += __shfl_xor(ss, o);
+            hx += __shfl_xor(hx, o);
           }
+          const float r = rsqrtf(fmaf(ss, a.inv_hd, a.eps));
+          const float m = hx * a.inv_hd * r * r;
+#pragma unroll
+          for (int n = 0; n < NU; ++n)
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              const float g = v[n][j];
+              // a lane without a row holds zeros, and r may be infinite
+              if (on) acc[p][n][j] = fmaf(g, x[n][j] * r, acc[p][n][j]);
+              v[n][j] = r * (g * w[n][j] - x[n][j] * m);
+            }
         }
+#pragma unroll
+        for (int n = 0; n < NU; ++n)
+          if (on && live[n]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              VT r;
+#pragma unroll
+              for (int j = 0; j < V; ++j) r.v[j] = f2el<T>(v[n][e * V + j]);
+              *reinterpret_cast<VT*>(dst + (long long)it * a.hd + off[n][e]) = r;
+            }
+          }
+        t += dt;
+        h += dh;
+        if (h >= nh) {
+          h -= nh;
+          ++t;
+        }
+      }
     }
   }
-  if constexpr (MODE == RM_NORM_BWD) {
-    // sum the head slots in order; unit u's values of slot s at [p][s][u][j]
-    __shared__ float sm[2 * 256 * NU * 2 * V];
+  if constexpr (BWD) {
+    // sum the head slots in order; unit u's values of slot s at [s][u][j]
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < 2; ++p) {
+      __syncthreads();
 #pragma unroll
       for (int n = 0; n < NU; ++n)
 #pragma unroll
-        for (int j = 0; j < 2 * V; ++j)
-          sm[((p * nslot + slot) * (NU * lph) + ul + n * lph) * 2 * V + j] = acc[p][n][j];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.hd; i += 256) {
-      const int p = i >= a.hd, c = i - p * a.hd;   // c counts in unit order
-      const int u = c / (2 * V), j = c % (2 * V);
-      float s = 0.f;
-      for (int k = 0; k < nslot; ++k) s += sm[((p * nslot + k) * (NU * lph) + u) * 2 * V + j];
-      // the head position of value j of unit u
-      int at = c;
-      if (!INTER && u < npair) at = (j / V) * (a.rot / 2) + V * u + j % V;
-      a.part[((long long)blockIdx.x * 2 + p) * a.hd + at] = s;
+        for (int j = 0; j < W; ++j) red[(slot * (NU * lph) + ul + n * lph) * W + j] = acc[p][n][j];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.hd; c += 256) {   // c counts in unit order
+        const int u = c / W, j = c % W;
+        float s = 0.f;
+        for (int k = 0; k < nslot; ++k) s += red[(k * (NU * lph) + u) * W + j];
+        // the head position of value j of unit u
+        int at = c;
+        if (!INTER && u < npair) at = (j / V) * (a.rot / 2) + V * u + j % V;
+        a.part[((long long)blockIdx.x * 2 + p) * a.hd + at] = s;
+      }
     }
   }
 }
 
-// dw = the blocks' sums, added in a fixed order: 64 row groups per column, then
-// the groups in order.
+// dw = the blocks' sums, added in a fixed order: 128 row groups of 8 columns,
+// then the groups in order.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int nblk, int hd,
                                                        float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ float sm[64][17];
-  const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int col = blockIdx.x * 16 + c;
+  __shared__ float sm[128][9];
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int col = blockIdx.x * 8 + c;
   float s = 0.f;
-  if (col < 2 * hd)
-    for (int i = g; i < nblk; i += 64) s += part[(long long)i * 2 * hd + col];
+  if (col < 2 * hd) {
+#pragma unroll 8
+    for (int i = g; i < nblk; i += 128) s += part[(long long)i * 2 * hd + col];
+  }
   sm[g][c] = s;
   __syncthreads();
-  if (g == 0 && col < 2 * hd) {
+  if (threadIdx.x < 64) {   // 8 sums of 16 groups for each column, then those 8
     s = 0.f;
-    for (int i = 0; i < 64; ++i) s += sm[i][c];
-    if (col < hd) dwq[col] = s;
-    else if (dwk) dwk[col - hd] = s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += sm[(threadIdx.x >> 3) * 16 + i][c];
+    for (int o = 8; o < 64; o <<= 1) s += __shfl_xor(s, o);
+    if (threadIdx.x < 8 && col < 2 * hd) {
+      if (col < hd) dwq[col] = s;
+      else if (dwk) dwk[col - hd] = s;
+    }
   }
 }
 
-// blocks of the norm's backward: enough to fill the GPU four times over (the
-// register sums want long walks, the loads want many waves)
+// Tokens per block and blocks.  Up to four tokens share a block's set-up where
+// that leaves 512 blocks, two to a CU (norms of 2048 tokens of 64 heads of 128 in
+// bf16, forward and backward: 53-57 us with four, 64 us with one); a launch holds
+// fewer than 2^32 threads, so past 2^20 blocks they walk on.  The norm's backward walks from 1024 blocks,
+// whose weight-gradient sums one more launch adds.
 constexpr int kNormBwdBlocks = 1024;
-// a launch holds fewer than 2^32 threads: past 2^20 tokens blocks walk on
-constexpr int kMaxTokenBlocks = 1 << 20;
-inline int norm_bwd_blocks(long long T) { return (int)(T < kNormBwdBlocks ? T : kNormBwdBlocks); }
+inline int rot_tokens(long long T) { return T >= 512 * kTokens ? kTokens : T >= 1024 ? 2 : 1; }
+inline int rot_blocks(long long T, int most) {
+  const long long n = (T + rot_tokens(T) - 1) / rot_tokens(T);
+  return (int)(n < most ? n : most);
+}
 
 template <typename T, int V, bool INTER>
 static void launch_mode(int mode, const RotArgs& a, dim3 grid, hipStream_t s) {
@@ -321,19 +341,9 @@ static sl_status run_rotary(int mode, sl_dtype dt, RotArgs& a, int inter, hipStr
   int lg = 0;
   while ((per_lane << lg) < nunit) ++lg;
   a.lph_log2 = lg;
-  const int nslot = 256 >> lg, H = a.nh[0] + a.nh[1];
-  long long blocks;
-  if (mode == RM_NORM_BWD) {
-    a.nchunk = 1;
-    blocks = norm_bwd_blocks(a.T);
-  } else {
-    // a thread visits several heads with the same angles while 2048 blocks are
-    // left; below that the heads of a token spread over more blocks
-    const int most = ceil_div(H, nslot);
-    long long n = ceil_div(2048, a.T);
-    a.nchunk = (int)(n < most ? n : most);
-    blocks = (long long)(a.T < kMaxTokenBlocks ? a.T : kMaxTokenBlocks) * a.nchunk;
-  }
+  a.tokens = rot_tokens(a.T);
+  a.inv_hd = 1.0f / a.hd;
+  const int blocks = rot_blocks(a.T, mode == RM_NORM_BWD ? kNormBwdBlocks : 1 << 20);
   if (dt == SL_BF16) launch_vec<bf16>(V, inter != 0, mode, a, dim3((unsigned)blocks), s);
   else launch_vec<float>(V, inter != 0, mode, a, dim3((unsigned)blocks), s);
   SL_HIP(hipGetLastError());
@@ -474,7 +484,7 @@ extern "C" size_t sl_head_norm_workspace_bytes(const sl_layout* lay, const sl_he
   RotArgs a;
   int inter;
   if (rot_args(a, SL_F32, lay, heads, nullptr, true, 1.f, &inter) != SL_OK) return 0;
-  return (size_t)norm_bwd_blocks(a.T) * 2 * a.hd * sizeof(float);
+  return (size_t)rot_blocks(a.T, kNormBwdBlocks) * 2 * a.hd * sizeof(float);
 }
 
 extern "C" sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_heads* heads, const sl_rotary* rot,
@@ -492,7 +502,7 @@ extern "C" sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const s
   if (!aligned16(q) || !aligned16(k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) ||
       !aligned16(wq) || !aligned16(wk) || !aligned16(dwq) || !aligned16(dwk) || !aligned16(ws))
     SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
-  const int nblk = norm_bwd_blocks(a.T);
+  const int nblk = rot_blocks(a.T, kNormBwdBlocks);
   if (!ws || ws_bytes < (size_t)nblk * 2 * a.hd * sizeof(float))
     SL_FAIL(SL_ERR_WORKSPACE, "head norm workspace too small (%zu bytes)", ws_bytes);
   st = check_arch();
@@ -503,7 +513,7 @@ extern "C" sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const s
   a.part = reinterpret_cast<float*>(ws);
   st = run_rotary(RM_NORM_BWD, dt, a, inter, s);
   if (st != SL_OK) return st;
-  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)ceil_div(2 * a.hd, 16)), dim3(1024), 0, s, a.part, nblk, a.hd,
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)ceil_div(2 * a.hd, 8)), dim3(1024), 0, s, a.part, nblk, a.hd,
                      dwq, dwk);
   SL_HIP(hipGetLastError());
   return SL_OK;
