@@ -39,7 +39,7 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   const long long T = (long long)lay->batch * lay->seq_len;
   sl_status st = check_extent("q", T, (long long)hq * hd);
   if (st != SL_OK) return st;
-  const long long stats = T * hq;   // two rows of statistics per head pair
+  const long long stats = (long long)lay->batch * hq * (lay->seq_len + 1);   // two rows per head pair
   Bump s, w;
   pl.lse = s.take(stats * 4);
   pl.lam = s.take(16);
@@ -62,6 +62,7 @@ static sl_status diff_args(DiffArgs& a, const sl_layout* lay, const sl_diff_attn
   a = DiffArgs{};
   a.B = lay->batch;
   a.L = lay->seq_len;
+  a.ls = a.L + 1;
   a.hp = p->heads.n_q_heads / 2;
   a.gp = p->heads.n_kv_heads / 2;
   a.hd = p->heads.head_dim;

@@ -26,10 +26,10 @@ struct DiffArgs {
   void *o, *o2;              // forward: output and O_2 = P_2 V (also read by the backward): fp32, or
                              // 16-bit integers times the row's rsc[1]
   signed char* res;          // bf16 calls: what rounding O to bf16 dropped, times the row's rsc[0]
-  float* rsc;                // [batch][pairs][2][L]
+  float* rsc;                // [batch][pairs][2][ls]
   float* lam;                // lambda and its two exponentials, written by the forward
-  float* lse;                // [batch][pairs][2][L], log2 units
-  float* dsum;               // [batch][pairs][2][L] row sums D_1, D_2
+  float* lse;                // [batch][pairs][2][ls], log2 units; +inf for rows past the length
+  float* dsum;               // [batch][pairs][2][ls] row sums D_1, D_2; 0 for rows past the length
   void *dq, *dk, *dv;
   float *dk_part, *dv_part;  // [split][tokens][kv columns] sums of the heads' parts, split > 1
   double* dlam_part;         // one partial sum of D_2 per wave of the dQ kernel
@@ -37,6 +37,7 @@ struct DiffArgs {
   const float *lq1, *lk1, *lq2, *lk2;
   float lambda_init, scale;
   int B, L, hp, gp, hd;      // hp query pairs, gp kv pairs
+  int ls;                    // L + 1: statistics of one row more than there are, past every length
   int causal, npart, split;
   int lens[SL_MAX_SEQS];
 };

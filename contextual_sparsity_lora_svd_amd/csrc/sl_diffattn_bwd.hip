@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256, D > 64 ? 1 : 2) diff_dq_lds(const DiffArg
   float lse[2], ds[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.L + row;
+    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
     lse[m] = rok ? a.lse[at] : INFINITY;      // weights of rows past the end: 0
     ds[m] = rok ? a.dsum[at] : 0.f;
   }
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   const unsigned ldb = (unsigned)ldq * 2u;
   int it_pr = pr0, it_t = t0;                                   // the next tile to load
   // statistics: wave w loads lse (w < 2) or D of map w % 2, 64 rows
-  const float* const sbase = (wave < 2 ? a.lse : a.dsum) + (long long)b * a.hp * 2 * a.L + (wave & 1) * a.L;
+  const float* const sbase = (wave < 2 ? a.lse : a.dsum) + (long long)b * a.hp * 2 * a.ls + (wave & 1) * a.ls;
   auto issue_next = [&](int it) __attribute__((always_inline)) {
     const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((it & 1) * R::BYTES + wave * PW * 1024));
     const bf16* qb = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.q) + tok0 * ldq + it_pr * 2 * a.hd));
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
       dma16(gb, off, lds_addr(sg) + d0 + i * 1024);
     }
     int r = it_t * 32 + lane;
-    r = r < last ? r : last;
-    const float* sb = reinterpret_cast<const float*>(uniform(sbase + (long long)it_pr * 2 * a.L));
+    r = r < len ? r : len;                                      // lse there is +inf: weights 0
+    const float* sb = reinterpret_cast<const float*>(uniform(sbase + (long long)it_pr * 2 * a.ls));
     const unsigned sd = __builtin_amdgcn_readfirstlane(lds_addr(ss) + (unsigned)((it & 1) * STAT + wave * 256));
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, %2"
                  :: "v"((unsigned)r * 4u), "s"(sd), "s"(sb) : "memory", "m0");
@@ -299,59 +299,108 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
       lds_barrier();              // ... for every wave, and the other slot is read by none
       issue_next(it + 1);
     };
+    // One query tile: the products in order S_1, S_2, dP, dV, dK, each with its
+    // operand read from LDS `AHEAD` products before, and between them the
+    // vector work that is ready: the weights while dP is formed, the score
+    // gradients while dV is.  One wave has the SIMD to itself, so only this
+    // order covers the LDS reads and the exponentials.
+    constexpr int N1 = 2 * KS, N2 = 2 * KS, N3 = 2 * NT, N4 = 4 * DT, NOP = N1 + N2 + N3 + N4, AHEAD = 3;
+    auto tile = [&](int q0, auto diag) __attribute__((always_inline)) {
+      constexpr bool DIAG = decltype(diag)::value;
+      const unsigned char* qt = sq + (it & 1) * R::BYTES;
+      const unsigned char* gt = sg + (it & 1) * R::BYTES;
+      const unsigned char* vt = sv + wave * R::BYTES;
+      const float* st = reinterpret_cast<const float*>(ss + (it & 1) * STAT) + 4 * h;
+      f32x16 s[2], dp, w;
+      Frag<bf16> wf[2], df[2][2], fa[AHEAD], fb[AHEAD];
+      float4 l4[2], d4[2];
+      zero16(s[0]);
+      zero16(s[1]);
+      zero16(dp);
+      auto read = [&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value, x = i % AHEAD;
+        if constexpr (i < N1) {
+          fa[x] = ad.row(qt, (i / KS) * (D / 8) + 2 * (i % KS));
+        } else if constexpr (i < N1 + N2) {
+          fa[x] = ad.row(gt, 2 * (i - N1));
+          if constexpr (!VREG) fb[x] = ad.row(vt, 2 * (i - N1));
+        } else if constexpr (i < N1 + N2 + N3) {
+          fa[x] = ad.col(gt, (i - N1 - N2) % NT, (i - N1 - N2) / NT);
+        } else if constexpr (i < NOP) {
+          fa[x] = ad.col(qt, (i - N1 - N2 - N3) % (2 * DT), (i - N1 - N2 - N3) / (2 * DT));
+        }
+      };
+      // statistics of elements e .. e + 3 (map e / 16): lse while weights are formed, then D
+      auto stats = [&](float4 (&x)[2], int e, int which) __attribute__((always_inline)) {
+        if (e < 32) x[(e / 4) & 1] = *reinterpret_cast<const float4*>(st + (which + e / 16) * 64 + 2 * (e % 16));
+      };
+      auto part4 = [](const float4& x, int e) __attribute__((always_inline)) {
+        return e % 4 == 0 ? x.x : e % 4 == 1 ? x.y : e % 4 == 2 ? x.z : x.w;
+      };
+      each<AHEAD>(read);
+      each<NOP>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i < N1) {
+          mma(s[i / KS], fa[i % AHEAD], kf[i / KS][i % KS]);
+        } else if constexpr (i < N1 + N2) {
+          if constexpr (VREG) mma(dp, fa[i % AHEAD], vf[i - N1]);
+          else mma(dp, fa[i % AHEAD], fb[i % AHEAD]);
+        } else if constexpr (i < N1 + N2 + N3) {
+          mma(dv[(i - N1 - N2) % NT], fa[i % AHEAD], wf[(i - N1 - N2) / NT]);
+        } else {
+          constexpr int j = i - N1 - N2 - N3, mt = j % (2 * DT);
+          mma(dk[mt / DT][mt % DT], fa[i % AHEAD], df[mt / DT][j / (2 * DT)]);
+        }
+        read(std::integral_constant<int, i + AHEAD>{});
+        if constexpr (i == N1 - 1) stats(l4, 0, 0);
+        if constexpr (i == N1 + N2 - 1) stats(d4, 0, 2);
+        if constexpr (i >= N1 && i < N1 + N2) {
+          constexpr int e0 = 32 * (i - N1) / N2, e1 = 32 * (i - N1 + 1) / N2;
+#pragma unroll
+          for (int e = e0; e < e1; ++e) {
+            const int m = e / 16, x = e % 16;
+            if (e % 4 == 0) stats(l4, e + 4, 0);
+            float p = fast_exp2(fmaf(s[m][x], sc, -part4(l4[(e / 4) & 1], e)));
+            if constexpr (DIAG) p = q0 + 2 * (x & ~3) + 4 * h + (x & 3) < key ? 0.f : p;
+            s[m][x] = p;
+            w[x] = m ? fmaf(-lam, p, w[x]) : p;
+          }
+        }
+        if constexpr (i == N1 + N2 - 1) {
+          wf[0] = acc_frag<bf16>(w, 0);
+          wf[1] = acc_frag<bf16>(w, 1);
+        }
+        if constexpr (i >= N1 + N2 && i < N1 + N2 + N3) {
+          constexpr int e0 = 32 * (i - N1 - N2) / N3, e1 = 32 * (i - N1 - N2 + 1) / N3;
+#pragma unroll
+          for (int e = e0; e < e1; ++e) {
+            if (e % 4 == 0) stats(d4, e + 4, 2);
+            s[e / 16][e % 16] *= dp[e % 16] - part4(d4[(e / 4) & 1], e);
+          }
+        }
+        if constexpr (i == N1 + N2 + N3 - 1) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            df[m][0] = acc_frag<bf16>(s[m], 0);
+            df[m][1] = acc_frag<bf16>(s[m], 1);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
     const int skip = a.causal ? (wave < ntile ? wave : ntile) : 0;   // tiles before this wave's keys
     for (int n = 0; n < nh; ++n) {
-      for (int j = 0; j < skip; ++j, ++it) advance();
-      for (int j = skip; j < ntile; ++j, ++it) {
+      int j = 0;
+      for (; j < skip; ++j, ++it) advance();
+      if (a.causal && j < ntile) {
         advance();
-        const int q0 = (t0 + j) * 32;
-        const unsigned char* qt = sq + (it & 1) * R::BYTES;
-        const unsigned char* gt = sg + (it & 1) * R::BYTES;
-        const float* st = reinterpret_cast<const float*>(ss + (it & 1) * STAT);
-        f32x16 dp, s, w;
-        zero16(dp);
-#pragma unroll
-        for (int x = 0; x < 2 * KS; ++x) {
-          if constexpr (VREG) mma(dp, ad.row(gt, 2 * x), vf[x]);
-          else mma(dp, ad.row(gt, 2 * x), ad.row(sv + wave * R::BYTES, 2 * x));
-        }
-        const bool masked = q0 + 32 > len || (a.causal && q0 < k0 + wave * 32 + 31);
-        const int first = a.causal ? key : 0;                   // queries that read this key: first .. len - 1
-        Frag<bf16> df[2][2];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          zero16(s);
-#pragma unroll
-          for (int x = 0; x < KS; ++x) mma(s, ad.row(qt, m * (D / 8) + 2 * x), kf[m][x]);
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(st + m * 64 + 2 * i + 4 * h);
-            const float4 d4 = *reinterpret_cast<const float4*>(st + (2 + m) * 64 + 2 * i + 4 * h);
-            const float le[4] = {l4.x, l4.y, l4.z, l4.w}, de[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float p = fast_exp2(fmaf(s[i + e], sc, -le[e]));
-              if (masked) {
-                const int qr = q0 + 2 * i + 4 * h + e;
-                p = qr < first || qr >= len ? 0.f : p;
-              }
-              w[i + e] = m ? fmaf(-lam, p, w[i + e]) : p;
-              s[i + e] = p * (dp[i + e] - de[e]);
-            }
-          }
-          df[m][0] = acc_frag<bf16>(s, 0);
-          df[m][1] = acc_frag<bf16>(s, 1);
-        }
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          const Frag<bf16> wf = acc_frag<bf16>(w, cc);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma(dv[t], ad.col(gt, t, cc), wf);
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int t = 0; t < DT; ++t) mma(dk[m][t], ad.col(qt, m * DT + t, cc), df[m][cc]);
-        }
+        tile((t0 + j) * 32, std::true_type{});
+        ++j;
+        ++it;
+      }
+      for (; j < ntile; ++j, ++it) {
+        advance();
+        tile((t0 + j) * 32, std::false_type{});
       }
     }
     wait_vm<0>();
@@ -415,7 +464,7 @@ __global__ void __launch_bounds__(256) diff_dsum_q(const DiffArgs a, int lp_log2
   const int pair = on ? (int)(w % a.hp) : 0;
   const long long tok = on ? w / a.hp : 0;
   const int b = (int)(tok / a.L), row = (int)(tok % a.L);
-  const long long st = (long long)(b * a.hp + pair) * 2 * a.L + row;
+  const long long st = (long long)(b * a.hp + pair) * 2 * a.ls + row;
   float d1 = 0.f, d2 = 0.f, r1 = 0.f;
   if (on && row < a.lens[b] && 8 * sub < 2 * a.hd) {
     const long long at = (tok * a.hp + pair) * 2 * a.hd + 8 * sub;
@@ -434,7 +483,7 @@ __global__ void __launch_bounds__(256) diff_dsum_q(const DiffArgs a, int lp_log2
       r1 = fmaf(gx, r, r1);
       d2 = fmaf(gx, y, d2);
     }
-    d2 *= a.rsc[st + a.L];
+    d2 *= a.rsc[st + a.ls];
     d1 = fmaf(r1, a.rsc[st], d1);
     d1 = fmaf(lam, d2, d1);
   }
@@ -444,7 +493,8 @@ __global__ void __launch_bounds__(256) diff_dsum_q(const DiffArgs a, int lp_log2
   }
   if (on && sub == 0) {
     a.dsum[st] = d1;
-    a.dsum[st + a.L] = d2;
+    a.dsum[st + a.ls] = d2;
+    if (row == a.L - 1) a.dsum[st + 1] = a.dsum[st + a.ls + 1] = 0.f;
   }
 }
 
@@ -474,7 +524,7 @@ __global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
   }
   d1 = wave_sum(d1);
   d2 = wave_sum(d2);
-  if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.L + row] = lane ? d2 : d1;
+  if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.ls + row] = lane ? d2 : d1;
 }
 
 // dQ: one wave per 32 queries, keys in order.  It also sums P_2 dP, whose total
@@ -505,7 +555,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   float lse[2], ds[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.L + row;
+    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
     lse[m] = rok ? a.lse[at] : INFINITY;
     ds[m] = rok ? a.dsum[at] : 0.f;
   }
@@ -617,8 +667,8 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
   for (int pr = g * grp; pr < (g + 1) * grp; ++pr) {
     const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * ldq + pr * 2 * a.hd;
     const T* dop = reinterpret_cast<const T*>(a.da) + tok0 * ldq + pr * 2 * a.hd;
-    const float* lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.L;
-    const float* dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.L;
+    const float* lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.ls;
+    const float* dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.ls;
     for (int q0 = kb * 32 < len ? qbeg : len; q0 < len; q0 += 32) {
       const int kz = opaque(0);
       f32x16 dp, s[2], w;
@@ -647,9 +697,9 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
           const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3);
           const bool hidden = q >= len || (a.causal && key > q) || !kok;
           const int qq = q < len ? q : 0;
-          const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m * a.L + qq]));
+          const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m * a.ls + qq]));
           w[i] = m ? w[i] - lam * p : p;
-          s[m][i] = p * (dp[i] - dsm[m * a.L + qq]);
+          s[m][i] = p * (dp[i] - dsm[m * a.ls + qq]);
         }
       }
 #pragma unroll

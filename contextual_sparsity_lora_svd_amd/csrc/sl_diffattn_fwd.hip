@@ -245,14 +245,18 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
   // rounding to bf16 drops in 8 bits: D_m = dO . (P_m V) is then exact to 2^-16,
   // where an error of D would add up over the whole row of keys.
   const float lam = slam[0];
-  const long long stat = (long long)(b * a.hp + pair) * 2 * a.L + row;
+  const long long stat = (long long)(b * a.hp + pair) * 2 * a.ls + row;
   const long long goff = (tok0 + row0) * ldq + pair * 2 * a.hd;   // the wave's first row
   const int rows = a.L - row0 < 32 ? a.L - row0 : 32;
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     const float l = pair_sum(sum[m]);
     const float inv = rok ? 1.f / l : 0.f;
-    if (h == 0 && row < a.L) a.lse[stat + (m0 + m) * a.L] = rok ? mx[m] * sc + __log2f(l) : INFINITY;
+    if (h == 0 && row < a.L) {
+      float* const at = a.lse + stat + (m0 + m) * a.ls;
+      *at = rok ? mx[m] * sc + __log2f(l) : INFINITY;
+      if (row == a.L - 1) at[1] = INFINITY;
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
         if ((32 * t) % D + 8 * (i >> 2) + 4 * h < a.hd) top = fmaxf(top, fabsf(o[m][t][i]));
     top = pair_max(top);
     const float f = top > 0.f ? 32767.f / top : 0.f;
-    if (h == 0 && row < a.L) a.rsc[stat + a.L] = top / 32767.f;
+    if (h == 0 && row < a.L) a.rsc[stat + a.ls] = top / 32767.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -452,7 +456,11 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   for (int m = 0; m < 2; ++m) {
     const float l = sum[m] + __shfl_xor(sum[m], 32);
     inv[m] = rok ? 1.f / l : 0.f;
-    if (h == 0) a.lse[((long long)(b * a.hp + pair) * 2 + m) * a.L + row] = rok ? mx[m] * sc + log2f(l) : INFINITY;
+    if (h == 0) {
+      float* const at = a.lse + ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
+      *at = rok ? mx[m] * sc + log2f(l) : INFINITY;
+      if (row == a.L - 1) at[1] = INFINITY;
+    }
   }
   const long long orow = (tok0 + row) * ldq + pair * 2 * a.hd;
   T* op = reinterpret_cast<T*>(a.o) + orow;

@@ -16,6 +16,8 @@
 // outside the sequence is read.
 #pragma once
 
+#include <utility>
+
 #include "sl_diffattn.hpp"
 
 namespace sl {
@@ -138,6 +140,15 @@ __device__ inline void locate(int bid, int n, int hp, int& blk, int& pair, int& 
   const int u = xcd_remap(bid % n, n);
   b = u / hp;
   pair = u % hp;
+}
+
+// f(0) .. f(N - 1) with compile-time indices, unrolled however long.
+template <typename F, int... I>
+__device__ inline __attribute__((always_inline)) void each_of(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F> __device__ inline __attribute__((always_inline)) void each(F f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
 }
 
 // 32 rows that a wave has laid out in LDS (`pitch` bytes apart) to memory, 16
