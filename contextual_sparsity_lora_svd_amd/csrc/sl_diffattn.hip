@@ -6,7 +6,7 @@ namespace sl {
 // ---------------------------------------------------------------------------
 // host side
 struct DiffPlan {
-  size_t lse, lam, rsc, o2, res, saved;    // offsets and size of the saved buffer
+  size_t lse, lam, fix, rsc, o2, res, saved;    // offsets and size of the saved buffer
   size_t dsum, dlam, part, ws;             // of the workspace
   int npart, split;
   long long part_elems;                    // of one part of dK or dV
@@ -43,6 +43,7 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   Bump s, w;
   pl.lse = s.take(stats * 4);
   pl.lam = s.take(16);
+  pl.fix = s.take(dt == SL_BF16 ? stats * 2 : 0);
   pl.rsc = s.take(dt == SL_BF16 ? stats * 4 : 0);
   pl.o2 = s.take(T * hq * hd * (dt == SL_BF16 ? 2 : 4));
   pl.res = s.take(dt == SL_BF16 ? T * hq * hd : 0);
@@ -86,6 +87,7 @@ static void saved_args(DiffArgs& a, const DiffPlan& pl, void* saved) {
   char* p = reinterpret_cast<char*>(saved);
   a.lse = reinterpret_cast<float*>(p + pl.lse);
   a.lam = reinterpret_cast<float*>(p + pl.lam);
+  a.fix = reinterpret_cast<float*>(p + pl.fix);
   a.rsc = reinterpret_cast<float*>(p + pl.rsc);
   a.o2 = p + pl.o2;
   a.res = reinterpret_cast<signed char*>(p + pl.res);

@@ -29,6 +29,7 @@ struct DiffArgs {
   float* rsc;                // [batch][pairs][2][ls]
   float* lam;                // lambda and its two exponentials, written by the forward
   float* lse;                // [batch][pairs][2][ls], log2 units; +inf for rows past the length
+  float* fix;                // bf16 calls: [batch][pairs][ls], the second map's weights times 1 + this are free of the lse's rounding
   float* dsum;               // [batch][pairs][2][ls] row sums D_1, D_2; 0 for rows past the length
   void *dq, *dk, *dv;
   float *dk_part, *dv_part;  // [split][tokens][kv columns] sums of the heads' parts, split > 1

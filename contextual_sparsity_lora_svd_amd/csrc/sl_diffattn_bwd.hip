@@ -8,12 +8,20 @@ namespace sl {
 // in registers) and walks the key tiles, scores and dP = V dO^T transposed, so
 // that P and dS stay where they are formed.  K's tile is read twice, by rows
 // for the scores and by columns for dQ^T += K^T dS^T.
+//
+// dS goes to the matrix cores as the sum of two bf16 (2^-16): a row of dS sums to
+// zero, so what one rounding of 2^-8 leaves behind is not small beside dQ where
+// the keys have something in common.  It costs a third more products (1 x 4096,
+// 8 kv heads of 128: dQ's error 1.5 to 1.1 times that of its own rounding to bf16).
+// The sum of P_2 dP, which is -dlambda, stays in fp32 over a tile and in fp64
+// beyond, with what the log-sum-exp's rounding did to the row taken out again.
 template <int D>
-__global__ void __launch_bounds__(256, D > 64 ? 1 : 2) diff_dq_lds(const DiffArgs a) {
+__global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   using R = RowTile<D>;
-  constexpr int DT = D / 32, KS = D / 16, NST = 4, PW = R::PER_WAVE;
-  constexpr bool PIPE = D > 64;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * NST * R::BYTES];
+  constexpr int DT = D / 32, KS = D / 16, NST = 4, PW = R::PER_WAVE, P2 = 4 * D + 16;
+  constexpr int RING = 2 * NST * R::BYTES;
+  static_assert(4 * 32 * P2 <= RING, "the staged results fit the ring");
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[RING];
   unsigned char* const sk = smem;
   unsigned char* const sv = smem + NST * R::BYTES;
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
@@ -81,21 +89,9 @@ __global__ void __launch_bounds__(256, D > 64 ? 1 : 2) diff_dq_lds(const DiffArg
 #pragma unroll
     for (int t = 0; t < DT; ++t) zero16(dq[m][t]);
   const float sc = a.scale * kLog2e;
+  const double fix = rok ? 1.0 + (double)a.fix[((long long)b * a.hp + pair) * a.ls + row] : 1.0;
   double dlam = 0.0;
 
-  auto scores = [&](f32x16 (&s)[2], f32x16& dp, int tile) __attribute__((always_inline)) {
-    const unsigned char* kt = sk + (tile & (NST - 1)) * R::BYTES;
-    const unsigned char* vt = sv + (tile & (NST - 1)) * R::BYTES;
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      zero16(s[m]);
-#pragma unroll
-      for (int x = 0; x < KS; ++x) mma(s[m], ad.row(kt, m * (D / 8) + 2 * x), q[m][x]);
-    }
-    zero16(dp);
-#pragma unroll
-    for (int x = 0; x < 2 * KS; ++x) mma(dp, ad.row(vt, 2 * x), go[x]);
-  };
   auto mask = [&](f32x16 (&s)[2], int tile) __attribute__((always_inline)) {
     const int lim = a.causal && row + 1 < len ? row + 1 : len;
     const int k0 = tile * 32 + 4 * h;
@@ -106,75 +102,111 @@ __global__ void __launch_bounds__(256, D > 64 ? 1 : 2) diff_dq_lds(const DiffArg
       s[1][i] = hidden ? -INFINITY : s[1][i];
     }
   };
-  // S and dP of a tile -> dS of both maps
-  auto grads = [&](f32x16 (&s)[2], const f32x16& dp) __attribute__((always_inline)) {
+  // Step i in a fixed order: the scores of tile i, while the first map's dS of
+  // tile i - 1 is formed; the first map's dQ, while the second's dS is; the second
+  // map's dQ and then dP of tile i, while the weights of tile i are.  Operands are
+  // read AHEAD products early.
+  constexpr int N1 = 2 * KS, N2 = 2 * DT, NG = 2 * N1 + 2 * N2, AHEAD = 3;
+  f32x16 s[2], dp;
+  auto step = [&](int i, auto has_prev, auto has_next, auto masked) __attribute__((always_inline)) {
+    constexpr bool PREV = decltype(has_prev)::value, NEXT = decltype(has_next)::value;
+    const unsigned char* kt = sk + (i & (NST - 1)) * R::BYTES;
+    const unsigned char* vt = sv + (i & (NST - 1)) * R::BYTES;
+    const unsigned char* kp = sk + ((i - 1) & (NST - 1)) * R::BYTES;
+    f32x16 n[2], ndp;
+    Frag<bf16> hi[2][2], lo[2][2], fa[AHEAD];
     float part = 0.f;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float p = fast_exp2(fmaf(s[m][i], sc, -lse[m]));
-        if (m == 1) part = fmaf(p, dp[i], part);
-        s[m][i] = p * (dp[i] - ds[m]);
+    zero16(n[0]);
+    zero16(n[1]);
+    zero16(ndp);
+    auto read = [&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value, x = g % AHEAD;
+      if constexpr (g < N1) {
+        if constexpr (NEXT) fa[x] = ad.row(kt, (g / KS) * (D / 8) + 2 * (g % KS));
+      } else if constexpr (g < N1 + 2 * N2) {
+        constexpr int m = (g - N1) / N2, j = (g - N1) % N2;
+        if constexpr (PREV) fa[x] = ad.col(kp, m * DT + j % DT, j / DT);
+      } else if constexpr (g < NG) {
+        if constexpr (NEXT) fa[x] = ad.row(vt, 2 * (g - N1 - 2 * N2));
       }
-    dlam += (double)part;
-  };
-  auto accumulate = [&](const f32x16 (&s)[2], int tile) __attribute__((always_inline)) {
-    const unsigned char* kt = sk + (tile & (NST - 1)) * R::BYTES;
+    };
+    // dS of elements e0 .. e1 - 1 (pairs) of map m, as the sum of two bf16
+    auto grads = [&](int m, int e0, int e1) __attribute__((always_inline)) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const Frag<bf16> sf = acc_frag<bf16>(s[m], cc);
-#pragma unroll
-        for (int t = 0; t < DT; ++t) mma(dq[m][t], ad.col(kt, m * DT + t, cc), sf);
+      for (int x = e0; x < e1; x += 2) {
+        if (m == 1) part = fmaf(s[1][x], dp[x], fmaf(s[1][x + 1], dp[x + 1], part));
+        const float g0 = s[m][x] * (dp[x] - ds[m]), g1 = s[m][x + 1] * (dp[x + 1] - ds[m]);
+        const uint32_t top = round2(g0, g1);
+        set2(hi[m][x / 8], x % 8, top);
+        set2(lo[m][x / 8], x % 8, round2(g0 - __uint_as_float(top << 16), g1 - __uint_as_float(top & 0xFFFF0000u)));
       }
+    };
+    auto weigh = [&](int e0, int e1) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = e0; e < e1; ++e) n[e / 16][e % 16] = fast_exp2(fmaf(n[e / 16][e % 16], sc, -lse[e / 16]));
+    };
+    each<AHEAD>(read);
+    each<NG>([&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value;
+      if constexpr (g < N1) {
+        if constexpr (NEXT) mma(n[g / KS], fa[g % AHEAD], q[g / KS][g % KS]);
+      } else if constexpr (g < N1 + 2 * N2) {
+        constexpr int m = (g - N1) / N2, j = (g - N1) % N2;
+        if constexpr (PREV) {
+          mma(dq[m][j % DT], fa[g % AHEAD], hi[m][j / DT]);
+          mma(dq[m][j % DT], fa[g % AHEAD], lo[m][j / DT]);
+        }
+      } else {
+        if constexpr (NEXT) mma(ndp, fa[g % AHEAD], go[g - N1 - 2 * N2]);
+      }
+      read(std::integral_constant<int, g + AHEAD>{});
+      if constexpr (g < N1 && PREV) grads(0, 2 * (8 * g / N1), 2 * (8 * (g + 1) / N1));
+      if constexpr (g >= N1 && g < N1 + N2 && PREV) grads(1, 2 * (8 * (g - N1) / N2), 2 * (8 * (g - N1 + 1) / N2));
+      if constexpr (g == N1 - 1 && NEXT && decltype(masked)::value) mask(n, i);
+      if constexpr (g >= N1 + N2 && NEXT) weigh(32 * (g - N1 - N2) / (N1 + N2), 32 * (g - N1 - N2 + 1) / (N1 + N2));
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (PREV) dlam = fma((double)part, fix, dlam);
+    if constexpr (NEXT) {
+      s[0] = n[0];
+      s[1] = n[1];
+      dp = ndp;
+    }
   };
 
   if (nt > 0) {
-    // PIPE: tile i + 1's products run in iteration i, which still needs K of tile i
-    constexpr int AHEAD = PIPE ? 1 : 0;
-    f32x16 s[2], dp;
-    if constexpr (PIPE) issue_tile(0);
-    issue_tile(AHEAD);
-    issue_tile(AHEAD + 1);
-    if constexpr (PIPE) {
-      wait_vm<4 * PW>();
-      lds_barrier();
-      scores(s, dp, 0);
-      if (wfull <= 0) mask(s, 0);
-    }
+    issue_tile(0);
+    issue_tile(1);
     auto advance = [&](int i) __attribute__((always_inline)) {
-      wait_vm<2 * PW>();          // tile i + AHEAD has landed
-      lds_barrier();
-      issue_tile(i + AHEAD + 2);  // into the slot of tile i - 1 or i - 2
+      wait_vm<2 * PW>();          // tile i has landed
+      lds_barrier();              // ... for every wave, and all are done with tile i - 2
+      issue_tile(i + 2);
     };
-    for (int i = 0; i < wt; ++i) {
-      advance(i);
-      f32x16 nx[2], ndp;
-      if constexpr (PIPE) {
-        scores(nx, ndp, i + 1);
-      } else {
-        scores(s, dp, i);
-        if (i >= wfull) mask(s, i);
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    int i = 0;
+    if (wt > 0) {
+      advance(0);
+      if (wfull > 0) step(0, no, yes, no);
+      else step(0, no, yes, yes);
+      for (i = 1; i < wfull && i < wt; ++i) {
+        advance(i);
+        step(i, yes, yes, no);
       }
-      grads(s, dp);
-      accumulate(s, i);
-      if constexpr (PIPE) {
-        if (i + 1 >= wfull) mask(nx, i + 1);
-        s[0] = nx[0];
-        s[1] = nx[1];
-        dp = ndp;
+      for (; i < wt; ++i) {
+        advance(i);
+        step(i, yes, yes, yes);
       }
+      step(i, yes, no, no);       // tile wt - 1: its slot is refilled from tile wt + 1's advance on
     }
-    for (int i = wt; i < nt; ++i) advance(i);
+    for (; i < nt; ++i) advance(i);
     wait_vm<0>();
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) dlam += __shfl_xor(dlam, o);
   if (lane == 0) a.dlam_part[blockIdx.x * 4 + wave] = dlam;
-  if (row >= a.L) return;
-  bf16* out = reinterpret_cast<bf16*>(a.dq) + qoff;
+  lds_barrier();                  // the ring is free
+  unsigned char* const st = smem + wave * 32 * P2;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const float f = m ? -lam * a.scale : a.scale;
@@ -187,9 +219,11 @@ __global__ void __launch_bounds__(256, D > 64 ? 1 : 2) diff_dq_lds(const DiffArg
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = rok ? dq[m][t][i + e] * f : 0.f;
-        store4<bf16>(out + m * a.hd + d, x[0], x[1], x[2], x[3]);
+        store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + m * a.hd + d, x[0], x[1], x[2], x[3]);
       }
   }
+  const int row0 = q0 + wave * 32, rows = a.L - row0 < 32 ? a.L - row0 : 32;
+  store_rows(st, P2, reinterpret_cast<bf16*>(a.dq) + (tok0 + row0) * ldq + pair * 2 * a.hd, ldq * 2, 4 * a.hd, rows, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -282,13 +316,13 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
 
   TileAddr<D> ad;
   ad.init(lane, true, true);
-  f32x16 dk[2][DT], dv[NT];
+  f32x16 dk[2][DT], dv[2][DT];   // dV's columns as the two halves of its tile
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int t = 0; t < DT; ++t) zero16(dk[m][t]);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) zero16(dv[t]);
+  for (int t = 0; t < NT; ++t) zero16(dv[t / DT][t % DT]);
   const float sc = a.scale * kLog2e;
 
   if (total > 0) {
@@ -346,7 +380,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
           if constexpr (VREG) mma(dp, fa[i % AHEAD], vf[i - N1]);
           else mma(dp, fa[i % AHEAD], fb[i % AHEAD]);
         } else if constexpr (i < N1 + N2 + N3) {
-          mma(dv[(i - N1 - N2) % NT], fa[i % AHEAD], wf[(i - N1 - N2) / NT]);
+          mma(dv[(i - N1 - N2) % NT / DT][(i - N1 - N2) % DT], fa[i % AHEAD], wf[(i - N1 - N2) / NT]);
         } else {
           constexpr int j = i - N1 - N2 - N3, mt = j % (2 * DT);
           mma(dk[mt / DT][mt % DT], fa[i % AHEAD], df[mt / DT][j / (2 * DT)]);
@@ -405,36 +439,37 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
     }
     wait_vm<0>();
   }
-  if (key >= a.L) return;
-  const long long pofs = (long long)part * a.B * a.L * ldk + koff;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int e = (32 * t) % D + 2 * i + 4 * h, m = 32 * t / D;
-      if (e >= a.hd) continue;
-      float x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = kok ? dv[t][i + j] : 0.f;
-      if (a.split > 1) store4<float>(a.dv_part + pofs + m * a.hd + e, x[0], x[1], x[2], x[3]);
-      else store4<bf16>(reinterpret_cast<bf16*>(a.dv) + koff + m * a.hd + e, x[0], x[1], x[2], x[3]);
-    }
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float f = m ? -lam * a.scale : a.scale;
+  // results by rows through LDS: both maps' halves of dV, then dK's, in bf16 or
+  // (parts) one half at a time in fp32
+  lds_barrier();                  // the tiles are read by none
+  constexpr int P2 = 4 * D + 16;
+  static_assert(4 * 32 * P2 <= (int)sizeof(smem), "the staged results fit");
+  unsigned char* const st = smem + wave * 32 * P2;
+  const int row0 = k0 + wave * 32, rows = a.L - row0 < 32 ? a.L - row0 : 32;
+  const long long roff = (tok0 + row0) * ldk + g * 2 * a.hd, poff = (long long)part * a.B * a.L * ldk + roff;
+  auto put = [&](const f32x16 (&x)[DT], int m, float f, bf16* out, float* parts, bool last) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const int d = 32 * t + 2 * i + 4 * h;
         if (d >= a.hd) continue;
-        float x[4];
+        float y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = kok ? dk[m][t][i + j] * f : 0.f;
-        if (a.split > 1) store4<float>(a.dk_part + pofs + m * a.hd + d, x[0], x[1], x[2], x[3]);
-        else store4<bf16>(reinterpret_cast<bf16*>(a.dk) + koff + m * a.hd + d, x[0], x[1], x[2], x[3]);
+        for (int e = 0; e < 4; ++e) y[e] = kok ? x[t][i + e] * f : 0.f;
+        if (a.split > 1) store4<float>(reinterpret_cast<float*>(st + c * P2) + d, y[0], y[1], y[2], y[3]);
+        else store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + m * a.hd + d, y[0], y[1], y[2], y[3]);
       }
-  }
+    if (a.split > 1) store_rows(st, P2, parts + poff + m * a.hd, ldk * 4, 4 * a.hd, rows, lane);
+    else if (last) store_rows(st, P2, out + roff, ldk * 2, 4 * a.hd, rows, lane);
+  };
+  bf16* const dko = reinterpret_cast<bf16*>(a.dk);
+  bf16* const dvo = reinterpret_cast<bf16*>(a.dv);
+  // V's tile has D columns per half: its first DT accumulators are the first
+  put(dv[0], 0, 1.f, dvo, a.dv_part, false);
+  put(dv[1], 1, 1.f, dvo, a.dv_part, true);
+  put(dk[0], 0, a.scale, dko, a.dk_part, false);
+  put(dk[1], 1, -lam * a.scale, dko, a.dk_part, true);
 }
 
 // dK and dV from the parts' sums, in order; 4 values per thread.

@@ -4,47 +4,36 @@
 namespace sl {
 
 // ---------------------------------------------------------------------------
-// Forward.  A wave owns 32 queries of both maps (D <= 64) or of one (D > 64: two
-// maps' accumulators of 2 D columns would leave no register for a second wave
-// on the SIMD).  The score tiles are formed transposed (keys x queries), so a
-// lane holds 16 keys of one query: the weights are the next product's operand
-// as they stand and nothing is exchanged between lanes.
+// Forward.  A workgroup of 8 waves owns 128 queries of a head pair; a wave owns
+// 32 of them and one map (both maps' accumulators of 2 D columns would leave no
+// registers for a second wave on the SIMD).  The score tiles are formed
+// transposed (keys x queries), so a lane holds 16 keys of one query: the weights
+// are the next product's operand as they stand and nothing is exchanged
+// between lanes.
 //
 // The weights are taken relative to the maximum of the row's first tile and the
 // accumulators never rescaled (fp32 and bf16 reach 2^127 alike, and a sum of at
 // least 1 loses nothing to small weights).  A row whose sum passes 2^64 makes
 // the workgroup go again, after a pass that finds every row's maximum.
 //
-// Two waves of a SIMD cover each other's exponentials and LDS reads.  One barrier
-// per tile keeps a workgroup's waves in step; where both waves of a SIMD belong
-// to one workgroup (D > 64) the second map's waves pass it half a tile later, so
-// that one does its exponentials while the other feeds the matrix cores.  The
-// weights are rounded to bf16 for the matrix cores (half a step, 2^-8); their
+// The weights are rounded to bf16 for the matrix cores (half a step, 2^-8); their
 // sum is not.
-template <int D> struct FwdShape {
-  static constexpr int MAPS = D > 64 ? 1 : 2;            // maps per wave
-  static constexpr int WAVES = 8 / MAPS;
-  static constexpr int NDMA = RowTile<D>::NDMA;
-  static constexpr int PW = (NDMA + WAVES - 1) / WAVES;  // the last instruction may be issued twice
-};
-
 template <int D>
-__global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const DiffArgs a) {
+__global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
   using R = RowTile<D>;
-  using S = FwdShape<D>;
-  constexpr int NT = D / 16, KS = D / 16, NST = 4, PW = S::PW, M = S::MAPS;
+  constexpr int NT = D / 16, KS = D / 16, NST = 4;
+  constexpr int PW = (R::NDMA + 7) / 8;                   // DMA per wave; the last may be issued twice
   constexpr int P2 = 4 * D + 16, P1 = 2 * D + 16;         // staged result rows: 2-byte and 1-byte values
-  constexpr int STAGED = S::WAVES * 32 * P2;
+  constexpr int STAGED = 8 * 32 * P2;
   constexpr int RING = 2 * NST * R::BYTES > STAGED ? 2 * NST * R::BYTES : STAGED;
-  static_assert(M == 2 || 4 * NT * 4096 <= RING, "four waves' P_2 V fit the ring");
+  static_assert(4 * NT * 4096 <= RING, "four waves' P_2 V fit the ring");
   __shared__ __attribute__((aligned(1024))) unsigned char smem[RING + 64];
   unsigned char* const sk = smem;
   unsigned char* const sv = smem + NST * R::BYTES;
   float* const slam = reinterpret_cast<float*>(smem + RING);
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m0 = M == 1 ? wave >> 2 : 0, rb = wave & 3;   // first (or only) map, block of 32 rows
-  const bool late = M == 1 && m0 == 1;
+  const int m = wave >> 2, rb = wave & 3;                 // map, block of 32 rows
   const int nqb = (a.L + 127) / 128;
   int blk, pair, b;
   locate(blockIdx.x, a.hp * a.B, a.hp, blk, pair, b);
@@ -65,14 +54,12 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
   // tiles from here on hold keys that some query of the wave does not read
   const int wfull = (a.causal && row0 + 1 < len ? row0 + 1 : len) / 32;
 
-  Frag<bf16> q[M][KS];
+  Frag<bf16> q[KS];
 #pragma unroll
-  for (int m = 0; m < M; ++m)
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int col = s * 16 + h * 8;
-      q[m][s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.q) + qoff + (m0 + m) * a.hd + col, rok && col < a.hd);
-    }
+  for (int s = 0; s < KS; ++s) {
+    const int col = s * 16 + h * 8;
+    q[s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.q) + qoff + m * a.hd + col, rok && col < a.hd);
+  }
   int srow[PW], sins[PW];
   unsigned scol[PW];
 #pragma unroll
@@ -98,39 +85,28 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
   };
 
   TileAddr<D> ad;
-  ad.init(lane, M == 2, true);
-  unsigned kx[KS];                // M = 1: addresses of this wave's map in a row of K
+  ad.init(lane, false, true);
+  unsigned kx[KS];                // this wave's map in a row of K
 #pragma unroll
   for (int x = 0; x < KS; ++x)
-    kx[x] = (unsigned)c * R::PITCH + 16 * (((unsigned)(m0 * (D / 8) + 2 * x) + h) ^ swz<D>((unsigned)c));
-  f32x16 o[M][NT];
-  float mx[M], sum[M];
+    kx[x] = (unsigned)c * R::PITCH + 16 * (((unsigned)(m * (D / 8) + 2 * x) + h) ^ swz<D>((unsigned)c));
+  f32x16 o[NT];
+  float mx = 0.f, sum = 0.f, rest = 0.f;
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    mx[m] = sum[m] = 0.f;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) zero16(o[m][t]);
-  }
+  for (int t = 0; t < NT; ++t) zero16(o[t]);
   const float sc = a.scale * kLog2e;
 
-  auto scores = [&](f32x16 (&s)[M], int tile) __attribute__((always_inline)) {
+  auto scores = [&](f32x16& s, int tile) __attribute__((always_inline)) {
     const unsigned char* kt = sk + (tile & (NST - 1)) * R::BYTES;
+    zero16(s);
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      zero16(s[m]);
-#pragma unroll
-      for (int x = 0; x < KS; ++x) mma(s[m], M == 1 ? lds_row(kt + kx[x]) : ad.row(kt, m * (D / 8) + 2 * x), q[m][x]);
-    }
+    for (int x = 0; x < KS; ++x) mma(s, lds_row(kt + kx[x]), q[x]);
   };
-  auto mask = [&](f32x16 (&s)[M], int tile) __attribute__((always_inline)) {
+  auto mask = [&](f32x16& s, int tile) __attribute__((always_inline)) {
     const int lim = a.causal && row + 1 < len ? row + 1 : len;   // keys this query reads
     const int k0 = tile * 32 + 4 * h;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const bool hidden = k0 + 8 * (i >> 2) + (i & 3) >= lim;
-#pragma unroll
-      for (int m = 0; m < M; ++m) s[m][i] = hidden ? -INFINITY : s[m][i];
-    }
+    for (int i = 0; i < 16; ++i) s[i] = k0 + 8 * (i >> 2) + (i & 3) >= lim ? -INFINITY : s[i];
   };
   auto tile_max = [&](const f32x16& s) __attribute__((always_inline)) {
     float t = s[0];
@@ -154,7 +130,7 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
   for (bool exact = false;; exact = true) {
     float big = 0.f;
     if (nt > 0) {
-      f32x16 s[M];
+      f32x16 s;
       if (exact) {
         for (int i = 0; i < nt; ++i) {
           issue(kbase, sk, i);
@@ -163,8 +139,7 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
           if (i < wt) {
             scores(s, i);
             if (i >= wfull) mask(s, i);
-#pragma unroll
-            for (int m = 0; m < M; ++m) mx[m] = i == 0 ? tile_max(s[m]) : fmaxf(mx[m], tile_max(s[m]));
+            mx = i == 0 ? tile_max(s) : fmaxf(mx, tile_max(s));
           }
         }
         lds_barrier();
@@ -176,56 +151,62 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
       lds_barrier();
       scores(s, 0);
       if (wfull <= 0) mask(s, 0);
+      if (!exact) mx = tile_max(s);
+      sum = rest = 0.f;
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        if (!exact) mx[m] = tile_max(s[m]);
-        sum[m] = 0.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) zero16(o[m][t]);
-      }
+      for (int t = 0; t < NT; ++t) zero16(o[t]);
       auto sync = [&](int n) __attribute__((always_inline)) {
         wait_vm<2 * PW>();        // group n has landed, n + 1 may be in flight
-        lds_barrier();            // ... for every wave, and all are done with group n - 2
+        lds_barrier();            // ... for every wave, and all are done with group n - 1
         issue_group(n + 2);       // past the last tile: rows of the end again, read by none
       };
-      if (late) sync(0);
+      // A tile's step in a fixed order: the next tile's scores, then the values
+      // times the first and the second half of the weights; each operand is read
+      // from LDS AHEAD products before its use, and the exponentials of a half
+      // stand between the products before it.
+      constexpr int NG = KS + 2 * NT, AHEAD = 2;
       for (int i = 0; i < wt; ++i) {
-        if (!late) sync(i);
-        Frag<bf16> p[M][2];
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-          const float ms = mx[m] * sc;
-          float ts = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            s[m][e] = fast_exp2(fmaf(s[m][e], sc, -ms));
-            ts += s[m][e];
-          }
-          sum[m] += ts;
-          p[m][0] = acc_frag<bf16>(s[m], 0);
-          p[m][1] = acc_frag<bf16>(s[m], 1);
-        }
-        if (late) sync(i + 1);
+        sync(i);
         const unsigned char* vt = sv + (i & (NST - 1)) * R::BYTES;
+        const unsigned char* kt = sk + ((i + 1) & (NST - 1)) * R::BYTES;
+        f32x16 nx;
+        Frag<bf16> p[2], fa[AHEAD];
+        const float ms = mx * sc;
+        float ts = 0.f;
+        zero16(nx);
+        auto read = [&](auto gc) __attribute__((always_inline)) {
+          constexpr int g = decltype(gc)::value, x = g % AHEAD;
+          if constexpr (g < KS) fa[x] = lds_row(kt + kx[g]);
+          else if constexpr (g < NG) fa[x] = ad.col(vt, (g - KS) % NT, (g - KS) / NT);
+        };
+        auto weigh = [&](int half, int e0, int e1) __attribute__((always_inline)) {
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const Frag<bf16> vf = ad.col(vt, t, cc);
-#pragma unroll
-            for (int m = 0; m < M; ++m) mma(o[m][t], vf, p[m][cc]);
+          for (int e = e0; e < e1; ++e) {
+            const float w = fast_exp2(fmaf(s[8 * half + e], sc, -ms));
+            ts += w;
+            p[half].v[e] = (__bf16)w;
           }
-        scores(s, i + 1);         // past the last tile: unused
-        if (i + 1 >= wfull) mask(s, i + 1);
+        };
+        each<AHEAD>(read);
+        each<NG>([&](auto gc) __attribute__((always_inline)) {
+          constexpr int g = decltype(gc)::value;
+          if constexpr (g < KS) mma(nx, fa[g % AHEAD], q[g]);
+          else mma(o[(g - KS) % NT], fa[g % AHEAD], p[(g - KS) / NT]);
+          read(std::integral_constant<int, g + AHEAD>{});
+          if constexpr (g < KS) weigh(0, 8 * g / KS, 8 * (g + 1) / KS);
+          else if constexpr (g < KS + NT) weigh(1, 8 * (g - KS) / NT, 8 * (g - KS + 1) / NT);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        if (i + 1 >= wfull) mask(nx, i + 1);   // (past the last tile: unused)
+        // the tiles' sums, with what each addition dropped
+        const float both = sum + ts;
+        rest += ts - (both - sum);
+        sum = both;
+        s = nx;
       }
-      for (int i = wt; i < nt; ++i) sync(late ? i + 1 : i);
-      if (!late) sync(nt);
+      for (int i = wt; i < nt; ++i) sync(i);
       wait_vm<0>();               // no DMA outlives the sweep
-#pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const float l = pair_sum(sum[m]);
-        if (rok && !(l < 0x1p64f)) big = 1.f;
-      }
+      if (rok && !(pair_sum(sum) < 0x1p64f)) big = 1.f;
     }
     lds_barrier();
     if (exact) break;
@@ -234,7 +215,7 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
     lds_barrier();
     int any = 0;
 #pragma unroll
-    for (int w = 0; w < S::WAVES; ++w) any |= reinterpret_cast<const int*>(smem)[w];
+    for (int w = 0; w < 8; ++w) any |= reinterpret_cast<const int*>(smem)[w];
     lds_barrier();
     if (!any) break;
   }
@@ -248,20 +229,22 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
   const long long stat = (long long)(b * a.hp + pair) * 2 * a.ls + row;
   const long long goff = (tok0 + row0) * ldq + pair * 2 * a.hd;   // the wave's first row
   const int rows = a.L - row0 < 32 ? a.L - row0 : 32;
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const float l = pair_sum(sum[m]);
-    const float inv = rok ? 1.f / l : 0.f;
-    if (h == 0 && row < a.L) {
-      float* const at = a.lse + stat + (m0 + m) * a.ls;
-      *at = rok ? mx[m] * sc + __log2f(l) : INFINITY;
-      if (row == a.L - 1) at[1] = INFINITY;
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[m][t][i] = rok ? o[m][t][i] * inv : 0.f;
+  const float l = pair_sum(sum) + pair_sum(rest), inv = rok ? 1.f / l : 0.f;
+  if (h == 0 && row < a.L) {
+    // log2-sum-exp, from l = f 2^e; and, for the second map, by how much its
+    // rounding to fp32 makes the weights too small
+    int e;
+    const float lf = __log2f(frexpf(l, &e));
+    const double exact = (double)(mx * sc) + ((double)e + (double)lf);   // the weights were taken relative to mx sc
+    float* const at = a.lse + stat + m * a.ls;
+    *at = rok ? (float)exact : INFINITY;
+    if (row == a.L - 1) at[1] = INFINITY;
+    if (m == 1) a.fix[((long long)b * a.hp + pair) * a.ls + row] = (float)((double)(float)exact - exact) * 0.693147181f;
   }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[t][i] = rok ? o[t][i] * inv : 0.f;
   // column of accumulator value (t, i): V's tile has D per half, hd of them in
   // use, and 4 neighbours are in or out together
   auto column = [&](int t, int i, bool& in) __attribute__((always_inline)) {
@@ -269,45 +252,37 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
     in = e0 < a.hd;
     return 32 * t / D * a.hd + e0;
   };
-  if constexpr (M == 1) {
-    unsigned char* const xch = smem + rb * NT * 4096 + lane * 16;
-    if (m0 == 1) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(xch + (t * 4 + (i >> 2)) * 1024) =
-              make_float4(o[0][t][i], o[0][t][i + 1], o[0][t][i + 2], o[0][t][i + 3]);
-    }
-    lds_barrier();
-    if (m0 == 0) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(xch + (t * 4 + (i >> 2)) * 1024);
-          o[0][t][i] = fmaf(-lam, y.x, o[0][t][i]);
-          o[0][t][i + 1] = fmaf(-lam, y.y, o[0][t][i + 1]);
-          o[0][t][i + 2] = fmaf(-lam, y.z, o[0][t][i + 2]);
-          o[0][t][i + 3] = fmaf(-lam, y.w, o[0][t][i + 3]);
-        }
-    }
-    lds_barrier();
-  } else {
+  unsigned char* const xch = smem + rb * NT * 4096 + lane * 16;
+  if (m == 1) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[0][t][i] = fmaf(-lam, o[1][t][i], o[0][t][i]);
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(xch + (t * 4 + (i >> 2)) * 1024) =
+            make_float4(o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]);
   }
+  lds_barrier();
+  if (m == 0) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(xch + (t * 4 + (i >> 2)) * 1024);
+        o[t][i] = fmaf(-lam, y.x, o[t][i]);
+        o[t][i + 1] = fmaf(-lam, y.y, o[t][i + 1]);
+        o[t][i + 2] = fmaf(-lam, y.z, o[t][i + 2]);
+        o[t][i + 3] = fmaf(-lam, y.w, o[t][i + 3]);
+      }
+  }
+  lds_barrier();
   unsigned char* const st = smem + wave * 32 * P2;
-  if (M == 2 || m0 == 1) {
-    constexpr int m = M - 1;
+  if (m == 1) {
     float top = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if ((32 * t) % D + 8 * (i >> 2) + 4 * h < a.hd) top = fmaxf(top, fabsf(o[m][t][i]));
+        if ((32 * t) % D + 8 * (i >> 2) + 4 * h < a.hd) top = fmaxf(top, fabsf(o[t][i]));
     top = pair_max(top);
     const float f = top > 0.f ? 32767.f / top : 0.f;
     if (h == 0 && row < a.L) a.rsc[stat + a.ls] = top / 32767.f;
@@ -319,12 +294,12 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
         const int dv = column(t, i, in);
         uint32_t y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = (uint32_t)__float2int_rn(o[m][t][i + e] * f) & 0xFFFFu;
+        for (int e = 0; e < 4; ++e) y[e] = (uint32_t)__float2int_rn(o[t][i + e] * f) & 0xFFFFu;
         if (in) *reinterpret_cast<uint2*>(st + c * P2 + 2 * dv) = make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
       }
     store_rows(st, P2, reinterpret_cast<short*>(a.o2) + goff, ldq * 2, 4 * a.hd, rows, lane);
   }
-  if (M == 2 || m0 == 0) {
+  if (m == 0) {
     float top = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -333,11 +308,11 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
         bool in;
         const int dv = column(t, i, in);
         if (in)
-          store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + dv, o[0][t][i], o[0][t][i + 1], o[0][t][i + 2], o[0][t][i + 3]);
+          store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + dv, o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          o[0][t][i + e] -= bf2f(f2bf(o[0][t][i + e]));
-          top = fmaxf(top, in ? fabsf(o[0][t][i + e]) : 0.f);
+          o[t][i + e] -= bf2f(f2bf(o[t][i + e]));
+          top = fmaxf(top, in ? fabsf(o[t][i + e]) : 0.f);
         }
       }
     top = pair_max(top);
@@ -352,7 +327,7 @@ __global__ void __launch_bounds__(FwdShape<D>::WAVES * 64, 2) diff_fwd_lds(const
         const int dv = column(t, i, in);
         uint32_t r4 = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r4 |= ((uint32_t)__float2int_rn(o[0][t][i + e] * f) & 0xFFu) << (8 * e);
+        for (int e = 0; e < 4; ++e) r4 |= ((uint32_t)__float2int_rn(o[t][i + e] * f) & 0xFFu) << (8 * e);
         if (in) *reinterpret_cast<uint32_t*>(st + c * P1 + dv) = r4;
       }
     store_rows(st, P1, a.res + goff, ldq, 2 * a.hd, rows, lane);
@@ -486,7 +461,7 @@ void launch_diff_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.L + 127) / 128 * a.hp * a.B));
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, grid, dim3(FwdShape<D>::WAVES * 64), 0, s, a);
+    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, grid, dim3(512), 0, s, a);
     else hipLaunchKernelGGL(diff_fwd_direct<D>, grid, dim3(256), 0, s, a);
   });
 }

@@ -142,6 +142,20 @@ __device__ inline void locate(int bid, int n, int hp, int& blk, int& pair, int& 
   pair = u % hp;
 }
 
+// Two values rounded to bf16 (to nearest even), the first in the low half; and
+// their place in an operand.
+__device__ inline uint32_t round2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ inline void set2(Frag<bf16>& f, int i, uint32_t v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 w = __builtin_bit_cast(u32x4, f.v);
+  w[i / 2] = v;
+  f.v = __builtin_bit_cast(bf16x8, w);
+}
+
 // f(0) .. f(N - 1) with compile-time indices, unrolled however long.
 template <typename F, int... I>
 __device__ inline __attribute__((always_inline)) void each_of(F& f, std::integer_sequence<int, I...>) {
