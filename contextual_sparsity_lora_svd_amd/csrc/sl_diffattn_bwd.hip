@@ -69,16 +69,17 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   for (int i = 0; i < PW; ++i) R::source(wave * PW + i, lane, a.hd, srow[i], scol[i]);
   const unsigned ldb = (unsigned)ldk * 2u;
   const int last = len - 1;
-  auto issue_tile = [&](int tile) __attribute__((always_inline)) {
+  auto issue_part = [&](int tile, int i) __attribute__((always_inline)) {
     const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((tile & (NST - 1)) * R::BYTES + wave * PW * 1024));
+    int r = tile * 32 + srow[i];
+    r = r < last ? r : last;
+    const unsigned off = (unsigned)r * ldb + scol[i];
+    dma16(kbase, off, lds_addr(sk) + d0 + i * 1024);
+    dma16(vbase, off, lds_addr(sv) + d0 + i * 1024);
+  };
+  auto issue_tile = [&](int tile) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < PW; ++i) {
-      int r = tile * 32 + srow[i];
-      r = r < last ? r : last;
-      const unsigned off = (unsigned)r * ldb + scol[i];
-      dma16(kbase, off, lds_addr(sk) + d0 + i * 1024);
-      dma16(vbase, off, lds_addr(sv) + d0 + i * 1024);
-    }
+    for (int i = 0; i < PW; ++i) issue_part(tile, i);
   };
 
   TileAddr<D> ad;
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
         if constexpr (NEXT) mma(ndp, fa[g % AHEAD], go[g - N1 - 2 * N2]);
       }
       read(std::integral_constant<int, g + AHEAD>{});
+      if constexpr (NEXT && g % (NG / PW) == 1 && g / (NG / PW) < PW) issue_part(i + 2, g / (NG / PW));
       if constexpr (g < N1 && PREV) grads(0, 2 * (8 * g / N1), 2 * (8 * (g + 1) / N1));
       if constexpr (g >= N1 && g < N1 + N2 && PREV) grads(1, 2 * (8 * (g - N1) / N2), 2 * (8 * (g - N1 + 1) / N2));
       if constexpr (g == N1 - 1 && NEXT && decltype(masked)::value) mask(n, i);
@@ -177,29 +179,32 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   if (nt > 0) {
     issue_tile(0);
     issue_tile(1);
-    auto advance = [&](int i) __attribute__((always_inline)) {
+    // after it, step i (or the wave's wait for the others) loads tile i + 2
+    auto arrive = [&]() __attribute__((always_inline)) {
       wait_vm<2 * PW>();          // tile i has landed
       lds_barrier();              // ... for every wave, and all are done with tile i - 2
-      issue_tile(i + 2);
     };
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
     int i = 0;
     if (wt > 0) {
-      advance(0);
+      arrive();
       if (wfull > 0) step(0, no, yes, no);
       else step(0, no, yes, yes);
       for (i = 1; i < wfull && i < wt; ++i) {
-        advance(i);
+        arrive();
         step(i, yes, yes, no);
       }
       for (; i < wt; ++i) {
-        advance(i);
+        arrive();
         step(i, yes, yes, yes);
       }
-      step(i, yes, no, no);       // tile wt - 1: its slot is refilled from tile wt + 1's advance on
+      step(i, yes, no, no);       // tile wt - 1: its slot is refilled from tile wt + 1's arrival on
     }
-    for (; i < nt; ++i) advance(i);
+    for (; i < nt; ++i) {
+      arrive();
+      issue_tile(i + 2);
+    }
     wait_vm<0>();
   }
 #pragma unroll
@@ -290,28 +295,34 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   int it_pr = pr0, it_t = t0;                                   // the next tile to load
   // statistics: wave w loads lse (w < 2) or D of map w % 2, 64 rows
   const float* const sbase = (wave < 2 ? a.lse : a.dsum) + (long long)b * a.hp * 2 * a.ls + (wave & 1) * a.ls;
-  auto issue_next = [&](int it) __attribute__((always_inline)) {
+  auto issue_part = [&](int it, int i) __attribute__((always_inline)) {
     const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((it & 1) * R::BYTES + wave * PW * 1024));
-    const bf16* qb = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.q) + tok0 * ldq + it_pr * 2 * a.hd));
-    const bf16* gb = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.da) + tok0 * ldq + it_pr * 2 * a.hd));
-#pragma unroll
-    for (int i = 0; i < PW; ++i) {
-      int r = it_t * 32 + srow[i];
-      r = r < last ? r : last;
-      const unsigned off = (unsigned)r * ldb + scol[i];
-      dma16(qb, off, lds_addr(sq) + d0 + i * 1024);
-      dma16(gb, off, lds_addr(sg) + d0 + i * 1024);
-    }
+    const long long ofs = tok0 * ldq + it_pr * 2 * a.hd;
+    int r = it_t * 32 + srow[i];
+    r = r < last ? r : last;
+    const unsigned off = (unsigned)r * ldb + scol[i];
+    dma16(uniform(reinterpret_cast<const bf16*>(a.q) + ofs), off, lds_addr(sq) + d0 + i * 1024);
+    dma16(uniform(reinterpret_cast<const bf16*>(a.da) + ofs), off, lds_addr(sg) + d0 + i * 1024);
+  };
+  auto issue_stats = [&](int it) __attribute__((always_inline)) {
     int r = it_t * 32 + lane;
     r = r < len ? r : len;                                      // lse there is +inf: weights 0
     const float* sb = reinterpret_cast<const float*>(uniform(sbase + (long long)it_pr * 2 * a.ls));
     const unsigned sd = __builtin_amdgcn_readfirstlane(lds_addr(ss) + (unsigned)((it & 1) * STAT + wave * 256));
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, %2"
                  :: "v"((unsigned)r * 4u), "s"(sd), "s"(sb) : "memory", "m0");
+  };
+  auto issued = [&]() __attribute__((always_inline)) {
     if (++it_t == t0 + ntile) {
       it_t = t0;
       if (it_pr + 1 < pr0 + nh) ++it_pr;                        // past the last: read again, used by none
     }
+  };
+  auto issue_next = [&](int it) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < PW; ++i) issue_part(it, i);
+    issue_stats(it);
+    issued();
   };
 
   TileAddr<D> ad;
@@ -328,15 +339,15 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   if (total > 0) {
     issue_next(0);
     int it = 0;
-    auto advance = [&]() __attribute__((always_inline)) {
+    // after it, tile `it` (or the wave's wait for the others) loads the next one
+    auto arrive = [&]() __attribute__((always_inline)) {
       wait_vm<0>();               // tile `it` has landed
       lds_barrier();              // ... for every wave, and the other slot is read by none
-      issue_next(it + 1);
     };
     // One query tile: the products in order S_1, S_2, dP, dV, dK, each with its
     // operand read from LDS `AHEAD` products before, and between them the
-    // vector work that is ready: the weights while dP is formed, the score
-    // gradients while dV is.  One wave has the SIMD to itself, so only this
+    // vector work that is ready (the weights while dP is formed, the score
+    // gradients while dV is) and the next tile's loads.  One wave has the SIMD to itself, so only this
     // order covers the LDS reads and the exponentials.
     constexpr int N1 = 2 * KS, N2 = 2 * KS, N3 = 2 * NT, N4 = 4 * DT, NOP = N1 + N2 + N3 + N4, AHEAD = 3;
     auto tile = [&](int q0, auto diag) __attribute__((always_inline)) {
@@ -386,15 +397,26 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
           mma(dk[mt / DT][mt % DT], fa[i % AHEAD], df[mt / DT][j / (2 * DT)]);
         }
         read(std::integral_constant<int, i + AHEAD>{});
-        if constexpr (i == N1 - 1) stats(l4, 0, 0);
+        if constexpr (i % 4 == 1 && i / 4 < PW) issue_part(it + 1, i / 4);
+        if constexpr (i == 4 * PW + 1) issue_stats(it + 1);
+        if constexpr (i == 4 * PW + 2) issued();
+        if constexpr (i == KS - 1) stats(l4, 0, 0);
         if constexpr (i == N1 + N2 - 1) stats(d4, 0, 2);
+        if constexpr (i >= KS && i < N1) {   // out of the matrix cores' registers before dP needs them
+          constexpr int e0 = 16 * (i - KS) / KS, e1 = 16 * (i - KS + 1) / KS;
+#pragma unroll
+          for (int e = e0; e < e1; ++e) {
+            if (e % 4 == 0) stats(l4, e + 4, 0);
+            s[0][e] = fmaf(s[0][e], sc, -part4(l4[(e / 4) & 1], e));
+          }
+        }
         if constexpr (i >= N1 && i < N1 + N2) {
           constexpr int e0 = 32 * (i - N1) / N2, e1 = 32 * (i - N1 + 1) / N2;
 #pragma unroll
           for (int e = e0; e < e1; ++e) {
             const int m = e / 16, x = e % 16;
-            if (e % 4 == 0) stats(l4, e + 4, 0);
-            float p = fast_exp2(fmaf(s[m][x], sc, -part4(l4[(e / 4) & 1], e)));
+            if (m == 1 && e % 4 == 0) stats(l4, e + 4, 0);
+            float p = fast_exp2(m == 0 ? s[0][x] : fmaf(s[1][x], sc, -part4(l4[(e / 4) & 1], e)));
             if constexpr (DIAG) p = q0 + 2 * (x & ~3) + 4 * h + (x & 3) < key ? 0.f : p;
             s[m][x] = p;
             w[x] = m ? fmaf(-lam, p, w[x]) : p;
@@ -425,15 +447,18 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
     const int skip = a.causal ? (wave < ntile ? wave : ntile) : 0;   // tiles before this wave's keys
     for (int n = 0; n < nh; ++n) {
       int j = 0;
-      for (; j < skip; ++j, ++it) advance();
+      for (; j < skip; ++j, ++it) {
+        arrive();
+        issue_next(it + 1);
+      }
       if (a.causal && j < ntile) {
-        advance();
+        arrive();
         tile((t0 + j) * 32, std::true_type{});
         ++j;
         ++it;
       }
       for (; j < ntile; ++j, ++it) {
-        advance();
+        arrive();
         tile((t0 + j) * 32, std::false_type{});
       }
     }

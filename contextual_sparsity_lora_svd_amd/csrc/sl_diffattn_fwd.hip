@@ -69,14 +69,15 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
   }
   const unsigned ldb = (unsigned)ldk * 2u;
   const int last = len - 1;
+  auto issue_part = [&](const bf16* base, unsigned char* ring, int tile, int i) __attribute__((always_inline)) {
+    int r = tile * 32 + srow[i];
+    r = r < last ? r : last;
+    dma16(base, (unsigned)r * ldb + scol[i],
+          __builtin_amdgcn_readfirstlane(lds_addr(ring) + (unsigned)((tile & (NST - 1)) * R::BYTES + sins[i] * 1024)));
+  };
   auto issue = [&](const bf16* base, unsigned char* ring, int tile) __attribute__((always_inline)) {
-    const unsigned dst = lds_addr(ring) + (unsigned)((tile & (NST - 1)) * R::BYTES);
 #pragma unroll
-    for (int i = 0; i < PW; ++i) {
-      int r = tile * 32 + srow[i];
-      r = r < last ? r : last;
-      dma16(base, (unsigned)r * ldb + scol[i], __builtin_amdgcn_readfirstlane(dst + sins[i] * 1024));
-    }
+    for (int i = 0; i < PW; ++i) issue_part(base, ring, tile, i);
   };
   // group j: V of tile j, K of the tile after it
   auto issue_group = [&](int j) __attribute__((always_inline)) {
@@ -155,10 +156,11 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
       sum = rest = 0.f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) zero16(o[t]);
-      auto sync = [&](int n) __attribute__((always_inline)) {
+      // after it, tile n's step (or the wave's wait for the others) loads group
+      // n + 2; past the last tile that is rows of the end again, read by none
+      auto arrive = [&]() __attribute__((always_inline)) {
         wait_vm<2 * PW>();        // group n has landed, n + 1 may be in flight
-        lds_barrier();            // ... for every wave, and all are done with group n - 1
-        issue_group(n + 2);       // past the last tile: rows of the end again, read by none
+        lds_barrier();            // ... for every wave, and all are done with group n - 2
       };
       // A tile's step in a fixed order: the next tile's scores, then the values
       // times the first and the second half of the weights; each operand is read
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
       // stand between the products before it.
       constexpr int NG = KS + 2 * NT, AHEAD = 2;
       for (int i = 0; i < wt; ++i) {
-        sync(i);
+        arrive();
         const unsigned char* vt = sv + (i & (NST - 1)) * R::BYTES;
         const unsigned char* kt = sk + ((i + 1) & (NST - 1)) * R::BYTES;
         f32x16 nx;
@@ -193,6 +195,10 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
           if constexpr (g < KS) mma(nx, fa[g % AHEAD], q[g]);
           else mma(o[(g - KS) % NT], fa[g % AHEAD], p[(g - KS) / NT]);
           read(std::integral_constant<int, g + AHEAD>{});
+          if constexpr (g % 2 == 1 && g / 2 < PW) {
+            issue_part(kbase, sk, i + 3, g / 2);
+            issue_part(vbase, sv, i + 2, g / 2);
+          }
           if constexpr (g < KS) weigh(0, 8 * g / KS, 8 * (g + 1) / KS);
           else if constexpr (g < KS + NT) weigh(1, 8 * (g - KS) / NT, 8 * (g - KS + 1) / NT);
           __builtin_amdgcn_sched_barrier(0);
@@ -204,7 +210,10 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
         sum = both;
         s = nx;
       }
-      for (int i = wt; i < nt; ++i) sync(i);
+      for (int i = wt; i < nt; ++i) {
+        arrive();
+        issue_group(i + 2);
+      }
       wait_vm<0>();               // no DMA outlives the sweep
       if (rok && !(pair_sum(sum) < 0x1p64f)) big = 1.f;
     }
