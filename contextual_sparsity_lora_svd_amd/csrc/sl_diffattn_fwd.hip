@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
       // from LDS AHEAD products before its use, and the exponentials of a half
       // stand between the products before it.
       constexpr int NG = KS + 2 * NT, AHEAD = 2;
-      for (int i = 0; i < wt; ++i) {
-        arrive();
+      auto step = [&](int i, auto masked) __attribute__((always_inline)) {
         const unsigned char* vt = sv + (i & (NST - 1)) * R::BYTES;
         const unsigned char* kt = sk + ((i + 1) & (NST - 1)) * R::BYTES;
         f32x16 nx;
@@ -203,14 +202,23 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
           else if constexpr (g < KS + NT) weigh(1, 8 * (g - KS) / NT, 8 * (g - KS + 1) / NT);
           __builtin_amdgcn_sched_barrier(0);
         });
-        if (i + 1 >= wfull) mask(nx, i + 1);   // (past the last tile: unused)
+        if constexpr (decltype(masked)::value) mask(nx, i + 1);   // (past the last tile: unused)
         // the tiles' sums, with what each addition dropped
         const float both = sum + ts;
         rest += ts - (both - sum);
         sum = both;
         s = nx;
+      };
+      int i = 0;
+      for (; i + 1 < wfull && i < wt; ++i) {
+        arrive();
+        step(i, std::false_type{});
       }
-      for (int i = wt; i < nt; ++i) {
+      for (; i < wt; ++i) {
+        arrive();
+        step(i, std::true_type{});
+      }
+      for (; i < nt; ++i) {
         arrive();
         issue_group(i + 2);
       }

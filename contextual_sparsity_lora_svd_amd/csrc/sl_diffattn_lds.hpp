@@ -146,8 +146,8 @@ __device__ inline void locate(int bid, int n, int hp, int& blk, int& pair, int& 
 // their place in an operand.
 __device__ inline uint32_t round2(float a, float b) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 __device__ inline void set2(Frag<bf16>& f, int i, uint32_t v) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
