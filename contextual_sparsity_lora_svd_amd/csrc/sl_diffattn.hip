@@ -49,7 +49,9 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   pl.res = s.take(dt == SL_BF16 ? T * hq * hd : 0);
   pl.saved = s.off;
   const long long blocks = (long long)((lay->seq_len + 127) / 128) * lay->batch;   // of 4 waves
-  pl.npart = (int)(4 * blocks * (hq / 2));
+  // one partial sum of dlambda per wave: 128 rows per workgroup in bf16, 32 in fp32
+  const long long nwg = dt == SL_BF16 ? blocks : (long long)((lay->seq_len + 31) / 32) * lay->batch;
+  pl.npart = (int)(4 * nwg * (hq / 2));
   pl.dsum = w.take(stats * 4);
   pl.dlam = w.take((size_t)pl.npart * 8);
   pl.split = dt == SL_BF16 ? dkv_split(blocks * (hkv / 2), hq / hkv, (lay->seq_len + 31) / 32) : 1;

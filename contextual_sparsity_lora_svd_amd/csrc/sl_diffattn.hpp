@@ -149,6 +149,27 @@ __device__ inline int opaque(int x) {
   return x;
 }
 
+// The four waves' values added in order; the last wave ends with the sum.  sm holds
+// N tiles of 1024 floats.
+template <int N> __device__ inline void add_waves(f32x16 (&x)[N], float* sm, int wave, int lane) {
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          float4* const p = reinterpret_cast<float4*>(sm + (n * 4 + i / 4) * 256) + lane;
+          if (w > 0) {
+            const float4 y = *p;
+            x[n][i] += y.x; x[n][i + 1] += y.y; x[n][i + 2] += y.z; x[n][i + 3] += y.w;
+          }
+          if (w < 3) *p = make_float4(x[n][i], x[n][i + 1], x[n][i + 2], x[n][i + 3]);
+        }
+    }
+    __syncthreads();
+  }
+}
+
 // Run f with the row width D that serves head_dim hd.
 template <typename F> inline void by_width(int hd, F f) {
   if (hd <= 32) f(std::integral_constant<int, 32>{});

@@ -61,7 +61,40 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   for (int m = 0; m < 2; ++m) {
     const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
     lse[m] = rok ? a.lse[at] : INFINITY;      // weights of rows past the end: 0
-    ds[m] = rok ? a.dsum[at] : 0.f;
+    ds[m] = 0.f;
+  }
+  // D_2 = dO . O_2 and D_1 = dO . (O + lambda O_2) of the row, from the saved
+  // integers; dK and dV read them from memory
+  {
+    const long long st = (long long)(b * a.hp + pair) * 2 * a.ls + row;
+    float dres = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2 * KS; ++x) {
+      const int col = (x % KS) * 16 + h * 8;
+      if (rok && col < a.hd) {
+        const long long at = qoff + x / KS * a.hd + col;
+        const Frag<bf16> of = load_row<bf16>(reinterpret_cast<const bf16*>(a.a) + at, true);
+        const uint4 yv = *reinterpret_cast<const uint4*>(reinterpret_cast<const short*>(a.o2) + at);
+        const uint2 rv = *reinterpret_cast<const uint2*>(a.res + at);
+        const uint32_t yw[4] = {yv.x, yv.y, yv.z, yv.w}, rw[2] = {rv.x, rv.y};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float gx = (float)go[x].v[e];
+          ds[0] = fmaf(gx, (float)of.v[e], ds[0]);
+          ds[1] = fmaf(gx, (float)(short)(yw[e >> 1] >> (16 * (e & 1))), ds[1]);
+          dres = fmaf(gx, (float)(signed char)(rw[e >> 2] >> (8 * (e & 3))), dres);
+        }
+      }
+    }
+    if (rok) {
+      ds[1] = pair_sum(ds[1]) * a.rsc[st + a.ls];
+      ds[0] = fmaf(lam, ds[1], fmaf(pair_sum(dres), a.rsc[st], pair_sum(ds[0])));
+    }
+    if (h == 0 && row < a.L) {
+      a.dsum[st] = ds[0];
+      a.dsum[st + a.ls] = ds[1];
+      if (row == a.L - 1) a.dsum[st + 1] = a.dsum[st + a.ls + 1] = 0.f;
+    }
   }
   int srow[PW];
   unsigned scol[PW];
@@ -231,6 +264,27 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   store_rows(st, P2, reinterpret_cast<bf16*>(a.dq) + (tok0 + row0) * ldq + pair * 2 * a.hd, ldq * 2, 4 * a.hd, rows, lane);
 }
 
+// dlambda = -(the waves' sums of D_2, added in a fixed order) and the four
+// vectors' gradients: the work of one block of 256 threads.
+__device__ inline void dlambda_block(const DiffArgs& a, double* sm) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < a.npart; i += 256) s += a.dlam_part[i];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = ((sm[0] + sm[1]) + sm[2]) + sm[3];
+  const int i = threadIdx.x;
+  if (i < a.hd) {
+    const float g1 = -(float)s * a.lam[1], g2 = (float)s * a.lam[2];
+    const float q1 = a.lq1[i], k1 = a.lk1[i], q2 = a.lq2[i], k2 = a.lk2[i];
+    a.dlq1[i] = g1 * k1;
+    a.dlk1[i] = g1 * q1;
+    a.dlq2[i] = g2 * k2;
+    a.dlk2[i] = g2 * q2;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // dK and dV.  A wave owns 32 keys (K's rows in registers; V's rows in registers
 // up to D = 64, else in LDS) and walks the query tiles of its group's heads:
@@ -251,6 +305,10 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   unsigned char* const sg = smem + NST * R::BYTES;
   unsigned char* const sv = smem + 2 * NST * R::BYTES;
   unsigned char* const ss = sv + (VREG ? 0 : 4 * R::BYTES);
+  if (blockIdx.x == gridDim.x - 1) {   // the last block sums up dlambda, beside the others
+    dlambda_block(a, reinterpret_cast<double*>(smem));
+    return;
+  }
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int blk, gs, b;
@@ -513,51 +571,6 @@ __global__ void __launch_bounds__(256) diff_dkv_sum(const DiffArgs a) {
   store4<bf16>(reinterpret_cast<bf16*>(v ? a.dv : a.dk) + 4 * i, x.x, x.y, x.z, x.w);
 }
 
-// D_1 = dO . (O + lambda O_2) and D_2 = dO . O_2 from the saved integers.  LP
-// lanes (a power of two) per row and head pair, 8 values each.
-__global__ void __launch_bounds__(256) diff_dsum_q(const DiffArgs a, int lp_log2) {
-  const int lp = 1 << lp_log2, sub = threadIdx.x & (lp - 1);
-  const long long n = (long long)a.B * a.L * a.hp;
-  const float lam = a.lam[0];
-  const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> lp_log2;
-  const bool on = w < n;
-  const int pair = on ? (int)(w % a.hp) : 0;
-  const long long tok = on ? w / a.hp : 0;
-  const int b = (int)(tok / a.L), row = (int)(tok % a.L);
-  const long long st = (long long)(b * a.hp + pair) * 2 * a.ls + row;
-  float d1 = 0.f, d2 = 0.f, r1 = 0.f;
-  if (on && row < a.lens[b] && 8 * sub < 2 * a.hd) {
-    const long long at = (tok * a.hp + pair) * 2 * a.hd + 8 * sub;
-    const uint4 gv = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.da) + at);
-    const uint4 ov = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.a) + at);
-    const uint4 yv = *reinterpret_cast<const uint4*>(reinterpret_cast<const short*>(a.o2) + at);
-    const uint2 rv = *reinterpret_cast<const uint2*>(a.res + at);
-    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, ow[4] = {ov.x, ov.y, ov.z, ov.w}, yw[4] = {yv.x, yv.y, yv.z, yv.w};
-    const uint32_t rw[2] = {rv.x, rv.y};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float gx = bf2f((uint16_t)(gw[j >> 1] >> (16 * (j & 1)))), ox = bf2f((uint16_t)(ow[j >> 1] >> (16 * (j & 1))));
-      const float y = (float)(short)(yw[j >> 1] >> (16 * (j & 1)));
-      const float r = (float)(signed char)(rw[j >> 2] >> (8 * (j & 3)));
-      d1 = fmaf(gx, ox, d1);
-      r1 = fmaf(gx, r, r1);
-      d2 = fmaf(gx, y, d2);
-    }
-    d2 *= a.rsc[st + a.ls];
-    d1 = fmaf(r1, a.rsc[st], d1);
-    d1 = fmaf(lam, d2, d1);
-  }
-  for (int o = lp >> 1; o; o >>= 1) {
-    d1 += __shfl_xor(d1, o);
-    d2 += __shfl_xor(d2, o);
-  }
-  if (on && sub == 0) {
-    a.dsum[st] = d1;
-    a.dsum[st + a.ls] = d2;
-    if (row == a.L - 1) a.dsum[st + 1] = a.dsum[st + a.ls + 1] = 0.f;
-  }
-}
-
 // ---------------------------------------------------------------------------
 // fp32: D_1 = dO . (O + lambda O_2), D_2 = dO . O_2, one wave per row and head pair.
 __global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
@@ -587,21 +600,17 @@ __global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
   if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.ls + row] = lane ? d2 : d1;
 }
 
-// dQ: one wave per 32 queries, keys in order.  It also sums P_2 dP, whose total
-// is -dlambda, in fp32 (D_2 of the saved, rounded O_2 would not be exact enough).
+// dQ: 32 queries per workgroup, every fourth key tile per wave.  The sum of P_2 dP
+// is -dlambda.
 template <int D>
 __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   using T = float;
   constexpr int DT = D / 32;
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int nqb = (a.L + 31) / 32;
-  if (wave >= nqb * a.hp * a.B) {
-    if (lane == 0) a.dlam_part[wave] = 0.0;
-    return;
-  }
-  const int qb = nqb - 1 - wave / (a.hp * a.B);
-  const int pair = (wave / a.B) % a.hp, b = wave % a.B;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(16))) float sm[DT * 1024];
+  const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);
+  const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
   const int g = pair / (a.hp / a.gp), len = a.lens[b];
   const float lam = a.lam[0];
   const int row = qb * 32 + c;
@@ -629,7 +638,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   int kend = len;
   if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
   if (qb * 32 >= len) kend = 0;
-  for (int k0 = 0; k0 < kend; k0 += 32) {
+  for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
     const int kz = opaque(0);
     f32x16 dp, s[2];
     float part = 0.f;
@@ -678,8 +687,10 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) dlam += __shfl_xor(dlam, o);
-  if (lane == 0) a.dlam_part[wave] = dlam;
-  if (row >= a.L) return;
+  if (lane == 0) a.dlam_part[blockIdx.x * 4 + wave] = dlam;
+  add_waves(dq[0], sm, wave, lane);
+  add_waves(dq[1], sm, wave, lane);
+  if (wave != 3 || row >= a.L) return;
   T* out = reinterpret_cast<T*>(a.dq) + qoff;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -695,18 +706,20 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   }
 }
 
-// dK and dV: one wave per 32 keys; the query pairs of the group in order, their
-// queries in order.
+// dK and dV: 32 keys per workgroup, every fourth of the group's query tiles per wave.
 template <int D>
 __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
   using T = float;
   constexpr int DT = D / 32, NT = D / 16;
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int nkb = (a.L + 31) / 32;
-  if (wave >= nkb * a.gp * a.B) return;
-  const int kb = wave / (a.gp * a.B);                 // causal: the first keys have the most queries
-  const int g = (wave / a.B) % a.gp, b = wave % a.B;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(16))) float sm[NT * 1024];
+  if (blockIdx.x == gridDim.x - 1) {
+    dlambda_block(a, reinterpret_cast<double*>(sm));
+    return;
+  }
+  const int kb = blockIdx.x / (a.gp * a.B);           // causal: the first keys have the most queries
+  const int g = blockIdx.x / a.B % a.gp, b = blockIdx.x % a.B;
   const int grp = a.hp / a.gp, len = a.lens[b];
   const float lam = a.lam[0];
   const int key = kb * 32 + c;
@@ -724,12 +737,14 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
   for (int t = 0; t < NT; ++t) zero16(dv[t]);
   const float sc = a.scale * kLog2e;
   const int qbeg = a.causal ? kb * 32 : 0;
+  int turn = 0;                                       // tiles go round the waves
   for (int pr = g * grp; pr < (g + 1) * grp; ++pr) {
     const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * ldq + pr * 2 * a.hd;
     const T* dop = reinterpret_cast<const T*>(a.da) + tok0 * ldq + pr * 2 * a.hd;
     const float* lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.ls;
     const float* dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.ls;
     for (int q0 = kb * 32 < len ? qbeg : len; q0 < len; q0 += 32) {
+      if ((turn++ & 3) != wave) continue;
       const int kz = opaque(0);
       f32x16 dp, s[2], w;
       zero16(dp);
@@ -784,7 +799,10 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
       }
     }
   }
-  if (key >= a.L) return;
+  add_waves(dv, sm, wave, lane);
+  add_waves(dk[0], sm, wave, lane);
+  add_waves(dk[1], sm, wave, lane);
+  if (wave != 3 || key >= a.L) return;
   T* dkp = reinterpret_cast<T*>(a.dk) + koff;
   T* dvp = reinterpret_cast<T*>(a.dv) + koff;
 #pragma unroll
@@ -808,55 +826,24 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
   }
 }
 
-// dlambda = -(sum of the partial sums, in a fixed order); the four vectors' gradients.
-__global__ void __launch_bounds__(1024) diff_dlambda(const DiffArgs a) {
-  __shared__ double sm[16];
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.npart; i += 1024) s += a.dlam_part[i];
-#pragma unroll
-  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
-  __syncthreads();
-  s = 0.0;
-  for (int i = 0; i < 16; ++i) s += sm[i];
-  const int i = threadIdx.x;
-  if (i < a.hd) {
-    const float g1 = -(float)s * a.lam[1], g2 = (float)s * a.lam[2];
-    const float q1 = a.lq1[i], k1 = a.lk1[i], q2 = a.lq2[i], k2 = a.lk2[i];
-    a.dlq1[i] = g1 * k1;
-    a.dlk1[i] = g1 * q1;
-    a.dlq2[i] = g2 * k2;
-    a.dlk2[i] = g2 * q2;
-  }
-}
-
 void launch_diff_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
   const long long rows = (long long)a.B * a.L * a.hp;
-  const int blocks = (a.L + 127) / 128 * a.B;
-  if (dt == SL_BF16) {
-    int lg = 0;
-    while ((8 << lg) < 2 * a.hd) ++lg;
-    const long long per = 256 >> lg;
-    hipLaunchKernelGGL(diff_dsum_q, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a, lg);
-  } else {
-    hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
-  }
+  const int blocks = (a.L + 127) / 128 * a.B, narrow = (a.L + 31) / 32 * a.B;
+  if (dt == SL_F32) hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    const dim3 gq((unsigned)(blocks * a.hp)), gk((unsigned)(blocks * a.gp * a.split));
     if (dt == SL_BF16) {
-      hipLaunchKernelGGL(diff_dq_lds<D>, gq, dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_lds<D>, gk, dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dq_lds<D>, dim3((unsigned)(blocks * a.hp)), dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_lds<D>, dim3((unsigned)(blocks * a.gp * a.split + 1)), dim3(256), 0, s, a);
     } else {
-      hipLaunchKernelGGL(diff_dq_direct<D>, gq, dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_direct<D>, gk, dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dq_direct<D>, dim3((unsigned)(narrow * a.hp)), dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_direct<D>, dim3((unsigned)(narrow * a.gp + 1)), dim3(256), 0, s, a);
     }
   });
   if (a.split > 1) {
     const long long n = 2 * ((long long)a.B * a.L * a.gp * 2 * a.hd / 4);
     hipLaunchKernelGGL(diff_dkv_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
   }
-  hipLaunchKernelGGL(diff_dlambda, dim3(1), dim3(1024), 0, s, a);
 }
 
 }  // namespace sl

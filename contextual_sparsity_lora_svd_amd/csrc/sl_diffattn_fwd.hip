@@ -352,26 +352,28 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// fp32: operands straight from memory: the fp32
-// matrix instructions run at a sixteenth of the bf16 rate, so L1 and L2 feed
-// them (2 bytes per cycle and wave at full rate) and LDS would only add waits.
-// One wave per 32 rows; the transposed score
-// tile (keys x queries) leaves a query in a lane pair, so the softmax needs one
-// exchange per tile and its weights feed the second product from registers.
+// fp32: operands straight from memory.  The fp32 matrix instructions run at a
+// sixteenth of the bf16 rate, so L1 and L2 feed them (2 bytes per cycle and wave
+// at full rate) and LDS would only add waits.  A workgroup owns 32 queries; its
+// four waves take every fourth key tile, each with a running maximum and sum,
+// and the results are joined in order through LDS (short rows and few heads then
+// still fill the GPU).  The transposed score tile (keys x queries) leaves a query
+// in a lane pair, so the softmax needs one exchange per tile and its weights
+// feed the second product from registers.
 template <int D>
 __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   using T = float;
   constexpr int NT = D / 16;   // 32-value tiles of the 2 D wide output
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int nqb = (a.L + 31) / 32;
-  if (wave >= nqb * a.hp * a.B) return;
-  const int qb = nqb - 1 - wave / (a.hp * a.B);       // the longest rows first
-  const int pair = (wave / a.B) % a.hp, b = wave % a.B;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(16))) float sm[NT * 1024];
+  __shared__ float smx[2][4][64], ssum[2][4][64];
+  const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);   // the longest rows first
+  const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
   const int g = pair / (a.hp / a.gp), len = a.lens[b];
   float e1, e2;
   const float lam = lambda_of(a, e1, e2);
-  if (wave == 0 && lane == 0) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.lam[0] = lam;
     a.lam[1] = e1;
     a.lam[2] = e2;
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   int kend = len;
   if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
   if (qb * 32 >= len) kend = 0;
-  for (int k0 = 0; k0 < kend; k0 += 32) {
+  for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
     const int kz = opaque(0);
     f32x16 s[2];
 #pragma unroll
@@ -442,18 +444,38 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
       }
     }
   }
-  if (row >= a.L) return;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    smx[m][wave][lane] = mx[m];
+    ssum[m][wave][lane] = sum[m];
+  }
+  __syncthreads();
   float inv[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const float l = sum[m] + __shfl_xor(sum[m], 32);
+    float top = smx[m][0][lane], l = 0.f;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, smx[m][w][lane]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float x = smx[m][w][lane];
+      if (x > -INFINITY) l = fmaf(exp2f((x - top) * sc), ssum[m][w][lane], l);   // else it saw no key
+    }
+    const float f = mx[m] > -INFINITY ? exp2f((mx[m] - top) * sc) : 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
+    l += __shfl_xor(l, 32);
     inv[m] = rok ? 1.f / l : 0.f;
-    if (h == 0) {
+    if (wave == 0 && h == 0 && row < a.L) {
       float* const at = a.lse + ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
-      *at = rok ? mx[m] * sc + log2f(l) : INFINITY;
+      *at = rok ? top * sc + log2f(l) : INFINITY;
       if (row == a.L - 1) at[1] = INFINITY;
     }
+    add_waves(o[m], sm, wave, lane);
   }
+  if (wave != 3 || row >= a.L) return;
   const long long orow = (tok0 + row) * ldq + pair * 2 * a.hd;
   T* op = reinterpret_cast<T*>(a.o) + orow;
   T* o2p = reinterpret_cast<T*>(a.o2) + orow;
@@ -475,11 +497,11 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
 }
 
 void launch_diff_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.L + 127) / 128 * a.hp * a.B));
+  const dim3 wide((unsigned)((a.L + 127) / 128 * a.hp * a.B)), narrow((unsigned)((a.L + 31) / 32 * a.hp * a.B));
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL(diff_fwd_direct<D>, grid, dim3(256), 0, s, a);
+    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, wide, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL(diff_fwd_direct<D>, narrow, dim3(256), 0, s, a);
   });
 }
 
