@@ -18,26 +18,40 @@ namespace sl {
 //
 // The weights are rounded to bf16 for the matrix cores (half a step, 2^-8); their
 // sum is not.
-template <int D>
-__global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
+//
+// RB blocks of 32 queries per workgroup.  Four, with tiles loaded two ahead, move
+// the fewest bytes.  Two, loaded one ahead, leave room for a second workgroup on
+// the CU: causal ones of very different lengths then share it, a long one with a
+// short one (they are dispatched in that order), and the long one has the SIMDs to
+// itself once the other is done; and where there is no second one, it has them
+// from the start.  Measured with four / two, causal, heads of 128 (128-row
+// workgroups): 2 x 1024 tokens of 32 heads (256) 62 / 54 us, 1 x 2048 of 8 (64)
+// 82 / 65, 1 x 4096 of 16 (256) 166 / 153, 1 x 4096 of 32 (512) 233 / 256; not
+// causal, 1 x 1024 of 16 (64) 53 / 44, 1 x 2048 of 32 (256) 123 / 133.
+template <int D, int RB>
+__global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
   using R = RowTile<D>;
-  constexpr int NT = D / 16, KS = D / 16, NST = 4;
-  constexpr int PW = (R::NDMA + 7) / 8;                   // DMA per wave; the last may be issued twice
+  constexpr int NT = D / 16, KS = D / 16, WAVES = 2 * RB, ROWS = 32 * RB;
+  constexpr int NST = RB == 4 ? 4 : 2, DIST = NST / 2;    // tiles in the ring, tiles loaded ahead
+  constexpr int PW = (R::NDMA + WAVES - 1) / WAVES;       // DMA per wave; the last may be issued twice
   constexpr int P2 = 4 * D + 16, P1 = 2 * D + 16;         // staged result rows: 2-byte and 1-byte values
-  constexpr int STAGED = 8 * 32 * P2;
+  constexpr int STAGED = WAVES * 32 * P2;
   constexpr int RING = 2 * NST * R::BYTES > STAGED ? 2 * NST * R::BYTES : STAGED;
-  static_assert(4 * NT * 4096 <= RING, "four waves' P_2 V fit the ring");
+  static_assert(RB * NT * 4096 <= RING, "four waves' P_2 V fit the ring");
   __shared__ __attribute__((aligned(1024))) unsigned char smem[RING + 64];
   unsigned char* const sk = smem;
   unsigned char* const sv = smem + NST * R::BYTES;
   float* const slam = reinterpret_cast<float*>(smem + RING);
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m = wave >> 2, rb = wave & 3;                 // map, block of 32 rows
-  const int nqb = (a.L + 127) / 128;
+  const int m = wave / RB, rb = wave % RB;                // map, block of 32 rows
+  const int nqb = (a.L + ROWS - 1) / ROWS;
   int blk, pair, b;
   locate(blockIdx.x, a.hp * a.B, a.hp, blk, pair, b);
-  const int q0 = (nqb - 1 - blk) * 128, len = a.lens[b], g = pair / (a.hp / a.gp);
+  // the longest rows first; with two workgroups to a CU, the second half of the
+  // blocks the other way round
+  if (RB == 2 && 2 * blk >= nqb) blk = nqb - 1 - (blk - (nqb + 1) / 2);
+  const int q0 = (nqb - 1 - blk) * ROWS, len = a.lens[b], g = pair / (a.hp / a.gp);
   const int row0 = q0 + rb * 32, row = row0 + c;
   const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
   const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd;
@@ -47,7 +61,7 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
 
   int kend = q0 < len ? len : 0, wend = row0 < len ? len : 0;
   if (a.causal) {
-    kend = kend < q0 + 128 ? kend : q0 + 128;
+    kend = kend < q0 + ROWS ? kend : q0 + ROWS;
     wend = wend < row0 + 32 ? wend : row0 + 32;
   }
   const int nt = (kend + 31) / 32, wt = (wend + 31) / 32;      // key tiles of the workgroup, of this wave
@@ -147,8 +161,8 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
       }
       issue(kbase, sk, 0);
       issue_group(0);
-      issue_group(1);
-      wait_vm<4 * PW>();
+      if constexpr (DIST == 2) issue_group(1);
+      wait_vm<2 * DIST * PW>();
       lds_barrier();
       scores(s, 0);
       if (wfull <= 0) mask(s, 0);
@@ -157,10 +171,10 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) zero16(o[t]);
       // after it, tile n's step (or the wave's wait for the others) loads group
-      // n + 2; past the last tile that is rows of the end again, read by none
+      // n + DIST; past the last tile that is rows of the end again, read by none
       auto arrive = [&]() __attribute__((always_inline)) {
-        wait_vm<2 * PW>();        // group n has landed, n + 1 may be in flight
-        lds_barrier();            // ... for every wave, and all are done with group n - 2
+        wait_vm<2 * (DIST - 1) * PW>();   // group n has landed, a later one may be in flight
+        lds_barrier();                    // ... for every wave, and all are done with group n - 1
       };
       // A tile's step in a fixed order: the next tile's scores, then the values
       // times the first and the second half of the weights; each operand is read
@@ -195,8 +209,8 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
           else mma(o[(g - KS) % NT], fa[g % AHEAD], p[(g - KS) / NT]);
           read(std::integral_constant<int, g + AHEAD>{});
           if constexpr (g % 2 == 1 && g / 2 < PW) {
-            issue_part(kbase, sk, i + 3, g / 2);
-            issue_part(vbase, sv, i + 2, g / 2);
+            issue_part(kbase, sk, i + DIST + 1, g / 2);
+            issue_part(vbase, sv, i + DIST, g / 2);
           }
           if constexpr (g < KS) weigh(0, 8 * g / KS, 8 * (g + 1) / KS);
           else if constexpr (g < KS + NT) weigh(1, 8 * (g - KS) / NT, 8 * (g - KS + 1) / NT);
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
       }
       for (; i < nt; ++i) {
         arrive();
-        issue_group(i + 2);
+        issue_group(i + DIST);
       }
       wait_vm<0>();               // no DMA outlives the sweep
       if (rok && !(pair_sum(sum) < 0x1p64f)) big = 1.f;
@@ -232,7 +246,7 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_lds(const DiffArgs a) {
     lds_barrier();
     int any = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) any |= reinterpret_cast<const int*>(smem)[w];
+    for (int w = 0; w < WAVES; ++w) any |= reinterpret_cast<const int*>(smem)[w];
     lds_barrier();
     if (!any) break;
   }
@@ -497,11 +511,13 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
 }
 
 void launch_diff_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
-  const dim3 wide((unsigned)((a.L + 127) / 128 * a.hp * a.B)), narrow((unsigned)((a.L + 31) / 32 * a.hp * a.B));
+  const int n = a.hp * a.B;
+  auto grid = [&](int rows) { return dim3((unsigned)((a.L + rows - 1) / rows * n)); };
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (dt == SL_BF16) hipLaunchKernelGGL(diff_fwd_lds<D>, wide, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL(diff_fwd_direct<D>, narrow, dim3(256), 0, s, a);
+    if (dt != SL_BF16) hipLaunchKernelGGL(diff_fwd_direct<D>, grid(32), dim3(256), 0, s, a);
+    else if (a.causal ? grid(128).x >= 512 : grid(64).x > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((diff_fwd_lds<D, 2>), grid(64), dim3(256), 0, s, a);
   });
 }
 
