@@ -8,21 +8,40 @@ namespace sl {
 struct DiffPlan {
   size_t lse, lam, fix, rsc, o2, res, saved;    // offsets and size of the saved buffer
   size_t dsum, dlam, part, ws;             // of the workspace
-  int npart, split;
   long long part_elems;                    // of one part of dK or dV
 };
 
-// Parts that a kv group's heads are cut into for dK and dV: one workgroup per
-// 128 keys leaves CUs idle (or waiting for the longest) below two rounds of
-// 256; short loops are not worth the second launch.
-static int dkv_split(long long blocks, int grp, int tiles) {
-  int s = 1;
-  if (grp * tiles <= 16) return s;
-  while (s < grp && blocks * s < 512) {
-    ++s;
-    while (grp % s) ++s;
-  }
-  return s;
+// Work of the bf16 backward's workgroups: 128 rows (or keys) each, every wave 32
+// of them, or 64 with two waves to a row taking turns at the tiles, which doubles
+// the workgroups and halves their length but loads each tile for half the rows.
+// The second kind is taken where the first leaves CUs idle: while there are not
+// more than 256 of the second, and, of causal workgroups (whose lengths differ, so
+// that the longest decides), up to 256 or, in long sequences, 512 of the first.
+// Measured, 128 / 64 rows, heads of 128, dQ and dK/dV apart: 1 x 1024 of 16 heads,
+// 8 kv (64 workgroups of 128) 64 / 47 and 73 / 55 us; causal 1 x 2048 of 8 (64)
+// 112 / 72 and 125 / 84, 1 x 4096 of 16 (256) 221 / 185 and 249 / 207, but 2 x 1024
+// of 32 (256) 76 / 75 and 81 / 86, 1 x 4096 of 32 (512) 345 / 400 and 388 / 455.
+struct DiffGrid {
+  int dq_rows, dkv_rows, split;
+};
+static DiffGrid diff_grid(int B, int L, int hp, int gp, bool causal) {
+  auto blocks = [&](int rows) { return (long long)((L + rows - 1) / rows) * B; };
+  auto rows = [&](int n) {       // n workgroups per block of rows
+    return blocks(64) * n <= 256 || (causal && blocks(128) * n < (L > 1024 ? 512 : 256)) ? 64 : 128;
+  };
+  DiffGrid g;
+  g.dq_rows = rows(hp);
+  // parts that a kv group's heads are cut into, while there are fewer workgroups
+  // than two rounds of 256; short loops are not worth the launch that adds them
+  const int grp = hp / gp;
+  g.split = 1;
+  if (grp * ((L + 31) / 32) > 16)
+    while (g.split < grp && blocks(128) * gp * g.split < 512) {
+      ++g.split;
+      while (grp % g.split) ++g.split;
+    }
+  g.dkv_rows = rows(gp * g.split);
+  return g;
 }
 
 static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs, DiffPlan& pl) {
@@ -48,15 +67,12 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   pl.o2 = s.take(T * hq * hd * (dt == SL_BF16 ? 2 : 4));
   pl.res = s.take(dt == SL_BF16 ? T * hq * hd : 0);
   pl.saved = s.off;
-  const long long blocks = (long long)((lay->seq_len + 127) / 128) * lay->batch;   // of 4 waves
-  // one partial sum of dlambda per wave: 128 rows per workgroup in bf16, 32 in fp32
-  const long long nwg = dt == SL_BF16 ? blocks : (long long)((lay->seq_len + 31) / 32) * lay->batch;
-  pl.npart = (int)(4 * nwg * (hq / 2));
   pl.dsum = w.take(stats * 4);
-  pl.dlam = w.take((size_t)pl.npart * 8);
-  pl.split = dt == SL_BF16 ? dkv_split(blocks * (hkv / 2), hq / hkv, (lay->seq_len + 31) / 32) : 1;
+  // a partial sum of dlambda per wave, 4 to a workgroup of 32 rows or more
+  pl.dlam = w.take(4 * (size_t)((lay->seq_len + 31) / 32) * lay->batch * (hq / 2) * 8);
+  const int split = dt == SL_BF16 ? diff_grid(lay->batch, lay->seq_len, hq / 2, hkv / 2, false).split : 1;
   pl.part_elems = T * hkv * hd;
-  pl.part = w.take(pl.split > 1 ? 2 * (size_t)pl.split * pl.part_elems * 4 : 0);
+  pl.part = w.take(split > 1 ? 2 * (size_t)split * pl.part_elems * 4 : 0);
   pl.ws = w.off;
   return SL_OK;
 }
@@ -159,10 +175,13 @@ extern "C" sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const s
   saved_args(a, pl, const_cast<void*>(saved));
   a.dsum = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.dsum);
   a.dlam_part = reinterpret_cast<double*>(reinterpret_cast<char*>(ws) + pl.dlam);
-  a.npart = pl.npart;
-  a.split = pl.split;
+  const DiffGrid grid = dt == SL_BF16 ? diff_grid(a.B, a.L, a.hp, a.gp, a.causal) : DiffGrid{32, 32, 1};
+  a.split = grid.split;
+  a.dq_rows = grid.dq_rows;
+  a.dkv_rows = grid.dkv_rows;
+  a.npart = 4 * ((a.L + grid.dq_rows - 1) / grid.dq_rows) * a.B * a.hp;
   a.dk_part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.part);
-  a.dv_part = a.dk_part + pl.split * pl.part_elems;
+  a.dv_part = a.dk_part + grid.split * pl.part_elems;
   a.dlq1 = g->dlq1; a.dlk1 = g->dlk1; a.dlq2 = g->dlq2; a.dlk2 = g->dlk2;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   launch_diff_bwd(dt, a, s);

@@ -40,6 +40,7 @@ struct DiffArgs {
   int B, L, hp, gp, hd;      // hp query pairs, gp kv pairs
   int ls;                    // L + 1: statistics of one row more than there are, past every length
   int causal, npart, split;
+  int dq_rows, dkv_rows;     // bf16: rows, or keys, of a workgroup
   int lens[SL_MAX_SEQS];
 };
 

@@ -13,36 +13,44 @@ namespace sl {
 // zero, so what one rounding of 2^-8 leaves behind is not small beside dQ where
 // the keys have something in common.  It costs a third more products (1 x 4096,
 // 8 kv heads of 128: dQ's error 1.5 to 1.1 times that of its own rounding to bf16).
+// H = 1: four row blocks to a workgroup, tiles loaded two ahead.  H = 2: two row
+// blocks, each with two waves that take every other tile and add their sums in the
+// end (where each kind pays: DiffGrid).
 // The sum of P_2 dP, which is -dlambda, stays in fp32 over a tile and in fp64
 // beyond, with what the log-sum-exp's rounding did to the row taken out again.
-template <int D>
+template <int D, int H>
 __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   using R = RowTile<D>;
-  constexpr int DT = D / 32, KS = D / 16, NST = 4, PW = R::PER_WAVE, P2 = 4 * D + 16;
-  constexpr int RING = 2 * NST * R::BYTES;
-  static_assert(4 * 32 * P2 <= RING, "the staged results fit the ring");
+  constexpr int DT = D / 32, KS = D / 16, PW = R::PER_WAVE, P2 = 4 * D + 16;
+  constexpr int STEP = H * R::BYTES, ROWS = 128 / H;
+  constexpr int DIST = H == 1 ? 2 : 1;                    // steps that tiles are loaded ahead
+  constexpr int NK = H == 1 ? 4 : 3, NV = H == 1 ? 4 : 2; // ring; K is read for one step more than V
+  constexpr int RING = (NK + NV) * STEP;
+  static_assert(4 / H * 32 * P2 <= RING && 4 * DT * 4096 <= RING, "the halves and the staged results fit the ring");
   __shared__ __attribute__((aligned(1024))) unsigned char smem[RING];
   unsigned char* const sk = smem;
-  unsigned char* const sv = smem + NST * R::BYTES;
+  unsigned char* const sv = smem + NK * STEP;
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nqb = (a.L + 127) / 128;
+  const int rb = wave / H, half = wave % H;               // block of 32 rows, every H-th key tile
+  const int nqb = (a.L + ROWS - 1) / ROWS;
   int blk, pair, b;
   locate(blockIdx.x, a.hp * a.B, a.hp, blk, pair, b);
-  const int q0 = (nqb - 1 - blk) * 128, len = a.lens[b], g = pair / (a.hp / a.gp);
-  const int row = q0 + wave * 32 + c;
+  const int q0 = (nqb - 1 - blk) * ROWS, len = a.lens[b], g = pair / (a.hp / a.gp);
+  const int row0 = q0 + rb * 32, row = row0 + c;
   const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
   const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd;
   const bf16* kbase = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.k) + tok0 * ldk + g * 2 * a.hd));
   const bf16* vbase = reinterpret_cast<const bf16*>(uniform(reinterpret_cast<const bf16*>(a.v) + tok0 * ldk + g * 2 * a.hd));
   const bool rok = row < len;
-  int kend = q0 < len ? len : 0, wend = q0 + wave * 32 < len ? len : 0;
+  int kend = q0 < len ? len : 0, wend = row0 < len ? len : 0;
   if (a.causal) {
-    kend = kend < q0 + 128 ? kend : q0 + 128;
-    wend = wend < q0 + wave * 32 + 32 ? wend : q0 + wave * 32 + 32;
+    kend = kend < q0 + ROWS ? kend : q0 + ROWS;
+    wend = wend < row0 + 32 ? wend : row0 + 32;
   }
-  const int nt = (kend + 31) / 32, wt = (wend + 31) / 32;
-  const int wfull = a.causal ? ((q0 + wave * 32 + 1 < len ? q0 + wave * 32 + 1 : len) / 32) : len / 32;
+  // steps of H tiles: of the workgroup, of this wave, and those that need no mask
+  const int nt = (kend + 32 * H - 1) / (32 * H), wt = ((wend + 31) / 32 + H - 1 - half) / H;
+  const int wfull = ((a.causal && row0 + 1 < len ? row0 + 1 : len) / 32 + H - 1 - half) / H;
   const float lam = a.lam[0];
 
   Frag<bf16> q[2][KS], go[2 * KS];
@@ -90,7 +98,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
       ds[1] = pair_sum(ds[1]) * a.rsc[st + a.ls];
       ds[0] = fmaf(lam, ds[1], fmaf(pair_sum(dres), a.rsc[st], pair_sum(ds[0])));
     }
-    if (h == 0 && row < a.L) {
+    if (h == 0 && half == 0 && row < a.L) {
       a.dsum[st] = ds[0];
       a.dsum[st + a.ls] = ds[1];
       if (row == a.L - 1) a.dsum[st + 1] = a.dsum[st + a.ls + 1] = 0.f;
@@ -102,17 +110,17 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   for (int i = 0; i < PW; ++i) R::source(wave * PW + i, lane, a.hd, srow[i], scol[i]);
   const unsigned ldb = (unsigned)ldk * 2u;
   const int last = len - 1;
-  auto issue_part = [&](int tile, int i) __attribute__((always_inline)) {
-    const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((tile & (NST - 1)) * R::BYTES + wave * PW * 1024));
-    int r = tile * 32 + srow[i];
+  auto issue_part = [&](int step, int i) __attribute__((always_inline)) {   // i < PW: the first tile
+    const unsigned d0 = (unsigned)(i / PW * R::BYTES + (wave * PW + i % PW) * 1024);
+    int r = step * 32 * H + i / PW * 32 + srow[i % PW];
     r = r < last ? r : last;
-    const unsigned off = (unsigned)r * ldb + scol[i];
-    dma16(kbase, off, lds_addr(sk) + d0 + i * 1024);
-    dma16(vbase, off, lds_addr(sv) + d0 + i * 1024);
+    const unsigned off = (unsigned)r * ldb + scol[i % PW];
+    dma16(kbase, off, __builtin_amdgcn_readfirstlane(lds_addr(sk) + (unsigned)(step % NK * STEP) + d0));
+    dma16(vbase, off, __builtin_amdgcn_readfirstlane(lds_addr(sv) + (unsigned)(step % NV * STEP) + d0));
   };
-  auto issue_tile = [&](int tile) __attribute__((always_inline)) {
+  auto issue_step = [&](int step) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < PW; ++i) issue_part(tile, i);
+    for (int i = 0; i < H * PW; ++i) issue_part(step, i);
   };
 
   TileAddr<D> ad;
@@ -126,9 +134,9 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   const double fix = rok ? 1.0 + (double)a.fix[((long long)b * a.hp + pair) * a.ls + row] : 1.0;
   double dlam = 0.0;
 
-  auto mask = [&](f32x16 (&s)[2], int tile) __attribute__((always_inline)) {
+  auto mask = [&](f32x16 (&s)[2], int step) __attribute__((always_inline)) {
     const int lim = a.causal && row + 1 < len ? row + 1 : len;
-    const int k0 = tile * 32 + 4 * h;
+    const int k0 = (H * step + half) * 32 + 4 * h;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const bool hidden = k0 + 8 * (i >> 2) + (i & 3) >= lim;
@@ -141,12 +149,13 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   // map's dQ and then dP of tile i, while the weights of tile i are.  Operands are
   // read AHEAD products early.
   constexpr int N1 = 2 * KS, N2 = 2 * DT, NG = 2 * N1 + 2 * N2, AHEAD = 3;
+  constexpr int GAP = H == 1 ? NG / PW : 2;               // products between loads
   f32x16 s[2], dp;
   auto step = [&](int i, auto has_prev, auto has_next, auto masked) __attribute__((always_inline)) {
     constexpr bool PREV = decltype(has_prev)::value, NEXT = decltype(has_next)::value;
-    const unsigned char* kt = sk + (i & (NST - 1)) * R::BYTES;
-    const unsigned char* vt = sv + (i & (NST - 1)) * R::BYTES;
-    const unsigned char* kp = sk + ((i - 1) & (NST - 1)) * R::BYTES;
+    const unsigned char* kt = sk + i % NK * STEP + half * R::BYTES;
+    const unsigned char* vt = sv + i % NV * STEP + half * R::BYTES;
+    const unsigned char* kp = sk + (i + NK - 1) % NK * STEP + half * R::BYTES;
     f32x16 n[2], ndp;
     Frag<bf16> hi[2][2], lo[2][2], fa[AHEAD];
     float part = 0.f;
@@ -194,7 +203,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
         if constexpr (NEXT) mma(ndp, fa[g % AHEAD], go[g - N1 - 2 * N2]);
       }
       read(std::integral_constant<int, g + AHEAD>{});
-      if constexpr (NEXT && g % (NG / PW) == 1 && g / (NG / PW) < PW) issue_part(i + 2, g / (NG / PW));
+      if constexpr (NEXT && g % GAP == 1 && g / GAP < H * PW) issue_part(i + DIST, g / GAP);
       if constexpr (g < N1 && PREV) grads(0, 2 * (8 * g / N1), 2 * (8 * (g + 1) / N1));
       if constexpr (g >= N1 && g < N1 + N2 && PREV) grads(1, 2 * (8 * (g - N1) / N2), 2 * (8 * (g - N1 + 1) / N2));
       if constexpr (g == N1 - 1 && NEXT && decltype(masked)::value) mask(n, i);
@@ -210,12 +219,12 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   };
 
   if (nt > 0) {
-    issue_tile(0);
-    issue_tile(1);
-    // after it, step i (or the wave's wait for the others) loads tile i + 2
+    issue_step(0);
+    if (DIST == 2) issue_step(1);
+    // after it, step i (or the wave's wait for the others) loads the tiles of step i + DIST
     auto arrive = [&]() __attribute__((always_inline)) {
-      wait_vm<2 * PW>();          // tile i has landed
-      lds_barrier();              // ... for every wave, and all are done with tile i - 2
+      wait_vm<2 * PW * (DIST - 1)>();   // the tiles of step i have landed
+      lds_barrier();                    // ... for every wave, and all are done with step i - 1
     };
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
@@ -232,36 +241,50 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
         arrive();
         step(i, yes, yes, yes);
       }
-      step(i, yes, no, no);       // tile wt - 1: its slot is refilled from tile wt + 1's arrival on
+      step(i, yes, no, no);       // K of step wt - 1: refilled from step wt + 1's arrival on
     }
     for (; i < nt; ++i) {
       arrive();
-      issue_tile(i + 2);
+      issue_step(i + DIST);
     }
     wait_vm<0>();
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) dlam += __shfl_xor(dlam, o);
   if (lane == 0) a.dlam_part[blockIdx.x * 4 + wave] = dlam;
+  // the two waves of a row block: the first ends with the sum of map 1, the second of map 2
   lds_barrier();                  // the ring is free
-  unsigned char* const st = smem + wave * 32 * P2;
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float f = m ? -lam * a.scale : a.scale;
+  if constexpr (H == 2) {
+    unsigned char* const mine = smem + wave * DT * 4096;
+    unsigned char* const other = smem + (wave ^ 1) * DT * 4096;
+    if (half) put_acc(dq[0], mine, lane);
+    else put_acc(dq[1], mine, lane);
+    lds_barrier();
+    if (half) add_acc(dq[1], other, lane);
+    else add_acc(dq[0], other, lane);
+    lds_barrier();
+  }
+  unsigned char* const st = smem + rb * 32 * P2;
+  auto stage = [&](const f32x16 (&x)[DT], int m, float f) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const int d = 32 * t + 2 * i + 4 * h;
         if (d >= a.hd) continue;
-        float x[4];
+        float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = rok ? dq[m][t][i + e] * f : 0.f;
-        store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + m * a.hd + d, x[0], x[1], x[2], x[3]);
+        for (int e = 0; e < 4; ++e) y[e] = rok ? x[t][i + e] * f : 0.f;
+        store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + m * a.hd + d, y[0], y[1], y[2], y[3]);
       }
-  }
-  const int row0 = q0 + wave * 32, rows = a.L - row0 < 32 ? a.L - row0 : 32;
-  store_rows(st, P2, reinterpret_cast<bf16*>(a.dq) + (tok0 + row0) * ldq + pair * 2 * a.hd, ldq * 2, 4 * a.hd, rows, lane);
+  };
+  if (H == 1 || half == 0) stage(dq[0], 0, a.scale);
+  if (H == 1 || half == 1) stage(dq[1], 1, -lam * a.scale);
+  if (H == 2) lds_barrier();
+  constexpr int NR = 32 / H;
+  const int r0 = row0 + NR * half, rows = a.L - r0 < NR ? a.L - r0 : NR;
+  store_rows(st + NR * half * P2, P2, reinterpret_cast<bf16*>(a.dq) + (tok0 + r0) * ldq + pair * 2 * a.hd, ldq * 2, 4 * a.hd,
+             rows, lane);
 }
 
 // dlambda = -(the waves' sums of D_2, added in a fixed order) and the four
@@ -291,45 +314,49 @@ __device__ inline void dlambda_block(const DiffArgs& a, double* sm) {
 // scores and dP = dO V^T with a key per lane, then dV^T += dO^T (P_1 - lambda P_2)
 // and dK_m^T += Q_m^T dS_m with the tile's rows read by columns.  A key's column
 // never meets another's, so keys past the end need no mask: their results are
-// written as 0.  The heads of a group are cut into `split` parts where one
+// written as 0.  H as in dQ, of key blocks and query tiles.  The heads of a group are cut into `split` parts where one
 // workgroup per key block would leave CUs idle; the parts' sums are then fp32
 // and diff_dkv_sum adds them in order.
-template <int D>
+template <int D, int H>
 __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   using R = RowTile<D>;
-  constexpr int DT = D / 32, NT = D / 16, KS = D / 16, NST = 2, PW = R::PER_WAVE;
-  constexpr bool VREG = D <= 64;
-  constexpr int STAT = 4 * 64 * 4;      // lse and D of both maps for 64 rows (32 in use)
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * NST * R::BYTES + (VREG ? 0 : 4 * R::BYTES) + NST * STAT];
+  constexpr int DT = D / 32, NT = D / 16, KS = D / 16, NST = 2, PW = R::PER_WAVE, STEP = H * R::BYTES, NB = 4 / H;
+  // V's operands in registers, the others in LDS as they are read; at D = 128 one
+  // makes room for the statistics in 160 KB
+  constexpr int VR = D <= 64 ? 2 * KS : D == 128 && H == 2 ? 1 : 0, VL = 2 * KS - VR;
+  constexpr int STAT = 4 * 64 * 4;      // lse and D of both maps for 64 rows, a step's or more
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * NST * STEP + NB * VL * 1024 + NST * STAT];
   unsigned char* const sq = smem;
-  unsigned char* const sg = smem + NST * R::BYTES;
-  unsigned char* const sv = smem + 2 * NST * R::BYTES;
-  unsigned char* const ss = sv + (VREG ? 0 : 4 * R::BYTES);
+  unsigned char* const sg = smem + NST * STEP;
+  unsigned char* const sv = smem + 2 * NST * STEP;
+  unsigned char* const ss = sv + NB * VL * 1024;
   if (blockIdx.x == gridDim.x - 1) {   // the last block sums up dlambda, beside the others
     dlambda_block(a, reinterpret_cast<double*>(smem));
     return;
   }
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rb = wave / H, half = wave % H;                     // block of 32 keys, every H-th query tile
   int blk, gs, b;
   locate(blockIdx.x, a.gp * a.split * a.B, a.gp * a.split, blk, gs, b);
   const int g = gs / a.split, part = gs % a.split;
   const int grp = a.hp / a.gp, nh = grp / a.split, len = a.lens[b];
-  const int k0 = blk * 128, key = k0 + wave * 32 + c;           // causal: the first keys have the most queries
+  const int k0 = blk * 32 * NB, key = k0 + rb * 32 + c;              // causal: the first keys have the most queries
   const bool kok = key < len;
   const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
   const long long koff = (tok0 + key) * ldk + g * 2 * a.hd;
   const float lam = a.lam[0];
   const int pr0 = g * grp + part * nh;
   const int t0 = a.causal ? k0 / 32 : 0;                        // first query tile
-  const int ntile = k0 < len ? (len + 31) / 32 - t0 : 0, total = ntile * nh;
+  const int ntile = k0 < len ? (len + 31) / 32 - t0 : 0, ns = (ntile + H - 1) / H;   // steps of H tiles
 
   int srow[PW];
   unsigned scol[PW];
 #pragma unroll
   for (int i = 0; i < PW; ++i) R::source(wave * PW + i, lane, a.hd, srow[i], scol[i]);
   const int last = len - 1;
-  Frag<bf16> kf[2][KS], vf[VREG ? 2 * KS : 1];
+  unsigned char* const vt = sv + rb * VL * 1024 + lane * 16;    // this lane's operands of V
+  Frag<bf16> kf[2][KS], vf[VR > 0 ? VR : 1];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -337,30 +364,22 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
       const int col = s * 16 + h * 8;
       const bool ok = kok && col < a.hd;
       kf[m][s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.k) + koff + m * a.hd + col, ok);
-      if constexpr (VREG) vf[m * KS + s] = load_row<bf16>(reinterpret_cast<const bf16*>(a.v) + koff + m * a.hd + col, ok);
+      const Frag<bf16> x = load_row<bf16>(reinterpret_cast<const bf16*>(a.v) + koff + m * a.hd + col, ok);
+      if (m * KS + s < VR) vf[m * KS + s] = x;
+      else if (half == s % H) *reinterpret_cast<bf16x8*>(vt + (m * KS + s - VR) * 1024) = x.v;
     }
-  if constexpr (!VREG) {
-    // the workgroup's 128 rows of V, zeros where dO's tile repeats columns
-    for (int i = threadIdx.x; i < 128 * R::CH; i += 256) {
-      const int r = i / R::CH, p = i % R::CH, cl = p ^ (int)swz<D>((unsigned)r & 31);
-      const int m = cl / (D / 8), d = (cl % (D / 8)) * 8;
-      const bool ok = k0 + r < len && d < a.hd;
-      const Frag<bf16> x = load_row<bf16>(reinterpret_cast<const bf16*>(a.v) + (tok0 + k0 + r) * ldk + g * 2 * a.hd + m * a.hd + d, ok);
-      *reinterpret_cast<bf16x8*>(sv + r * R::PITCH + p * 16) = x.v;
-    }
-  }
   const unsigned ldb = (unsigned)ldq * 2u;
   int it_pr = pr0, it_t = t0;                                   // the next tile to load
   // statistics: wave w loads lse (w < 2) or D of map w % 2, 64 rows
   const float* const sbase = (wave < 2 ? a.lse : a.dsum) + (long long)b * a.hp * 2 * a.ls + (wave & 1) * a.ls;
-  auto issue_part = [&](int it, int i) __attribute__((always_inline)) {
-    const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((it & 1) * R::BYTES + wave * PW * 1024));
+  auto issue_part = [&](int it, int i) __attribute__((always_inline)) {   // i < PW: the first tile
+    const unsigned d0 = __builtin_amdgcn_readfirstlane((unsigned)((it & 1) * STEP + i / PW * R::BYTES + (wave * PW + i % PW) * 1024));
     const long long ofs = tok0 * ldq + it_pr * 2 * a.hd;
-    int r = it_t * 32 + srow[i];
+    int r = (it_t + i / PW) * 32 + srow[i % PW];
     r = r < last ? r : last;
-    const unsigned off = (unsigned)r * ldb + scol[i];
-    dma16(uniform(reinterpret_cast<const bf16*>(a.q) + ofs), off, lds_addr(sq) + d0 + i * 1024);
-    dma16(uniform(reinterpret_cast<const bf16*>(a.da) + ofs), off, lds_addr(sg) + d0 + i * 1024);
+    const unsigned off = (unsigned)r * ldb + scol[i % PW];
+    dma16(uniform(reinterpret_cast<const bf16*>(a.q) + ofs), off, lds_addr(sq) + d0);
+    dma16(uniform(reinterpret_cast<const bf16*>(a.da) + ofs), off, lds_addr(sg) + d0);
   };
   auto issue_stats = [&](int it) __attribute__((always_inline)) {
     int r = it_t * 32 + lane;
@@ -371,14 +390,15 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
                  :: "v"((unsigned)r * 4u), "s"(sd), "s"(sb) : "memory", "m0");
   };
   auto issued = [&]() __attribute__((always_inline)) {
-    if (++it_t == t0 + ntile) {
+    it_t += H;
+    if (it_t >= t0 + ntile) {
       it_t = t0;
       if (it_pr + 1 < pr0 + nh) ++it_pr;                        // past the last: read again, used by none
     }
   };
   auto issue_next = [&](int it) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < PW; ++i) issue_part(it, i);
+    for (int i = 0; i < H * PW; ++i) issue_part(it, i);
     issue_stats(it);
     issued();
   };
@@ -394,12 +414,12 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   for (int t = 0; t < NT; ++t) zero16(dv[t / DT][t % DT]);
   const float sc = a.scale * kLog2e;
 
-  if (total > 0) {
+  if (ns > 0) {
     issue_next(0);
     int it = 0;
-    // after it, tile `it` (or the wave's wait for the others) loads the next one
+    // after it, step `it` (or the wave's wait for the others) loads the next one's tiles
     auto arrive = [&]() __attribute__((always_inline)) {
-      wait_vm<0>();               // tile `it` has landed
+      wait_vm<0>();               // the tiles of step `it` have landed
       lds_barrier();              // ... for every wave, and the other slot is read by none
     };
     // One query tile: the products in order S_1, S_2, dP, dV, dK, each with its
@@ -410,10 +430,9 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
     constexpr int N1 = 2 * KS, N2 = 2 * KS, N3 = 2 * NT, N4 = 4 * DT, NOP = N1 + N2 + N3 + N4, AHEAD = 3;
     auto tile = [&](int q0, auto diag) __attribute__((always_inline)) {
       constexpr bool DIAG = decltype(diag)::value;
-      const unsigned char* qt = sq + (it & 1) * R::BYTES;
-      const unsigned char* gt = sg + (it & 1) * R::BYTES;
-      const unsigned char* vt = sv + wave * R::BYTES;
-      const float* st = reinterpret_cast<const float*>(ss + (it & 1) * STAT) + 4 * h;
+      const unsigned char* qt = sq + (it & 1) * STEP + half * R::BYTES;
+      const unsigned char* gt = sg + (it & 1) * STEP + half * R::BYTES;
+      const float* st = reinterpret_cast<const float*>(ss + (it & 1) * STAT) + 32 * half + 4 * h;
       f32x16 s[2], dp, w;
       Frag<bf16> wf[2], df[2][2], fa[AHEAD], fb[AHEAD];
       float4 l4[2], d4[2];
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
           fa[x] = ad.row(qt, (i / KS) * (D / 8) + 2 * (i % KS));
         } else if constexpr (i < N1 + N2) {
           fa[x] = ad.row(gt, 2 * (i - N1));
-          if constexpr (!VREG) fb[x] = ad.row(vt, 2 * (i - N1));
+          if constexpr (i - N1 >= VR) fb[x] = lds_row(vt + (i - N1 - VR) * 1024);
         } else if constexpr (i < N1 + N2 + N3) {
           fa[x] = ad.col(gt, (i - N1 - N2) % NT, (i - N1 - N2) / NT);
         } else if constexpr (i < NOP) {
@@ -446,7 +465,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
         if constexpr (i < N1) {
           mma(s[i / KS], fa[i % AHEAD], kf[i / KS][i % KS]);
         } else if constexpr (i < N1 + N2) {
-          if constexpr (VREG) mma(dp, fa[i % AHEAD], vf[i - N1]);
+          if constexpr (i - N1 < VR) mma(dp, fa[i % AHEAD], vf[i - N1]);
           else mma(dp, fa[i % AHEAD], fb[i % AHEAD]);
         } else if constexpr (i < N1 + N2 + N3) {
           mma(dv[(i - N1 - N2) % NT / DT][(i - N1 - N2) % DT], fa[i % AHEAD], wf[(i - N1 - N2) / NT]);
@@ -455,9 +474,9 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
           mma(dk[mt / DT][mt % DT], fa[i % AHEAD], df[mt / DT][j / (2 * DT)]);
         }
         read(std::integral_constant<int, i + AHEAD>{});
-        if constexpr (i % 4 == 1 && i / 4 < PW) issue_part(it + 1, i / 4);
-        if constexpr (i == 4 * PW + 1) issue_stats(it + 1);
-        if constexpr (i == 4 * PW + 2) issued();
+        if constexpr (i % (4 / H) == 1 && i / (4 / H) < H * PW) issue_part(it + 1, i / (4 / H));
+        if constexpr (i == 4 * PW) issue_stats(it + 1);
+        if constexpr (i == 4 * PW + 1) issued();
         if constexpr (i == KS - 1) stats(l4, 0, 0);
         if constexpr (i == N1 + N2 - 1) stats(d4, 0, 2);
         if constexpr (i >= KS && i < N1) {   // out of the matrix cores' registers before dP needs them
@@ -502,33 +521,56 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
         __builtin_amdgcn_sched_barrier(0);
       });
     };
-    const int skip = a.causal ? (wave < ntile ? wave : ntile) : 0;   // tiles before this wave's keys
     for (int n = 0; n < nh; ++n) {
       int j = 0;
-      for (; j < skip; ++j, ++it) {
+      if (a.causal) {             // tiles before this wave's keys, and the diagonal
+        for (; H * j + half < rb && j < ns; ++j, ++it) {
+          arrive();
+          issue_next(it + 1);
+        }
+        if (H * j + half < ntile) {
+          arrive();
+          tile((t0 + H * j + half) * 32, std::true_type{});
+          ++j;
+          ++it;
+        }
+      }
+      for (; H * j + half < ntile; ++j, ++it) {
+        arrive();
+        tile((t0 + H * j + half) * 32, std::false_type{});
+      }
+      for (; j < ns; ++j, ++it) {
         arrive();
         issue_next(it + 1);
-      }
-      if (a.causal && j < ntile) {
-        arrive();
-        tile((t0 + j) * 32, std::true_type{});
-        ++j;
-        ++it;
-      }
-      for (; j < ntile; ++j, ++it) {
-        arrive();
-        tile((t0 + j) * 32, std::false_type{});
       }
     }
     wait_vm<0>();
   }
+  // the two waves of a key block: the first ends with the sum of dV, the second of dK
+  lds_barrier();                  // the tiles are read by none
+  if constexpr (H == 2) {
+    static_assert(4 * NT * 4096 <= (int)sizeof(smem), "the halves fit");
+    unsigned char* const mine = smem + wave * NT * 4096;
+    unsigned char* const other = smem + (wave ^ 1) * NT * 4096;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (half) put_acc(dv[m], mine + m * DT * 4096, lane);
+      else put_acc(dk[m], mine + m * DT * 4096, lane);
+    }
+    lds_barrier();
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (half) add_acc(dk[m], other + m * DT * 4096, lane);
+      else add_acc(dv[m], other + m * DT * 4096, lane);
+    }
+    lds_barrier();                // the sums are read
+  }
   // results by rows through LDS: both maps' halves of dV, then dK's, in bf16 or
   // (parts) one half at a time in fp32
-  lds_barrier();                  // the tiles are read by none
   constexpr int P2 = 4 * D + 16;
   static_assert(4 * 32 * P2 <= (int)sizeof(smem), "the staged results fit");
   unsigned char* const st = smem + wave * 32 * P2;
-  const int row0 = k0 + wave * 32, rows = a.L - row0 < 32 ? a.L - row0 : 32;
+  const int row0 = k0 + rb * 32, rows = a.L - row0 < 32 ? a.L - row0 : 32;
   const long long roff = (tok0 + row0) * ldk + g * 2 * a.hd, poff = (long long)part * a.B * a.L * ldk + roff;
   auto put = [&](const f32x16 (&x)[DT], int m, float f, bf16* out, float* parts, bool last) __attribute__((always_inline)) {
 #pragma unroll
@@ -549,10 +591,14 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   bf16* const dko = reinterpret_cast<bf16*>(a.dk);
   bf16* const dvo = reinterpret_cast<bf16*>(a.dv);
   // V's tile has D columns per half: its first DT accumulators are the first
-  put(dv[0], 0, 1.f, dvo, a.dv_part, false);
-  put(dv[1], 1, 1.f, dvo, a.dv_part, true);
-  put(dk[0], 0, a.scale, dko, a.dk_part, false);
-  put(dk[1], 1, -lam * a.scale, dko, a.dk_part, true);
+  if (H == 1 || half == 0) {
+    put(dv[0], 0, 1.f, dvo, a.dv_part, false);
+    put(dv[1], 1, 1.f, dvo, a.dv_part, true);
+  }
+  if (H == 1 || half == 1) {
+    put(dk[0], 0, a.scale, dko, a.dk_part, false);
+    put(dk[1], 1, -lam * a.scale, dko, a.dk_part, true);
+  }
 }
 
 // dK and dV from the parts' sums, in order; 4 values per thread.
@@ -828,16 +874,19 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
 
 void launch_diff_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
   const long long rows = (long long)a.B * a.L * a.hp;
-  const int blocks = (a.L + 127) / 128 * a.B, narrow = (a.L + 31) / 32 * a.B;
+  auto blocks = [&](int rows) { return (a.L + rows - 1) / rows * a.B; };
   if (dt == SL_F32) hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
     if (dt == SL_BF16) {
-      hipLaunchKernelGGL(diff_dq_lds<D>, dim3((unsigned)(blocks * a.hp)), dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_lds<D>, dim3((unsigned)(blocks * a.gp * a.split + 1)), dim3(256), 0, s, a);
+      const dim3 dq((unsigned)(blocks(a.dq_rows) * a.hp)), dkv((unsigned)(blocks(a.dkv_rows) * a.gp * a.split + 1));
+      if (a.dq_rows == 64) hipLaunchKernelGGL((diff_dq_lds<D, 2>), dq, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((diff_dq_lds<D, 1>), dq, dim3(256), 0, s, a);
+      if (a.dkv_rows == 64) hipLaunchKernelGGL((diff_dkv_lds<D, 2>), dkv, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((diff_dkv_lds<D, 1>), dkv, dim3(256), 0, s, a);
     } else {
-      hipLaunchKernelGGL(diff_dq_direct<D>, dim3((unsigned)(narrow * a.hp)), dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_direct<D>, dim3((unsigned)(narrow * a.gp + 1)), dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dq_direct<D>, dim3((unsigned)(blocks(32) * a.hp)), dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_direct<D>, dim3((unsigned)(blocks(32) * a.gp + 1)), dim3(256), 0, s, a);
     }
   });
   if (a.split > 1) {

@@ -165,6 +165,24 @@ template <int N, typename F> __device__ inline __attribute__((always_inline)) vo
   each_of(f, std::make_integer_sequence<int, N>{});
 }
 
+// Accumulators to LDS, and added to from there; 4 KB per tile.
+template <int N> __device__ inline void put_acc(const f32x16 (&x)[N], unsigned char* p, int lane) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      reinterpret_cast<float4*>(p + (n * 4 + i / 4) * 1024)[lane] = make_float4(x[n][i], x[n][i + 1], x[n][i + 2], x[n][i + 3]);
+}
+template <int N> __device__ inline void add_acc(f32x16 (&x)[N], const unsigned char* p, int lane) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 y = reinterpret_cast<const float4*>(p + (n * 4 + i / 4) * 1024)[lane];
+      x[n][i] += y.x; x[n][i + 1] += y.y; x[n][i + 2] += y.z; x[n][i + 3] += y.w;
+    }
+}
+
 // 32 rows that a wave has laid out in LDS (`pitch` bytes apart) to memory, 16
 // bytes a lane and whole rows at a time: an accumulator tile's own layout would
 // write 8 bytes of 32 rows per instruction.
