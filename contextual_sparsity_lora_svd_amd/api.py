@@ -723,9 +723,18 @@ class DiffAttnWorkspace:
         if lens is not None and len(lens) != layout.batch:
             raise SparseLoraError(f"lens holds {len(lens)} lengths for {layout.batch} sequences")
         self.lens = None if lens is None else (_i32 * len(lens))(*[int(n) for n in lens])
+        self.made_for = (layout.batch, layout.seq_len, p.heads, dtype)
         h = SlHeads(*p.heads)
         self.saved = _bytes_tensor(L.sl_diff_attn_saved_bytes(code, layout.ref, ctypes.byref(h)), device)
         self.ws = _bytes_tensor(L.sl_diff_attn_workspace_bytes(code, layout.ref, ctypes.byref(h)), device)
+
+
+def _diff_buffers(buf: DiffAttnWorkspace, p: DiffAttnParams, layout: Layout, q: torch.Tensor):
+    """(saved, bytes, ws, bytes) of a call over q."""
+    if buf.made_for != (layout.batch, layout.seq_len, p.heads, q.dtype):
+        raise SparseLoraError(f"buffers made for (batch, seq_len, heads, dtype) = {buf.made_for}, "
+                              f"call of {(layout.batch, layout.seq_len, p.heads, q.dtype)}")
+    return _check_scratch("saved", buf.saved, q), buf.saved.numel(), _check_scratch("ws", buf.ws, q), buf.ws.numel()
 
 
 def diff_attn_fwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, layout: Layout,
@@ -744,10 +753,12 @@ def diff_attn_fwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
         raise SparseLoraError("lens belongs to the buffers: give it to DiffAttnWorkspace")
     a = out if out is not None else torch.empty_like(q)
     ap = _check_rows("a", a, q.shape, q.dtype, dev)
+    if ap in (qp, kp, vp):
+        raise SparseLoraError("a may not be q, k or v")
+    saved, ns, ws, nw = _diff_buffers(buf, p, layout, q)
     c = p._c(buf.lens, dev)
-    _check(lib().sl_diff_attn_fwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
-                                  _check_scratch("saved", buf.saved, q), buf.saved.numel(),
-                                  _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()), "sl_diff_attn_fwd")
+    _check(lib().sl_diff_attn_fwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap, saved, ns, ws, nw, _stream()),
+           "sl_diff_attn_fwd")
     return a, buf
 
 
@@ -772,11 +783,12 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
             out["d" + n] = torch.empty_like(p.t[n])
     dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out["dk"], T, p.heads, q.dtype, dev)
     dvp = _check_rows("dv", out["dv"], v.shape, q.dtype, dev)
+    if len({qp, kp, vp, ap, gp, dqp, dkp, dvp} - {qp, kp, vp, ap, gp}) < 3:
+        raise SparseLoraError("dq, dk and dv may not be inputs or each other")
     shape = (p.heads[2],)
     g = SlDiffAttnGrads(*[_check_rows("d" + n, out["d" + n], shape, torch.float32, dev) for n in p.NAMES])
+    saved, ns, ws, nw = _diff_buffers(buf, p, layout, q)
     c = p._c(buf.lens, dev)
-    _check(lib().sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap,
-                                  _check_scratch("saved", buf.saved, q), buf.saved.numel(), gp, dqp, dkp, dvp,
-                                  ctypes.byref(g), _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()),
-           "sl_diff_attn_bwd")
+    _check(lib().sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap, saved, ns, gp, dqp, dkp, dvp,
+                                  ctypes.byref(g), ws, nw, _stream()), "sl_diff_attn_bwd")
     return out

@@ -363,7 +363,10 @@ class DiffAttention(torch.nn.Module):
         core = DiffAttention(heads, rot=Rotary(head_dim), qk_norm=True)
         out = proj(X, layout, core.bind(layout), step)     # proj: SparseLoRAQKVO
 
-    ``lens`` (valid rows per sequence) and ``pos`` [T] int32 go with each call."""
+    ``lens`` (valid rows per sequence) and ``pos`` [T] int32 go with each call.
+    Padding rows of q, k and v have no gradient and may hold anything, but
+    finite values under ``qk_norm``, whose weights' gradients sum over every row
+    (0 times what the padding holds)."""
 
     def __init__(self, heads: Sequence[int], lambda_init: float = 0.8, causal: bool = True,
                  scale: Optional[float] = None, rot: Optional[sl.Rotary] = None, qk_norm: bool = False,

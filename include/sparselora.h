@@ -391,6 +391,9 @@ sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_heads* he
  *   fwd: q, k, v -> a [T, Hq*hd]; writes `saved` for the backward.
  *   bwd: q, k, v, a (the forward's) and da -> dq, dk, dv and the fp32 gradients
  *        of the four vectors, overwritten.  Sums run in a fixed order.
+ * No output may overlap an input, the buffers or another output.  The backward
+ * takes the forward's inputs, p and `saved` as they were.  bf16: |v| below 2^63
+ * (the weights are kept relative to 2^64 of a row's first maximum).
  * Hq and Hkv even, Hq a multiple of Hkv; hd a multiple of 8, at most 128; every
  * tensor fewer than 2^31 elements.
  * ------------------------------------------------------------------------- */

@@ -159,3 +159,19 @@ def test_binding_refusals(sl):
         sl.diff_attn_fwd(p, q, None, None, lay)
     with pytest.raises(E):
         sl.diff_attn_fwd(p, q, k, k, lay)
+
+
+def test_diff_attention_buffers_of_another_call_are_refused(sl):
+    torch = pytest.importorskip("torch")
+    heads, t = (4, 2, 16), {n: torch.ones(16) for n in sl.DiffAttnParams.NAMES}
+    lay, p = sl.Layout([4, 4], 4), sl.DiffAttnParams(t, heads)
+    q, kv = torch.zeros(8, 64), torch.zeros(8, 32)
+    like = sl.api._diff_buffers
+    buf = sl.DiffAttnWorkspace(p, lay, torch.float32, "cpu", lens=[4, 3])
+    assert like(buf, p, lay, q)[1] == buf.saved.numel()
+    for other in (sl.DiffAttnWorkspace(p, sl.Layout([8], 8), torch.float32, "cpu", lens=[8]),
+                  sl.DiffAttnWorkspace(p, sl.Layout([2] * 4, 2), torch.float32, "cpu"),
+                  sl.DiffAttnWorkspace(p, lay, torch.bfloat16, "cpu"),
+                  sl.DiffAttnWorkspace(sl.DiffAttnParams(t, (4, 4, 16)), lay, torch.float32, "cpu")):
+        with pytest.raises(sl.SparseLoraError, match="buffers made for"):
+            like(other, p, lay, q)

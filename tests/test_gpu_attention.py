@@ -200,6 +200,44 @@ def test_diff_attention(case, dt):
                 assert not t[b * Ls + n:(b + 1) * Ls].any()
 
 
+# The bf16 kernels' other halves: workgroups of 128 rows (many head pairs and
+# sequences), a kv group's heads cut into three parts, the most sequences of a
+# layout; head widths that fill no tile.
+MANY = [  # batch, seq, hq, hkv, hd, causal, lens
+    (6, 140, 32, 32, 24, False, None),
+    (6, 140, 32, 32, 64, False, [140, 0, 129, 1, 64, 97]),
+    (6, 140, 32, 32, 72, False, None),
+    (6, 140, 32, 32, 128, False, [140, 139, 128, 127, 33, 32]),
+    (16, 140, 32, 16, 64, True, [140, 1, 32, 33, 64, 65, 96, 97, 127, 128, 129, 0, 139, 31, 63, 95]),
+    (16, 140, 32, 32, 120, True, None),
+    (16, 140, 32, 32, 8, True, None),
+    (16, 140, 32, 32, 96, True, None),
+    (6, 300, 24, 8, 32, False, [300, 256, 257, 0, 1, 290]),
+    (8, 300, 24, 8, 128, True, [300, 256, 257, 0, 1, 290, 128, 129]),
+    (1, 300, 20, 4, 56, True, None),
+    (64, 9, 4, 2, 16, True, list(range(10)) * 6 + [9, 0, 9, 1]),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "x".join(map(str, c[:6])))
+def test_diff_attention_many_heads(case):
+    test_diff_attention(case, "bf16")
+
+
+@pytest.mark.parametrize("hd,causal,L", [(64, True, 150), (128, False, 150), (32, True, 77), (96, True, 200)])
+def test_diff_attention_scores_that_outgrow_the_first_tile(hd, causal, L):
+    """Every 40 keys the scores rise by about 2^92 in the weights: relative to the
+    first tile's maximum the rows' sums overflow fp32 from the second step on.  One
+    sequence's rows do, the other's stay small."""
+    sl = _sl()
+    case = (2, L, 4, 2, hd, causal, None)
+    x, lv = _diff_inputs(case, "bf16", seed=12)
+    rise = (64.0 / np.sqrt(hd)) * (np.arange(L)[:, None] // 40) * 0.5
+    x["q"][:L] = 2.0
+    x["k"][:L] = round_to_bf16((rise + 0.125 * x["k"][:L]).astype(np.float32))
+    _, _, _, a, g, _ = _run_diff(sl, case, "bf16", x, lv)
+    _check_diff(case, "bf16", x, lv, a, g)
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["peaked", "flat", "late", "negative"])
 def test_diff_attention_distributions(dt, kind):
@@ -364,3 +402,16 @@ def test_long_sequence_last_rows():
         ref = (maps[0] - lam * maps[1]) @ v[:r + 1]
         mag = (maps[0] + abs(lam) * maps[1]) @ np.abs(v[:r + 1])
         _within(a[r], ref, HALF["bf16"] * np.abs(ref) + (HALF["bf16"] + U32 * (r + 2000)) * mag, f"row {r}")
+
+
+def test_outputs_that_are_inputs_are_refused():
+    sl = _sl()
+    case = (1, 20, 2, 2, 16, True, None)
+    x, lv = _diff_inputs(case, "bf16")
+    p, d, lay, a, g, buf = _run_diff(sl, case, "bf16", x, lv)
+    for out in (d["q"], d["k"], d["v"]):
+        with pytest.raises(sl.SparseLoraError):
+            sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], lay, buf=buf, out=out)
+    for out in ({"dq": d["da"]}, {"dk": d["k"]}, {"dq": g["dk"], "dk": g["dk"]}):
+        with pytest.raises(sl.SparseLoraError):
+            sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a, lay, buf, d["da"], out=out)
