@@ -24,23 +24,24 @@ struct DiffPlan {
 struct DiffGrid {
   int dq_rows, dkv_rows, split;
 };
-static DiffGrid diff_grid(int B, int L, int hp, int gp, bool causal) {
+static DiffGrid diff_grid(sl_dtype dt, int B, int L, int hp, int gp, bool causal) {
   auto blocks = [&](int rows) { return (long long)((L + rows - 1) / rows) * B; };
   auto rows = [&](int n) {       // n workgroups per block of rows
     return blocks(64) * n <= 256 || (causal && blocks(128) * n < (L > 1024 ? 512 : 256)) ? 64 : 128;
   };
+  const bool f32 = dt == SL_F32;
   DiffGrid g;
-  g.dq_rows = rows(hp);
+  g.dq_rows = f32 ? 32 : rows(hp);
   // parts that a kv group's heads are cut into, while there are fewer workgroups
   // than two rounds of 256; short loops are not worth the launch that adds them
   const int grp = hp / gp;
   g.split = 1;
   if (grp * ((L + 31) / 32) > 16)
-    while (g.split < grp && blocks(128) * gp * g.split < 512) {
+    while (g.split < grp && blocks(f32 ? 32 : 128) * gp * g.split < 512) {
       ++g.split;
       while (grp % g.split) ++g.split;
     }
-  g.dkv_rows = rows(gp * g.split);
+  g.dkv_rows = f32 ? 32 : rows(gp * g.split);
   return g;
 }
 
@@ -70,7 +71,7 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   pl.dsum = w.take(stats * 4);
   // a partial sum of dlambda per wave, 4 to a workgroup of 32 rows or more
   pl.dlam = w.take(4 * (size_t)((lay->seq_len + 31) / 32) * lay->batch * (hq / 2) * 8);
-  const int split = dt == SL_BF16 ? diff_grid(lay->batch, lay->seq_len, hq / 2, hkv / 2, false).split : 1;
+  const int split = diff_grid(dt, lay->batch, lay->seq_len, hq / 2, hkv / 2, false).split;
   pl.part_elems = T * hkv * hd;
   pl.part = w.take(split > 1 ? 2 * (size_t)split * pl.part_elems * 4 : 0);
   pl.ws = w.off;
@@ -175,7 +176,7 @@ extern "C" sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const s
   saved_args(a, pl, const_cast<void*>(saved));
   a.dsum = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.dsum);
   a.dlam_part = reinterpret_cast<double*>(reinterpret_cast<char*>(ws) + pl.dlam);
-  const DiffGrid grid = dt == SL_BF16 ? diff_grid(a.B, a.L, a.hp, a.gp, a.causal) : DiffGrid{32, 32, 1};
+  const DiffGrid grid = diff_grid(dt, a.B, a.L, a.hp, a.gp, a.causal);
   a.split = grid.split;
   a.dq_rows = grid.dq_rows;
   a.dkv_rows = grid.dkv_rows;

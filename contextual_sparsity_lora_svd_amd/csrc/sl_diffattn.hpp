@@ -11,6 +11,8 @@
 // log2-sum-exp and O_2 = P_2 V; the backward forms the weights again from them.
 #pragma once
 
+#include <utility>
+
 #include <cmath>
 
 #include "sl_common.hpp"
@@ -94,16 +96,39 @@ template <> __device__ inline Frag<float> acc_frag<float>(const f32x16& x, int c
   return f;
 }
 
-// The matching operand from memory: column `col` of rows row0 + 8 (j / 4)
-// + 4 h + j % 4, rows at or past `rows` as 0.
-__device__ inline Frag<float> load_col(const float* base, long long ld, int row0, int rows, int h, bool ok) {
-  Frag<float> f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = row0 + 8 * (j >> 2) + 4 * h + (j & 3);
-    f.v[j] = ok && r < rows ? base[r * ld] : 0.f;
+// fp32 operands come straight from memory, each read some products before its
+// use.  A tile is 32 rows from row0 on of which `n` exist; rows past them read
+// the last one again (their weights are zero, or their results dropped), columns
+// past the width `w` the first or the last (zero() clears them in one of two
+// operands; as columns of a result they are dropped).
+struct Rows32 {
+  const float* base;         // row row0, first column of the head or pair (uniform)
+  unsigned ld;               // row stride in values
+  int last;                  // n - 1
+  // 8 values of row l % 32 from column 16 s + 8 h on
+  __device__ inline Frag<float> row(int c, int col, int w) const {
+    Frag<float> f;
+    const float* p = base + (unsigned)(c < last ? c : last) * ld + (col < w ? col : 0);
+    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+    f.v[0] = x.x; f.v[1] = x.y; f.v[2] = x.z; f.v[3] = x.w;
+    f.v[4] = y.x; f.v[5] = y.y; f.v[6] = y.z; f.v[7] = y.w;
+    return f;
   }
-  return f;
+  // column col of rows 16 cc + 8 (j / 4) + 4 h + j % 4
+  __device__ inline Frag<float> col(int cc, int h, int col, int w) const {
+    Frag<float> f;
+    const int cl = col < w ? col : w - 1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = 16 * cc + 8 * (j >> 2) + 4 * h + (j & 3);
+      f.v[j] = base[(unsigned)(r < last ? r : last) * ld + cl];
+    }
+    return f;
+  }
+};
+__device__ inline void zero(Frag<float>& f, bool gone) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j] = gone ? 0.f : f.v[j];
 }
 
 // four consecutive values of a row
@@ -169,6 +194,15 @@ template <int N> __device__ inline void add_waves(f32x16 (&x)[N], float* sm, int
     }
     __syncthreads();
   }
+}
+
+// f(0) .. f(N - 1) with compile-time indices, unrolled however long.
+template <typename F, int... I>
+__device__ inline __attribute__((always_inline)) void each_of(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F> __device__ inline __attribute__((always_inline)) void each(F f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
 }
 
 // Run f with the row width D that serves head_dim hd.

@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
 }
 
 // dK and dV from the parts' sums, in order; 4 values per thread.
-__global__ void __launch_bounds__(256) diff_dkv_sum(const DiffArgs a) {
+template <typename T> __global__ void __launch_bounds__(256) diff_dkv_sum(const DiffArgs a) {
   const long long n = (long long)a.B * a.L * a.gp * 2 * a.hd / 4;
   long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const bool v = i >= n;
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(256) diff_dkv_sum(const DiffArgs a) {
     const float4 y = src[p * n];
     x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
   }
-  store4<bf16>(reinterpret_cast<bf16*>(v ? a.dv : a.dk) + 4 * i, x.x, x.y, x.z, x.w);
+  store4<T>(reinterpret_cast<T*>(v ? a.dv : a.dk) + 4 * i, x.x, x.y, x.z, x.w);
 }
 
 // ---------------------------------------------------------------------------
@@ -662,8 +662,9 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   const int row = qb * 32 + c;
   const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
   const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd, koff = tok0 * ldk + g * 2 * a.hd;
-  const T* qp = reinterpret_cast<const T*>(a.q) + qoff;
-  const T* dop = reinterpret_cast<const T*>(a.da) + qoff;
+  const long long toff = (tok0 + qb * 32) * ldq + pair * 2 * a.hd;
+  const T* qp = reinterpret_cast<const T*>(a.q) + toff;
+  const T* dop = reinterpret_cast<const T*>(a.da) + toff;
   const T* kp = reinterpret_cast<const T*>(a.k) + koff;
   const T* vp = reinterpret_cast<const T*>(a.v) + koff;
   const bool rok = row < len;
@@ -684,52 +685,61 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   int kend = len;
   if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
   if (qb * 32 >= len) kend = 0;
+  // products in order dP, S_1, S_2, then over the keys; operands read as in the forward
+  constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, NG = N0 + N1 + 4 * DT, AHEAD = 2;
   for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
-    const int kz = opaque(0);
+    const int kz = opaque(0), kl = len - 1 - k0, ql = len - 1 - qb * 32;
+    const T* const kt = kp + (long long)k0 * ldk;
+    const Rows32 vt{vp + (long long)k0 * ldk, (unsigned)ldk, kl}, gt{dop + kz, (unsigned)ldq, ql};
     f32x16 dp, s[2];
     float part = 0.f;
+    Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
     zero16(dp);
-#pragma unroll
-    for (int ks = 0; ks < D / 8; ++ks) {
-      const int col = ks * 16 + h * 8;
-      const bool cok = col < 2 * a.hd;
-      const Frag<T> vf = load_row<T>(vp + (long long)(k0 + c) * ldk + col, cok && k0 + c < len);
-      const Frag<T> gf = load_row<T>(dop + col + kz, cok && rok);
-      mma(dp, vf, gf);
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      zero16(s[m]);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int col = ks * 16 + h * 8;
-        const bool cok = col < a.hd;
-        const Frag<T> kf = load_row<T>(kp + (long long)(k0 + c) * ldk + m * a.hd + col, cok && k0 + c < len);
-        const Frag<T> qf = load_row<T>(qp + m * a.hd + col + kz, cok && rok);
-        mma(s[m], kf, qf);
+    zero16(s[0]);
+    zero16(s[1]);
+    auto fetch = [&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
+      if constexpr (g < N0) {
+        fa[x] = vt.row(c, g * 16 + h * 8, 2 * a.hd);
+        fb[x] = gt.row(c, g * 16 + h * 8, 2 * a.hd);
+      } else if constexpr (g < N0 + N1) {
+        const int m = (g - N0) / KS, col = (g - N0) % KS * 16 + h * 8;
+        fa[x] = Rows32{kt + m * a.hd, (unsigned)ldk, kl}.row(c, col, a.hd);
+        fb[x] = Rows32{qp + kz + m * a.hd, (unsigned)ldq, ql}.row(c, col, a.hd);
+      } else if constexpr (g < NG) {
+        constexpr int j = g - N0 - N1;
+        fa[x] = Rows32{kt + j / (2 * DT) * a.hd, (unsigned)ldk, kl}.col(j / DT % 2, h, j % DT * 32 + c, a.hd);
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
-        const bool hidden = key >= len || (a.causal && key > row) || !rok;
-        const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m]));
-        if (m == 1) part = fmaf(p, dp[i], part);
-        s[m][i] = p * (dp[i] - ds[m]);
+    };
+    each<AHEAD>(fetch);
+    each<NG>([&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
+      fetch(std::integral_constant<int, g + AHEAD>{});
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (g < N0) {
+        zero(fb[x], g * 16 + h * 8 >= 2 * a.hd);
+        mma(dp, fa[x], fb[x]);
+      } else if constexpr (g < N0 + N1) {
+        zero(fb[x], (g - N0) % KS * 16 + h * 8 >= a.hd);
+        mma(s[(g - N0) / KS], fa[x], fb[x]);
+      } else {
+        constexpr int j = g - N0 - N1, m = j / (2 * DT);
+        mma(dq[m][j % DT], fa[x], acc_frag<T>(s[m], j / DT % 2));
       }
-    }
-    dlam += (double)part;
+      if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == KS - 1) {
+        constexpr int m = (g - N0) / KS;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const Frag<T> sf = acc_frag<T>(s[m], cc);
-#pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          const int d = 32 * t + c;
-          const Frag<T> kf = load_col(kp + m * a.hd + d, ldk, k0 + 16 * cc, len, h, d < a.hd);
-          mma(dq[m][t], kf, sf);
+        for (int i = 0; i < 16; ++i) {
+          const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
+          const bool hidden = key >= len || (a.causal && key > row) || !rok;
+          const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m]));
+          if (m == 1) part = fmaf(p, dp[i], part);
+          s[m][i] = p * (dp[i] - ds[m]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    dlam += (double)part;
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) dlam += __shfl_xor(dlam, o);
@@ -764,16 +774,17 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
     dlambda_block(a, reinterpret_cast<double*>(sm));
     return;
   }
-  const int kb = blockIdx.x / (a.gp * a.B);           // causal: the first keys have the most queries
-  const int g = blockIdx.x / a.B % a.gp, b = blockIdx.x % a.B;
+  const int n = a.gp * a.split * a.B, kb = blockIdx.x / n;      // causal: the first keys have the most queries
+  const int gs = blockIdx.x % n / a.B, b = blockIdx.x % a.B, g = gs / a.split, hpart = gs % a.split;
   const int grp = a.hp / a.gp, len = a.lens[b];
   const float lam = a.lam[0];
   const int key = kb * 32 + c;
-  const bool kok = key < len;
+  const bool kok = key < len;                                  // else: its results are 0
   const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
   const long long koff = (tok0 + key) * ldk + g * 2 * a.hd;
-  const T* kp = reinterpret_cast<const T*>(a.k) + koff;
-  const T* vp = reinterpret_cast<const T*>(a.v) + koff;
+  const long long toff = (tok0 + kb * 32) * ldk + g * 2 * a.hd;
+  const T* kp = reinterpret_cast<const T*>(a.k) + toff;
+  const T* vp = reinterpret_cast<const T*>(a.v) + toff;
   f32x16 dk[2][DT], dv[NT];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -782,85 +793,97 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) zero16(dv[t]);
   const float sc = a.scale * kLog2e;
-  const int qbeg = a.causal ? kb * 32 : 0;
-  int turn = 0;                                       // tiles go round the waves
-  for (int pr = g * grp; pr < (g + 1) * grp; ++pr) {
-    const T* qp = reinterpret_cast<const T*>(a.q) + tok0 * ldq + pr * 2 * a.hd;
-    const T* dop = reinterpret_cast<const T*>(a.da) + tok0 * ldq + pr * 2 * a.hd;
-    const float* lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.ls;
-    const float* dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.ls;
-    for (int q0 = kb * 32 < len ? qbeg : len; q0 < len; q0 += 32) {
-      if ((turn++ & 3) != wave) continue;
-      const int kz = opaque(0);
-      f32x16 dp, s[2], w;
-      zero16(dp);
-#pragma unroll
-      for (int ks = 0; ks < D / 8; ++ks) {
-        const int col = ks * 16 + h * 8;
-        const bool cok = col < 2 * a.hd;
-        const Frag<T> gf = load_row<T>(dop + (long long)(q0 + c) * ldq + col, cok && q0 + c < len);
-        const Frag<T> vf = load_row<T>(vp + col + kz, cok && kok);
-        mma(dp, gf, vf);
+  const int t0 = a.causal ? kb : 0, ntile = kb * 32 < len ? (len + 31) / 32 - t0 : 0;
+  const int nh = grp / a.split, pr0 = g * grp + hpart * nh, kl = len - 1 - kb * 32;
+  // products in order dP, S_1, S_2, dV, dK; operands read as in the forward
+  constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, N2 = 2 * NT, NG = N0 + N1 + N2 + 4 * DT, AHEAD = 2;
+  for (int x = wave; x < ntile * nh; x += 4) {
+    const int pr = pr0 + x / ntile, q0 = (t0 + x % ntile) * 32, ql = len - 1 - q0, kz = opaque(0);
+    const T* const qt = reinterpret_cast<const T*>(a.q) + (tok0 + q0) * ldq + pr * 2 * a.hd;
+    const Rows32 gt{reinterpret_cast<const T*>(a.da) + (tok0 + q0) * ldq + pr * 2 * a.hd, (unsigned)ldq, ql};
+    const Rows32 vt{vp + kz, (unsigned)ldk, kl};
+    const float* const lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.ls;
+    const float* const dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.ls;
+    f32x16 dp, s[2], w;
+    float sl[16], sd[16];
+    Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
+    zero16(dp);
+    zero16(s[0]);
+    zero16(s[1]);
+    auto fetch = [&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value, y = g % (AHEAD + 1);
+      if constexpr (g < N0) {
+        fa[y] = gt.row(c, g * 16 + h * 8, 2 * a.hd);
+        fb[y] = vt.row(c, g * 16 + h * 8, 2 * a.hd);
+      } else if constexpr (g < N0 + N1) {
+        const int m = (g - N0) / KS, col = (g - N0) % KS * 16 + h * 8;
+        fa[y] = Rows32{qt + m * a.hd, (unsigned)ldq, ql}.row(c, col, a.hd);
+        fb[y] = Rows32{kp + kz + m * a.hd, (unsigned)ldk, kl}.row(c, col, a.hd);
+      } else if constexpr (g < N0 + N1 + N2) {
+        constexpr int j = g - N0 - N1;
+        fa[y] = gt.col(j / NT, h, j % NT * 32 + c, 2 * a.hd);
+      } else if constexpr (g < NG) {
+        constexpr int j = g - N0 - N1 - N2;
+        fa[y] = Rows32{qt + j / (2 * DT) * a.hd, (unsigned)ldq, ql}.col(j / DT % 2, h, j % DT * 32 + c, a.hd);
       }
+    };
+    each<AHEAD>(fetch);
+    each<NG>([&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value, y = g % (AHEAD + 1);
+      fetch(std::integral_constant<int, g + AHEAD>{});
+      if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == 0) {
+        constexpr int m = (g - N0) / KS;
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        zero16(s[m]);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const int col = ks * 16 + h * 8;
-          const bool cok = col < a.hd;
-          const Frag<T> qf = load_row<T>(qp + (long long)(q0 + c) * ldq + m * a.hd + col, cok && q0 + c < len);
-          const Frag<T> kf = load_row<T>(kp + m * a.hd + col + kz, cok && kok);
-          mma(s[m], qf, kf);
+        for (int i = 0; i < 16; ++i) {
+          const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3), at = m * a.ls + (q < len ? q : len);   // past the end: weights 0
+          sl[i] = lse[at];
+          sd[i] = dsm[at];
         }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (g < N0) {
+        zero(fb[y], g * 16 + h * 8 >= 2 * a.hd);
+        mma(dp, fa[y], fb[y]);
+      } else if constexpr (g < N0 + N1) {
+        zero(fb[y], (g - N0) % KS * 16 + h * 8 >= a.hd);
+        mma(s[(g - N0) / KS], fa[y], fb[y]);
+      } else if constexpr (g < N0 + N1 + N2) {
+        constexpr int j = g - N0 - N1;
+        mma(dv[j % NT], fa[y], acc_frag<T>(w, j / NT));
+      } else {
+        constexpr int j = g - N0 - N1 - N2, m = j / (2 * DT);
+        mma(dk[m][j % DT], fa[y], acc_frag<T>(s[m], j / DT % 2));
+      }
+      if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == KS - 1) {
+        constexpr int m = (g - N0) / KS;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3);
-          const bool hidden = q >= len || (a.causal && key > q) || !kok;
-          const int qq = q < len ? q : 0;
-          const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m * a.ls + qq]));
+          const float p = a.causal && key > q ? 0.f : exp2f(fmaf(s[m][i], sc, -sl[i]));
           w[i] = m ? w[i] - lam * p : p;
-          s[m][i] = p * (dp[i] - dsm[m * a.ls + qq]);
+          s[m][i] = p * (dp[i] - sd[i]);
         }
       }
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const Frag<T> wf = acc_frag<T>(w, cc);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int d = 32 * t + c;
-          const Frag<T> gf = load_col(dop + d, ldq, q0 + 16 * cc, len, h, d < 2 * a.hd);
-          mma(dv[t], gf, wf);
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const Frag<T> sf = acc_frag<T>(s[m], cc);
-#pragma unroll
-          for (int t = 0; t < DT; ++t) {
-            const int d = 32 * t + c;
-            const Frag<T> qf = load_col(qp + m * a.hd + d, ldq, q0 + 16 * cc, len, h, d < a.hd);
-            mma(dk[m][t], qf, sf);
-          }
-        }
-      }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+    });
   }
   add_waves(dv, sm, wave, lane);
   add_waves(dk[0], sm, wave, lane);
   add_waves(dk[1], sm, wave, lane);
   if (wave != 3 || key >= a.L) return;
-  T* dkp = reinterpret_cast<T*>(a.dk) + koff;
-  T* dvp = reinterpret_cast<T*>(a.dv) + koff;
+  const long long poff = (long long)hpart * a.B * a.L * ldk + koff;
+  T* dkp = (a.split > 1 ? a.dk_part + poff : reinterpret_cast<T*>(a.dk) + koff);
+  T* dvp = (a.split > 1 ? a.dv_part + poff : reinterpret_cast<T*>(a.dv) + koff);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const int d = 32 * t + 2 * i + 4 * h;
-      if (d < 2 * a.hd) store4<T>(dvp + d, dv[t][i], dv[t][i + 1], dv[t][i + 2], dv[t][i + 3]);
+      if (d < 2 * a.hd) store4<T>(dvp + d, kok ? dv[t][i] : 0.f, kok ? dv[t][i + 1] : 0.f, kok ? dv[t][i + 2] : 0.f, kok ? dv[t][i + 3] : 0.f);
     }
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const float f = m ? -lam * a.scale : a.scale;
+    const float f = kok ? (m ? -lam * a.scale : a.scale) : 0.f;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -886,12 +909,14 @@ void launch_diff_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
       else hipLaunchKernelGGL((diff_dkv_lds<D, 1>), dkv, dim3(256), 0, s, a);
     } else {
       hipLaunchKernelGGL(diff_dq_direct<D>, dim3((unsigned)(blocks(32) * a.hp)), dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_direct<D>, dim3((unsigned)(blocks(32) * a.gp + 1)), dim3(256), 0, s, a);
+      hipLaunchKernelGGL(diff_dkv_direct<D>, dim3((unsigned)(blocks(32) * a.gp * a.split + 1)), dim3(256), 0, s, a);
     }
   });
   if (a.split > 1) {
     const long long n = 2 * ((long long)a.B * a.L * a.gp * 2 * a.hd / 4);
-    hipLaunchKernelGGL(diff_dkv_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)((n + 255) / 256));
+    if (dt == SL_BF16) hipLaunchKernelGGL(diff_dkv_sum<bf16>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(diff_dkv_sum<float>, grid, dim3(256), 0, s, a);
   }
 }
 

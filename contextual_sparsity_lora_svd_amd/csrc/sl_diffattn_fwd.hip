@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   }
   const int row = qb * 32 + c;
   const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
-  const T* qp = reinterpret_cast<const T*>(a.q) + (tok0 + row) * ldq + pair * 2 * a.hd;
+  const T* qp = reinterpret_cast<const T*>(a.q) + (tok0 + qb * 32) * ldq + pair * 2 * a.hd;
   const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * ldk + g * 2 * a.hd;
   const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * ldk + g * 2 * a.hd;
   const bool rok = row < len;
@@ -408,55 +408,68 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   int kend = len;
   if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
   if (qb * 32 >= len) kend = 0;
+  // products over the columns (S_1, S_2), then over the keys; an operand is read
+  // AHEAD groups of 8 matrix instructions before its use
+  constexpr int KS = D / 16, N1 = 2 * KS, NG = N1 + 2 * NT, AHEAD = 2;
   for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
     const int kz = opaque(0);
+    const Rows32 kt{kp + (long long)k0 * ldk, (unsigned)ldk, len - 1 - k0}, vt{vp + (long long)k0 * ldk, (unsigned)ldk, len - 1 - k0};
+    const Rows32 qt{qp + kz, (unsigned)ldq, len - 1 - qb * 32};
     f32x16 s[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      zero16(s[m]);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int col = ks * 16 + h * 8;
-        const bool cok = col < a.hd;
-        const Frag<T> kf = load_row<T>(kp + (long long)(k0 + c) * ldk + m * a.hd + col, cok && k0 + c < len);
-        const Frag<T> qf = load_row<T>(qp + m * a.hd + col + kz, cok && rok);
-        mma(s[m], kf, qf);
+    Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
+    zero16(s[0]);
+    zero16(s[1]);
+    auto fetch = [&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
+      if constexpr (g < N1) {
+        const int m = g / KS, col = g % KS * 16 + h * 8;
+        fa[x] = Rows32{kt.base + m * a.hd, kt.ld, kt.last}.row(c, col, a.hd);
+        fb[x] = Rows32{qt.base + m * a.hd, qt.ld, qt.last}.row(c, col, a.hd);
+      } else if constexpr (g < NG) {
+        fa[x] = vt.col((g - N1) / NT, h, (g - N1) % NT * 32 + c, 2 * a.hd);
       }
-      float tm = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
-        if (key >= len || (a.causal && key > row)) s[m][i] = -INFINITY;
-        tm = fmaxf(tm, s[m][i]);
+    };
+    each<AHEAD>(fetch);
+    each<NG>([&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
+      fetch(std::integral_constant<int, g + AHEAD>{});
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (g < N1) {
+        zero(fb[x], g % KS * 16 + h * 8 >= a.hd);
+        mma(s[g / KS], fa[x], fb[x]);
+      } else {
+        constexpr int cc = (g - N1) / NT, t = (g - N1) % NT;
+        mma(o[0][t], fa[x], acc_frag<T>(s[0], cc));
+        mma(o[1][t], fa[x], acc_frag<T>(s[1], cc));
       }
-      tm = fmaxf(tm, __shfl_xor(tm, 32));
-      const float nm = fmaxf(mx[m], tm);
-      const float ms = nm == -INFINITY ? 0.f : nm * sc;   // nothing seen yet: weights 0
-      const float f = exp2f(mx[m] * sc - ms);
-      float ts = 0.f;
+      if constexpr (g < N1 && g % KS == KS - 1) {
+        constexpr int m = g / KS;
+        float tm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[m][i] = exp2f(fmaf(s[m][i], sc, -ms));
-        ts += s[m][i];
+        for (int i = 0; i < 16; ++i) {
+          const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
+          if (key >= len || (a.causal && key > row)) s[m][i] = -INFINITY;
+          tm = fmaxf(tm, s[m][i]);
+        }
+        tm = fmaxf(tm, __shfl_xor(tm, 32));
+        const float nm = fmaxf(mx[m], tm);
+        const float ms = nm == -INFINITY ? 0.f : nm * sc;   // nothing seen yet: weights 0
+        const float f = exp2f(mx[m] * sc - ms);
+        float ts = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[m][i] = exp2f(fmaf(s[m][i], sc, -ms));
+          ts += s[m][i];
+        }
+        sum[m] = sum[m] * f + ts;
+        mx[m] = nm;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
       }
-      sum[m] = sum[m] * f + ts;
-      mx[m] = nm;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
-    }
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      const Frag<T> p0 = acc_frag<T>(s[0], cc), p1 = acc_frag<T>(s[1], cc);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int dv = 32 * t + c;
-        const Frag<T> vf = load_col(vp + dv, ldk, k0 + 16 * cc, len, h, dv < 2 * a.hd);
-        mma(o[0][t], vf, p0);
-        mma(o[1][t], vf, p1);
-      }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+    });
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m) {

@@ -156,15 +156,6 @@ __device__ inline void set2(Frag<bf16>& f, int i, uint32_t v) {
   f.v = __builtin_bit_cast(bf16x8, w);
 }
 
-// f(0) .. f(N - 1) with compile-time indices, unrolled however long.
-template <typename F, int... I>
-__device__ inline __attribute__((always_inline)) void each_of(F& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F> __device__ inline __attribute__((always_inline)) void each(F f) {
-  each_of(f, std::make_integer_sequence<int, N>{});
-}
-
 // Accumulators to LDS, and added to from there; 4 KB per tile.
 template <int N> __device__ inline void put_acc(const f32x16 (&x)[N], unsigned char* p, int lane) {
 #pragma unroll
