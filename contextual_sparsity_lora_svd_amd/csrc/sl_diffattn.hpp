@@ -56,17 +56,6 @@ template <> __device__ inline Frag<bf16> load_row<bf16>(const bf16* p, bool ok) 
   if (ok) x = *reinterpret_cast<const uint4*>(p);
   return Frag<bf16>{__builtin_bit_cast(bf16x8, x)};
 }
-template <> __device__ inline Frag<float> load_row<float>(const float* p, bool ok) {
-  Frag<float> f;
-  float4 x = make_float4(0, 0, 0, 0), y = x;
-  if (ok) {
-    x = *reinterpret_cast<const float4*>(p);
-    y = *reinterpret_cast<const float4*>(p + 4);
-  }
-  f.v[0] = x.x; f.v[1] = x.y; f.v[2] = x.z; f.v[3] = x.w;
-  f.v[4] = y.x; f.v[5] = y.y; f.v[6] = y.z; f.v[7] = y.w;
-  return f;
-}
 
 // acc (32 x 32) += A (32 x 16) B (16 x 32).  Lane l holds row l % 32 of A and
 // column l % 32 of B, 8 k values of half l / 32; any order of k serves as long
@@ -75,9 +64,8 @@ template <> __device__ inline Frag<float> load_row<float>(const float* p, bool o
 __device__ inline void mma(f32x16& acc, const Frag<bf16>& a, const Frag<bf16>& b) {
   acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
 }
-__device__ inline void mma(f32x16& acc, const Frag<float>& a, const Frag<float>& b) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], acc, 0, 0, 0);
+__device__ inline void mma1(f32x16& acc, const Frag<float>& a, float b, int j) {   // one of the 8 k values
+  acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b, acc, 0, 0, 0);
 }
 
 // Accumulator values 8 c .. 8 c + 7 as the k values of an operand: k position j
@@ -89,43 +77,35 @@ template <> __device__ inline Frag<bf16> acc_frag<bf16>(const f32x16& x, int c) 
   for (int j = 0; j < 8; ++j) f.v[j] = (__bf16)x[8 * c + j];
   return f;
 }
-template <> __device__ inline Frag<float> acc_frag<float>(const f32x16& x, int c) {
-  Frag<float> f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f.v[j] = x[8 * c + j];
-  return f;
-}
 
 // fp32 operands come straight from memory, each read some products before its
-// use.  A tile is 32 rows from row0 on of which `n` exist; rows past them read
-// the last one again (their weights are zero, or their results dropped), columns
-// past the width `w` the first or the last (zero() clears them in one of two
-// operands; as columns of a result they are dropped).
+// use.  A tile is 32 rows; rows past the sequence's last read that one again
+// (their weights are zero, or their results dropped), columns past the width the
+// first or the last (zero() clears them in one of two operands; as columns of a
+// result they are dropped).
 struct Rows32 {
-  const float* base;         // row row0, first column of the head or pair (uniform)
-  unsigned ld;               // row stride in values
-  int last;                  // n - 1
-  // 8 values of row l % 32 from column 16 s + 8 h on
-  __device__ inline Frag<float> row(int c, int col, int w) const {
-    Frag<float> f;
-    const float* p = base + (unsigned)(c < last ? c : last) * ld + (col < w ? col : 0);
-    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-    f.v[0] = x.x; f.v[1] = x.y; f.v[2] = x.z; f.v[3] = x.w;
-    f.v[4] = y.x; f.v[5] = y.y; f.v[6] = y.z; f.v[7] = y.w;
-    return f;
-  }
-  // column col of rows 16 cc + 8 (j / 4) + 4 h + j % 4
-  __device__ inline Frag<float> col(int cc, int h, int col, int w) const {
-    Frag<float> f;
-    const int cl = col < w ? col : w - 1;
+  unsigned row, col[16];     // bytes from the tile's first row: of row l % 32; of rows 8 (j / 4) + 4 h + j % 4
+  __device__ inline void init(int c, int h, int last, unsigned ld) {
+    row = (unsigned)(c < last ? c : last) * ld * 4u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = 16 * cc + 8 * (j >> 2) + 4 * h + (j & 3);
-      f.v[j] = base[(unsigned)(r < last ? r : last) * ld + cl];
+    for (int j = 0; j < 16; ++j) {
+      const int r = 8 * (j >> 2) + 4 * h + (j & 3);
+      col[j] = (unsigned)(r < last ? r : last) * ld * 4u;
     }
-    return f;
   }
 };
+// Part j of 8 of an operand: 8 values of a row from byte `at` on (parts 0 and 1) ...
+__device__ inline void read_row(Frag<float>& f, int j, const float* base, unsigned at) {
+  if (j != 0 && j != 1) return;
+  const float4 x = reinterpret_cast<const float4*>(reinterpret_cast<const char*>(base) + at)[j];
+  f.v[4 * j] = x.x; f.v[4 * j + 1] = x.y; f.v[4 * j + 2] = x.z; f.v[4 * j + 3] = x.w;
+}
+// ... or the column at byte `at` of row j of half cc
+__device__ inline void read_col(Frag<float>& f, int j, const float* base, const Rows32& r, int cc, unsigned at) {
+  f.v[j] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(base) + (r.col[8 * cc + j] + at));
+}
+__device__ inline unsigned first_if_past(int col, int w) { return (col < w ? col : 0) * 4u; }
+__device__ inline unsigned last_if_past(int col, int w) { return (col < w ? col : w - 1) * 4u; }
 __device__ inline void zero(Frag<float>& f, bool gone) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f.v[j] = gone ? 0.f : f.v[j];
@@ -174,6 +154,8 @@ __device__ inline int opaque(int x) {
   asm volatile("" : "+v"(x));
   return x;
 }
+
+__device__ inline float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }   // subnormal results are 0
 
 // The four waves' values added in order; the last wave ends with the sum.  sm holds
 // N tiles of 1024 floats.

@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   const T* kp = reinterpret_cast<const T*>(a.k) + koff;
   const T* vp = reinterpret_cast<const T*>(a.v) + koff;
   const bool rok = row < len;
+  const unsigned qrow = (unsigned)(rok ? c : 0) * (unsigned)ldq * 4u;   // (a row past the end: any)
   float lse[2], ds[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -688,43 +689,50 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   // products in order dP, S_1, S_2, then over the keys; operands read as in the forward
   constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, NG = N0 + N1 + 4 * DT, AHEAD = 2;
   for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
-    const int kz = opaque(0), kl = len - 1 - k0, ql = len - 1 - qb * 32;
     const T* const kt = kp + (long long)k0 * ldk;
-    const Rows32 vt{vp + (long long)k0 * ldk, (unsigned)ldk, kl}, gt{dop + kz, (unsigned)ldq, ql};
+    const T* const vt = vp + (long long)k0 * ldk;
+    Rows32 r;
+    r.init(c, h, len - 1 - k0, (unsigned)ldk);
+    const unsigned qo = qrow + opaque(0);
     f32x16 dp, s[2];
     float part = 0.f;
     Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
     zero16(dp);
     zero16(s[0]);
     zero16(s[1]);
-    auto fetch = [&](auto gc) __attribute__((always_inline)) {
+    auto fetch = [&](auto gc, int j) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
       if constexpr (g < N0) {
-        fa[x] = vt.row(c, g * 16 + h * 8, 2 * a.hd);
-        fb[x] = gt.row(c, g * 16 + h * 8, 2 * a.hd);
+        const unsigned col = first_if_past(g * 16 + h * 8, 2 * a.hd);
+        read_row(fa[x], j, vt, r.row + col);
+        read_row(fb[x], j - 2, dop, qo + col);
       } else if constexpr (g < N0 + N1) {
-        const int m = (g - N0) / KS, col = (g - N0) % KS * 16 + h * 8;
-        fa[x] = Rows32{kt + m * a.hd, (unsigned)ldk, kl}.row(c, col, a.hd);
-        fb[x] = Rows32{qp + kz + m * a.hd, (unsigned)ldq, ql}.row(c, col, a.hd);
+        const int m = (g - N0) / KS;
+        const unsigned col = first_if_past((g - N0) % KS * 16 + h * 8, a.hd);
+        read_row(fa[x], j, kt + m * a.hd, r.row + col);
+        read_row(fb[x], j - 2, qp + m * a.hd, qo + col);
       } else if constexpr (g < NG) {
-        constexpr int j = g - N0 - N1;
-        fa[x] = Rows32{kt + j / (2 * DT) * a.hd, (unsigned)ldk, kl}.col(j / DT % 2, h, j % DT * 32 + c, a.hd);
+        constexpr int y = g - N0 - N1;
+        read_col(fa[x], j, kt + y / (2 * DT) * a.hd, r, y / DT % 2, last_if_past(y % DT * 32 + c, a.hd));
       }
     };
-    each<AHEAD>(fetch);
+    each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
     each<NG>([&](auto gc) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-      fetch(std::integral_constant<int, g + AHEAD>{});
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (g < N0) {
-        zero(fb[x], g * 16 + h * 8 >= 2 * a.hd);
-        mma(dp, fa[x], fb[x]);
-      } else if constexpr (g < N0 + N1) {
-        zero(fb[x], (g - N0) % KS * 16 + h * 8 >= a.hd);
-        mma(s[(g - N0) / KS], fa[x], fb[x]);
-      } else {
-        constexpr int j = g - N0 - N1, m = j / (2 * DT);
-        mma(dq[m][j % DT], fa[x], acc_frag<T>(s[m], j / DT % 2));
+      if constexpr (g < N0) zero(fb[x], g * 16 + h * 8 >= 2 * a.hd);
+      else if constexpr (g < N0 + N1) zero(fb[x], (g - N0) % KS * 16 + h * 8 >= a.hd);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        fetch(std::integral_constant<int, g + AHEAD>{}, j);
+        if constexpr (g < N0) {
+          mma1(dp, fa[x], fb[x].v[j], j);
+        } else if constexpr (g < N0 + N1) {
+          mma1(s[(g - N0) / KS], fa[x], fb[x].v[j], j);
+        } else {
+          constexpr int y = g - N0 - N1, m = y / (2 * DT);
+          mma1(dq[m][y % DT], fa[x], s[m][8 * (y / DT % 2) + j], j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == KS - 1) {
         constexpr int m = (g - N0) / KS;
@@ -732,7 +740,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
         for (int i = 0; i < 16; ++i) {
           const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
           const bool hidden = key >= len || (a.causal && key > row) || !rok;
-          const float p = hidden ? 0.f : exp2f(fmaf(s[m][i], sc, -lse[m]));
+          const float p = hidden ? 0.f : fast_exp2(fmaf(s[m][i], sc, -lse[m]));
           if (m == 1) part = fmaf(p, dp[i], part);
           s[m][i] = p * (dp[i] - ds[m]);
         }
@@ -794,14 +802,17 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
   for (int t = 0; t < NT; ++t) zero16(dv[t]);
   const float sc = a.scale * kLog2e;
   const int t0 = a.causal ? kb : 0, ntile = kb * 32 < len ? (len + 31) / 32 - t0 : 0;
-  const int nh = grp / a.split, pr0 = g * grp + hpart * nh, kl = len - 1 - kb * 32;
+  const int nh = grp / a.split, pr0 = g * grp + hpart * nh;
+  const unsigned krow = (unsigned)(kok ? c : 0) * (unsigned)ldk * 4u;   // (a key past the end: any)
   // products in order dP, S_1, S_2, dV, dK; operands read as in the forward
   constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, N2 = 2 * NT, NG = N0 + N1 + N2 + 4 * DT, AHEAD = 2;
   for (int x = wave; x < ntile * nh; x += 4) {
-    const int pr = pr0 + x / ntile, q0 = (t0 + x % ntile) * 32, ql = len - 1 - q0, kz = opaque(0);
+    const int pr = pr0 + x / ntile, q0 = (t0 + x % ntile) * 32;
     const T* const qt = reinterpret_cast<const T*>(a.q) + (tok0 + q0) * ldq + pr * 2 * a.hd;
-    const Rows32 gt{reinterpret_cast<const T*>(a.da) + (tok0 + q0) * ldq + pr * 2 * a.hd, (unsigned)ldq, ql};
-    const Rows32 vt{vp + kz, (unsigned)ldk, kl};
+    const T* const gt = reinterpret_cast<const T*>(a.da) + (tok0 + q0) * ldq + pr * 2 * a.hd;
+    Rows32 r;
+    r.init(c, h, len - 1 - q0, (unsigned)ldq);
+    const unsigned ko = krow + opaque(0);
     const float* const lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.ls;
     const float* const dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.ls;
     f32x16 dp, s[2], w;
@@ -810,27 +821,28 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
     zero16(dp);
     zero16(s[0]);
     zero16(s[1]);
-    auto fetch = [&](auto gc) __attribute__((always_inline)) {
+    auto fetch = [&](auto gc, int j) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, y = g % (AHEAD + 1);
       if constexpr (g < N0) {
-        fa[y] = gt.row(c, g * 16 + h * 8, 2 * a.hd);
-        fb[y] = vt.row(c, g * 16 + h * 8, 2 * a.hd);
+        const unsigned col = first_if_past(g * 16 + h * 8, 2 * a.hd);
+        read_row(fa[y], j, gt, r.row + col);
+        read_row(fb[y], j - 2, vp, ko + col);
       } else if constexpr (g < N0 + N1) {
-        const int m = (g - N0) / KS, col = (g - N0) % KS * 16 + h * 8;
-        fa[y] = Rows32{qt + m * a.hd, (unsigned)ldq, ql}.row(c, col, a.hd);
-        fb[y] = Rows32{kp + kz + m * a.hd, (unsigned)ldk, kl}.row(c, col, a.hd);
+        const int m = (g - N0) / KS;
+        const unsigned col = first_if_past((g - N0) % KS * 16 + h * 8, a.hd);
+        read_row(fa[y], j, qt + m * a.hd, r.row + col);
+        read_row(fb[y], j - 2, kp + m * a.hd, ko + col);
       } else if constexpr (g < N0 + N1 + N2) {
-        constexpr int j = g - N0 - N1;
-        fa[y] = gt.col(j / NT, h, j % NT * 32 + c, 2 * a.hd);
+        constexpr int z = g - N0 - N1;
+        read_col(fa[y], j, gt, r, z / NT, last_if_past(z % NT * 32 + c, 2 * a.hd));
       } else if constexpr (g < NG) {
-        constexpr int j = g - N0 - N1 - N2;
-        fa[y] = Rows32{qt + j / (2 * DT) * a.hd, (unsigned)ldq, ql}.col(j / DT % 2, h, j % DT * 32 + c, a.hd);
+        constexpr int z = g - N0 - N1 - N2;
+        read_col(fa[y], j, qt + z / (2 * DT) * a.hd, r, z / DT % 2, last_if_past(z % DT * 32 + c, a.hd));
       }
     };
-    each<AHEAD>(fetch);
+    each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
     each<NG>([&](auto gc) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, y = g % (AHEAD + 1);
-      fetch(std::integral_constant<int, g + AHEAD>{});
       if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == 0) {
         constexpr int m = (g - N0) / KS;
 #pragma unroll
@@ -840,26 +852,30 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
           sd[i] = dsm[at];
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (g < N0) {
-        zero(fb[y], g * 16 + h * 8 >= 2 * a.hd);
-        mma(dp, fa[y], fb[y]);
-      } else if constexpr (g < N0 + N1) {
-        zero(fb[y], (g - N0) % KS * 16 + h * 8 >= a.hd);
-        mma(s[(g - N0) / KS], fa[y], fb[y]);
-      } else if constexpr (g < N0 + N1 + N2) {
-        constexpr int j = g - N0 - N1;
-        mma(dv[j % NT], fa[y], acc_frag<T>(w, j / NT));
-      } else {
-        constexpr int j = g - N0 - N1 - N2, m = j / (2 * DT);
-        mma(dk[m][j % DT], fa[y], acc_frag<T>(s[m], j / DT % 2));
+      if constexpr (g < N0) zero(fb[y], g * 16 + h * 8 >= 2 * a.hd);
+      else if constexpr (g < N0 + N1) zero(fb[y], (g - N0) % KS * 16 + h * 8 >= a.hd);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        fetch(std::integral_constant<int, g + AHEAD>{}, j);
+        if constexpr (g < N0) {
+          mma1(dp, fa[y], fb[y].v[j], j);
+        } else if constexpr (g < N0 + N1) {
+          mma1(s[(g - N0) / KS], fa[y], fb[y].v[j], j);
+        } else if constexpr (g < N0 + N1 + N2) {
+          constexpr int z = g - N0 - N1;
+          mma1(dv[z % NT], fa[y], w[8 * (z / NT) + j], j);
+        } else {
+          constexpr int z = g - N0 - N1 - N2, m = z / (2 * DT);
+          mma1(dk[m][z % DT], fa[y], s[m][8 * (z / DT % 2) + j], j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == KS - 1) {
         constexpr int m = (g - N0) / KS;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3);
-          const float p = a.causal && key > q ? 0.f : exp2f(fmaf(s[m][i], sc, -sl[i]));
+          const float p = a.causal && key > q ? 0.f : fast_exp2(fmaf(s[m][i], sc, -sl[i]));
           w[i] = m ? w[i] - lam * p : p;
           s[m][i] = p * (dp[i] - sd[i]);
         }

@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * ldk + g * 2 * a.hd;
   const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * ldk + g * 2 * a.hd;
   const bool rok = row < len;
+  const unsigned qrow = (unsigned)(rok ? c : 0) * (unsigned)ldq * 4u;   // (a row past the end: any)
   f32x16 o[2][NT];
   float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -412,35 +413,41 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   // AHEAD groups of 8 matrix instructions before its use
   constexpr int KS = D / 16, N1 = 2 * KS, NG = N1 + 2 * NT, AHEAD = 2;
   for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
-    const int kz = opaque(0);
-    const Rows32 kt{kp + (long long)k0 * ldk, (unsigned)ldk, len - 1 - k0}, vt{vp + (long long)k0 * ldk, (unsigned)ldk, len - 1 - k0};
-    const Rows32 qt{qp + kz, (unsigned)ldq, len - 1 - qb * 32};
+    const T* const kt = kp + (long long)k0 * ldk;
+    const T* const vt = vp + (long long)k0 * ldk;
+    Rows32 r;
+    r.init(c, h, len - 1 - k0, (unsigned)ldk);
+    const unsigned qo = qrow + opaque(0);
     f32x16 s[2];
     Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
     zero16(s[0]);
     zero16(s[1]);
-    auto fetch = [&](auto gc) __attribute__((always_inline)) {
+    auto fetch = [&](auto gc, int j) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
       if constexpr (g < N1) {
-        const int m = g / KS, col = g % KS * 16 + h * 8;
-        fa[x] = Rows32{kt.base + m * a.hd, kt.ld, kt.last}.row(c, col, a.hd);
-        fb[x] = Rows32{qt.base + m * a.hd, qt.ld, qt.last}.row(c, col, a.hd);
+        const int m = g / KS;
+        const unsigned col = first_if_past(g % KS * 16 + h * 8, a.hd);
+        read_row(fa[x], j, kt + m * a.hd, r.row + col);
+        read_row(fb[x], j - 2, qp + m * a.hd, qo + col);
       } else if constexpr (g < NG) {
-        fa[x] = vt.col((g - N1) / NT, h, (g - N1) % NT * 32 + c, 2 * a.hd);
+        read_col(fa[x], j, vt, r, (g - N1) / NT, last_if_past((g - N1) % NT * 32 + c, 2 * a.hd));
       }
     };
-    each<AHEAD>(fetch);
+    each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
     each<NG>([&](auto gc) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-      fetch(std::integral_constant<int, g + AHEAD>{});
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (g < N1) {
-        zero(fb[x], g % KS * 16 + h * 8 >= a.hd);
-        mma(s[g / KS], fa[x], fb[x]);
-      } else {
-        constexpr int cc = (g - N1) / NT, t = (g - N1) % NT;
-        mma(o[0][t], fa[x], acc_frag<T>(s[0], cc));
-        mma(o[1][t], fa[x], acc_frag<T>(s[1], cc));
+      if constexpr (g < N1) zero(fb[x], g % KS * 16 + h * 8 >= a.hd);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        fetch(std::integral_constant<int, g + AHEAD>{}, j);
+        if constexpr (g < N1) {
+          mma1(s[g / KS], fa[x], fb[x].v[j], j);
+        } else {
+          constexpr int cc = (g - N1) / NT, t = (g - N1) % NT;
+          mma1(o[0][t], fa[x], s[0][8 * cc + j], j);
+          mma1(o[1][t], fa[x], s[1][8 * cc + j], j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (g < N1 && g % KS == KS - 1) {
         constexpr int m = g / KS;
@@ -454,19 +461,21 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
         tm = fmaxf(tm, __shfl_xor(tm, 32));
         const float nm = fmaxf(mx[m], tm);
         const float ms = nm == -INFINITY ? 0.f : nm * sc;   // nothing seen yet: weights 0
-        const float f = exp2f(mx[m] * sc - ms);
+        const float f = fast_exp2(mx[m] * sc - ms);
         float ts = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[m][i] = exp2f(fmaf(s[m][i], sc, -ms));
+          s[m][i] = fast_exp2(fmaf(s[m][i], sc, -ms));
           ts += s[m][i];
         }
         sum[m] = sum[m] * f + ts;
         mx[m] = nm;
+        if (__any(f != 1.f)) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
+            for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     });

@@ -130,8 +130,6 @@ __device__ inline float pair_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-__device__ inline float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }   // subnormal results are 0
-
 // Block -> (row block, head pair, sequence): the longest causal rows first, and
 // the pairs of a kv group on one XCD (blocks go round the 8 XCDs), whose L2
 // then holds the group's K and V.
