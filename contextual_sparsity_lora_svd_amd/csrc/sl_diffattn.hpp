@@ -81,8 +81,8 @@ template <> __device__ inline Frag<bf16> acc_frag<bf16>(const f32x16& x, int c) 
 // fp32 operands come straight from memory, each read some products before its
 // use.  A tile is 32 rows; rows past the sequence's last read that one again
 // (their weights are zero, or their results dropped), columns past the width the
-// first or the last (zero() clears them in one of two operands; as columns of a
-// result they are dropped).
+// first or the last (the other operand is zero there; as columns of a result they
+// are dropped).
 struct Rows32 {
   unsigned row, col[16];     // bytes from the tile's first row: of row l % 32; of rows 8 (j / 4) + 4 h + j % 4
   __device__ inline void init(int c, int h, int last, unsigned ld) {
@@ -106,9 +106,24 @@ __device__ inline void read_col(Frag<float>& f, int j, const float* base, const 
 }
 __device__ inline unsigned first_if_past(int col, int w) { return (col < w ? col : 0) * 4u; }
 __device__ inline unsigned last_if_past(int col, int w) { return (col < w ? col : w - 1) * 4u; }
-__device__ inline void zero(Frag<float>& f, bool gone) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f.v[j] = gone ? 0.f : f.v[j];
+// The workgroup's own 32 rows of `w` values in LDS, as operands: operand f is columns
+// 16 f + 8 h on, zero past the width.  A wave writes every fourth.
+__device__ inline void put_own(float4* own, int nf, const float* row, int w, int wave, int lane) {
+  for (int f = wave; f < nf; f += 4) {
+    const int col = f * 16 + (lane >> 5) * 8;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    if (col < w) {
+      x = *reinterpret_cast<const float4*>(row + col);
+      y = *reinterpret_cast<const float4*>(row + col + 4);
+    }
+    own[f * 128 + lane] = x;
+    own[f * 128 + 64 + lane] = y;
+  }
+}
+__device__ inline void read_own(Frag<float>& f, int j, const float4* own, int n) {   // own: + lane
+  if (j != 0 && j != 1) return;
+  const float4 x = own[n * 128 + j * 64];
+  f.v[4 * j] = x.x; f.v[4 * j + 1] = x.y; f.v[4 * j + 2] = x.z; f.v[4 * j + 3] = x.w;
 }
 
 // four consecutive values of a row

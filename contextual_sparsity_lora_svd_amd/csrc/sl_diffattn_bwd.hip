@@ -655,6 +655,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ __attribute__((aligned(16))) float sm[DT * 1024];
+  __shared__ float4 own[(D / 4) * 128];
   const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);
   const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
   const int g = pair / (a.hp / a.gp), len = a.lens[b];
@@ -668,7 +669,6 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   const T* kp = reinterpret_cast<const T*>(a.k) + koff;
   const T* vp = reinterpret_cast<const T*>(a.v) + koff;
   const bool rok = row < len;
-  const unsigned qrow = (unsigned)(rok ? c : 0) * (unsigned)ldq * 4u;   // (a row past the end: any)
   float lse[2], ds[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -686,6 +686,12 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   int kend = len;
   if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
   if (qb * 32 >= len) kend = 0;
+  if (kend > 0) {                                      // (a row past the end: any)
+    const long long at = (rok ? c : 0) * ldq;
+    put_own(own, D / 8, dop + at, 2 * a.hd, wave, lane);
+    for (int m = 0; m < 2; ++m) put_own(own + (2 + m) * (D / 16) * 128, D / 16, qp + at + m * a.hd, a.hd, wave, lane);
+  }
+  __syncthreads();
   // products in order dP, S_1, S_2, then over the keys; operands read as in the forward
   constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, NG = N0 + N1 + 4 * DT, AHEAD = 2;
   for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
@@ -693,7 +699,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
     const T* const vt = vp + (long long)k0 * ldk;
     Rows32 r;
     r.init(c, h, len - 1 - k0, (unsigned)ldk);
-    const unsigned qo = qrow + opaque(0);
+    const float4* const mine = own + opaque(lane);
     f32x16 dp, s[2];
     float part = 0.f;
     Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
@@ -705,12 +711,12 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
       if constexpr (g < N0) {
         const unsigned col = first_if_past(g * 16 + h * 8, 2 * a.hd);
         read_row(fa[x], j, vt, r.row + col);
-        read_row(fb[x], j - 2, dop, qo + col);
+        read_own(fb[x], j - 2, mine, g);
       } else if constexpr (g < N0 + N1) {
         const int m = (g - N0) / KS;
         const unsigned col = first_if_past((g - N0) % KS * 16 + h * 8, a.hd);
         read_row(fa[x], j, kt + m * a.hd, r.row + col);
-        read_row(fb[x], j - 2, qp + m * a.hd, qo + col);
+        read_own(fb[x], j - 2, mine, g);
       } else if constexpr (g < NG) {
         constexpr int y = g - N0 - N1;
         read_col(fa[x], j, kt + y / (2 * DT) * a.hd, r, y / DT % 2, last_if_past(y % DT * 32 + c, a.hd));
@@ -719,8 +725,6 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
     each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
     each<NG>([&](auto gc) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-      if constexpr (g < N0) zero(fb[x], g * 16 + h * 8 >= 2 * a.hd);
-      else if constexpr (g < N0 + N1) zero(fb[x], (g - N0) % KS * 16 + h * 8 >= a.hd);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         fetch(std::integral_constant<int, g + AHEAD>{}, j);
@@ -778,6 +782,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
   const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ __attribute__((aligned(16))) float sm[NT * 1024];
+  __shared__ float4 own[(D / 4) * 128];
   if (blockIdx.x == gridDim.x - 1) {
     dlambda_block(a, reinterpret_cast<double*>(sm));
     return;
@@ -803,7 +808,12 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
   const float sc = a.scale * kLog2e;
   const int t0 = a.causal ? kb : 0, ntile = kb * 32 < len ? (len + 31) / 32 - t0 : 0;
   const int nh = grp / a.split, pr0 = g * grp + hpart * nh;
-  const unsigned krow = (unsigned)(kok ? c : 0) * (unsigned)ldk * 4u;   // (a key past the end: any)
+  if (ntile > 0) {                                             // (a key past the end: any)
+    const long long at = (kok ? c : 0) * ldk;
+    put_own(own, D / 8, vp + at, 2 * a.hd, wave, lane);
+    for (int m = 0; m < 2; ++m) put_own(own + (2 + m) * (D / 16) * 128, D / 16, kp + at + m * a.hd, a.hd, wave, lane);
+  }
+  __syncthreads();
   // products in order dP, S_1, S_2, dV, dK; operands read as in the forward
   constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, N2 = 2 * NT, NG = N0 + N1 + N2 + 4 * DT, AHEAD = 2;
   for (int x = wave; x < ntile * nh; x += 4) {
@@ -812,7 +822,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
     const T* const gt = reinterpret_cast<const T*>(a.da) + (tok0 + q0) * ldq + pr * 2 * a.hd;
     Rows32 r;
     r.init(c, h, len - 1 - q0, (unsigned)ldq);
-    const unsigned ko = krow + opaque(0);
+    const float4* const mine = own + opaque(lane);
     const float* const lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.ls;
     const float* const dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.ls;
     f32x16 dp, s[2], w;
@@ -826,12 +836,12 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
       if constexpr (g < N0) {
         const unsigned col = first_if_past(g * 16 + h * 8, 2 * a.hd);
         read_row(fa[y], j, gt, r.row + col);
-        read_row(fb[y], j - 2, vp, ko + col);
+        read_own(fb[y], j - 2, mine, g);
       } else if constexpr (g < N0 + N1) {
         const int m = (g - N0) / KS;
         const unsigned col = first_if_past((g - N0) % KS * 16 + h * 8, a.hd);
         read_row(fa[y], j, qt + m * a.hd, r.row + col);
-        read_row(fb[y], j - 2, kp + m * a.hd, ko + col);
+        read_own(fb[y], j - 2, mine, g);
       } else if constexpr (g < N0 + N1 + N2) {
         constexpr int z = g - N0 - N1;
         read_col(fa[y], j, gt, r, z / NT, last_if_past(z % NT * 32 + c, 2 * a.hd));
@@ -852,8 +862,6 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
           sd[i] = dsm[at];
         }
       }
-      if constexpr (g < N0) zero(fb[y], g * 16 + h * 8 >= 2 * a.hd);
-      else if constexpr (g < N0 + N1) zero(fb[y], (g - N0) % KS * 16 + h * 8 >= a.hd);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         fetch(std::integral_constant<int, g + AHEAD>{}, j);

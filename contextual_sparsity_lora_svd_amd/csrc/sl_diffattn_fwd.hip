@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ __attribute__((aligned(16))) float sm[NT * 1024];
   __shared__ float smx[2][4][64], ssum[2][4][64];
+  __shared__ float4 own[2 * (D / 16) * 128];
   const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);   // the longest rows first
   const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
   const int g = pair / (a.hp / a.gp), len = a.lens[b];
@@ -398,7 +399,6 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * ldk + g * 2 * a.hd;
   const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * ldk + g * 2 * a.hd;
   const bool rok = row < len;
-  const unsigned qrow = (unsigned)(rok ? c : 0) * (unsigned)ldq * 4u;   // (a row past the end: any)
   f32x16 o[2][NT];
   float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -409,6 +409,9 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
   int kend = len;
   if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
   if (qb * 32 >= len) kend = 0;
+  for (int m = 0; m < 2 && kend > 0; ++m)                // (a row past the end: any)
+    put_own(own + m * (D / 16) * 128, D / 16, qp + (rok ? c : 0) * ldq + m * a.hd, a.hd, wave, lane);
+  __syncthreads();
   // products over the columns (S_1, S_2), then over the keys; an operand is read
   // AHEAD groups of 8 matrix instructions before its use
   constexpr int KS = D / 16, N1 = 2 * KS, NG = N1 + 2 * NT, AHEAD = 2;
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
     const T* const vt = vp + (long long)k0 * ldk;
     Rows32 r;
     r.init(c, h, len - 1 - k0, (unsigned)ldk);
-    const unsigned qo = qrow + opaque(0);
+    const float4* const mine = own + opaque(lane);
     f32x16 s[2];
     Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
     zero16(s[0]);
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
         const int m = g / KS;
         const unsigned col = first_if_past(g % KS * 16 + h * 8, a.hd);
         read_row(fa[x], j, kt + m * a.hd, r.row + col);
-        read_row(fb[x], j - 2, qp + m * a.hd, qo + col);
+        read_own(fb[x], j - 2, mine, g);
       } else if constexpr (g < NG) {
         read_col(fa[x], j, vt, r, (g - N1) / NT, last_if_past((g - N1) % NT * 32 + c, 2 * a.hd));
       }
@@ -436,7 +439,6 @@ __global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
     each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
     each<NG>([&](auto gc) __attribute__((always_inline)) {
       constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-      if constexpr (g < N1) zero(fb[x], g % KS * 16 + h * 8 >= a.hd);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         fetch(std::integral_constant<int, g + AHEAD>{}, j);
