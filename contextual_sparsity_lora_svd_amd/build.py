@@ -17,7 +17,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparselora.so")
 
 SOURCES = ["sl_host.hip", "sl_estimate.hip", "sl_ffn.hip", "sl_qkvo.hip", "sl_svd.hip", "sl_quant.hip",
-           "sl_rotary.hip", "sl_diffattn.hip", "sl_diffattn_fwd.hip", "sl_diffattn_bwd.hip"]
+           "sl_rotary.hip", "sl_diffattn.hip", "sl_diffattn_fwd.hip", "sl_diffattn_bwd.hip", "sl_diffattn_f32.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

@@ -146,7 +146,8 @@ extern "C" sl_status sl_diff_attn_fwd(sl_dtype dt, const sl_layout* lay, const s
   a.q = q; a.k = k; a.v = v; a.o = o;
   saved_args(a, pl, saved);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  launch_diff_fwd(dt, a, s);
+  if (dt == SL_BF16) launch_diff_fwd_bf16(a, s);
+  else launch_diff_fwd_f32(a, s);
   SL_HIP(hipGetLastError());
   return SL_OK;
 }
@@ -185,7 +186,8 @@ extern "C" sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const s
   a.dv_part = a.dk_part + grid.split * pl.part_elems;
   a.dlq1 = g->dlq1; a.dlk1 = g->dlk1; a.dlq2 = g->dlq2; a.dlk2 = g->dlk2;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  launch_diff_bwd(dt, a, s);
+  if (dt == SL_BF16) launch_diff_bwd_bf16(a, s);
+  else launch_diff_bwd_f32(a, s);
   SL_HIP(hipGetLastError());
   return SL_OK;
 }

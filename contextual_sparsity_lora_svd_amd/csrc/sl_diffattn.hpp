@@ -210,8 +210,47 @@ template <typename F> inline void by_width(int hd, F f) {
   else f(std::integral_constant<int, 128>{});
 }
 
-// Enqueue the forward, and the backward, on s.
-void launch_diff_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s);
-void launch_diff_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s);
+// dlambda = -(the waves' sums of D_2, added in a fixed order) and the four
+// vectors' gradients: the work of one block of 256 threads.
+__device__ inline void dlambda_block(const DiffArgs& a, double* sm) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < a.npart; i += 256) s += a.dlam_part[i];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = ((sm[0] + sm[1]) + sm[2]) + sm[3];
+  const int i = threadIdx.x;
+  if (i < a.hd) {
+    const float g1 = -(float)s * a.lam[1], g2 = (float)s * a.lam[2];
+    const float q1 = a.lq1[i], k1 = a.lk1[i], q2 = a.lq2[i], k2 = a.lk2[i];
+    a.dlq1[i] = g1 * k1;
+    a.dlk1[i] = g1 * q1;
+    a.dlq2[i] = g2 * k2;
+    a.dlk2[i] = g2 * q2;
+  }
+}
+
+// dK and dV from the parts' sums, in order; 4 values per thread.
+template <typename T> __global__ void __launch_bounds__(256) diff_dkv_sum(const DiffArgs a) {
+  const long long n = (long long)a.B * a.L * a.gp * 2 * a.hd / 4;
+  long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const bool v = i >= n;
+  if (v) i -= n;
+  if (i >= n) return;
+  const float4* src = reinterpret_cast<const float4*>(v ? a.dv_part : a.dk_part) + i;
+  float4 x = src[0];
+  for (int p = 1; p < a.split; ++p) {
+    const float4 y = src[p * n];
+    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+  }
+  store4<T>(reinterpret_cast<T*>(v ? a.dv : a.dk) + 4 * i, x.x, x.y, x.z, x.w);
+}
+
+// Enqueue the forward, and the backward, of one type on s.
+void launch_diff_fwd_bf16(const DiffArgs& a, hipStream_t s);
+void launch_diff_bwd_bf16(const DiffArgs& a, hipStream_t s);
+void launch_diff_fwd_f32(const DiffArgs& a, hipStream_t s);
+void launch_diff_bwd_f32(const DiffArgs& a, hipStream_t s);
 
 }  // namespace sl

@@ -287,27 +287,6 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
              rows, lane);
 }
 
-// dlambda = -(the waves' sums of D_2, added in a fixed order) and the four
-// vectors' gradients: the work of one block of 256 threads.
-__device__ inline void dlambda_block(const DiffArgs& a, double* sm) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.npart; i += 256) s += a.dlam_part[i];
-#pragma unroll
-  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = s;
-  __syncthreads();
-  s = ((sm[0] + sm[1]) + sm[2]) + sm[3];
-  const int i = threadIdx.x;
-  if (i < a.hd) {
-    const float g1 = -(float)s * a.lam[1], g2 = (float)s * a.lam[2];
-    const float q1 = a.lq1[i], k1 = a.lk1[i], q2 = a.lq2[i], k2 = a.lk2[i];
-    a.dlq1[i] = g1 * k1;
-    a.dlk1[i] = g1 * q1;
-    a.dlq2[i] = g2 * k2;
-    a.dlk2[i] = g2 * q2;
-  }
-}
-
 // ---------------------------------------------------------------------------
 // dK and dV.  A wave owns 32 keys (K's rows in registers; V's rows in registers
 // up to D = 64, else in LDS) and walks the query tiles of its group's heads:
@@ -601,346 +580,19 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   }
 }
 
-// dK and dV from the parts' sums, in order; 4 values per thread.
-template <typename T> __global__ void __launch_bounds__(256) diff_dkv_sum(const DiffArgs a) {
-  const long long n = (long long)a.B * a.L * a.gp * 2 * a.hd / 4;
-  long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const bool v = i >= n;
-  if (v) i -= n;
-  if (i >= n) return;
-  const float4* src = reinterpret_cast<const float4*>(v ? a.dv_part : a.dk_part) + i;
-  float4 x = src[0];
-  for (int p = 1; p < a.split; ++p) {
-    const float4 y = src[p * n];
-    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-  }
-  store4<T>(reinterpret_cast<T*>(v ? a.dv : a.dk) + 4 * i, x.x, x.y, x.z, x.w);
-}
-
-// ---------------------------------------------------------------------------
-// fp32: D_1 = dO . (O + lambda O_2), D_2 = dO . O_2, one wave per row and head pair.
-__global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
-  using T = float;
-  const int lane = threadIdx.x & 63;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const long long rows = (long long)a.B * a.L;
-  if (w >= rows * a.hp) return;
-  const int pair = (int)(w % a.hp);
-  const long long tok = w / a.hp;
-  const int b = (int)(tok / a.L), row = (int)(tok % a.L);
-  const float lam = a.lam[0];
-  float d1 = 0.f, d2 = 0.f;
-  if (row < a.lens[b]) {
-    const long long at = (tok * a.hp + pair) * 2 * a.hd;
-    const T* dop = reinterpret_cast<const T*>(a.da) + at;
-    const T* op = reinterpret_cast<const T*>(a.a) + at;
-    const T* o2p = reinterpret_cast<const T*>(a.o2) + at;
-    for (int i = lane; i < 2 * a.hd; i += 64) {
-      const float g = ldv(dop, i), y = ldv(o2p, i);
-      d1 = fmaf(g, ldv(op, i) + lam * y, d1);
-      d2 = fmaf(g, y, d2);
-    }
-  }
-  d1 = wave_sum(d1);
-  d2 = wave_sum(d2);
-  if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.ls + row] = lane ? d2 : d1;
-}
-
-// dQ: 32 queries per workgroup, every fourth key tile per wave.  The sum of P_2 dP
-// is -dlambda.
-template <int D>
-__global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
-  using T = float;
-  constexpr int DT = D / 32;
-  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  __shared__ __attribute__((aligned(16))) float sm[DT * 1024];
-  __shared__ float4 own[(D / 4) * 128];
-  const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);
-  const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
-  const int g = pair / (a.hp / a.gp), len = a.lens[b];
-  const float lam = a.lam[0];
-  const int row = qb * 32 + c;
-  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
-  const long long qoff = (tok0 + row) * ldq + pair * 2 * a.hd, koff = tok0 * ldk + g * 2 * a.hd;
-  const long long toff = (tok0 + qb * 32) * ldq + pair * 2 * a.hd;
-  const T* qp = reinterpret_cast<const T*>(a.q) + toff;
-  const T* dop = reinterpret_cast<const T*>(a.da) + toff;
-  const T* kp = reinterpret_cast<const T*>(a.k) + koff;
-  const T* vp = reinterpret_cast<const T*>(a.v) + koff;
-  const bool rok = row < len;
-  float lse[2], ds[2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
-    lse[m] = rok ? a.lse[at] : INFINITY;
-    ds[m] = rok ? a.dsum[at] : 0.f;
-  }
-  f32x16 dq[2][DT];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int t = 0; t < DT; ++t) zero16(dq[m][t]);
-  const float sc = a.scale * kLog2e;
-  double dlam = 0.0;
-  int kend = len;
-  if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
-  if (qb * 32 >= len) kend = 0;
-  if (kend > 0) {                                      // (a row past the end: any)
-    const long long at = (rok ? c : 0) * ldq;
-    put_own(own, D / 8, dop + at, 2 * a.hd, wave, lane);
-    for (int m = 0; m < 2; ++m) put_own(own + (2 + m) * (D / 16) * 128, D / 16, qp + at + m * a.hd, a.hd, wave, lane);
-  }
-  __syncthreads();
-  // products in order dP, S_1, S_2, then over the keys; operands read as in the forward
-  constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, NG = N0 + N1 + 4 * DT, AHEAD = 2;
-  for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
-    const T* const kt = kp + (long long)k0 * ldk;
-    const T* const vt = vp + (long long)k0 * ldk;
-    Rows32 r;
-    r.init(c, h, len - 1 - k0, (unsigned)ldk);
-    const float4* const mine = own + opaque(lane);
-    f32x16 dp, s[2];
-    float part = 0.f;
-    Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
-    zero16(dp);
-    zero16(s[0]);
-    zero16(s[1]);
-    auto fetch = [&](auto gc, int j) __attribute__((always_inline)) {
-      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-      if constexpr (g < N0) {
-        const unsigned col = first_if_past(g * 16 + h * 8, 2 * a.hd);
-        read_row(fa[x], j, vt, r.row + col);
-        read_own(fb[x], j - 2, mine, g);
-      } else if constexpr (g < N0 + N1) {
-        const int m = (g - N0) / KS;
-        const unsigned col = first_if_past((g - N0) % KS * 16 + h * 8, a.hd);
-        read_row(fa[x], j, kt + m * a.hd, r.row + col);
-        read_own(fb[x], j - 2, mine, g);
-      } else if constexpr (g < NG) {
-        constexpr int y = g - N0 - N1;
-        read_col(fa[x], j, kt + y / (2 * DT) * a.hd, r, y / DT % 2, last_if_past(y % DT * 32 + c, a.hd));
-      }
-    };
-    each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
-    each<NG>([&](auto gc) __attribute__((always_inline)) {
-      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        fetch(std::integral_constant<int, g + AHEAD>{}, j);
-        if constexpr (g < N0) {
-          mma1(dp, fa[x], fb[x].v[j], j);
-        } else if constexpr (g < N0 + N1) {
-          mma1(s[(g - N0) / KS], fa[x], fb[x].v[j], j);
-        } else {
-          constexpr int y = g - N0 - N1, m = y / (2 * DT);
-          mma1(dq[m][y % DT], fa[x], s[m][8 * (y / DT % 2) + j], j);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == KS - 1) {
-        constexpr int m = (g - N0) / KS;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
-          const bool hidden = key >= len || (a.causal && key > row) || !rok;
-          const float p = hidden ? 0.f : fast_exp2(fmaf(s[m][i], sc, -lse[m]));
-          if (m == 1) part = fmaf(p, dp[i], part);
-          s[m][i] = p * (dp[i] - ds[m]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    dlam += (double)part;
-  }
-#pragma unroll
-  for (int o = 32; o; o >>= 1) dlam += __shfl_xor(dlam, o);
-  if (lane == 0) a.dlam_part[blockIdx.x * 4 + wave] = dlam;
-  add_waves(dq[0], sm, wave, lane);
-  add_waves(dq[1], sm, wave, lane);
-  if (wave != 3 || row >= a.L) return;
-  T* out = reinterpret_cast<T*>(a.dq) + qoff;
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float f = m ? -lam * a.scale : a.scale;
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int d = 32 * t + 2 * i + 4 * h;
-        if (d >= a.hd) continue;
-        store4<T>(out + m * a.hd + d, dq[m][t][i] * f, dq[m][t][i + 1] * f, dq[m][t][i + 2] * f, dq[m][t][i + 3] * f);
-      }
-  }
-}
-
-// dK and dV: 32 keys per workgroup, every fourth of the group's query tiles per wave.
-template <int D>
-__global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
-  using T = float;
-  constexpr int DT = D / 32, NT = D / 16;
-  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  __shared__ __attribute__((aligned(16))) float sm[NT * 1024];
-  __shared__ float4 own[(D / 4) * 128];
-  if (blockIdx.x == gridDim.x - 1) {
-    dlambda_block(a, reinterpret_cast<double*>(sm));
-    return;
-  }
-  const int n = a.gp * a.split * a.B, kb = blockIdx.x / n;      // causal: the first keys have the most queries
-  const int gs = blockIdx.x % n / a.B, b = blockIdx.x % a.B, g = gs / a.split, hpart = gs % a.split;
-  const int grp = a.hp / a.gp, len = a.lens[b];
-  const float lam = a.lam[0];
-  const int key = kb * 32 + c;
-  const bool kok = key < len;                                  // else: its results are 0
-  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
-  const long long koff = (tok0 + key) * ldk + g * 2 * a.hd;
-  const long long toff = (tok0 + kb * 32) * ldk + g * 2 * a.hd;
-  const T* kp = reinterpret_cast<const T*>(a.k) + toff;
-  const T* vp = reinterpret_cast<const T*>(a.v) + toff;
-  f32x16 dk[2][DT], dv[NT];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int t = 0; t < DT; ++t) zero16(dk[m][t]);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) zero16(dv[t]);
-  const float sc = a.scale * kLog2e;
-  const int t0 = a.causal ? kb : 0, ntile = kb * 32 < len ? (len + 31) / 32 - t0 : 0;
-  const int nh = grp / a.split, pr0 = g * grp + hpart * nh;
-  if (ntile > 0) {                                             // (a key past the end: any)
-    const long long at = (kok ? c : 0) * ldk;
-    put_own(own, D / 8, vp + at, 2 * a.hd, wave, lane);
-    for (int m = 0; m < 2; ++m) put_own(own + (2 + m) * (D / 16) * 128, D / 16, kp + at + m * a.hd, a.hd, wave, lane);
-  }
-  __syncthreads();
-  // products in order dP, S_1, S_2, dV, dK; operands read as in the forward
-  constexpr int N0 = D / 8, KS = D / 16, N1 = 2 * KS, N2 = 2 * NT, NG = N0 + N1 + N2 + 4 * DT, AHEAD = 2;
-  for (int x = wave; x < ntile * nh; x += 4) {
-    const int pr = pr0 + x / ntile, q0 = (t0 + x % ntile) * 32;
-    const T* const qt = reinterpret_cast<const T*>(a.q) + (tok0 + q0) * ldq + pr * 2 * a.hd;
-    const T* const gt = reinterpret_cast<const T*>(a.da) + (tok0 + q0) * ldq + pr * 2 * a.hd;
-    Rows32 r;
-    r.init(c, h, len - 1 - q0, (unsigned)ldq);
-    const float4* const mine = own + opaque(lane);
-    const float* const lse = a.lse + (long long)(b * a.hp + pr) * 2 * a.ls;
-    const float* const dsm = a.dsum + (long long)(b * a.hp + pr) * 2 * a.ls;
-    f32x16 dp, s[2], w;
-    float sl[16], sd[16];
-    Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
-    zero16(dp);
-    zero16(s[0]);
-    zero16(s[1]);
-    auto fetch = [&](auto gc, int j) __attribute__((always_inline)) {
-      constexpr int g = decltype(gc)::value, y = g % (AHEAD + 1);
-      if constexpr (g < N0) {
-        const unsigned col = first_if_past(g * 16 + h * 8, 2 * a.hd);
-        read_row(fa[y], j, gt, r.row + col);
-        read_own(fb[y], j - 2, mine, g);
-      } else if constexpr (g < N0 + N1) {
-        const int m = (g - N0) / KS;
-        const unsigned col = first_if_past((g - N0) % KS * 16 + h * 8, a.hd);
-        read_row(fa[y], j, qt + m * a.hd, r.row + col);
-        read_own(fb[y], j - 2, mine, g);
-      } else if constexpr (g < N0 + N1 + N2) {
-        constexpr int z = g - N0 - N1;
-        read_col(fa[y], j, gt, r, z / NT, last_if_past(z % NT * 32 + c, 2 * a.hd));
-      } else if constexpr (g < NG) {
-        constexpr int z = g - N0 - N1 - N2;
-        read_col(fa[y], j, qt + z / (2 * DT) * a.hd, r, z / DT % 2, last_if_past(z % DT * 32 + c, a.hd));
-      }
-    };
-    each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
-    each<NG>([&](auto gc) __attribute__((always_inline)) {
-      constexpr int g = decltype(gc)::value, y = g % (AHEAD + 1);
-      if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == 0) {
-        constexpr int m = (g - N0) / KS;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3), at = m * a.ls + (q < len ? q : len);   // past the end: weights 0
-          sl[i] = lse[at];
-          sd[i] = dsm[at];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        fetch(std::integral_constant<int, g + AHEAD>{}, j);
-        if constexpr (g < N0) {
-          mma1(dp, fa[y], fb[y].v[j], j);
-        } else if constexpr (g < N0 + N1) {
-          mma1(s[(g - N0) / KS], fa[y], fb[y].v[j], j);
-        } else if constexpr (g < N0 + N1 + N2) {
-          constexpr int z = g - N0 - N1;
-          mma1(dv[z % NT], fa[y], w[8 * (z / NT) + j], j);
-        } else {
-          constexpr int z = g - N0 - N1 - N2, m = z / (2 * DT);
-          mma1(dk[m][z % DT], fa[y], s[m][8 * (z / DT % 2) + j], j);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (g >= N0 && g < N0 + N1 && (g - N0) % KS == KS - 1) {
-        constexpr int m = (g - N0) / KS;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3);
-          const float p = a.causal && key > q ? 0.f : fast_exp2(fmaf(s[m][i], sc, -sl[i]));
-          w[i] = m ? w[i] - lam * p : p;
-          s[m][i] = p * (dp[i] - sd[i]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-  }
-  add_waves(dv, sm, wave, lane);
-  add_waves(dk[0], sm, wave, lane);
-  add_waves(dk[1], sm, wave, lane);
-  if (wave != 3 || key >= a.L) return;
-  const long long poff = (long long)hpart * a.B * a.L * ldk + koff;
-  T* dkp = (a.split > 1 ? a.dk_part + poff : reinterpret_cast<T*>(a.dk) + koff);
-  T* dvp = (a.split > 1 ? a.dv_part + poff : reinterpret_cast<T*>(a.dv) + koff);
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int d = 32 * t + 2 * i + 4 * h;
-      if (d < 2 * a.hd) store4<T>(dvp + d, kok ? dv[t][i] : 0.f, kok ? dv[t][i + 1] : 0.f, kok ? dv[t][i + 2] : 0.f, kok ? dv[t][i + 3] : 0.f);
-    }
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float f = kok ? (m ? -lam * a.scale : a.scale) : 0.f;
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int d = 32 * t + 2 * i + 4 * h;
-        if (d < a.hd)
-          store4<T>(dkp + m * a.hd + d, dk[m][t][i] * f, dk[m][t][i + 1] * f, dk[m][t][i + 2] * f, dk[m][t][i + 3] * f);
-      }
-  }
-}
-
-void launch_diff_bwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
-  const long long rows = (long long)a.B * a.L * a.hp;
+void launch_diff_bwd_bf16(const DiffArgs& a, hipStream_t s) {
   auto blocks = [&](int rows) { return (a.L + rows - 1) / rows * a.B; };
-  if (dt == SL_F32) hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (dt == SL_BF16) {
-      const dim3 dq((unsigned)(blocks(a.dq_rows) * a.hp)), dkv((unsigned)(blocks(a.dkv_rows) * a.gp * a.split + 1));
-      if (a.dq_rows == 64) hipLaunchKernelGGL((diff_dq_lds<D, 2>), dq, dim3(256), 0, s, a);
-      else hipLaunchKernelGGL((diff_dq_lds<D, 1>), dq, dim3(256), 0, s, a);
-      if (a.dkv_rows == 64) hipLaunchKernelGGL((diff_dkv_lds<D, 2>), dkv, dim3(256), 0, s, a);
-      else hipLaunchKernelGGL((diff_dkv_lds<D, 1>), dkv, dim3(256), 0, s, a);
-    } else {
-      hipLaunchKernelGGL(diff_dq_direct<D>, dim3((unsigned)(blocks(32) * a.hp)), dim3(256), 0, s, a);
-      hipLaunchKernelGGL(diff_dkv_direct<D>, dim3((unsigned)(blocks(32) * a.gp * a.split + 1)), dim3(256), 0, s, a);
-    }
+    const dim3 dq((unsigned)(blocks(a.dq_rows) * a.hp)), dkv((unsigned)(blocks(a.dkv_rows) * a.gp * a.split + 1));
+    if (a.dq_rows == 64) hipLaunchKernelGGL((diff_dq_lds<D, 2>), dq, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((diff_dq_lds<D, 1>), dq, dim3(256), 0, s, a);
+    if (a.dkv_rows == 64) hipLaunchKernelGGL((diff_dkv_lds<D, 2>), dkv, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((diff_dkv_lds<D, 1>), dkv, dim3(256), 0, s, a);
   });
   if (a.split > 1) {
     const long long n = 2 * ((long long)a.B * a.L * a.gp * 2 * a.hd / 4);
-    const dim3 grid((unsigned)((n + 255) / 256));
-    if (dt == SL_BF16) hipLaunchKernelGGL(diff_dkv_sum<bf16>, grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(diff_dkv_sum<float>, grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL(diff_dkv_sum<bf16>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
   }
 }
 

@@ -365,182 +365,12 @@ __global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// fp32: operands straight from memory.  The fp32 matrix instructions run at a
-// sixteenth of the bf16 rate, so L1 and L2 feed them (2 bytes per cycle and wave
-// at full rate) and LDS would only add waits.  A workgroup owns 32 queries; its
-// four waves take every fourth key tile, each with a running maximum and sum,
-// and the results are joined in order through LDS (short rows and few heads then
-// still fill the GPU).  The transposed score tile (keys x queries) leaves a query
-// in a lane pair, so the softmax needs one exchange per tile and its weights
-// feed the second product from registers.
-template <int D>
-__global__ void __launch_bounds__(256, 1) diff_fwd_direct(const DiffArgs a) {
-  using T = float;
-  constexpr int NT = D / 16;   // 32-value tiles of the 2 D wide output
-  const int lane = threadIdx.x & 63, h = lane >> 5, c = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  __shared__ __attribute__((aligned(16))) float sm[NT * 1024];
-  __shared__ float smx[2][4][64], ssum[2][4][64];
-  __shared__ float4 own[2 * (D / 16) * 128];
-  const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);   // the longest rows first
-  const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
-  const int g = pair / (a.hp / a.gp), len = a.lens[b];
-  float e1, e2;
-  const float lam = lambda_of(a, e1, e2);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.lam[0] = lam;
-    a.lam[1] = e1;
-    a.lam[2] = e2;
-  }
-  const int row = qb * 32 + c;
-  const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
-  const T* qp = reinterpret_cast<const T*>(a.q) + (tok0 + qb * 32) * ldq + pair * 2 * a.hd;
-  const T* kp = reinterpret_cast<const T*>(a.k) + tok0 * ldk + g * 2 * a.hd;
-  const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * ldk + g * 2 * a.hd;
-  const bool rok = row < len;
-  f32x16 o[2][NT];
-  float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) zero16(o[m][t]);
-  const float sc = a.scale * kLog2e;
-  int kend = len;
-  if (a.causal && kend > qb * 32 + 32) kend = qb * 32 + 32;
-  if (qb * 32 >= len) kend = 0;
-  for (int m = 0; m < 2 && kend > 0; ++m)                // (a row past the end: any)
-    put_own(own + m * (D / 16) * 128, D / 16, qp + (rok ? c : 0) * ldq + m * a.hd, a.hd, wave, lane);
-  __syncthreads();
-  // products over the columns (S_1, S_2), then over the keys; an operand is read
-  // AHEAD groups of 8 matrix instructions before its use
-  constexpr int KS = D / 16, N1 = 2 * KS, NG = N1 + 2 * NT, AHEAD = 2;
-  for (int k0 = 32 * wave; k0 < kend; k0 += 128) {
-    const T* const kt = kp + (long long)k0 * ldk;
-    const T* const vt = vp + (long long)k0 * ldk;
-    Rows32 r;
-    r.init(c, h, len - 1 - k0, (unsigned)ldk);
-    const float4* const mine = own + opaque(lane);
-    f32x16 s[2];
-    Frag<T> fa[AHEAD + 1], fb[AHEAD + 1];
-    zero16(s[0]);
-    zero16(s[1]);
-    auto fetch = [&](auto gc, int j) __attribute__((always_inline)) {
-      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-      if constexpr (g < N1) {
-        const int m = g / KS;
-        const unsigned col = first_if_past(g % KS * 16 + h * 8, a.hd);
-        read_row(fa[x], j, kt + m * a.hd, r.row + col);
-        read_own(fb[x], j - 2, mine, g);
-      } else if constexpr (g < NG) {
-        read_col(fa[x], j, vt, r, (g - N1) / NT, last_if_past((g - N1) % NT * 32 + c, 2 * a.hd));
-      }
-    };
-    each<8 * AHEAD>([&](auto i) __attribute__((always_inline)) { fetch(std::integral_constant<int, decltype(i)::value / 8>{}, decltype(i)::value % 8); });
-    each<NG>([&](auto gc) __attribute__((always_inline)) {
-      constexpr int g = decltype(gc)::value, x = g % (AHEAD + 1);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        fetch(std::integral_constant<int, g + AHEAD>{}, j);
-        if constexpr (g < N1) {
-          mma1(s[g / KS], fa[x], fb[x].v[j], j);
-        } else {
-          constexpr int cc = (g - N1) / NT, t = (g - N1) % NT;
-          mma1(o[0][t], fa[x], s[0][8 * cc + j], j);
-          mma1(o[1][t], fa[x], s[1][8 * cc + j], j);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (g < N1 && g % KS == KS - 1) {
-        constexpr int m = g / KS;
-        float tm = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = k0 + 8 * (i >> 2) + 4 * h + (i & 3);
-          if (key >= len || (a.causal && key > row)) s[m][i] = -INFINITY;
-          tm = fmaxf(tm, s[m][i]);
-        }
-        tm = fmaxf(tm, __shfl_xor(tm, 32));
-        const float nm = fmaxf(mx[m], tm);
-        const float ms = nm == -INFINITY ? 0.f : nm * sc;   // nothing seen yet: weights 0
-        const float f = fast_exp2(mx[m] * sc - ms);
-        float ts = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[m][i] = fast_exp2(fmaf(s[m][i], sc, -ms));
-          ts += s[m][i];
-        }
-        sum[m] = sum[m] * f + ts;
-        mx[m] = nm;
-        if (__any(f != 1.f)) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-  }
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    smx[m][wave][lane] = mx[m];
-    ssum[m][wave][lane] = sum[m];
-  }
-  __syncthreads();
-  float inv[2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    float top = smx[m][0][lane], l = 0.f;
-#pragma unroll
-    for (int w = 1; w < 4; ++w) top = fmaxf(top, smx[m][w][lane]);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float x = smx[m][w][lane];
-      if (x > -INFINITY) l = fmaf(exp2f((x - top) * sc), ssum[m][w][lane], l);   // else it saw no key
-    }
-    const float f = mx[m] > -INFINITY ? exp2f((mx[m] - top) * sc) : 0.f;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[m][t][i] *= f;
-    l += __shfl_xor(l, 32);
-    inv[m] = rok ? 1.f / l : 0.f;
-    if (wave == 0 && h == 0 && row < a.L) {
-      float* const at = a.lse + ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
-      *at = rok ? top * sc + log2f(l) : INFINITY;
-      if (row == a.L - 1) at[1] = INFINITY;
-    }
-    add_waves(o[m], sm, wave, lane);
-  }
-  if (wave != 3 || row >= a.L) return;
-  const long long orow = (tok0 + row) * ldq + pair * 2 * a.hd;
-  T* op = reinterpret_cast<T*>(a.o) + orow;
-  T* o2p = reinterpret_cast<T*>(a.o2) + orow;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int dv = 32 * t + 2 * i + 4 * h;
-      if (dv >= 2 * a.hd) continue;
-      float x[4], y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = rok ? o[1][t][i + e] * inv[1] : 0.f;
-        x[e] = rok ? o[0][t][i + e] * inv[0] - lam * y[e] : 0.f;
-      }
-      store4<T>(op + dv, x[0], x[1], x[2], x[3]);
-      store4<T>(o2p + dv, y[0], y[1], y[2], y[3]);
-    }
-}
-
-void launch_diff_fwd(sl_dtype dt, const DiffArgs& a, hipStream_t s) {
+void launch_diff_fwd_bf16(const DiffArgs& a, hipStream_t s) {
   const int n = a.hp * a.B;
   auto grid = [&](int rows) { return dim3((unsigned)((a.L + rows - 1) / rows * n)); };
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (dt != SL_BF16) hipLaunchKernelGGL(diff_fwd_direct<D>, grid(32), dim3(256), 0, s, a);
-    else if (a.causal ? grid(128).x >= 512 : grid(64).x > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
+    if (a.causal ? grid(128).x >= 512 : grid(64).x > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
     else hipLaunchKernelGGL((diff_fwd_lds<D, 2>), grid(64), dim3(256), 0, s, a);
   });
 }
