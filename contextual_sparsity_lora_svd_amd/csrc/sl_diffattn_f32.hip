@@ -201,7 +201,11 @@ __global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
   }
   d1 = wave_sum(d1);
   d2 = wave_sum(d2);
-  if (lane < 2) a.dsum[((long long)(b * a.hp + pair) * 2 + lane) * a.ls + row] = lane ? d2 : d1;
+  if (lane < 2) {
+    float* const at = a.dsum + ((long long)(b * a.hp + pair) * 2 + lane) * a.ls + row;
+    *at = lane ? d2 : d1;
+    if (row == a.L - 1) at[1] = 0.f;
+  }
 }
 
 // dQ: 32 queries per workgroup, every fourth key tile per wave.  The sum of P_2 dP

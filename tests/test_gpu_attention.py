@@ -415,3 +415,71 @@ def test_outputs_that_are_inputs_are_refused():
     for out in ({"dq": d["da"]}, {"dk": d["k"]}, {"dq": g["dk"], "dk": g["dk"]}):
         with pytest.raises(sl.SparseLoraError):
             sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a, lay, buf, d["da"], out=out)
+
+
+@pytest.mark.parametrize("case", [(2, 97, 4, 2, 64, True, None), (1, 70, 8, 2, 24, False, [65]), (1, 600, 8, 2, 32, True, None)],
+                         ids=lambda c: "x".join(map(str, c[:6])))
+def test_fp32_results_do_not_depend_on_what_the_buffers_held(case):
+    sl = _sl()
+    x, lv = _diff_inputs(case, "f32", seed=4)
+    p, d, lay, a, g, _ = _run_diff(sl, case, "f32", x, lv, pad=0.0)
+    buf = sl.DiffAttnWorkspace(p, lay, torch.float32, "cuda", lens=case[6])
+    for t in (buf.saved, buf.ws):
+        t.fill_(0xFF)
+    a2, _ = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], lay, buf=buf)
+    buf.ws.fill_(0xFF)
+    g2 = sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a2, lay, buf, d["da"])
+    assert torch.equal(a, a2)
+    for n in g:
+        assert torch.equal(g[n], g2[n]), n
+    _check_diff(case, "f32", x, lv, a, g)
+
+
+@pytest.mark.parametrize("case", MANY[3:5] + MANY[8:11], ids=lambda c: "x".join(map(str, c[:6])))
+def test_diff_attention_many_heads_fp32(case):
+    test_diff_attention(case, "f32")
+
+
+def test_fp32_scores_that_outgrow_the_first_tile():
+    sl = _sl()
+    case = (1, 150, 4, 2, 64, True, None)
+    x, lv = _diff_inputs(case, "f32", seed=12)
+    x["q"][:] = 2.0
+    x["k"][:] = (np.arange(150)[:, None] // 40) * 4.0 + 0.125 * x["k"]
+    _, _, _, a, g, _ = _run_diff(sl, case, "f32", x, lv)
+    _check_diff(case, "f32", x, lv, a, g)
+
+
+def test_two_graphs_with_their_own_buffers():
+    """Two captured steps with buffers of their own, replayed in turn and at once
+    on two streams, give what the eager calls give."""
+    sl = _sl()
+    cases = [(2, 70, 4, 2, 64, True, [70, 50]), (1, 190, 4, 4, 32, False, None)]
+    made, alive = [], []                # a graph reads the tensors it was captured with
+    for c in cases:
+        x, lv = _diff_inputs(c, "bf16", seed=6)
+        p, d, lay, a, g, _ = _run_diff(sl, c, "bf16", x, lv, pad=0.0)
+        buf = sl.DiffAttnWorkspace(p, lay, torch.bfloat16, "cuda", lens=c[6])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            a2, _ = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], lay, buf=buf)
+            g2 = sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a2, lay, buf, d["da"])
+        made.append((graph, a, g, a2, g2))
+        alive.append((p, d, buf))
+    streams = [torch.cuda.Stream() for _ in made]
+    for together in (False, True, True):
+        for s, (graph, a, g, a2, g2) in zip(streams, made):
+            a2.fill_(float("nan"))
+            torch.cuda.synchronize()
+            if not together:
+                graph.replay()
+        if together:
+            for s, m in zip(streams, made):
+                with torch.cuda.stream(s):
+                    m[0].replay()
+        torch.cuda.synchronize()
+        for _, a, g, a2, g2 in made:
+            assert torch.equal(a, a2)
+            for n in g:
+                assert torch.equal(g[n], g2[n]), n
