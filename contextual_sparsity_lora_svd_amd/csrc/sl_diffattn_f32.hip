@@ -176,39 +176,9 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_direct(const DiffArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// fp32: D_1 = dO . (O + lambda O_2), D_2 = dO . O_2, one wave per row and head pair.
-__global__ void __launch_bounds__(256) diff_dsum(const DiffArgs a) {
-  using T = float;
-  const int lane = threadIdx.x & 63;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const long long rows = (long long)a.B * a.L;
-  if (w >= rows * a.hp) return;
-  const int pair = (int)(w % a.hp);
-  const long long tok = w / a.hp;
-  const int b = (int)(tok / a.L), row = (int)(tok % a.L);
-  const float lam = a.lam[0];
-  float d1 = 0.f, d2 = 0.f;
-  if (row < a.lens[b]) {
-    const long long at = (tok * a.hp + pair) * 2 * a.hd;
-    const T* dop = reinterpret_cast<const T*>(a.da) + at;
-    const T* op = reinterpret_cast<const T*>(a.a) + at;
-    const T* o2p = reinterpret_cast<const T*>(a.o2) + at;
-    for (int i = lane; i < 2 * a.hd; i += 64) {
-      const float g = ldv(dop, i), y = ldv(o2p, i);
-      d1 = fmaf(g, ldv(op, i) + lam * y, d1);
-      d2 = fmaf(g, y, d2);
-    }
-  }
-  d1 = wave_sum(d1);
-  d2 = wave_sum(d2);
-  if (lane < 2) {
-    float* const at = a.dsum + ((long long)(b * a.hp + pair) * 2 + lane) * a.ls + row;
-    *at = lane ? d2 : d1;
-    if (row == a.L - 1) at[1] = 0.f;
-  }
-}
-
-// dQ: 32 queries per workgroup, every fourth key tile per wave.  The sum of P_2 dP
+// dQ: 32 queries per workgroup, every fourth key tile per wave.  D_1 = dO . (O +
+// lambda O_2) and D_2 = dO . O_2 of the rows come first (a launch of their own took
+// 4 us at 2 x 64 tokens); dK and dV read them from memory.  The sum of P_2 dP
 // is -dlambda.
 template <int D>
 __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
@@ -218,6 +188,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   __shared__ __attribute__((aligned(16))) float sm[DT * 1024];
   __shared__ float4 own[(D / 4) * 128];
+  __shared__ float sds[2][4][32];
   const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);
   const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
   const int g = pair / (a.hp / a.gp), len = a.lens[b];
@@ -236,7 +207,36 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   for (int m = 0; m < 2; ++m) {
     const long long at = ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
     lse[m] = rok ? a.lse[at] : INFINITY;
-    ds[m] = rok ? a.dsum[at] : 0.f;
+    ds[m] = 0.f;
+  }
+  if (rok) {                       // every eighth chunk of 4 columns
+    const T* op = reinterpret_cast<const T*>(a.a) + qoff;
+    const T* o2p = reinterpret_cast<const T*>(a.o2) + qoff;
+    const T* gp = reinterpret_cast<const T*>(a.da) + qoff;
+    for (int i = 4 * (2 * wave + h); i < 2 * a.hd; i += 32) {
+      const float4 g4 = *reinterpret_cast<const float4*>(gp + i), o4 = *reinterpret_cast<const float4*>(op + i);
+      const float4 y4 = *reinterpret_cast<const float4*>(o2p + i);
+      ds[0] = fmaf(g4.x, fmaf(lam, y4.x, o4.x), ds[0]);
+      ds[0] = fmaf(g4.y, fmaf(lam, y4.y, o4.y), ds[0]);
+      ds[0] = fmaf(g4.z, fmaf(lam, y4.z, o4.z), ds[0]);
+      ds[0] = fmaf(g4.w, fmaf(lam, y4.w, o4.w), ds[0]);
+      ds[1] = fmaf(g4.x, y4.x, fmaf(g4.y, y4.y, fmaf(g4.z, y4.z, fmaf(g4.w, y4.w, ds[1]))));
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    ds[m] += __shfl_xor(ds[m], 32);
+    if (h == 0) sds[m][wave][c] = ds[m];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    ds[m] = ((sds[m][0][c] + sds[m][1][c]) + sds[m][2][c]) + sds[m][3][c];
+    if (wave == 0 && h == 0 && row < a.L) {
+      float* const at = a.dsum + ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
+      *at = ds[m];
+      if (row == a.L - 1) at[1] = 0.f;
+    }
   }
   f32x16 dq[2][DT];
 #pragma unroll
@@ -490,9 +490,7 @@ void launch_diff_fwd_f32(const DiffArgs& a, hipStream_t s) {
 }
 
 void launch_diff_bwd_f32(const DiffArgs& a, hipStream_t s) {
-  const long long rows = (long long)a.B * a.L * a.hp;
   const int blocks = (a.L + 31) / 32 * a.B;
-  hipLaunchKernelGGL(diff_dsum, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
     hipLaunchKernelGGL(diff_dq_direct<D>, dim3((unsigned)(blocks * a.hp)), dim3(256), 0, s, a);
