@@ -8,6 +8,7 @@ namespace sl {
 struct DiffPlan {
   size_t lse, lam, fix, rsc, o2, res, saved;    // offsets and size of the saved buffer
   size_t dsum, dlam, part, ws;             // of the workspace
+  int split;
   long long part_elems;                    // of one part of dK or dV
 };
 
@@ -21,28 +22,23 @@ struct DiffPlan {
 // 8 kv (64 workgroups of 128) 64 / 47 and 73 / 55 us; causal 1 x 2048 of 8 (64)
 // 112 / 72 and 125 / 84, 1 x 4096 of 16 (256) 221 / 185 and 249 / 207, but 2 x 1024
 // of 32 (256) 76 / 75 and 81 / 86, 1 x 4096 of 32 (512) 345 / 400 and 388 / 455.
-struct DiffGrid {
-  int dq_rows, dkv_rows, split;
-};
-static DiffGrid diff_grid(sl_dtype dt, int B, int L, int hp, int gp, bool causal) {
-  auto blocks = [&](int rows) { return (long long)((L + rows - 1) / rows) * B; };
-  auto rows = [&](int n) {       // n workgroups per block of rows
-    return blocks(64) * n <= 256 || (causal && blocks(128) * n < (L > 1024 ? 512 : 256)) ? 64 : 128;
-  };
-  const bool f32 = dt == SL_F32;
-  DiffGrid g;
-  g.dq_rows = f32 ? 32 : rows(hp);
-  // parts that a kv group's heads are cut into, while there are fewer workgroups
-  // than two rounds of 256; short loops are not worth the launch that adds them
-  const int grp = hp / gp;
-  g.split = 1;
-  if (grp * ((L + 31) / 32) > 16)
-    while (g.split < grp && blocks(f32 ? 32 : 128) * gp * g.split < 512) {
-      ++g.split;
-      while (grp % g.split) ++g.split;
-    }
-  g.dkv_rows = f32 ? 32 : rows(gp * g.split);
-  return g;
+static int bwd_rows(const DiffArgs& a, int n) {   // n workgroups per block of rows
+  return filled(a, 64) * n <= 256 || (a.causal && filled(a, 128) * n < (a.L > 1024 ? 512 : 256)) ? 64 : 128;
+}
+
+// Parts that a kv group's heads are cut into for dK and dV, while there are fewer
+// workgroups than two rounds of 256; short loops are not worth the launch that
+// adds them.
+static int dkv_split(sl_dtype dt, int B, int L, int hp, int gp) {
+  const int rows = dt == SL_F32 ? 32 : 128, grp = hp / gp;
+  const long long n = (long long)((L + rows - 1) / rows) * B * gp;
+  int s = 1;
+  if (grp * ((L + 31) / 32) <= 16) return s;
+  while (s < grp && n * s < 512) {
+    ++s;
+    while (grp % s) ++s;
+  }
+  return s;
 }
 
 static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs, DiffPlan& pl) {
@@ -71,9 +67,9 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   pl.dsum = w.take(stats * 4);
   // a partial sum of dlambda per wave, 4 to a workgroup of 32 rows or more
   pl.dlam = w.take(4 * (size_t)((lay->seq_len + 31) / 32) * lay->batch * (hq / 2) * 8);
-  const int split = diff_grid(dt, lay->batch, lay->seq_len, hq / 2, hkv / 2, false).split;
+  pl.split = dkv_split(dt, lay->batch, lay->seq_len, hq / 2, hkv / 2);
   pl.part_elems = T * hkv * hd;
-  pl.part = w.take(split > 1 ? 2 * (size_t)split * pl.part_elems * 4 : 0);
+  pl.part = w.take(pl.split > 1 ? 2 * (size_t)pl.split * pl.part_elems * 4 : 0);
   pl.ws = w.off;
   return SL_OK;
 }
@@ -98,6 +94,7 @@ static sl_status diff_args(DiffArgs& a, const sl_layout* lay, const sl_diff_attn
   for (int b = 0; b < a.B; ++b) {
     a.lens[b] = p->lens ? p->lens[b] : a.L;
     if (a.lens[b] < 0 || a.lens[b] > a.L) SL_FAIL(SL_ERR_RANGE, "lens[%d] = %d outside [0, %d]", b, a.lens[b], a.L);
+    if (a.lens[b] != a.lens[0]) a.mix = 1;
   }
   return SL_OK;
 }
@@ -177,13 +174,12 @@ extern "C" sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const s
   saved_args(a, pl, const_cast<void*>(saved));
   a.dsum = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.dsum);
   a.dlam_part = reinterpret_cast<double*>(reinterpret_cast<char*>(ws) + pl.dlam);
-  const DiffGrid grid = diff_grid(dt, a.B, a.L, a.hp, a.gp, a.causal);
-  a.split = grid.split;
-  a.dq_rows = grid.dq_rows;
-  a.dkv_rows = grid.dkv_rows;
-  a.npart = 4 * ((a.L + grid.dq_rows - 1) / grid.dq_rows) * a.B * a.hp;
+  a.split = pl.split;
+  a.dq_rows = dt == SL_F32 ? 32 : bwd_rows(a, a.hp);
+  a.dkv_rows = dt == SL_F32 ? 32 : bwd_rows(a, a.gp * a.split);
+  a.npart = 4 * ((a.L + a.dq_rows - 1) / a.dq_rows) * a.B * a.hp;
   a.dk_part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.part);
-  a.dv_part = a.dk_part + grid.split * pl.part_elems;
+  a.dv_part = a.dk_part + pl.split * pl.part_elems;
   a.dlq1 = g->dlq1; a.dlk1 = g->dlk1; a.dlq2 = g->dlq2; a.dlk2 = g->dlk2;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dt == SL_BF16) launch_diff_bwd_bf16(a, s);

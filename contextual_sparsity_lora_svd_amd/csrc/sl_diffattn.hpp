@@ -41,7 +41,7 @@ struct DiffArgs {
   float lambda_init, scale;
   int B, L, hp, gp, hd;      // hp query pairs, gp kv pairs
   int ls;                    // L + 1: statistics of one row more than there are, past every length
-  int causal, npart, split;
+  int causal, mix, npart, split;   // mix: the sequences' lengths differ
   int dq_rows, dkv_rows;     // bf16: rows, or keys, of a workgroup
   int lens[SL_MAX_SEQS];
 };
@@ -245,6 +245,13 @@ template <typename T> __global__ void __launch_bounds__(256) diff_dkv_sum(const 
     x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
   }
   store4<T>(reinterpret_cast<T*>(v ? a.dv : a.dk) + 4 * i, x.x, x.y, x.z, x.w);
+}
+
+// Blocks of `rows` rows that hold any of a sequence.
+inline long long filled(const DiffArgs& a, int rows) {
+  long long n = 0;
+  for (int b = 0; b < a.B; ++b) n += (a.lens[b] + rows - 1) / rows;
+  return n;
 }
 
 // Enqueue the forward, and the backward, of one type on s.

@@ -15,7 +15,7 @@ namespace sl {
 // 8 kv heads of 128: dQ's error 1.5 to 1.1 times that of its own rounding to bf16).
 // H = 1: four row blocks to a workgroup, tiles loaded two ahead.  H = 2: two row
 // blocks, each with two waves that take every other tile and add their sums in the
-// end (where each kind pays: DiffGrid).
+// end (where each kind pays: bwd_rows).
 // Bound by what its one wave per SIMD can issue (55 % of its cycles; 27 % wait for
 // loads and barriers): 1 x 2048 tokens, 32 heads, 8 kv, of 128, 146 us, 706 TFLOP/s
 // of scores, dP and dQ (dS counted once).
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
   const int rb = wave / H, half = wave % H;               // block of 32 rows, every H-th key tile
   const int nqb = (a.L + ROWS - 1) / ROWS;
   int blk, pair, b;
-  locate(blockIdx.x, a.hp * a.B, a.hp, blk, pair, b);
+  locate(blockIdx.x, a.B, a.hp, a.hp / a.gp, a.mix, blk, pair, b);
   const int q0 = (nqb - 1 - blk) * ROWS, len = a.lens[b], g = pair / (a.hp / a.gp);
   const int row0 = q0 + rb * 32, row = row0 + c;
   const long long ldq = (long long)a.hp * 2 * a.hd, ldk = (long long)a.gp * 2 * a.hd, tok0 = (long long)b * a.L;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rb = wave / H, half = wave % H;                     // block of 32 keys, every H-th query tile
   int blk, gs, b;
-  locate(blockIdx.x, a.gp * a.split * a.B, a.gp * a.split, blk, gs, b);
+  locate(blockIdx.x, a.B, a.gp * a.split, a.split, a.mix, blk, gs, b);
   const int g = gs / a.split, part = gs % a.split;
   const int grp = a.hp / a.gp, nh = grp / a.split, len = a.lens[b];
   const int k0 = blk * 32 * NB, key = k0 + rb * 32 + c;              // causal: the first keys have the most queries

@@ -3,6 +3,16 @@
 
 namespace sl {
 
+// Block -> (row block, head pair or part, sequence); where lengths differ each row
+// block starts one further, since workgroups go round the XCDs.
+__device__ inline void place(int bid, const DiffArgs& a, int units, int& blk, int& unit, int& b) {
+  const int n = units * a.B;
+  blk = bid / n;
+  const int u = (bid % n + (a.mix ? blk : 0)) % n;
+  unit = u / a.B;
+  b = u % a.B;
+}
+
 // ---------------------------------------------------------------------------
 // The fp32 matrix instructions run at a sixteenth of the bf16 rate, so L1 and L2
 // feed the walked tiles directly, each operand read two groups of 8 instructions
@@ -31,8 +41,10 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_direct(const DiffArgs a) {
   __shared__ float smx[2][4][64], ssum[2][4][64];
   __shared__ float4 own[2 * (D / 16) * 128];
   const int m = wave >> 2, kq = wave & 3;               // map, key tiles
-  const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);   // the longest rows first
-  const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
+  const int nqb = (a.L + 31) / 32;
+  int blk, pair, b;
+  place(blockIdx.x, a, a.hp, blk, pair, b);
+  const int qb = nqb - 1 - blk;                         // the longest rows first
   const int g = pair / (a.hp / a.gp), len = a.lens[b];
   float e1, e2;
   const float lam = lambda_of(a, e1, e2);
@@ -189,8 +201,10 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   __shared__ __attribute__((aligned(16))) float sm[DT * 1024];
   __shared__ float4 own[(D / 4) * 128];
   __shared__ float sds[2][4][32];
-  const int nqb = (a.L + 31) / 32, qb = nqb - 1 - (int)blockIdx.x / (a.hp * a.B);
-  const int pair = blockIdx.x / a.B % a.hp, b = blockIdx.x % a.B;
+  const int nqb = (a.L + 31) / 32;
+  int blk, pair, b;
+  place(blockIdx.x, a, a.hp, blk, pair, b);
+  const int qb = nqb - 1 - blk;
   const int g = pair / (a.hp / a.gp), len = a.lens[b];
   const float lam = a.lam[0];
   const int row = qb * 32 + c;
@@ -350,8 +364,9 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
     dlambda_block(a, reinterpret_cast<double*>(sm));
     return;
   }
-  const int n = a.gp * a.split * a.B, kb = blockIdx.x / n;      // causal: the first keys have the most queries
-  const int gs = blockIdx.x % n / a.B, b = blockIdx.x % a.B, g = gs / a.split, hpart = gs % a.split;
+  int kb, gs, b;
+  place(blockIdx.x, a, a.gp * a.split, kb, gs, b);    // causal: the first keys have the most queries
+  const int g = gs / a.split, hpart = gs % a.split;
   const int grp = a.hp / a.gp, len = a.lens[b];
   const float lam = a.lam[0];
   const int key = kb * 32 + c;

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
   const int m = wave / RB, rb = wave % RB;                // map, block of 32 rows
   const int nqb = (a.L + ROWS - 1) / ROWS;
   int blk, pair, b;
-  locate(blockIdx.x, a.hp * a.B, a.hp, blk, pair, b);
+  locate(blockIdx.x, a.B, a.hp, a.hp / a.gp, a.mix, blk, pair, b);
   // the longest rows first; with two workgroups to a CU, the second half of the
   // blocks the other way round
   if (RB == 2 && 2 * blk >= nqb) blk = nqb - 1 - (blk - (nqb + 1) / 2);
@@ -374,7 +374,7 @@ void launch_diff_fwd_bf16(const DiffArgs& a, hipStream_t s) {
   auto grid = [&](int rows) { return dim3((unsigned)((a.L + rows - 1) / rows * n)); };
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (a.causal ? grid(128).x >= 512 : grid(64).x > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
+    if (a.causal ? filled(a, 128) * a.hp >= 512 : filled(a, 64) * a.hp > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
     else hipLaunchKernelGGL((diff_fwd_lds<D, 2>), grid(64), dim3(256), 0, s, a);
   });
 }

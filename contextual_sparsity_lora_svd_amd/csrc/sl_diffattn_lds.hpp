@@ -131,13 +131,16 @@ __device__ inline float pair_sum(float x) {
 }
 
 // Block -> (row block, head pair, sequence): the longest causal rows first, and
-// the pairs of a kv group on one XCD (blocks go round the 8 XCDs), whose L2
-// then holds the group's K and V.
-__device__ inline void locate(int bid, int n, int hp, int& blk, int& pair, int& b) {
+// the pairs of a kv group (`grp` of `hp`) on one XCD (blocks go round the 8 XCDs),
+// whose L2 then holds the group's K and V.  Where lengths differ (`mix`) each row
+// block starts one XCD further, so that none has the long sequences alone (4 x 777
+// tokens, lengths 777 to 0: forward 33 -> 28 us, dQ 41 -> 31).
+__device__ inline void locate(int bid, int B, int hp, int grp, bool mix, int& blk, int& pair, int& b) {
+  const int n = hp * B;
   blk = bid / n;
-  const int u = xcd_remap(bid % n, n);
-  b = u / hp;
-  pair = u % hp;
+  const int u = xcd_remap((bid % n + (mix ? blk : 0)) % n, n), v = u / grp;
+  b = v % B;
+  pair = v / B * grp + u % grp;
 }
 
 // Two values rounded to bf16 (to nearest even), the first in the low half; and
