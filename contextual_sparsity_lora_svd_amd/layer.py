@@ -366,7 +366,9 @@ class DiffAttention(torch.nn.Module):
     ``lens`` (valid rows per sequence) and ``pos`` [T] int32 go with each call.
     Padding rows of q, k and v have no gradient and may hold anything, but
     finite values under ``qk_norm``, whose weights' gradients sum over every row
-    (0 times what the padding holds)."""
+    (0 times what the padding holds).  A backward pass captured into a graph
+    needs every eager result of the same parameters dropped before: torch joins
+    the streams of both where their gradients meet, which a capture forbids."""
 
     def __init__(self, heads: Sequence[int], lambda_init: float = 0.8, causal: bool = True,
                  scale: Optional[float] = None, rot: Optional[sl.Rotary] = None, qk_norm: bool = False,
