@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
     r = r < len ? r : len;                                      // lse there is +inf: weights 0
     const float* sb = reinterpret_cast<const float*>(uniform(sbase + (long long)it_pr * 2 * a.ls));
     const unsigned sd = __builtin_amdgcn_readfirstlane(lds_addr(ss) + (unsigned)((it & 1) * STAT + wave * 256));
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, %2"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, %2"
                  :: "v"((unsigned)r * 4u), "s"(sd), "s"(sb) : "memory", "m0");
   };
   auto issued = [&]() __attribute__((always_inline)) {

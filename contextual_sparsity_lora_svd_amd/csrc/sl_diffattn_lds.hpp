@@ -55,8 +55,10 @@ __device__ inline unsigned lds_addr(const unsigned char* p) {
 }
 
 // 64 chunks of 16 bytes from base + off (per lane) to LDS at dst (uniform), in lane order.
+// (A load to LDS may read m0 one wait state after it was written, and the compiler
+// adds none inside an asm string: the s_nop.)
 __device__ inline void dma16(const void* base, unsigned off, unsigned dst) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, %2"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2"
                :: "v"(off), "s"(dst), "s"(base) : "memory", "m0");
 }
 

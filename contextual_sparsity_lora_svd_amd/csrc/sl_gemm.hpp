@@ -611,7 +611,8 @@ gather_gemm_kernel(const GemmArgs args) {
       // outputs are dropped); rows past K hold a clamped row whose A columns
       // are zero.  Tiles past the range are not loaded.
       // (The row indices are read on every path, so the index load never
-      // stays pending into the next compute phase.)
+      // stays pending into the next compute phase.  The s_nop is the wait state
+      // that a load to LDS needs behind a write of m0, here as in every such load.)
       unsigned char* st = Bst0 + b_stage * B_STAGE;
       const bool issue = n_loaded < nkt;
 #pragma unroll
@@ -627,7 +628,7 @@ gather_gemm_kernel(const GemmArgs args) {
         const unsigned la = __builtin_amdgcn_readfirstlane(
             (unsigned)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)(st + (4 * j + wave) * 1024));
         if (issue)
-          asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, %2"
+          asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2"
                        :: "v"(off), "s"(la), "s"(b_base) : "memory", "m0");
       }
       b_stage ^= 1;
@@ -997,7 +998,7 @@ gather_gemm_kernel(const GemmArgs args) {
       for (int j = 0; j < W_AB; ++j) {
         const unsigned la = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(
             __attribute__((address_space(3))) unsigned char*)(sb + 1024 * (W_AB * wv + j)));
-        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, %2"
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2"
                      :: "v"((a_off[j] + (unsigned)(k0 + kcl(j & 1))) * 2u), "s"(la), "s"(uniform_ptr(a_base))
                      : "memory", "m0");
       }
@@ -1026,7 +1027,7 @@ gather_gemm_kernel(const GemmArgs args) {
         const unsigned kb = kc < cur_K ? (unsigned)kc : 0u;
         const unsigned la = __builtin_amdgcn_readfirstlane(
             (unsigned)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)(sb + BM * W_ROWB + 1024 * q));
-        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, %2"
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2"
                      :: "v"(((unsigned)bch[j] * (unsigned)cur_ldb + kb) * 2u), "s"(la), "s"(uniform_ptr(base))
                      : "memory", "m0");
       }
@@ -1044,7 +1045,7 @@ gather_gemm_kernel(const GemmArgs args) {
         const unsigned off = ((unsigned)(lane < 32 ? r0 : r1) * (unsigned)cur_ldb + (unsigned)col) * 2u;
         const unsigned la = __builtin_amdgcn_readfirstlane(
             (unsigned)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)(sb + BM * W_ROWB + 1024 * q));
-        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, %2"
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2"
                      :: "v"(off), "s"(la), "s"(uniform_ptr(b_base)) : "memory", "m0");
       }
     }
