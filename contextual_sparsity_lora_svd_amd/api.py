@@ -690,6 +690,17 @@ def head_norm_bwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, 
     return out
 
 
+def pair_heads(heads: Sequence[int]):
+    """The heads that the projections around differential attention of ``heads``
+    take (QKVOWeights, and the heads of the QK-norm criterion): its pairs, each
+    one head of twice the width, so that query head 2 h + m and the columns 2 h + m
+    of a keep the channels of kv head 2 (h / (Hq / Hkv)) + m, which they meet."""
+    hq, hkv, hd = (int(h) for h in heads)
+    if hq % 2 or hkv % 2:
+        raise SparseLoraError(f"differential heads come in pairs: {hq} query and {hkv} kv heads")
+    return hq // 2, hkv // 2, 2 * hd
+
+
 class DiffAttnParams:
     """Differential attention's learned vectors lq1, lk1, lq2, lk2 [head_dim]
     (fp32 device tensors; lambda = exp(lq1.lk1) - exp(lq2.lk2) + lambda_init)

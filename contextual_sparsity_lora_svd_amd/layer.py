@@ -16,6 +16,8 @@ libsparselora.so.  The attention core between the q/k/v and o projections is
 the caller's, or DiffAttention's.
 """
 import math
+import threading
+import warnings
 from dataclasses import dataclass
 from typing import Callable, Dict, Optional, Sequence, Tuple
 
@@ -219,6 +221,9 @@ class _OStep(torch.autograd.Function):
         return g["da"], g["dAo"], g["dBo"], None
 
 
+_around = threading.local()   # heads that the sparse projections around the running core took (None: none)
+
+
 class SparseLoRAQKVO(torch.nn.Module):
     """q/k/v/o projections with LoRA and contextual channel sparsity (QK-norm
     selection for q/k, L2 of v for v/o), around the caller's attention core:
@@ -226,7 +231,11 @@ class SparseLoRAQKVO(torch.nn.Module):
         out = module(X, layout, attention, step)
 
     with ``attention(q, k, v) -> a`` on token-major ``[T, H * head_dim]``
-    tensors (differentiable with torch autograd).  Frozen weights ``Wq [Hq hd, D]``,
+    tensors (differentiable with torch autograd).  Query head j and column block
+    j of a keep the channels of kv head j // (Hq / Hkv), as ordinary grouped
+    attention reads them; a core that reads other kv heads says so by an attribute
+    ``projection_heads`` (as ``DiffAttention.bind``'s has), which then stands in
+    for ``heads`` in that call.  Frozen weights ``Wq [Hq hd, D]``,
     ``Wk, Wv [Hkv hd, D]``, ``Wo [D, Hq hd]`` in the compute dtype; LoRA
     factors fp32 parameters.  ``base_bits=4``: the frozen weights as 4-bit
     codes and block scales (as in SparseLoRAFFN)."""
@@ -255,13 +264,13 @@ class SparseLoRAQKVO(torch.nn.Module):
         self.frozen = _quantized_base(self.frozen, base_bits, Wq.dtype)
         self.last_k, self.last_idx = None, None
 
-    def channel_sets(self, X, layout, k_qk, k_vo):
-        B = layout.batch
+    def channel_sets(self, X, layout, k_qk, k_vo, heads=None):
+        B, heads = layout.batch, self.heads if heads is None else heads
         if k_qk < self.nkv and k_vo < self.nkv:
             # both sets estimated: one call projects X once for q, k and v
             (Pq, Qq), (Pk, Qk), (Pv, Qv) = self.est["Wq"], self.est["Wk"], self.est["Wv"]
             jobs = [dict(crit=sl.SL_CRIT_QK_NORM, Pt0=Pq, Q0=Qq, Pt1=Pk, Q1=Qk, N=self.nkv, k=k_qk,
-                         heads=self.heads),
+                         heads=heads),
                     dict(crit=sl.SL_CRIT_L2, Pt0=Pv, Q0=Qv, N=self.nkv, k=k_vo)]
             (iqk, _), (ivo, _) = sl.estimate_select_multi(X, layout, self.est_rank, jobs)
             return iqk, ivo
@@ -270,7 +279,7 @@ class SparseLoRAQKVO(torch.nn.Module):
         else:
             (Pq, Qq), (Pk, Qk) = self.est["Wq"], self.est["Wk"]
             iqk, _ = sl.estimate_select(sl.SL_CRIT_QK_NORM, X, layout, self.est_rank, Pq, Qq, Pk, Qk,
-                                        self.nkv, k_qk, heads=self.heads)
+                                        self.nkv, k_qk, heads=heads)
             iqk = iqk.clone()
         if k_vo == self.nkv:
             ivo = _all_channels(B, self.nkv, X.device)
@@ -288,18 +297,35 @@ class SparseLoRAQKVO(torch.nn.Module):
             k_qk = s.k(self.layer, step, "qk", self.nkv) if s else self.nkv
         if k_vo is None:
             k_vo = s.k(self.layer, step, "vo", self.nkv) if s else self.nkv
-        iqk, ivo = self.channel_sets(X, layout, k_qk, k_vo)
+        heads = self._heads_around(attention)
+        iqk, ivo = self.channel_sets(X, layout, k_qk, k_vo, heads)
         lora = {n: getattr(self, n).detach().to(self.dtype).contiguous()
                 for n in ("Aq", "Bq", "Ak", "Bk", "Av", "Bv", "Ao", "Bo")}
         t = dict(self.frozen)
         t.update(lora)
-        w = sl.QKVOWeights(t, self.heads, self.lora_scale)
+        w = sl.QKVOWeights(t, heads, self.lora_scale)
         st = _QKVOState(w, layout, k_qk, iqk, k_vo, ivo, sl.QKVOWorkspace(w, layout, k_qk, k_vo, X.device))
         st.lora = lora   # keep the cast factors alive for the backward
         self.last_k, self.last_idx = (k_qk, k_vo), (iqk, ivo)
         q, k, v = _QKVStep.apply(X, self.Aq, self.Bq, self.Ak, self.Bk, self.Av, self.Bv, st)
-        a = attention(q, k, v)
+        outer = getattr(_around, "heads", None)
+        _around.heads = heads if min(k_qk, k_vo) < self.nkv else None
+        try:
+            a = attention(q, k, v)
+        finally:
+            _around.heads = outer
         return _OStep.apply(a.contiguous(), self.Ao, self.Bo, st)
+
+    def _heads_around(self, attention):
+        """The heads by which kv channel sets spread over q and a around this core."""
+        heads = getattr(attention, "projection_heads", None)
+        if heads is None:
+            return self.heads
+        hq, hkv, hd = heads = tuple(int(h) for h in heads)
+        if (hq * hd, hkv * hd) != (self.nq, self.nkv):
+            raise sl.SparseLoraError(f"the attention's projection_heads {heads} are {hq * hd} and {hkv * hd} channels, "
+                                     f"the projections have {self.nq} and {self.nkv}")
+        return heads
 
 
 class _RotaryStep(torch.autograd.Function):
@@ -363,6 +389,13 @@ class DiffAttention(torch.nn.Module):
         core = DiffAttention(heads, rot=Rotary(head_dim), qk_norm=True)
         out = proj(X, layout, core.bind(layout), step)     # proj: SparseLoRAQKVO
 
+    Query head 2 h + m reads kv head 2 (h / G) + m, G = Hq / Hkv, where ordinary
+    grouped attention reads (2 h + m) / G.  The projections around the core take
+    the channels of the heads that meet if they see a pair as one head of twice
+    the width: ``projection_heads``, which ``bind`` hands over.  A function around
+    the module has to carry that attribute too (or the projections be made with
+    those heads); a sparse call without it warns.
+
     ``lens`` (valid rows per sequence) and ``pos`` [T] int32 go with each call.
     Padding rows of q, k and v have no gradient and may hold anything, but
     finite values under ``qk_norm``, whose weights' gradients sum over every row
@@ -388,12 +421,22 @@ class DiffAttention(torch.nn.Module):
             self.wq = torch.nn.Parameter(torch.ones(hd, device=device))
             self.wk = torch.nn.Parameter(torch.ones(hd, device=device))
 
+    @property
+    def projection_heads(self) -> Tuple[int, int, int]:
+        """The heads that projections around this core take: its pairs."""
+        return sl.pair_heads(self.heads)
+
     def _params(self, lq1, lk1, lq2, lk2):
         t = {"lq1": lq1.detach(), "lk1": lk1.detach(), "lq2": lq2.detach(), "lk2": lk2.detach()}
         return sl.DiffAttnParams(t, self.heads, self.lambda_init, self.scale, self.causal)
 
     def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, layout: sl.Layout,
                 lens: Optional[Sequence[int]] = None, pos: Optional[torch.Tensor] = None):
+        around = getattr(_around, "heads", None)
+        if around is not None and around != self.projection_heads and around[0] != around[1]:
+            warnings.warn(f"sparse projections with heads {around} around differential attention of {self.heads}: q and k "
+                          "keep channels of heads that do not meet, and o reads other columns than a has; pass "
+                          "core.bind(layout), or give the function that calls the core its projection_heads")
         if self.qk_norm:
             q, k = _HeadNormStep.apply(q, k, self.wq, self.wk, layout, self.heads, self.rot, pos, self.eps)
         elif self.rot is not None:
@@ -403,4 +446,7 @@ class DiffAttention(torch.nn.Module):
     def bind(self, layout: sl.Layout, lens: Optional[Sequence[int]] = None,
              pos: Optional[torch.Tensor] = None) -> Callable:
         """The ``attention(q, k, v) -> a`` that SparseLoRAQKVO calls."""
-        return lambda q, k, v: self(q, k, v, layout, lens, pos)
+        def attention(q, k, v):
+            return self(q, k, v, layout, lens, pos)
+        attention.projection_heads = self.projection_heads
+        return attention

@@ -273,7 +273,7 @@ sl_status sl_ffn_bwd(sl_dtype dt, const sl_layout* lay, const sl_ffn_weights* w,
  * a6/a7 — sparse q/k/v/o projections (SparseLoRA article §一, §三, §六).
  * idx_qk [batch, k_qk] and idx_vo [batch, k_vo] are kv-channel sets (as written
  * by sl_estimate_select with QK_NORM and L2); q and o use them expanded to every
- * query head of the group.  At context rows, unselected channels of q, k, v are
+ * query head of the group (query head j is of the group of kv head j / (Hq / Hkv)).  At context rows, unselected channels of q, k, v are
  * written as 0 and unselected columns of the attention output a are ignored.
  *   fwd:  X [T, d_model] -> q [T, Hq*hd], k, v [T, Hkv*hd]   (if X != NULL)
  *         a [T, Hq*hd]   -> o [T, d_model]                  (if a != NULL)
@@ -383,6 +383,10 @@ sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_heads* he
  *   a[:, 2h*hd : 2(h+1)*hd] = softmax(s q_2h k_2g^T) V - lambda softmax(s q_2h+1 k_2g+1^T) V
  *   lambda = exp(lq1 . lk1) - exp(lq2 . lk2) + lambda_init
  *   lq1, lk1, lq2, lk2 [hd] fp32, 16-byte aligned: shared by the heads
+ *   Query head 2h+m so meets kv head 2g+m, not (2h+m) / (Hq / Hkv).  Sparse
+ *   projections around it (sl_qkvo_*, and QK_NORM, which choose and expand kv
+ *   channels by their heads) take the pairs as heads, {Hq/2, Hkv/2, 2 hd}: the
+ *   kept channels of q, k, v and a are then those that meet.
  *   scale   s (a positive number)
  *   causal  != 0: row i of a sequence reads keys 0..i
  *   lens    [host] batch valid lengths 0..seq_len, or NULL: every row.  Rows at
