@@ -60,7 +60,10 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_direct(const DiffArgs a) {
   const T* vp = reinterpret_cast<const T*>(a.v) + tok0 * ldk + g * 2 * a.hd;
   const bool rok = row < len;
   f32x16 o[NT];
-  float mx = -INFINITY, sum = 0.f;
+  // ms: the running maximum times sc as it was rounded, which the weights are relative
+  // to.  Only differences of such values rescale: mx * sc formed again (and fused with a
+  // subtraction) is off by its rounding, at every tile
+  float mx = -INFINITY, ms = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int t = 0; t < NT; ++t) zero16(o[t]);
   const float sc = a.scale * kLog2e;
@@ -110,17 +113,17 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_direct(const DiffArgs a) {
           tm = fmaxf(tm, s[i]);
         }
         tm = fmaxf(tm, __shfl_xor(tm, 32));
-        const float nm = fmaxf(mx, tm);
-        const float ms = nm == -INFINITY ? 0.f : nm * sc;   // nothing seen yet: weights 0
-        const float f = fast_exp2(mx * sc - ms);
+        mx = fmaxf(mx, tm);
+        const float ns = mx * sc, rel = ns == -INFINITY ? 0.f : ns;   // nothing seen yet: weights 0
+        const float f = ns == ms ? 1.f : fast_exp2(ms - rel);
         float ts = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[i] = fast_exp2(fmaf(s[i], sc, -ms));
+          s[i] = fast_exp2(fmaf(s[i], sc, -rel));
           ts += s[i];
         }
         sum = sum * f + ts;
-        mx = nm;
+        ms = ns;
         if (__any(f != 1.f)) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_direct(const DiffArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     });
   }
-  smx[m][kq][lane] = mx;
+  smx[m][kq][lane] = ms;
   ssum[m][kq][lane] = sum;
   __syncthreads();
   float top = smx[m][0][lane], l = 0.f;
@@ -140,9 +143,9 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_direct(const DiffArgs a) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const float x = smx[m][w][lane];
-    if (x > -INFINITY) l = fmaf(fast_exp2((x - top) * sc), ssum[m][w][lane], l);   // else it saw no key
+    if (x > -INFINITY) l = fmaf(fast_exp2(x - top), ssum[m][w][lane], l);   // else it saw no key
   }
-  const float f = mx > -INFINITY ? fast_exp2((mx - top) * sc) : 0.f;
+  const float f = ms > -INFINITY ? fast_exp2(ms - top) : 0.f;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(512, 2) diff_fwd_direct(const DiffArgs a) {
   const float inv = rok ? 1.f / l : 0.f;
   if (kq == 0 && h == 0 && row < a.L) {
     float* const at = a.lse + ((long long)(b * a.hp + pair) * 2 + m) * a.ls + row;
-    *at = rok ? top * sc + log2f(l) : INFINITY;
+    *at = rok ? top + log2f(l) : INFINITY;
     if (row == a.L - 1) at[1] = INFINITY;
   }
   add_waves(o, sm[m], kq, lane);

@@ -483,3 +483,30 @@ def test_two_graphs_with_their_own_buffers():
             assert torch.equal(a, a2)
             for n in g:
                 assert torch.equal(g[n], g2[n]), n
+
+
+def test_fp32_weights_do_not_drift_with_the_tiles():
+    """Scores near 31000 that are exact in fp32 and differ by at most 2, the maximum
+    in the first keys, values of opposite sign in the two halves.  A rescaling by the
+    rounding of maximum * scale (here 3e-4 in the exponent) at each of a wave's 33
+    tiles would move the result by 1e-3.  What remains: the exponential, within 2
+    half steps; a product over 33 tiles of 32 keys per wave, n / 4 additions; the
+    row sums and the join, fewer than 128 more."""
+    sl = _sl()
+    L, hd, lam, top = 4133, 16, -0.5, 31000.0
+    sc = np.float32(np.float32(hd ** -0.5) * np.float32(1.44269504088896341))
+    assert abs(top * float(sc) - float(np.float32(np.float32(top) * sc))) > 2.0 ** -12
+    raw = np.full(L, top - 1)                                # q . k
+    raw[5::7], raw[:32] = top - 2, top
+    d = {"q": torch.full((L, 2 * hd), 64.0, device="cuda"),
+         "k": _dev((raw / (64 * hd))[:, None].repeat(2 * hd, 1), "f32")}
+    assert np.array_equal(_np(d["k"])[:, 0] * 64 * hd, raw)
+    v = np.where(np.arange(L) < L // 2, 1.0, -1.0)[:, None] * (1 + np.arange(2 * hd) / 32)
+    d["v"] = _dev(v, "f32")
+    p = sl.DiffAttnParams({n: torch.zeros(hd, device="cuda") for n in sl.DiffAttnParams.NAMES}, (2, 2, hd), lam,
+                          causal=False)
+    a, _ = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], sl.Layout([L], L))
+    w = np.exp((raw - top) * hd ** -0.5)
+    w /= w.sum()
+    _within(a, np.broadcast_to((1 - lam) * (w @ v), a.shape),
+            (L / 4 + 128) * U32 * (1 - lam) * (w @ np.abs(v)), "a")
