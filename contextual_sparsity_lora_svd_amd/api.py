@@ -723,10 +723,12 @@ class DiffAttnParams:
 
 class DiffAttnWorkspace:
     """Saved and scratch buffers of one differential attention call and its
-    backward, with the sequences' valid lengths (None: every row)."""
+    backward, with the sequences' valid lengths (None: every row).  Only the
+    backward needs scratch (``ws``); without ``scratch`` it is made where it is
+    first asked for, by the first backward that gets these buffers."""
 
     def __init__(self, p: DiffAttnParams, layout: Layout, dtype: torch.dtype, device,
-                 lens: Optional[Sequence[int]] = None):
+                 lens: Optional[Sequence[int]] = None, scratch: bool = True):
         L = lib()
         code = {torch.bfloat16: SL_BF16, torch.float32: SL_F32}.get(dtype)
         if code is None:
@@ -737,15 +739,23 @@ class DiffAttnWorkspace:
         self.made_for = (layout.batch, layout.seq_len, p.heads, dtype)
         h = SlHeads(*p.heads)
         self.saved = _bytes_tensor(L.sl_diff_attn_saved_bytes(code, layout.ref, ctypes.byref(h)), device)
-        self.ws = _bytes_tensor(L.sl_diff_attn_workspace_bytes(code, layout.ref, ctypes.byref(h)), device)
+        nbytes = L.sl_diff_attn_workspace_bytes(code, layout.ref, ctypes.byref(h))
+        self._ws_bytes, self._ws = nbytes, _bytes_tensor(nbytes, device) if scratch else None
+
+    @property
+    def ws(self) -> torch.Tensor:
+        if self._ws is None:
+            self._ws = _bytes_tensor(self._ws_bytes, self.saved.device)
+        return self._ws
 
 
 def _diff_buffers(buf: DiffAttnWorkspace, p: DiffAttnParams, layout: Layout, q: torch.Tensor):
-    """(saved, bytes, ws, bytes) of a call over q."""
+    """(saved, bytes, ws, bytes) of a call over q; no ws where none has been made."""
     if buf.made_for != (layout.batch, layout.seq_len, p.heads, q.dtype):
         raise SparseLoraError(f"buffers made for (batch, seq_len, heads, dtype) = {buf.made_for}, "
                               f"call of {(layout.batch, layout.seq_len, p.heads, q.dtype)}")
-    return _check_scratch("saved", buf.saved, q), buf.saved.numel(), _check_scratch("ws", buf.ws, q), buf.ws.numel()
+    ws = (None, 0) if buf._ws is None else (_check_scratch("ws", buf._ws, q), buf._ws.numel())
+    return (_check_scratch("saved", buf.saved, q), buf.saved.numel(), *ws)
 
 
 def diff_attn_fwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, layout: Layout,
@@ -759,7 +769,7 @@ def diff_attn_fwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
     qp, kp = _pair_ptrs(("q", "k"), q, k, T, p.heads, q.dtype, dev)
     vp = _check_rows("v", v, k.shape, q.dtype, dev)
     if buf is None:
-        buf = DiffAttnWorkspace(p, layout, q.dtype, q.device, lens)
+        buf = DiffAttnWorkspace(p, layout, q.dtype, q.device, lens, scratch=False)
     elif lens is not None:
         raise SparseLoraError("lens belongs to the buffers: give it to DiffAttnWorkspace")
     a = out if out is not None else torch.empty_like(q)
@@ -798,6 +808,7 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
         raise SparseLoraError("dq, dk and dv may not be inputs or each other")
     shape = (p.heads[2],)
     g = SlDiffAttnGrads(*[_check_rows("d" + n, out["d" + n], shape, torch.float32, dev) for n in p.NAMES])
+    buf.ws                                       # made here, if not before
     saved, ns, ws, nw = _diff_buffers(buf, p, layout, q)
     c = p._c(buf.lens, dev)
     _check(lib().sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap, saved, ns, gp, dqp, dkp, dvp,

@@ -15,6 +15,7 @@ buffers, and the routing of gradients.  Every arithmetic step runs in
 libsparselora.so.  The attention core between the q/k/v and o projections is
 the caller's, or DiffAttention's.
 """
+import copy
 import math
 import threading
 import warnings
@@ -365,16 +366,21 @@ class _DiffAttnStep(torch.autograd.Function):
     def forward(ctx, q, k, v, lq1, lk1, lq2, lk2, mod, layout, lens):
         q, k, v = (x.detach().contiguous() for x in (q, k, v))
         p = mod._params(lq1, lk1, lq2, lk2)
-        buf = sl.DiffAttnWorkspace(p, layout, q.dtype, q.device, lens)
+        buf = sl.DiffAttnWorkspace(p, layout, q.dtype, q.device, lens, scratch=False)
         a, _ = sl.diff_attn_fwd(p, q, k, v, layout, buf=buf)
+        # what the forward saved is held as the tensors are, until the graph lets them go;
+        # the scratch lives in the backward alone
+        ctx.save_for_backward(q, k, v, a, lq1, lk1, lq2, lk2, buf.saved)
+        buf.saved = None
         ctx.args = (mod, layout, buf)
-        ctx.save_for_backward(q, k, v, a, lq1, lk1, lq2, lk2)
         return a
 
     @staticmethod
     def backward(ctx, da):
         mod, layout, buf = ctx.args
-        q, k, v, a, *lv = ctx.saved_tensors
+        q, k, v, a, *lv, saved = ctx.saved_tensors
+        buf = copy.copy(buf)
+        buf.saved = saved
         g = sl.diff_attn_bwd(mod._params(*lv), q, k, v, a, layout, buf, da.contiguous())
         return (g["dq"], g["dk"], g["dv"], g["dlq1"], g["dlk1"], g["dlq2"], g["dlk2"], None, None, None)
 

@@ -392,8 +392,9 @@ sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_heads* he
  *   lens    [host] batch valid lengths 0..seq_len, or NULL: every row.  Rows at
  *           or past a sequence's length are padding: they are never read, and
  *           their outputs and gradients are written as 0.
- *   fwd: q, k, v -> a [T, Hq*hd]; writes `saved` for the backward (and leaves ws,
- *        checked for size as the backward's, as it is).
+ *   fwd: q, k, v -> a [T, Hq*hd]; writes `saved` for the backward.  It uses no
+ *        scratch: ws may be NULL with ws_bytes 0 (one that is given is checked
+ *        for size as the backward's and left as it is).
  *   bwd: q, k, v, a (the forward's) and da -> dq, dk, dv and the fp32 gradients
  *        of the four vectors, overwritten.  Sums run in a fixed order.
  * No output may overlap an input, the buffers or another output.  The backward

@@ -175,3 +175,21 @@ def test_diff_attention_buffers_of_another_call_are_refused(sl):
                   sl.DiffAttnWorkspace(sl.DiffAttnParams(t, (4, 4, 16)), lay, torch.float32, "cpu")):
         with pytest.raises(sl.SparseLoraError, match="buffers made for"):
             like(other, p, lay, q)
+
+
+def test_diff_attention_forward_without_a_workspace(sl):
+    """The forward uses none: it takes NULL with 0 bytes, and buffers made without
+    scratch; the backward still needs its own."""
+    torch = pytest.importorskip("torch")
+    L, lay, R, big = sl.lib(), sl.Layout([4, 4], 4), ctypes.byref, 1 << 40
+    assert L.sl_diff_attn_fwd(1, lay.ref, R(_diff(sl)), P, P, P, P, P, big, None, 0, None) in (7, 8)
+    g = sl.api.SlDiffAttnGrads(P, P, P, P)
+    assert L.sl_diff_attn_bwd(1, lay.ref, R(_diff(sl)), P, P, P, P, P, big, P, P, P, P, R(g), None, 0, None) == 6
+    p = sl.DiffAttnParams({n: torch.ones(16) for n in sl.DiffAttnParams.NAMES}, (4, 2, 16))
+    q = torch.zeros(8, 64)
+    buf = sl.DiffAttnWorkspace(p, lay, torch.float32, "cpu", scratch=False)
+    assert sl.api._diff_buffers(buf, p, lay, q)[2:] == (None, 0)
+    n = L.sl_diff_attn_workspace_bytes(0, lay.ref, R(sl.api.SlHeads(4, 2, 16)))
+    assert buf.ws.numel() == n and buf.ws is buf.ws
+    assert sl.api._diff_buffers(buf, p, lay, q)[2:] == (buf.ws.data_ptr(), n)
+    assert sl.DiffAttnWorkspace(p, lay, torch.float32, "cpu")._ws.numel() == n

@@ -107,3 +107,39 @@ def test_module_backward_twice_is_refused_and_padding_has_no_gradient():
         assert not t.grad[27:].any() and t.grad[:27].any()
     with pytest.raises(RuntimeError):
         a.sum().backward()
+
+
+def test_module_holds_no_scratch_between_forward_and_backward():
+    """Between the passes: a, q, k, v and what the backward reads, not its scratch
+    (here 2.5 times as much); after the backward, or without gradients, nothing but
+    the results.  A second backward of a retained graph gives the same."""
+    import contextual_sparsity_lora_svd_amd as sl
+    heads, L = (16, 4, 64), 2048
+    lay = sl.Layout([L], L)
+    core = sl.DiffAttention(heads, generator=torch.Generator().manual_seed(1))
+    x = [torch.randn(L, h * 64, device="cuda").to(torch.bfloat16).requires_grad_(True) for h in (16, 4, 4)]
+    p = core._params(core.lq1, core.lk1, core.lq2, core.lk2)
+    buf = sl.DiffAttnWorkspace(p, lay, torch.bfloat16, "cuda")
+    saved, ws = buf.saved.numel(), buf.ws.numel()
+    assert ws > 2 << 20
+    del buf, p
+    out_bytes, slack = L * 16 * 64 * 2, 1 << 20
+    with torch.no_grad():
+        core(*x, lay)
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        a = core(*x, lay)
+        assert torch.cuda.memory_allocated() - before <= out_bytes + slack
+        assert torch.cuda.max_memory_allocated() - before <= out_bytes + saved + slack
+        del a
+    a = core(*x, lay)
+    assert torch.cuda.memory_allocated() - before <= out_bytes + saved + slack
+    da = torch.randn_like(a)
+    first = torch.autograd.grad(a, x, da, retain_graph=True)
+    again = torch.autograd.grad(a, x, da)
+    for u, v in zip(first, again):
+        assert torch.equal(u, v)
+    del first, again, u, v
+    held = torch.cuda.memory_allocated() - before - da.numel() * 2
+    assert held <= out_bytes + slack, held                  # a itself is still here
