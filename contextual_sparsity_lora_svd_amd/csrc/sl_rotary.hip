@@ -486,7 +486,8 @@ extern "C" sl_status sl_head_norm_fwd(sl_dtype dt, const sl_layout* lay, const s
 extern "C" size_t sl_head_norm_workspace_bytes(const sl_layout* lay, const sl_heads* heads) {
   RotArgs a;
   int inter;
-  if (rot_args(a, SL_F32, lay, heads, nullptr, true, 1.f, &inter) != SL_OK) return 0;
+  // (the size does not depend on k; without kv heads it is asked for calls without k)
+  if (rot_args(a, SL_F32, lay, heads, nullptr, heads && heads->n_kv_heads != 0, 1.f, &inter) != SL_OK) return 0;
   return (size_t)rot_blocks(a.T, kNormBwdBlocks) * 2 * a.hd * sizeof(float);
 }
 

@@ -360,7 +360,8 @@ sl_status sl_rotary_apply(sl_dtype dt, const sl_layout* lay, const sl_heads* hea
  * Norms of the q and k heads, with the rotation in the same pass:
  *   y = R(x r w),  r = (mean over the head of x^2 + eps)^(-1/2)
  * wq, wk [hd] fp32 weights shared by the heads; rot NULL (or rot_dim 0): no
- * rotation.  k, wk, k_out (and their gradients) may all be NULL.
+ * rotation.  k, wk, k_out (and their gradients) may all be NULL, and n_kv_heads
+ * is then 0 or any count.
  *   fwd: q, k -> q_out, k_out (q_out may be q, k_out k; keep x for the backward)
  *   bwd: x = q, k (the forward's inputs) and dq_out, dk_out -> dq, dk and the
  *        fp32 weight gradients dwq, dwk [hd], overwritten, summed over rows and

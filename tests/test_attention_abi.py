@@ -193,3 +193,19 @@ def test_diff_attention_forward_without_a_workspace(sl):
     assert buf.ws.numel() == n and buf.ws is buf.ws
     assert sl.api._diff_buffers(buf, p, lay, q)[2:] == (buf.ws.data_ptr(), n)
     assert sl.DiffAttnWorkspace(p, lay, torch.float32, "cpu")._ws.numel() == n
+
+
+def test_head_norm_workspace_of_calls_without_k(sl):
+    """The norms take q alone whatever the kv head count, none included: the size
+    query answers for all of them alike."""
+    L, lay, R = sl.lib(), sl.Layout([4, 4], 4), ctypes.byref
+    need = L.sl_head_norm_workspace_bytes(lay.ref, R(sl.api.SlHeads(4, 2, 16)))
+    assert need == L.sl_head_norm_workspace_bytes(lay.ref, R(sl.api.SlHeads(4, 0, 16))) > 0
+    assert L.sl_head_norm_workspace_bytes(lay.ref, R(sl.api.SlHeads(4, -1, 16))) == 0
+    assert L.sl_head_norm_workspace_bytes(lay.ref, None) == 0
+    h = sl.api.SlHeads(4, 0, 16)
+    assert L.sl_head_norm_fwd(1, lay.ref, R(h), None, 1e-6, P, None, P, None, P, None, None) in (7, 8)
+    bwd = lambda n: L.sl_head_norm_bwd(1, lay.ref, R(h), None, 1e-6, P, None, P, None, P, None, P, None, P, None, P, n,
+                                       None)
+    assert bwd(need) in (7, 8) and bwd(need - 1) == 6
+    assert sl.HeadNormWorkspace(lay, (4, 0, 16), "cpu").ws.numel() == need

@@ -510,3 +510,20 @@ def test_fp32_weights_do_not_drift_with_the_tiles():
     w /= w.sum()
     _within(a, np.broadcast_to((1 - lam) * (w @ v), a.shape),
             (L / 4 + 128) * U32 * (1 - lam) * (w @ np.abs(v)), "a")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_norm_of_q_without_kv_heads(dt):
+    """q alone, in a layout of heads that has no kv heads: forward and backward as
+    with any kv head count."""
+    sl = _sl()
+    lay, rng = sl.Layout([5], 5), np.random.default_rng(2)
+    x, g = (_dev(_draw(rng, (5, 96), dt), dt) for _ in range(2))
+    w = torch.rand(32, device="cuda") + 0.5
+    res = []
+    for hkv in (0, 1):
+        y, _ = sl.head_norm_fwd(x, None, w, None, lay, (3, hkv, 32))
+        gr = sl.head_norm_bwd(x, None, w, None, lay, (3, hkv, 32), g, None)
+        res.append((y, gr["dq"], gr["dwq"]))
+    for u, v in zip(*res):
+        assert torch.equal(u, v) and u.any()
