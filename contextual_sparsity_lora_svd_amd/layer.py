@@ -23,6 +23,7 @@ from dataclasses import dataclass
 from typing import Callable, Dict, Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api as sl
 
@@ -337,6 +338,7 @@ class _RotaryStep(torch.autograd.Function):
         return sl.rotary(q.detach().contiguous(), k.detach().contiguous(), layout, heads, rot, pos)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         layout, heads, rot = ctx.args
         (pos,) = ctx.saved_tensors
@@ -353,6 +355,7 @@ class _HeadNormStep(torch.autograd.Function):
         return sl.head_norm_fwd(q, k, wq.detach(), wk.detach(), layout, heads, rot, pos, eps)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         layout, heads, rot, eps = ctx.args
         q, k, wq, wk, pos = ctx.saved_tensors
@@ -376,6 +379,7 @@ class _DiffAttnStep(torch.autograd.Function):
         return a
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, da):
         mod, layout, buf = ctx.args
         q, k, v, a, *lv, saved = ctx.saved_tensors
@@ -403,6 +407,7 @@ class DiffAttention(torch.nn.Module):
     those heads); a sparse call without it warns.
 
     ``lens`` (valid rows per sequence) and ``pos`` [T] int32 go with each call.
+    Gradients are first derivatives: a second one is refused.
     Padding rows of q, k and v have no gradient and may hold anything, but
     finite values under ``qk_norm``, whose weights' gradients sum over every row
     (0 times what the padding holds).  A backward pass captured into a graph
