@@ -375,17 +375,17 @@ class _DiffAttnStep(torch.autograd.Function):
         # the scratch lives in the backward alone
         ctx.save_for_backward(q, k, v, a, lq1, lk1, lq2, lk2, buf.saved)
         buf.saved = None
-        ctx.args = (mod, layout, buf)
+        ctx.args = (p, layout, buf)
         return a
 
     @staticmethod
     @once_differentiable
     def backward(ctx, da):
-        mod, layout, buf = ctx.args
-        q, k, v, a, *lv, saved = ctx.saved_tensors
+        p, layout, buf = ctx.args
+        q, k, v, a, *_, saved = ctx.saved_tensors
         buf = copy.copy(buf)
         buf.saved = saved
-        g = sl.diff_attn_bwd(mod._params(*lv), q, k, v, a, layout, buf, da.contiguous())
+        g = sl.diff_attn_bwd(p, q, k, v, a, layout, buf, da.contiguous())
         return (g["dq"], g["dk"], g["dv"], g["dlq1"], g["dlk1"], g["dlq2"], g["dlk2"], None, None, None)
 
 

@@ -55,3 +55,20 @@ def test_a_second_derivative_is_refused(core, step):
     (g,) = torch.autograd.grad((x[0].sum() * y), x[0], create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.sum().backward()
+
+
+def test_the_backward_takes_the_settings_of_its_forward(core):
+    """Settings of the module that change between a forward and its backward (a
+    schedule, an evaluation in between) are the next forward's."""
+    make, calls, lay = core
+    m = make(False)
+    x = [torch.randn(3, 16, requires_grad=True) for _ in range(3)]
+    y = m(*x, lay)
+    m.causal, m.scale, m.lambda_init, m.heads = False, 3.0, 0.1, (4, 4, 4)
+    y.sum().backward()
+    (_, f), (_, b) = calls
+    for n in ("causal", "scale", "lambda_init", "heads"):
+        assert getattr(f, n) == getattr(b, n), n
+    assert (f.causal, f.scale, f.heads) == (True, 8 ** -0.5, (2, 2, 8))
+    for n in f.NAMES:
+        assert torch.equal(b.t[n], getattr(m, n))
