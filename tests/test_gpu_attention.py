@@ -527,3 +527,73 @@ def test_norm_of_q_without_kv_heads(dt):
         res.append((y, gr["dq"], gr["dwq"]))
     for u, v in zip(*res):
         assert torch.equal(u, v) and u.any()
+
+
+# Sequences of many tiles, so that every ring of tiles wraps several times, in enough
+# workgroups for the launch rules to take the 128-row kernels of every width (the first
+# nine, with a kv group's heads cut into parts of 3 or 4), and past 1024 rows, where the
+# backward's rule for causal sequences changes, on both of its sides.
+LONG = [  # batch, seq, hq, hkv, hd, causal, lens
+    (8, 330, 48, 16, 24, True, [330, 330, 329, 330, 257, 300, 290, 330]),
+    (2, 330, 48, 16, 32, False, None),
+    (8, 330, 48, 16, 64, True, None),
+    (2, 330, 48, 16, 56, False, [330, 321]),
+    (8, 330, 48, 16, 88, True, None),
+    (2, 330, 48, 16, 96, False, None),
+    (8, 330, 48, 16, 128, True, [330, 330, 329, 330, 257, 300, 290, 330]),
+    (2, 330, 48, 16, 128, False, [330, 322]),
+    (3, 600, 32, 8, 64, False, [600, 333, 64]),
+    (4, 520, 32, 8, 128, True, [520, 519, 385, 400]),
+    (4, 1100, 32, 8, 32, True, None),
+    (4, 1030, 32, 8, 128, True, [1030, 1029, 1030, 1025]),
+    (1, 2060, 32, 8, 72, True, None),
+    (1, 1100, 8, 4, 64, True, None),
+    (1, 1100, 4, 4, 128, False, None),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "x".join(map(str, c[:6])))
+def test_diff_attention_long(case):
+    test_diff_attention(case, "bf16")
+
+
+@pytest.mark.parametrize("case", [LONG[9], LONG[13]], ids=lambda c: "x".join(map(str, c[:6])))
+def test_diff_attention_long_fp32(case):
+    test_diff_attention(case, "f32")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.03, 0.7])
+@pytest.mark.parametrize("causal", [True, False])
+def test_diff_attention_scale(dt, scale, causal):
+    """A scale other than head_dim ** -0.5, in the forward and every gradient."""
+    sl = _sl()
+    B, Ls, hq, hkv, hd = 2, 150, 8, 4, 40
+    case = (B, Ls, hq, hkv, hd, causal, None)
+    x, lv = _diff_inputs(case, dt, seed=21)
+    d = {n: _dev(t, dt) for n, t in x.items()}
+    p = sl.DiffAttnParams(dict(zip(sl.DiffAttnParams.NAMES, (torch.from_numpy(t).cuda() for t in lv))), (hq, hkv, hd),
+                          lambda_init=0.6, scale=scale, causal=causal)
+    lay = sl.Layout([Ls] * B, Ls)
+    a, buf = sl.diff_attn_fwd(p, d["q"], d["k"], d["v"], lay)
+    g = sl.diff_attn_bwd(p, d["q"], d["k"], d["v"], a, lay, buf, d["da"])
+    ref = O.diff_attention(x["q"], x["k"], x["v"], lv, 0.6, B, (hq, hkv, hd), float(np.float32(scale)), causal, None,
+                           x["da"], rnd=HALF["bf16"] if dt == "bf16" else 0.0)
+    for n, got in [("a", a)] + sorted(g.items()):
+        half = U32 if n.startswith("dl") else HALF[dt]
+        _within(got, ref[n], half * np.abs(ref[n]) + ref["bound"][n] * (1 + half) + 1e-30, n)
+
+
+# more than 4096 tokens, in groups of four that the norm's backward walks twice and three
+# times over its blocks, the last group not whole
+WALK = [  # as ROT
+    (1, 4099, 2, 1, 32, 32, False, "none", 1.0),
+    (3, 2731, 3, 1, 16, 8, True, "linear", 4.0),
+    (1, 4101, 1, 1, 250, 250, False, "none", 1.0),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", WALK, ids=lambda c: "x".join(map(str, c)))
+def test_rotary_and_head_norm_over_many_tokens(case, dt):
+    test_rotary_and_head_norm(case, dt, "near")
