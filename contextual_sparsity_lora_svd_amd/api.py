@@ -545,6 +545,19 @@ def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, de
     raise SparseLoraError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
+def _refuse_overlap(outs, ins, in_place=()):
+    """Refuse outputs ((name, tensor) pairs, None left out) that share memory with each
+    other or with an input, but the ``in_place`` pairs (output, input) of the same rows.
+    Only outputs that a caller gives can."""
+    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+    outs = [(n, span(t)) for n, t in outs if t is not None]
+    ins = [(n, span(t)) for n, t in ins if t is not None]
+    for i, (n, o) in enumerate(outs):
+        for m, x in outs[:i] + ins:
+            if o[0] < x[1] and x[0] < o[1] and not (o == x and (n, m) in in_place):
+                raise SparseLoraError(f"{n} and {m} may not share memory here")
+
+
 def _current(t: torch.Tensor) -> Optional[int]:
     """The current device, where there is one to ask for."""
     return torch.cuda.current_device() if t.is_cuda else None
@@ -607,13 +620,16 @@ def _pair_ptrs(names, q, k, T, heads, dtype, dev):
     return qp, kp
 
 
+_IN_PLACE = (("q_out", "q"), ("k_out", "k"))
+
+
 def rotary(q: torch.Tensor, k: Optional[torch.Tensor], layout: Layout, heads: Sequence[int], rot: Rotary,
            pos: Optional[torch.Tensor] = None, inverse: bool = False,
            out: Optional[Sequence[Optional[torch.Tensor]]] = None):
     """(q, k) [T, H * head_dim] with the position rotation applied to every
     head; ``inverse`` turns back, which is the gradient.  ``pos`` [T] int32,
-    or None: the row's place in its sequence.  ``out`` may hold q and k
-    themselves.  k may be None."""
+    or None: the row's place in its sequence.  ``out`` (for q, for k) may hold
+    q and k themselves, each in its own place.  k may be None."""
     dt, T, dev = _dtype_code(q), layout.batch * layout.seq_len, _current(q)
     qp, kp = _pair_ptrs(("q", "k"), q, k, T, heads, q.dtype, dev)
     if out is None:
@@ -624,6 +640,7 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], layout: Layout, heads: Se
         if (k is None) != (ko is None):
             raise SparseLoraError("out must hold a tensor for each input")
         qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, T, heads, q.dtype, dev)
+        _refuse_overlap((("q_out", qo), ("k_out", ko)), (("q", q), ("k", k), ("pos", pos), ("turns", rot.turns)), _IN_PLACE)
     r = rot._c(pos, T, dev)
     _check(lib().sl_rotary_apply(dt, layout.ref, _heads_ref(tuple(heads))[1], ctypes.byref(r), qp, kp, qop, kop,
                                  int(inverse), _stream()), "sl_rotary_apply")
@@ -655,6 +672,7 @@ def head_norm_fwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, 
     else:
         qo, ko = out
         qop, kop = _pair_ptrs(("q_out", "k_out"), qo, ko, T, heads, q.dtype, dev)
+        _refuse_overlap((("q_out", qo), ("k_out", ko)), (("q", q), ("k", k), ("wq", wq), ("wk", wk), ("pos", pos)), _IN_PLACE)
     r = ctypes.byref(rot._c(pos, T, dev)) if rot is not None else None
     _check(lib().sl_head_norm_fwd(dt, layout.ref, _heads_ref(tuple(heads))[1], r, eps, qp, kp, wqp, wkp, qop, kop,
                                   _stream()), "sl_head_norm_fwd")
@@ -666,13 +684,15 @@ def head_norm_bwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, 
                   rot: Optional[Rotary] = None, pos: Optional[torch.Tensor] = None, eps: float = 1e-6,
                   buf: Optional[HeadNormWorkspace] = None, out: Optional[Dict[str, torch.Tensor]] = None):
     """Gradients dq, dk (call dtype) and dwq, dwk (fp32) of head_norm_fwd; q
-    and k are its inputs."""
+    and k are its inputs.  ``out`` may hold results to write into: dq may be
+    dq_out or q, and dk dk_out or k."""
     dt, T, dev, hd = _dtype_code(q), layout.batch * layout.seq_len, _current(q), heads[2]
     qp, kp = _pair_ptrs(("q", "k"), q, k, T, heads, q.dtype, dev)
     gqp, gkp = _pair_ptrs(("dq_out", "dk_out"), dq_out, dk_out, T, heads, q.dtype, dev)
     wqp = _check_rows("wq", wq, (hd,), torch.float32, dev)
     wkp = None if wk is None else _check_rows("wk", wk, (hd,), torch.float32, dev)
     buf = buf or HeadNormWorkspace(layout, heads, q.device)
+    given = bool(out)
     out = dict(out or {})
     for n, x, w in (("q", q, wq), ("k", k, wk)):
         if x is not None:
@@ -683,6 +703,10 @@ def head_norm_bwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, 
     dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out.get("dk"), T, heads, q.dtype, dev)
     dwq = _check_rows("dwq", out["dwq"], (hd,), torch.float32, dev)
     dwk = _check_rows("dwk", out["dwk"], (hd,), torch.float32, dev) if "dwk" in out else None
+    if given:
+        _refuse_overlap([(n, out.get(n)) for n in ("dq", "dk", "dwq", "dwk")],
+                        (("q", q), ("k", k), ("wq", wq), ("wk", wk), ("dq_out", dq_out), ("dk_out", dk_out), ("pos", pos),
+                         ("ws", buf.ws)), (("dq", "dq_out"), ("dk", "dk_out"), ("dq", "q"), ("dk", "k")))
     r = ctypes.byref(rot._c(pos, T, dev)) if rot is not None else None
     _check(lib().sl_head_norm_bwd(dt, layout.ref, _heads_ref(tuple(heads))[1], r, eps, qp, kp, wqp, wkp, gqp, gkp,
                                   dqp, dkp, dwq, dwk, _check_scratch("ws", buf.ws, q), buf.ws.numel(), _stream()),
@@ -774,9 +798,9 @@ def diff_attn_fwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
         raise SparseLoraError("lens belongs to the buffers: give it to DiffAttnWorkspace")
     a = out if out is not None else torch.empty_like(q)
     ap = _check_rows("a", a, q.shape, q.dtype, dev)
-    if ap in (qp, kp, vp):
-        raise SparseLoraError("a may not be q, k or v")
     saved, ns, ws, nw = _diff_buffers(buf, p, layout, q)
+    if out is not None:
+        _refuse_overlap((("a", a),), (("q", q), ("k", k), ("v", v), ("saved", buf.saved), *p.t.items()))
     c = p._c(buf.lens, dev)
     _check(lib().sl_diff_attn_fwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap, saved, ns, ws, nw, _stream()),
            "sl_diff_attn_fwd")
@@ -795,6 +819,7 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
     vp = _check_rows("v", v, k.shape, q.dtype, dev)
     ap = _check_rows("a", a, q.shape, q.dtype, dev)
     gp = _check_rows("da", da, q.shape, q.dtype, dev)
+    given = bool(out)
     out = dict(out or {})
     for n, x in (("dq", q), ("dk", k), ("dv", v)):
         if n not in out:
@@ -804,12 +829,14 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
             out["d" + n] = torch.empty_like(p.t[n])
     dqp, dkp = _pair_ptrs(("dq", "dk"), out["dq"], out["dk"], T, p.heads, q.dtype, dev)
     dvp = _check_rows("dv", out["dv"], v.shape, q.dtype, dev)
-    if len({qp, kp, vp, ap, gp, dqp, dkp, dvp} - {qp, kp, vp, ap, gp}) < 3:
-        raise SparseLoraError("dq, dk and dv may not be inputs or each other")
     shape = (p.heads[2],)
     g = SlDiffAttnGrads(*[_check_rows("d" + n, out["d" + n], shape, torch.float32, dev) for n in p.NAMES])
     buf.ws                                       # made here, if not before
     saved, ns, ws, nw = _diff_buffers(buf, p, layout, q)
+    if given:
+        _refuse_overlap([(n, out[n]) for n in ("dq", "dk", "dv", *("d" + m for m in p.NAMES))],
+                        (("q", q), ("k", k), ("v", v), ("a", a), ("da", da), ("saved", buf.saved), ("ws", buf.ws),
+                         *p.t.items()))
     c = p._c(buf.lens, dev)
     _check(lib().sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap, saved, ns, gp, dqp, dkp, dvp,
                                   ctypes.byref(g), ws, nw, _stream()), "sl_diff_attn_bwd")

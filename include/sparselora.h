@@ -332,8 +332,9 @@ sl_status sl_qkvo_bwd(sl_dtype dt, const sl_layout* lay, const sl_qkvo_weights* 
  * turns and amplitude are host memory; the table is made once per model.
  *
  * sl_rotary_apply: q_out / k_out = the rotated rows; inverse != 0 turns the
- * other way, which is the gradient.  q_out may be q, and k_out k.  k and k_out
- * may both be NULL.  head_dim even, at most 256; rot_dim even, 0..head_dim.
+ * other way, which is the gradient.  q_out may be q, and k_out k; otherwise no
+ * output may overlap an input or the other.  k and k_out may both be NULL.
+ * head_dim even, at most 256; rot_dim even, 0..head_dim.
  * ------------------------------------------------------------------------- */
 typedef enum sl_rope_scaling {
   SL_ROPE_NONE = 0, SL_ROPE_LINEAR = 1, SL_ROPE_BASE = 2, SL_ROPE_WAVELENGTH = 3, SL_ROPE_YARN = 4
@@ -365,7 +366,8 @@ sl_status sl_rotary_apply(sl_dtype dt, const sl_layout* lay, const sl_heads* hea
  *   fwd: q, k -> q_out, k_out (q_out may be q, k_out k; keep x for the backward)
  *   bwd: x = q, k (the forward's inputs) and dq_out, dk_out -> dq, dk and the
  *        fp32 weight gradients dwq, dwk [hd], overwritten, summed over rows and
- *        heads in a fixed order.  dq may be dq_out, and dk dk_out.
+ *        heads in a fixed order.  dq may be dq_out or q, and dk dk_out or k.
+ * Otherwise no output may overlap an input, the workspace or another output.
  * A row whose mean square and eps are both 0 has no norm: its outputs are NaN.
  * ------------------------------------------------------------------------- */
 sl_status sl_head_norm_fwd(sl_dtype dt, const sl_layout* lay, const sl_heads* heads, const sl_rotary* rot,

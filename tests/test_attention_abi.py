@@ -209,3 +209,19 @@ def test_head_norm_workspace_of_calls_without_k(sl):
                                        None)
     assert bwd(need) in (7, 8) and bwd(need - 1) == 6
     assert sl.HeadNormWorkspace(lay, (4, 0, 16), "cpu").ws.numel() == need
+
+
+def test_outputs_over_other_tensors_are_refused(sl):
+    """Outputs that share memory with an input (but where a call works in place),
+    with another output or with the buffers."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(64)
+    a, b, c, mid = x[:16], x[16:32], x[32:48], x[8:24]
+    no = sl.api._refuse_overlap
+    no((("a", a), ("b", b)), (("c", c), ("none", None)))
+    no((("a", a),), (("q", a), ("k", b)), in_place=(("a", "q"),))
+    for outs, ins, same in (((("a", a), ("b", a)), (), ()), ((("a", a), ("b", mid)), (), ()),
+                            ((("a", a),), (("q", a),), ()), ((("a", mid),), (("q", a),), (("a", "q"),)),
+                            ((("a", a), ("b", b)), (("q", b), ("k", a)), (("a", "q"), ("b", "k")))):
+        with pytest.raises(sl.SparseLoraError, match="may not share memory"):
+            no(outs, ins, in_place=same)

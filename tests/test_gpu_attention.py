@@ -597,3 +597,43 @@ WALK = [  # as ROT
 @pytest.mark.parametrize("case", WALK, ids=lambda c: "x".join(map(str, c)))
 def test_rotary_and_head_norm_over_many_tokens(case, dt):
     test_rotary_and_head_norm(case, dt, "near")
+
+
+def test_outputs_over_other_tensors_are_refused_by_every_call():
+    """q and k swapped as outputs, one output given twice, views that overlap in part,
+    vector gradients over parameters: refused before anything is launched."""
+    sl = _sl()
+    lay, heads, E = sl.Layout([6], 6), (2, 2, 16), sl.SparseLoraError
+    flat = torch.randn(8 * 6 * 32, device="cuda")
+    n = 6 * 32
+    q, k, v, da, y, z = (flat[i * n:(i + 1) * n].view(6, 32) for i in range(6))
+    part = flat[n // 2:n // 2 + n].view(6, 32)
+    w, rot = torch.ones(16, device="cuda"), sl.Rotary(16)
+    before = flat.clone()
+    for out in ((k, q), (y, y), (part, y), (y, q)):
+        with pytest.raises(E, match="may not share memory"):
+            sl.rotary(q, k, lay, heads, rot, out=out)
+        with pytest.raises(E, match="may not share memory"):
+            sl.head_norm_fwd(q, k, w, w, lay, heads, rot, out=out)
+    dw = torch.ones(16, device="cuda")
+    for out in ({"dq": k}, {"dq": da}, {"dk": y}, {"dq": z, "dk": z}, {"dwq": dw, "dwk": dw}, {"dwq": w}):
+        with pytest.raises(E, match="may not share memory"):
+            sl.head_norm_bwd(q, k, w, w, lay, heads, y, da, rot, out=out)
+    p = sl.DiffAttnParams({m: torch.ones(16, device="cuda") for m in sl.DiffAttnParams.NAMES}, heads)
+    buf = sl.DiffAttnWorkspace(p, lay, torch.float32, "cuda")
+    with pytest.raises(E, match="may not share memory"):
+        sl.diff_attn_fwd(p, q, k, v, lay, buf=buf, out=part)
+    for out in ({"dq": part}, {"dv": y}, {"dlq1": dw, "dlk2": dw}, {"dlq1": p.t["lk1"]},
+                {"dk": buf.saved[:n * 4].view(torch.float32).view(6, 32)}):
+        with pytest.raises(E, match="may not share memory"):
+            sl.diff_attn_bwd(p, q, k, v, y, lay, buf, da, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(flat, before)
+    # in place, and results beside each other, are as before
+    ref = sl.head_norm_bwd(q, k, w, w, lay, heads, y, da, rot)
+    for over in (("dq_out", "dk_out"), ("q", "k")):
+        t = {"q": q.clone(), "k": k.clone(), "dq_out": y.clone(), "dk_out": da.clone()}
+        g = sl.head_norm_bwd(t["q"], t["k"], w, w, lay, heads, t["dq_out"], t["dk_out"], rot,
+                             out={"dq": t[over[0]], "dk": t[over[1]]})
+        for m in ref:
+            assert torch.equal(ref[m], g[m]), m
