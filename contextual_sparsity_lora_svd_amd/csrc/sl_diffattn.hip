@@ -16,25 +16,42 @@ struct DiffPlan {
 // of them, or 64 with two waves to a row taking turns at the tiles, which doubles
 // the workgroups and halves their length but loads each tile for half the rows.
 // The second kind is taken where the first leaves CUs idle: while there are not
-// more than 256 of the second, and, of causal workgroups (whose lengths differ, so
-// that the longest decides), up to 256 or, in long sequences, 512 of the first.
-// Measured, 128 / 64 rows, heads of 128, dQ and dK/dV apart: 1 x 1024 of 16 heads,
-// 8 kv (64 workgroups of 128) 64 / 47 and 73 / 55 us; causal 1 x 2048 of 8 (64)
-// 112 / 72 and 125 / 84, 1 x 4096 of 16 (256) 221 / 185 and 249 / 207, but 2 x 1024
-// of 32 (256) 76 / 75 and 81 / 86, 1 x 4096 of 32 (512) 345 / 400 and 388 / 455.
+// more than 256 of the second; and, of causal workgroups, whose lengths differ so
+// that the longest decides, where one round of the first is to end early, up to 256
+// of them in long sequences and fewer in short ones, whose set-up weighs more.
+// Measured, 128 / 64 rows for dQ, dK and dV together, heads of 128, 128-row
+// workgroups in brackets.  Not causal: 1 x 1024 (128) 163 / 133 us, 1 x 1280 (160)
+// 191 / 249.  Causal: 16 x 128 (192) 85 / 118, 4 x 256 (96) 91 / 83, 8 x 256 (192) 96 / 122,
+// 2 x 512 (128) 115 / 99, 4 x 512 (192) 116 / 131, 2 x 768 (168) 142 / 137 and (216) 143 /
+// 151, 2 x 1024 (192) 162 / 152, (224) 166 / 165, (256) 166 / 171, 1 x 1200 (250) 188 / 190,
+// 1 x 1536 (240) 216 / 202 and (264) 221 / 248, 1 x 2048 (256) 263 / 232 and (272) 274 /
+// 294, 1 x 4096 (256) 460 / 361, (288) 480 / 463 and (384) 508 / 564.  Narrower heads lean to
+// the second: 2 x 1024 (256) of 64, 115 / 105.
 static int bwd_rows(const DiffArgs& a, int n) {   // n workgroups per block of rows
-  return filled(a, 64) * n <= 256 || (a.causal && filled(a, 128) * n < (a.L > 1024 ? 512 : 256)) ? 64 : 128;
+  const int most = a.L < 1280 ? 96 + a.L / 8 : 256;
+  return filled(a, 64) * n <= 256 || (a.causal && filled(a, 128) * n <= most) ? 64 : 128;
 }
 
-// Parts that a kv group's heads are cut into for dK and dV, while there are fewer
-// workgroups than two rounds of 256; short loops are not worth the launch that
-// adds them.
-static int dkv_split(sl_dtype dt, int B, int L, int hp, int gp) {
+// Parts that a kv group's heads are cut into for dK and dV: while there are fewer
+// workgroups than one round of 256, or, of causal ones (their lengths differ), two;
+// not where all tiles of the group are so few (fp32: one for each of the four waves)
+// that the launch which adds the parts costs what they save.  Padding counts as rows,
+// since the workspace's size does not know the lengths.
+// Measured, the whole backward with 1 / 2 / 4 parts, 32 + 8 heads of 128 (workgroups
+// with one part in brackets, bf16 of 128 keys):
+//   bf16 causal 1 x 128 (4) 82 / 78 / 76 us, 4 x 128 (16) 83 / 83 / 81, 16 x 128 of 64 (64)
+//   64 / 67 / 71, 1 x 1024 (32) 206 / 158 / 135, 2 x 1024 (64) 230 / 188 / 183, 1 x 4096 (128)
+//   786 / 640 / 622, 2 x 4096 (256) 1200 / 1176 / 1231; not causal 1 x 2048 (64) 416 / 334 / 326,
+//   4 x 1024 of 64 (128) 212 / 215 / 232
+//   fp32 causal 1 x 32 (4) 86 / 88 / 89, 1 x 64 (8) 104 / 89 / 89, 4 x 128 (64) 143 / 113 / 100,
+//   1 x 1024 (128) 771 / 497 / 385, 2 x 1024 (256) 926 / 690 / 747; not causal 1 x 1024 (128)
+//   878 / 599 / 615, 2 x 1024 (256) 1132 / 1161 / 1202
+static int dkv_split(sl_dtype dt, int B, int L, int hp, int gp, bool causal) {
   const int rows = dt == SL_F32 ? 32 : 128, grp = hp / gp;
   const long long n = (long long)((L + rows - 1) / rows) * B * gp;
   int s = 1;
-  if (grp * ((L + 31) / 32) <= 16) return s;
-  while (s < grp && n * s < 512) {
+  if (grp * ((L + 31) / 32) <= (dt == SL_F32 ? 4 : 16)) return s;
+  while (s < grp && n * s < (causal ? 512 : 256)) {
     ++s;
     while (grp % s) ++s;
   }
@@ -67,7 +84,7 @@ static sl_status diff_plan(sl_dtype dt, const sl_layout* lay, const sl_heads* hs
   pl.dsum = w.take(stats * 4);
   // a partial sum of dlambda per wave, 4 to a workgroup of 32 rows or more
   pl.dlam = w.take(4 * (size_t)((lay->seq_len + 31) / 32) * lay->batch * (hq / 2) * 8);
-  pl.split = dkv_split(dt, lay->batch, lay->seq_len, hq / 2, hkv / 2);
+  pl.split = dkv_split(dt, lay->batch, lay->seq_len, hq / 2, hkv / 2, true);   // the most parts
   pl.part_elems = T * hkv * hd;
   pl.part = w.take(pl.split > 1 ? 2 * (size_t)pl.split * pl.part_elems * 4 : 0);
   pl.ws = w.off;
@@ -175,12 +192,12 @@ extern "C" sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const s
   saved_args(a, pl, const_cast<void*>(saved));
   a.dsum = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.dsum);
   a.dlam_part = reinterpret_cast<double*>(reinterpret_cast<char*>(ws) + pl.dlam);
-  a.split = pl.split;
+  a.split = dkv_split(dt, a.B, a.L, a.hp, a.gp, a.causal != 0);
   a.dq_rows = dt == SL_F32 ? 32 : bwd_rows(a, a.hp);
   a.dkv_rows = dt == SL_F32 ? 32 : bwd_rows(a, a.gp * a.split);
   a.npart = 4 * ((a.L + a.dq_rows - 1) / a.dq_rows) * a.B * a.hp;
   a.dk_part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + pl.part);
-  a.dv_part = a.dk_part + pl.split * pl.part_elems;
+  a.dv_part = a.dk_part + a.split * pl.part_elems;
   a.dlq1 = g->dlq1; a.dlk1 = g->dlk1; a.dlq2 = g->dlq2; a.dlk2 = g->dlk2;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dt == SL_BF16) launch_diff_bwd_bf16(a, s);

@@ -531,8 +531,8 @@ def test_norm_of_q_without_kv_heads(dt):
 
 # Sequences of many tiles, so that every ring of tiles wraps several times, in enough
 # workgroups for the launch rules to take the 128-row kernels of every width (the first
-# nine, with a kv group's heads cut into parts of 3 or 4), and past 1024 rows, where the
-# backward's rule for causal sequences changes, on both of its sides.
+# ten, with a kv group's heads cut into parts), and sequences past 1024 rows in both the
+# 128-row and the 64-row kernels.
 LONG = [  # batch, seq, hq, hkv, hd, causal, lens
     (8, 330, 48, 16, 24, True, [330, 330, 329, 330, 257, 300, 290, 330]),
     (2, 330, 48, 16, 32, False, None),
@@ -547,6 +547,7 @@ LONG = [  # batch, seq, hq, hkv, hd, causal, lens
     (4, 1100, 32, 8, 32, True, None),
     (4, 1030, 32, 8, 128, True, [1030, 1029, 1030, 1025]),
     (1, 2060, 32, 8, 72, True, None),
+    (1, 2060, 28, 4, 32, True, None),
     (1, 1100, 8, 4, 64, True, None),
     (1, 1100, 4, 4, 128, False, None),
 ]
