@@ -28,10 +28,13 @@ namespace sl {
 // the CU: causal ones of very different lengths then share it, a long one with a
 // short one (they are dispatched in that order), and the long one has the SIMDs to
 // itself once the other is done; and where there is no second one, it has them
-// from the start.  Measured with four / two, causal, heads of 128 (128-row
-// workgroups): 2 x 1024 tokens of 32 heads (256) 62 / 54 us, 1 x 2048 of 8 (64)
-// 82 / 65, 1 x 4096 of 16 (256) 166 / 153, 1 x 4096 of 32 (512) 233 / 256; not
-// causal, 1 x 1024 of 16 (64) 53 / 44, 1 x 2048 of 32 (256) 123 / 133.
+// from the start: taken while the 128-row workgroups are no more than one round of
+// 256 (causal), or the 64-row ones (not causal).  Measured with four / two, heads of
+// 128 (128-row workgroups in brackets), causal: 4 x 512 tokens of 32 heads (256) 52 / 49 us,
+// of 48 (384) 71 / 73, 2 x 1024 of 32 (256) 67 / 62, 2 x 1280 of 32 (320) 77 / 82, 1 x 2048 of
+// 8 (64) 82 / 65, of 32 (256) 97 / 89, of 48 (384) 111 / 125, 1 x 4096 of 16 (256) 160 / 144,
+// of 24 (384) 181 / 200, of 32 (512) 217 / 253; not causal, 1 x 1024 of 32 (128) 62 / 57, 1 x
+// 1280 of 32 (160) 70 / 81, 1 x 2048 of 32 (256) 115 / 126.
 template <int D, int RB>
 __global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
   using R = RowTile<D>;
@@ -374,7 +377,7 @@ void launch_diff_fwd_bf16(const DiffArgs& a, hipStream_t s) {
   auto grid = [&](int rows) { return dim3((unsigned)((a.L + rows - 1) / rows * n)); };
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (a.causal ? filled(a, 128) * a.hp >= 512 : filled(a, 64) * a.hp > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
+    if (filled(a, a.causal ? 128 : 64) * a.hp > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
     else hipLaunchKernelGGL((diff_fwd_lds<D, 2>), grid(64), dim3(256), 0, s, a);
   });
 }

@@ -550,6 +550,7 @@ LONG = [  # batch, seq, hq, hkv, hd, causal, lens
     (1, 2060, 28, 4, 32, True, None),
     (1, 1100, 8, 4, 64, True, None),
     (1, 1100, 4, 4, 128, False, None),
+    (1, 700, 4, 2, 88, True, None),
 ]
 
 
