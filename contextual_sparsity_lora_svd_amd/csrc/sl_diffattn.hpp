@@ -157,6 +157,10 @@ __device__ inline float lambda_of(const DiffArgs& a, float& e1, float& e2) {
   return e1 - e2 + a.lambda_init;
 }
 
+// Whether a row reads a single key.  Its weights are 1 whatever the scores, so its
+// score gradients are 0, which D, summed from rounded values, leaves only nearly so.
+__device__ inline bool one_key(const DiffArgs& a, int row, int len) { return len == 1 || (a.causal && row == 0); }
+
 constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ inline void zero16(f32x16& x) {

@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
     lds_barrier();
   }
   unsigned char* const st = smem + rb * 32 * P2;
+  const bool some = rok && !one_key(a, row, len);
   auto stage = [&](const f32x16 (&x)[DT], int m, float f) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
         if (d >= a.hd) continue;
         float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = rok ? x[t][i + e] * f : 0.f;
+        for (int e = 0; e < 4; ++e) y[e] = some ? x[t][i + e] * f : 0.f;
         store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + m * a.hd + d, y[0], y[1], y[2], y[3]);
       }
   };
@@ -494,6 +495,8 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
           for (int e = e0; e < e1; ++e) {
             if (e % 4 == 0) stats(d4, e + 4, 2);
             s[e / 16][e % 16] *= dp[e % 16] - part4(d4[(e / 4) & 1], e);
+            if constexpr (DIAG && e0 % 16 == 0)   // the first query reads the first key alone
+              if (e % 16 == 0 && q0 + 4 * h == 0) s[e / 16][0] = 0.f;
           }
         }
         if constexpr (i == N1 + N2 + N3 - 1) {
@@ -557,7 +560,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   unsigned char* const st = smem + wave * 32 * P2;
   const int row0 = k0 + rb * 32, rows = a.L - row0 < 32 ? a.L - row0 : 32;
   const long long roff = (tok0 + row0) * ldk + g * 2 * a.hd, poff = (long long)part * a.B * a.L * ldk + roff;
-  auto put = [&](const f32x16 (&x)[DT], int m, float f, bf16* out, float* parts, bool last) __attribute__((always_inline)) {
+  auto put = [&](const f32x16 (&x)[DT], int m, float f, bool ok, bf16* out, float* parts, bool last) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
         if (d >= a.hd) continue;
         float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = kok ? x[t][i + e] * f : 0.f;
+        for (int e = 0; e < 4; ++e) y[e] = ok ? x[t][i + e] * f : 0.f;
         if (a.split > 1) store4<float>(reinterpret_cast<float*>(st + c * P2) + d, y[0], y[1], y[2], y[3]);
         else store4<bf16>(reinterpret_cast<bf16*>(st + c * P2) + m * a.hd + d, y[0], y[1], y[2], y[3]);
       }
@@ -577,12 +580,12 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   bf16* const dvo = reinterpret_cast<bf16*>(a.dv);
   // V's tile has D columns per half: its first DT accumulators are the first
   if (H == 1 || half == 0) {
-    put(dv[0], 0, 1.f, dvo, a.dv_part, false);
-    put(dv[1], 1, 1.f, dvo, a.dv_part, true);
+    put(dv[0], 0, 1.f, kok, dvo, a.dv_part, false);
+    put(dv[1], 1, 1.f, kok, dvo, a.dv_part, true);
   }
   if (H == 1 || half == 1) {
-    put(dk[0], 0, a.scale, dko, a.dk_part, false);
-    put(dk[1], 1, -lam * a.scale, dko, a.dk_part, true);
+    put(dk[0], 0, a.scale, kok && len > 1, dko, a.dk_part, false);
+    put(dk[1], 1, -lam * a.scale, kok && len > 1, dko, a.dk_part, true);
   }
 }
 

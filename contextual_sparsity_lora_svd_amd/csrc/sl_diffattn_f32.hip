@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
   add_waves(dq[1], sm, wave, lane);
   if (wave != 3 || row >= a.L) return;
   T* out = reinterpret_cast<T*>(a.dq) + qoff;
+  const bool some = !one_key(a, row, len);
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const float f = m ? -lam * a.scale : a.scale;
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(256, 1) diff_dq_direct(const DiffArgs a) {
       for (int i = 0; i < 16; i += 4) {
         const int d = 32 * t + 2 * i + 4 * h;
         if (d >= a.hd) continue;
-        store4<T>(out + m * a.hd + d, dq[m][t][i] * f, dq[m][t][i + 1] * f, dq[m][t][i + 2] * f, dq[m][t][i + 3] * f);
+        store4<T>(out + m * a.hd + d, some ? dq[m][t][i] * f : 0.f, some ? dq[m][t][i + 1] * f : 0.f,
+                  some ? dq[m][t][i + 2] * f : 0.f, some ? dq[m][t][i + 3] * f : 0.f);
       }
   }
 }
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_direct(const DiffArgs a) {
           const int q = q0 + 8 * (i >> 2) + 4 * h + (i & 3);
           const float p = a.causal && key > q ? 0.f : fast_exp2(fmaf(s[m][i], sc, -sl[i]));
           w[i] = m ? w[i] - lam * p : p;
-          s[m][i] = p * (dp[i] - sd[i]);
+          s[m][i] = one_key(a, q, len) ? 0.f : p * (dp[i] - sd[i]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);

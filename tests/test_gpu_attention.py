@@ -639,3 +639,22 @@ def test_outputs_over_other_tensors_are_refused_by_every_call():
                              out={"dq": t[over[0]], "dk": t[over[1]]})
         for m in ref:
             assert torch.equal(ref[m], g[m]), m
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [(3, 1, 8, 4, 64, True, None), (2, 1, 6, 2, 128, False, None), (4, 9, 4, 2, 40, False, [1, 9, 0, 1]),
+                                  (3, 70, 8, 2, 96, True, [70, 1, 33]), (6, 140, 32, 32, 128, True, None)],
+                         ids=lambda c: "x".join(map(str, c[:6])))
+def test_rows_with_a_single_key(case, dt):
+    """The weight of a single key is 1 whatever its score: the first row of a causal
+    sequence, and a sequence of one row, have no gradient to their scores at all."""
+    sl = _sl()
+    B, Ls, hq, hkv, hd, causal, lens = case
+    x, lv = _diff_inputs(case, dt, seed=14)
+    _, d, _, a, g, _ = _run_diff(sl, case, dt, x, lv)
+    _check_diff(case, dt, x, lv, a, g)
+    for b, n in enumerate(lens or [Ls] * B):
+        if n and (causal or n == 1):
+            assert not g["dq"][b * Ls].any()
+        if n == 1:
+            assert not g["dk"][b * Ls].any() and g["dv"][b * Ls].any()
