@@ -43,6 +43,7 @@ struct DiffArgs {
   int ls;                    // L + 1: statistics of one row more than there are, past every length
   int causal, mix, npart, split;   // mix: the sequences' lengths differ
   int dq_rows, dkv_rows;     // bf16: rows, or keys, of a workgroup
+  int fine;                  // bf16: weights and score gradients enter their products as two bf16 values
   int lens[SL_MAX_SEQS];
 };
 

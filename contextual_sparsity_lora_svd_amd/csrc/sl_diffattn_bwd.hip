@@ -301,9 +301,13 @@ __global__ void __launch_bounds__(256, 1) diff_dq_lds(const DiffArgs a) {
 // are cut into `split` parts where one workgroup per key block would leave CUs
 // idle; the parts' sums are then fp32 and diff_dkv_sum adds them in order.
 //
+// P_1 - lambda P_2 and dS are rounded to bf16 for the matrix cores, dS once where dQ's
+// is the sum of two: a key's column of dS does not sum to zero.  In short sequences
+// both are the sum of two (FINE; where and why: kFineRows).
+//
 // Bound as dQ (62 % of the wave's cycles issue, 23 % wait; at D = 128 144 of 344
 // vector instructions a tile move accumulators): the same call 157 us, 875 TFLOP/s.
-template <int D, int H>
+template <int D, int H, bool FINE>
 __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
   using R = RowTile<D>;
   constexpr int DT = D / 32, NT = D / 16, KS = D / 16, NST = 2, PW = R::PER_WAVE, STEP = H * R::BYTES, NB = 4 / H;
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
       const unsigned char* gt = sg + (it & 1) * STEP + half * R::BYTES;
       const float* st = reinterpret_cast<const float*>(ss + (it & 1) * STAT) + 32 * half + 4 * h;
       f32x16 s[2], dp, w;
-      Frag<bf16> wf[2], df[2][2], fa[AHEAD], fb[AHEAD];
+      Frag<bf16> wf[2], wl[2], df[2][2], dl[2][2], fa[AHEAD], fb[AHEAD];
       float4 l4[2], d4[2];
       zero16(s[0]);
       zero16(s[1]);
@@ -455,9 +459,11 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
           else mma(dp, fa[i % AHEAD], fb[i % AHEAD]);
         } else if constexpr (i < N1 + N2 + N3) {
           mma(dv[(i - N1 - N2) % NT / DT][(i - N1 - N2) % DT], fa[i % AHEAD], wf[(i - N1 - N2) / NT]);
+          if constexpr (FINE) mma(dv[(i - N1 - N2) % NT / DT][(i - N1 - N2) % DT], fa[i % AHEAD], wl[(i - N1 - N2) / NT]);
         } else {
           constexpr int j = i - N1 - N2 - N3, mt = j % (2 * DT);
           mma(dk[mt / DT][mt % DT], fa[i % AHEAD], df[mt / DT][j / (2 * DT)]);
+          if constexpr (FINE) mma(dk[mt / DT][mt % DT], fa[i % AHEAD], dl[mt / DT][j / (2 * DT)]);
         }
         read(std::integral_constant<int, i + AHEAD>{});
         if constexpr (i % (4 / H) == 1 && i / (4 / H) < H * PW) issue_part(it + 1, i / (4 / H));
@@ -486,8 +492,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
           }
         }
         if constexpr (i == N1 + N2 - 1) {
-          wf[0] = acc_frag<bf16>(w, 0);
-          wf[1] = acc_frag<bf16>(w, 1);
+          operand<FINE>(w, wf, wl);
         }
         if constexpr (i >= N1 + N2 && i < N1 + N2 + N3) {
           constexpr int e0 = 32 * (i - N1 - N2) / N3, e1 = 32 * (i - N1 - N2 + 1) / N3;
@@ -501,10 +506,7 @@ __global__ void __launch_bounds__(256, 1) diff_dkv_lds(const DiffArgs a) {
         }
         if constexpr (i == N1 + N2 + N3 - 1) {
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            df[m][0] = acc_frag<bf16>(s[m], 0);
-            df[m][1] = acc_frag<bf16>(s[m], 1);
-          }
+          for (int m = 0; m < 2; ++m) operand<FINE>(s[m], df[m], dl[m]);
         }
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -596,8 +598,13 @@ void launch_diff_bwd_bf16(const DiffArgs& a, hipStream_t s) {
     const dim3 dq((unsigned)(blocks(a.dq_rows) * a.hp)), dkv((unsigned)(blocks(a.dkv_rows) * a.gp * a.split + 1));
     if (a.dq_rows == 64) hipLaunchKernelGGL((diff_dq_lds<D, 2>), dq, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((diff_dq_lds<D, 1>), dq, dim3(256), 0, s, a);
-    if (a.dkv_rows == 64) hipLaunchKernelGGL((diff_dkv_lds<D, 2>), dkv, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((diff_dkv_lds<D, 1>), dkv, dim3(256), 0, s, a);
+    if (a.fine) {
+      if (a.dkv_rows == 64) hipLaunchKernelGGL((diff_dkv_lds<D, 2, true>), dkv, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((diff_dkv_lds<D, 1, true>), dkv, dim3(256), 0, s, a);
+    } else {
+      if (a.dkv_rows == 64) hipLaunchKernelGGL((diff_dkv_lds<D, 2, false>), dkv, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((diff_dkv_lds<D, 1, false>), dkv, dim3(256), 0, s, a);
+    }
   });
   if (a.split > 1) {
     const long long n = 2 * ((long long)a.B * a.L * a.gp * 2 * a.hd / 4);

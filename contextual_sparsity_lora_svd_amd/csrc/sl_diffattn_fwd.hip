@@ -16,8 +16,8 @@ namespace sl {
 // least 1 loses nothing to small weights).  A row whose sum passes 2^64 makes
 // the workgroup go again, after a pass that finds every row's maximum.
 //
-// The weights are rounded to bf16 for the matrix cores (half a step, 2^-8); their
-// sum is not.
+// The weights are rounded to bf16 for the matrix cores (half a step, 2^-8), in short
+// sequences to the sum of two (FINE; where and why: kFineRows); their sum is not.
 //
 // Bound by the matrix cores and, beside them, the issue of two waves' other
 // instructions: 1 x 4096 tokens, 32 heads, 8 kv, of 128, take 404 us (1020
@@ -35,7 +35,7 @@ namespace sl {
 // 8 (64) 82 / 65, of 32 (256) 97 / 89, of 48 (384) 111 / 125, 1 x 4096 of 16 (256) 160 / 144,
 // of 24 (384) 181 / 200, of 32 (512) 217 / 253; not causal, 1 x 1024 of 32 (128) 62 / 57, 1 x
 // 1280 of 32 (160) 70 / 81, 1 x 2048 of 32 (256) 115 / 126.
-template <int D, int RB>
+template <int D, int RB, bool FINE>
 __global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
   using R = RowTile<D>;
   constexpr int NT = D / 16, KS = D / 16, WAVES = 2 * RB, ROWS = 32 * RB;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
         const unsigned char* vt = sv + (i & (NST - 1)) * R::BYTES;
         const unsigned char* kt = sk + ((i + 1) & (NST - 1)) * R::BYTES;
         f32x16 nx;
-        Frag<bf16> p[2], fa[AHEAD];
+        Frag<bf16> p[2], lo[2], fa[AHEAD];
         const float ms = mx * sc;
         float ts = 0.f;
         zero16(nx);
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
             const float w = fast_exp2(fmaf(s[8 * half + e], sc, -ms));
             ts += w;
             p[half].v[e] = (__bf16)w;
+            if constexpr (FINE) lo[half].v[e] = (__bf16)(w - (float)p[half].v[e]);
           }
         };
         each<AHEAD>(read);
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(RB * 128, 2) diff_fwd_lds(const DiffArgs a) {
           constexpr int g = decltype(gc)::value;
           if constexpr (g < KS) mma(nx, fa[g % AHEAD], q[g]);
           else mma(o[(g - KS) % NT], fa[g % AHEAD], p[(g - KS) / NT]);
+          if constexpr (FINE && g >= KS) mma(o[(g - KS) % NT], fa[g % AHEAD], lo[(g - KS) / NT]);
           read(std::integral_constant<int, g + AHEAD>{});
           if constexpr (g % 2 == 1 && g / 2 < PW) {
             issue_part(kbase, sk, i + DIST + 1, g / 2);
@@ -377,8 +379,14 @@ void launch_diff_fwd_bf16(const DiffArgs& a, hipStream_t s) {
   auto grid = [&](int rows) { return dim3((unsigned)((a.L + rows - 1) / rows * n)); };
   by_width(a.hd, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (filled(a, a.causal ? 128 : 64) * a.hp > 256) hipLaunchKernelGGL((diff_fwd_lds<D, 4>), grid(128), dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((diff_fwd_lds<D, 2>), grid(64), dim3(256), 0, s, a);
+    const bool four = filled(a, a.causal ? 128 : 64) * a.hp > 256;
+    if (a.fine) {
+      if (four) hipLaunchKernelGGL((diff_fwd_lds<D, 4, true>), grid(128), dim3(512), 0, s, a);
+      else hipLaunchKernelGGL((diff_fwd_lds<D, 2, true>), grid(64), dim3(256), 0, s, a);
+    } else {
+      if (four) hipLaunchKernelGGL((diff_fwd_lds<D, 4, false>), grid(128), dim3(512), 0, s, a);
+      else hipLaunchKernelGGL((diff_fwd_lds<D, 2, false>), grid(64), dim3(256), 0, s, a);
+    }
   });
 }
 

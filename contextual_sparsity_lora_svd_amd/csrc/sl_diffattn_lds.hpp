@@ -159,6 +159,17 @@ __device__ inline void set2(Frag<bf16>& f, int i, uint32_t v) {
   f.v = __builtin_bit_cast(bf16x8, w);
 }
 
+// Accumulator values as operands rounded to bf16 (half a step, 2^-8) and, if FINE, what
+// the rounding dropped as second operands (2^-16 left).
+template <bool FINE> __device__ inline void operand(const f32x16& x, Frag<bf16> (&hi)[2], Frag<bf16> (&lo)[2]) {
+  hi[0] = acc_frag<bf16>(x, 0);
+  hi[1] = acc_frag<bf16>(x, 1);
+  if constexpr (FINE) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) lo[e / 8].v[e % 8] = (__bf16)(x[e] - (float)hi[e / 8].v[e % 8]);
+  }
+}
+
 // Accumulators to LDS, and added to from there; 4 KB per tile.
 template <int N> __device__ inline void put_acc(const f32x16 (&x)[N], unsigned char* p, int lane) {
 #pragma unroll

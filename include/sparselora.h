@@ -401,8 +401,17 @@ sl_status sl_head_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_heads* he
  *   bwd: q, k, v, a (the forward's) and da -> dq, dk, dv and the fp32 gradients
  *        of the four vectors, overwritten.  Sums run in a fixed order.
  * No output may overlap an input, the buffers or another output.  The backward
- * takes the forward's inputs, p and `saved` as they were.  bf16: |v| below 2^63
- * (the weights are kept relative to 2^64 of a row's first maximum).
+ * takes the forward's inputs, p and `saved` as they were.  Every value of a valid
+ * row is read: a non-finite one in row j of q, k, v, a or da, a key that the causal
+ * mask hides among them, may reach any row of its sequence.  A row that reads one key has
+ * no gradient to its scores.
+ * bf16: sums, softmax statistics and the vectors' gradients are fp32 or fp64.
+ * Operands of the matrix cores are bf16: in sequences (seq_len) of more than 256 rows
+ * the weights and the score gradients of dk are rounded to it once (2^-8; a, dk and
+ * dv are then off by 1.3 to 1.5 times their own rounding to bf16), in shorter ones, and for dq
+ * always the score gradients, to the sum of two (2^-16).  `saved` keeps the second
+ * map's output in 16 bits and a's rounding in 8.  fp32 calls round nothing.
+ * |v| below 2^63 (the weights are kept relative to 2^64 of a row's first maximum).
  * Hq and Hkv even, Hq a multiple of Hkv; hd a multiple of 8, at most 128; every
  * tensor fewer than 2^31 elements.
  * ------------------------------------------------------------------------- */

@@ -89,12 +89,15 @@ def _weights(q, k, scale, causal):
     return s / s.sum(-1, keepdims=True)
 
 
-def diff_attention(q, k, v, lv, lambda_init, batch, heads, scale, causal, lens=None, da=None, rnd=0.0):
+def diff_attention(q, k, v, lv, lambda_init, batch, heads, scale, causal, lens=None, da=None, rnd=0.0, stored=None):
     """Forward, and the backward when da is given.  Returns a dict of values
     and, under "bound", of error bounds for a kernel that keeps sums and
     statistics in fp32 and rounds its matrix operands (softmax weights, score
     gradients, the stored outputs) by at most ``rnd`` relative (0: not at all).
-    The results' own rounding is not in the bounds."""
+    ``stored``: the stored outputs are off by at most so much of their row's
+    largest value instead.  The results' own rounding is not in the bounds."""
+    kept = ((lambda x: rnd * np.abs(x)) if stored is None else
+            (lambda x: np.zeros_like(x) + stored * np.abs(x).max(-1, keepdims=True)))
     hq, hkv, hd = heads
     T = q.shape[0]
     L = T // batch
@@ -135,8 +138,8 @@ def diff_attention(q, k, v, lv, lambda_init, batch, heads, scale, causal, lens=N
             for m, coef in ((0, 1.0), (1, -lam)):
                 D = (G * O[m]).sum(-1, keepdims=True)
                 # D from the stored output and stored P_2 V
-                st = rnd * np.abs(O[0] - lam * O[1]) + bnd["a"][r, ca] if m == 0 else 0.0
-                st = st + (1 if m else 2 * abs(lam)) * (rnd * np.abs(O[1]) + eO[1])
+                st = kept(O[0] - lam * O[1]) + bnd["a"][r, ca] if m == 0 else 0.0
+                st = st + (1 if m else 2 * abs(lam)) * (kept(O[1]) + eO[1])
                 eD = (np.abs(G) * (st + c32 * (np.abs(O[0]) + (1 + abs(lam)) * np.abs(O[1])))).sum(-1, keepdims=True)
                 E = P[m] * (dP - D)
                 eE = P[m] * ((rel[m] + rnd) * np.abs(dP - D) + edP + eD + c32 * (np.abs(dP) + np.abs(D)))

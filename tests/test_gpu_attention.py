@@ -658,3 +658,42 @@ def test_rows_with_a_single_key(case, dt):
             assert not g["dq"][b * Ls].any()
         if n == 1:
             assert not g["dk"][b * Ls].any() and g["dv"][b * Ls].any()
+
+
+SHORT = [  # batch, seq, hq, hkv, hd, causal, lens: at most 256 rows, every width, 64- and 128-row kernels
+    (2, 1, 48, 16, 128, False, None),
+    (4, 2, 8, 4, 32, True, [2, 1, 2, 2]),
+    (1, 3, 2, 2, 80, True, None),
+    (8, 8, 32, 8, 128, True, None),
+    (7, 5, 4, 4, 128, False, [5, 4, 3, 2, 1, 0, 5]),
+    (1, 33, 6, 2, 16, False, None),
+    (1, 89, 8, 4, 96, True, None),
+    (6, 140, 32, 32, 64, False, [140, 0, 129, 1, 64, 97]),
+    (6, 140, 32, 32, 128, True, None),
+    (5, 256, 24, 8, 32, True, None),
+    (3, 256, 24, 8, 96, False, [256, 255, 97]),
+    (2, 255, 6, 2, 128, False, None),
+]
+
+
+@pytest.mark.parametrize("case", SHORT, ids=lambda c: "x".join(map(str, c[:6])))
+def test_bf16_products_of_short_sequences_keep_16_bits(case):
+    """Up to 256 rows the weights and the score gradients enter their products as the
+    sum of two bf16 values, half a step of a half step off (2^-16), O_2 is stored as
+    16-bit integers of its row's largest value and O's rounding as 8-bit ones of the
+    largest rounding (2^-8 of O): both within 2^-15.  The results' own rounding comes
+    on top."""
+    sl = _sl()
+    B, Ls, hq, hkv, hd, causal, lens = case
+    x, lv = _diff_inputs(case, "bf16", seed=17)
+    _, _, _, a, g, _ = _run_diff(sl, case, "bf16", x, lv)
+    ref = O.diff_attention(x["q"], x["k"], x["v"], lv, 0.6, B, (hq, hkv, hd), float(np.float32(hd ** -0.5)), causal,
+                           lens, x["da"], rnd=2.0 ** -16, stored=2.0 ** -15)
+    for n, got in [("a", a)] + sorted(g.items()):
+        half = U32 if n.startswith("dl") else HALF["bf16"]
+        _within(got, ref[n], half * np.abs(ref[n]) + ref["bound"][n] * (1 + half) + 1e-30, n)
+
+
+@pytest.mark.parametrize("hd,causal,L", [(64, True, 300), (128, False, 270), (24, True, 290), (96, False, 300)])
+def test_diff_attention_longer_scores_that_outgrow_the_first_tile(hd, causal, L):
+    test_diff_attention_scores_that_outgrow_the_first_tile(hd, causal, L)
