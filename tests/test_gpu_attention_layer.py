@@ -143,3 +143,37 @@ def test_module_holds_no_scratch_between_forward_and_backward():
     del first, again, u, v
     held = torch.cuda.memory_allocated() - before - da.numel() * 2
     assert held <= out_bytes + slack, held                  # a itself is still here
+
+
+def test_module_step_captured_and_replayed():
+    """Forward and backward of the module in one graph (no eager result of the same
+    leaves alive while it is captured), replayed on inputs that change, with eager
+    steps in between."""
+    import contextual_sparsity_lora_svd_amd as sl
+    heads, lay = (8, 4, 32), sl.Layout([300, 300], 300)
+    core = sl.DiffAttention(heads, rot=sl.Rotary(32), qk_norm=True, generator=torch.Generator().manual_seed(1))
+    x = [torch.randn(600, h * 32, device="cuda").to(torch.bfloat16).requires_grad_(True) for h in (8, 4, 4)]
+    da = torch.randn(600, 256, device="cuda").to(torch.bfloat16)
+
+    def step():
+        a = core(*x, lay, lens=[300, 211])
+        return [a.detach(), *torch.autograd.grad(a, [*x, *core.parameters()], da)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        with torch.no_grad():
+            x[0].copy_(torch.roll(x[0], 1, 0))
+            core.lq1.mul_(0.5 if i % 2 else 2.0)
+        graph.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        for u, v in zip(got, step()):
+            assert torch.equal(u, v)
