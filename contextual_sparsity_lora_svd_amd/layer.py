@@ -300,7 +300,8 @@ class SparseLoRAQKVO(torch.nn.Module):
         if k_vo is None:
             k_vo = s.k(self.layer, step, "vo", self.nkv) if s else self.nkv
         heads = self._heads_around(attention)
-        iqk, ivo = self.channel_sets(X, layout, k_qk, k_vo, heads)
+        other = {} if heads == self.heads else {"heads": heads}
+        iqk, ivo = self.channel_sets(X, layout, k_qk, k_vo, **other)
         lora = {n: getattr(self, n).detach().to(self.dtype).contiguous()
                 for n in ("Aq", "Bq", "Ak", "Bk", "Av", "Bv", "Ao", "Bo")}
         t = dict(self.frozen)
