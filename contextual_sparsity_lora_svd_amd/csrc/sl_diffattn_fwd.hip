@@ -20,8 +20,9 @@ namespace sl {
 // sequences to the sum of two (FINE; where and why: kFineRows); their sum is not.
 //
 // Bound by the matrix cores and, beside them, the issue of two waves' other
-// instructions: 1 x 4096 tokens, 32 heads, 8 kv, of 128, take 404 us (1020
-// TFLOP/s, where a large product reaches 1144 to 1244), causal 228.
+// instructions: 1 x 4096 tokens, 32 heads, 8 kv, of 128, take 375 to 404
+// us (1100 to 1020 TFLOP/s, where a large product reaches 1144 to 1244), causal 198, and
+// 220 to 232 in the first milliseconds after the GPU was idle.
 //
 // RB blocks of 32 queries per workgroup.  Four, with tiles loaded two ahead, move
 // the fewest bytes.  Two, loaded one ahead, leave room for a second workgroup on
