@@ -13,13 +13,13 @@ struct DiffPlan {
 };
 
 // bf16: up to so many rows the weights and the score gradients of dK enter their
-// products as the sum of two bf16 values (2^-16) instead of one (2^-8).  One rounding is
-// an error beside the result's own of 1.3 (O), 1.42 (dV) and 1.44 times (dK) that alone where
-// many terms are summed, up to 2.2 times where few are (2 rows; 1.5 at 33); two leave 1.00 and
-// cost half as many products again of dV and dK and two thirds of the forward's: 8 x 32
-// tokens of 16 + 8 heads of 64 forward 23 -> 24 us, backward 46 -> 46, 4 x 128 of 32 + 8 of 128
-// 33 -> 35 and 83 -> 88, 8 x 256 of 32 of 128 46 -> 51 and 102 -> 108, but 1 x 4096 of 32 + 8
-// 219 -> 304 and 628 -> 724.
+// products as the sum of two bf16 values (2^-16) instead of one (2^-8).  With one the
+// results are off by 1.3 (O), 1.42 (dV) and 1.44 times (dK) their own rounding to bf16 where
+// many terms are summed, and by up to 2.2 times where few are (2 rows; 1.5 at 33); with two
+// by 1.00 times.  Two cost half as many products again of dV and dK and two thirds of
+// the forward's: 8 x 32 tokens of 16 + 8 heads of 64 forward 23 -> 24 us, backward 46 -> 46, 4 x
+// 128 of 32 + 8 of 128 33 -> 35 and 83 -> 88, 8 x 256 of 32 of 128 46 -> 51 and 102 -> 108, but
+// 1 x 4096 of 32 + 8 219 -> 304 and 628 -> 724.
 constexpr int kFineRows = 256;
 
 // Work of the bf16 backward's workgroups: 128 rows (or keys) each, every wave 32
