@@ -21,6 +21,7 @@ SL_F32, SL_BF16 = 0, 1
 SL_CRIT_SWIGLU_L2, SL_CRIT_L2, SL_CRIT_QK_NORM = 0, 1, 2
 SL_MAX_SEQS = 64
 SL_EST_MAXJOBS = 3
+SL_DISTILL_MAX_TOP = 256
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -88,6 +89,15 @@ class SlDiffAttnGrads(ctypes.Structure):
     _fields_ = [("dlq1", _vp), ("dlk1", _vp), ("dlq2", _vp), ("dlk2", _vp)]
 
 
+class SlLayerNorm(ctypes.Structure):
+    _fields_ = [("d_model", _i64), ("centered", _i32), ("eps", ctypes.c_float), ("w", _vp), ("b", _vp)]
+
+
+class SlDistill(ctypes.Structure):
+    _fields_ = [("vocab", _i64), ("top", _i32), ("temperature", ctypes.c_float), ("hard", ctypes.c_float),
+                ("top_ids", _vp), ("top_logits", _vp), ("labels", _vp)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "sl_abi_version": (ctypes.c_int, []),
@@ -153,6 +163,22 @@ SIGNATURES = {
     "sl_diff_attn_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlDiffAttn),
                                         _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp, _vp, _vp,
                                         ctypes.POINTER(SlDiffAttnGrads), _vp, _sz, _vp]),
+    "sl_embed_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), _i64, _i64, ctypes.c_float, _vp, _vp, _vp,
+                                    _vp]),
+    "sl_embed_workspace_bytes": (_sz, [ctypes.POINTER(SlLayout), _i64]),
+    "sl_embed_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), _i64, _i64, ctypes.c_float, _vp, _vp,
+                                    ctypes.c_int, _vp, _vp, _sz, _vp]),
+    "sl_layer_norm_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlLayerNorm), _vp, _vp,
+                                         _vp, _vp, _vp, _vp]),
+    "sl_layer_norm_workspace_bytes": (_sz, [ctypes.POINTER(SlLayout), _i64]),
+    "sl_layer_norm_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlLayerNorm), _vp, _vp,
+                                         _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sl_distill_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlDistill), _vp, _i64, _vp,
+                                      _vp, _vp]),
+    "sl_distill_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlDistill), _vp, _i64, _vp,
+                                      _vp, _vp, _i64, _vp]),
+    "sl_distill_step": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(SlLayout), ctypes.POINTER(SlDistill), _vp, _i64, _vp,
+                                       _vp, _vp, _i64, _vp]),
 }
 
 _lib = None
@@ -841,3 +867,235 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
     _check(lib().sl_diff_attn_bwd(dt, layout.ref, ctypes.byref(c), qp, kp, vp, ap, saved, ns, gp, dqp, dkp, dvp,
                                   ctypes.byref(g), ws, nw, _stream()), "sl_diff_attn_bwd")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Around the layers: token embedding, norm of whole rows, distillation.
+def embed_fwd(E: torch.Tensor, ids: torch.Tensor, layout: Layout, scale: float = 1.0,
+              out: Optional[torch.Tensor] = None):
+    """Y [T, d_model]: scale * E[ids] (ids [T] int32; one outside E's rows is no
+    token, its row of Y is 0)."""
+    dt, T, dev = _dtype_code(E), layout.batch * layout.seq_len, _current(E)
+    V, D = E.shape
+    Ep, ip = _check_rows("E", E, (V, D), E.dtype, dev), _check_rows("ids", ids, (T,), torch.int32, dev)
+    Y = out if out is not None else torch.empty((T, D), dtype=E.dtype, device=E.device)
+    Yp = _check_rows("Y", Y, (T, D), E.dtype, dev)
+    if out is not None:
+        _refuse_overlap((("Y", Y),), (("E", E), ("ids", ids)))
+    _check(lib().sl_embed_fwd(dt, layout.ref, V, D, scale, Ep, ip, Yp, _stream()), "sl_embed_fwd")
+    return Y
+
+
+class EmbedWorkspace:
+    """Reusable scratch of embed_bwd."""
+
+    def __init__(self, layout: Layout, d_model: int, device):
+        self.ws = _bytes_tensor(lib().sl_embed_workspace_bytes(layout.ref, int(d_model)), device)
+
+
+def embed_bwd(ids: torch.Tensor, dY: torch.Tensor, layout: Layout, vocab: int, scale: float = 1.0,
+              grad_dtype: torch.dtype = torch.float32, buf: Optional[EmbedWorkspace] = None,
+              out: Optional[torch.Tensor] = None):
+    """dE [vocab, d_model] of embed_fwd in ``grad_dtype`` (float32, or bfloat16:
+    the fp32 sums rounded once); rows of ids without a token are 0."""
+    dt, T, dev = _dtype_code(dY), layout.batch * layout.seq_len, _current(dY)
+    D = dY.shape[-1]
+    ip, gp = _check_rows("ids", ids, (T,), torch.int32, dev), _check_rows("dY", dY, (T, D), dY.dtype, dev)
+    dE = out if out is not None else torch.empty((vocab, D), dtype=grad_dtype, device=dY.device)
+    dEp = _check_rows("dE", dE, (vocab, D), grad_dtype, dev)
+    buf = buf or EmbedWorkspace(layout, D, dY.device)
+    if out is not None:
+        _refuse_overlap((("dE", dE),), (("ids", ids), ("dY", dY), ("ws", buf.ws)))
+    _check(lib().sl_embed_bwd(dt, layout.ref, vocab, D, scale, ip, gp, _dtype_code(dE), dEp,
+                              _check_scratch("ws", buf.ws, dY), buf.ws.numel(), _stream()), "sl_embed_bwd")
+    return dE
+
+
+class LayerNormWorkspace:
+    """Reusable scratch of layer_norm_bwd."""
+
+    def __init__(self, layout: Layout, d_model: int, device):
+        self.ws = _bytes_tensor(lib().sl_layer_norm_workspace_bytes(layout.ref, int(d_model)), device)
+
+
+def layer_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor], layout: Layout, eps: float = 1e-5,
+                   centered: bool = True, residual: Optional[torch.Tensor] = None, want_stats: bool = True,
+                   out: Optional[Sequence[Optional[torch.Tensor]]] = None):
+    """(y, h, stats): h = x + residual (x itself without one), y its layer norm with
+    weight w and bias b [d_model] (fp32, b may be None), or, not ``centered``, its
+    root-mean-square norm (without a bias).  stats [T, 3] fp32 is what the backward
+    reads (None unless ``want_stats``).  ``out``: tensors for y and h; either may be
+    x or the residual."""
+    y, h = out if out is not None else (None, None)
+    if residual is None and h is not None and h is not x:
+        raise SparseLoraError("h is x where nothing is added")
+    dt, T, dev = _dtype_code(x), layout.batch * layout.seq_len, _current(x)
+    D = x.shape[-1]
+    xp, wp = _check_rows("x", x, (T, D), x.dtype, dev), _check_rows("w", w, (D,), torch.float32, dev)
+    bp = None if b is None else _check_rows("b", b, (D,), torch.float32, dev)
+    rp = None if residual is None else _check_rows("residual", residual, (T, D), x.dtype, dev)
+    y = y if y is not None else torch.empty_like(x)
+    yp = _check_rows("y", y, (T, D), x.dtype, dev)
+    hp = None
+    if residual is not None:
+        h = h if h is not None else torch.empty_like(x)
+        hp = _check_rows("h", h, (T, D), x.dtype, dev)
+    stats = torch.empty((T, 3), dtype=torch.float32, device=x.device) if want_stats else None
+    if out is not None:
+        _refuse_overlap((("y", y), ("h", None if residual is None else h)),
+                        (("x", x), ("residual", residual), ("w", w), ("b", b)),
+                        (("y", "x"), ("y", "residual"), ("h", "x"), ("h", "residual")))
+    c = SlLayerNorm(D, int(centered), eps, wp, bp)
+    _check(lib().sl_layer_norm_fwd(dt, layout.ref, ctypes.byref(c), xp, rp, hp, yp,
+                                   None if stats is None else stats.data_ptr(), _stream()), "sl_layer_norm_fwd")
+    return y, x if residual is None else h, stats
+
+
+def layer_norm_bwd(h: torch.Tensor, w: torch.Tensor, stats: torch.Tensor, layout: Layout, dy: torch.Tensor,
+                   dh: Optional[torch.Tensor] = None, centered: bool = True, bias: bool = True,
+                   buf: Optional[LayerNormWorkspace] = None, out: Optional[Dict[str, torch.Tensor]] = None):
+    """Gradients of layer_norm_fwd: dx (of x and of the residual alike) and dw, db
+    (fp32; db only with ``bias``).  h and stats are the forward's; ``dh`` is the
+    gradient that reaches h by its other way.  ``out`` may hold results to write
+    into: dx may be dy, dh or h."""
+    dt, T, dev = _dtype_code(h), layout.batch * layout.seq_len, _current(h)
+    D = h.shape[-1]
+    hp, wp = _check_rows("h", h, (T, D), h.dtype, dev), _check_rows("w", w, (D,), torch.float32, dev)
+    sp = _check_rows("stats", stats, (T, 3), torch.float32, dev)
+    gp = _check_rows("dy", dy, (T, D), h.dtype, dev)
+    rp = None if dh is None else _check_rows("dh", dh, (T, D), h.dtype, dev)
+    buf = buf or LayerNormWorkspace(layout, D, h.device)
+    given = bool(out)
+    out = dict(out or {})
+    if "dx" not in out:
+        out["dx"] = torch.empty_like(h)
+    for n in ("dw", "db") if bias else ("dw",):
+        if n not in out:
+            out[n] = torch.empty_like(w)
+    dxp = _check_rows("dx", out["dx"], (T, D), h.dtype, dev)
+    dwp = _check_rows("dw", out["dw"], (D,), torch.float32, dev)
+    dbp = _check_rows("db", out["db"], (D,), torch.float32, dev) if bias else None
+    if given:
+        _refuse_overlap([(n, out.get(n)) for n in ("dx", "dw", "db")],
+                        (("h", h), ("w", w), ("stats", stats), ("dy", dy), ("dh", dh), ("ws", buf.ws)),
+                        (("dx", "dy"), ("dx", "dh"), ("dx", "h")))
+    c = SlLayerNorm(D, int(centered), 0.0, wp, None)
+    _check(lib().sl_layer_norm_bwd(dt, layout.ref, ctypes.byref(c), hp, sp, gp, rp, dxp, dwp, dbp,
+                                   _check_scratch("ws", buf.ws, h), buf.ws.numel(), _stream()), "sl_layer_norm_bwd")
+    return out
+
+
+class DistillTargets:
+    """What a batch's logits are held to: the teacher's entries ``top_ids`` [T, top]
+    (int32; one outside the vocabulary is no entry) with their ``top_logits``
+    [T, top] (fp32), compared at ``temperature``, and ``labels`` [T] (int32; one
+    outside the vocabulary is none) with the weight ``hard``.  hard = 0 needs no
+    labels, hard = 1 no entries."""
+
+    def __init__(self, top_ids: Optional[torch.Tensor], top_logits: Optional[torch.Tensor],
+                 labels: Optional[torch.Tensor] = None, temperature: float = 1.0, hard: float = 0.0):
+        self.top_ids, self.top_logits, self.labels = top_ids, top_logits, labels
+        self.temperature, self.hard = float(temperature), float(hard)
+
+    def _c(self, T: int, V: int, dev: Optional[int]) -> SlDistill:
+        ip = tp = lp = None
+        top = 0
+        if self.hard < 1.0:
+            if self.top_ids is None or self.top_logits is None:
+                raise SparseLoraError("top_ids and top_logits are required where hard is below 1")
+            top = self.top_ids.shape[-1]
+            ip = _check_rows("top_ids", self.top_ids, (T, top), torch.int32, dev)
+            tp = _check_rows("top_logits", self.top_logits, (T, top), torch.float32, dev)
+        if self.hard > 0.0:
+            if self.labels is None:
+                raise SparseLoraError("labels are required where hard is above 0")
+            lp = _check_rows("labels", self.labels, (T,), torch.int32, dev)
+        return SlDistill(V, top, self.temperature, self.hard, ip, tp, lp)
+
+
+def _logit_rows(name: str, z: torch.Tensor, T: int, V: int, dtype: torch.dtype):
+    """(pointer, elements from row to row) of [T, V] logits; rows may stand apart."""
+    if z.dim() != 2 or tuple(z.shape) != (T, V) or z.dtype != dtype:
+        raise SparseLoraError(f"{name}: expected {dtype} {(T, V)}, got {z.dtype} {tuple(z.shape)}")
+    if not z.is_cuda or z.get_device() != torch.cuda.current_device():
+        raise SparseLoraError(f"{name}: on {z.device}, not on the current device")
+    ld = z.stride(0) if T > 1 else max(z.stride(0), V)
+    if (V > 1 and z.stride(1) != 1) or ld < V:
+        raise SparseLoraError(f"{name}: elements of a row must be contiguous, and rows apart; strides {tuple(z.stride())}")
+    return z.data_ptr(), ld
+
+
+def _distill_ins(p: DistillTargets, *more):
+    return (*more, ("top_ids", p.top_ids), ("top_logits", p.top_logits), ("labels", p.labels))
+
+
+def _distill_out(p, logits, out, T, V, more=()):
+    """(dlogits, pointer, row stride): made here, or the caller's (logits itself in place)."""
+    dz = out if out is not None else torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    dzp, ld = _logit_rows("dlogits", dz, T, V, logits.dtype)
+    if out is not None and not (dz.data_ptr() == logits.data_ptr() and dz.stride() == logits.stride()):
+        _refuse_spans(("dlogits", dz), _distill_ins(p, ("logits", logits), *more))
+    elif out is not None:
+        _refuse_spans(("dlogits", dz), _distill_ins(p, *more))
+    return dz, dzp, ld
+
+
+def _refuse_spans(out, ins):
+    """_refuse_overlap for an output whose rows stand apart: the memory from its
+    first to its last element."""
+    def span(t):
+        n = sum((s - 1) * st for s, st in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+    o = span(out[1])
+    for n, t in ins:
+        if t is not None:
+            x = span(t)
+            if o[0] < x[1] and x[0] < o[1]:
+                raise SparseLoraError(f"{out[0]} and {n} may not share memory here")
+
+
+def distill_fwd(p: DistillTargets, logits: torch.Tensor, layout: Layout):
+    """(loss [T], stats [T, 4]), fp32: each row's loss against ``p`` (0 for context
+    rows and rows without a target), and what the backward reads.  logits [T, vocab];
+    rows may stand apart, as in a view of a wider buffer."""
+    dt, T, dev = _dtype_code(logits), layout.batch * layout.seq_len, _current(logits)
+    V = logits.shape[-1]
+    zp, ld = _logit_rows("logits", logits, T, V, logits.dtype)
+    c = p._c(T, V, dev)
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    stats = torch.empty((T, 4), dtype=torch.float32, device=logits.device)
+    _check(lib().sl_distill_fwd(dt, layout.ref, ctypes.byref(c), zp, ld, loss.data_ptr(), stats.data_ptr(), _stream()),
+           "sl_distill_fwd")
+    return loss, stats
+
+
+def distill_bwd(p: DistillTargets, logits: torch.Tensor, stats: torch.Tensor, layout: Layout,
+                dloss: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """dlogits [T, vocab] of distill_fwd, with ``dloss`` [T] fp32 the gradient of each
+    row's loss (None: ones).  ``out`` may be logits itself."""
+    dt, T, dev = _dtype_code(logits), layout.batch * layout.seq_len, _current(logits)
+    V = logits.shape[-1]
+    zp, ld = _logit_rows("logits", logits, T, V, logits.dtype)
+    c = p._c(T, V, dev)
+    sp = _check_rows("stats", stats, (T, 4), torch.float32, dev)
+    gp = None if dloss is None else _check_rows("dloss", dloss, (T,), torch.float32, dev)
+    dz, dzp, ldo = _distill_out(p, logits, out, T, V, (("stats", stats), ("dloss", dloss)))
+    _check(lib().sl_distill_bwd(dt, layout.ref, ctypes.byref(c), zp, ld, sp, gp, dzp, ldo, _stream()), "sl_distill_bwd")
+    return dz
+
+
+def distill_step(p: DistillTargets, logits: torch.Tensor, layout: Layout, dloss: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None):
+    """(loss [T], dlogits [T, vocab]) in one call that reads logits from memory once,
+    for a loss whose rows' weights ``dloss`` are known beforehand (None: ones).
+    ``out`` may be logits itself."""
+    dt, T, dev = _dtype_code(logits), layout.batch * layout.seq_len, _current(logits)
+    V = logits.shape[-1]
+    zp, ld = _logit_rows("logits", logits, T, V, logits.dtype)
+    c = p._c(T, V, dev)
+    gp = None if dloss is None else _check_rows("dloss", dloss, (T,), torch.float32, dev)
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    dz, dzp, ldo = _distill_out(p, logits, out, T, V, (("dloss", dloss),))
+    _check(lib().sl_distill_step(dt, layout.ref, ctypes.byref(c), zp, ld, gp, loss.data_ptr(), dzp, ldo, _stream()),
+           "sl_distill_step")
+    return loss, dz

@@ -1,0 +1,420 @@
+// Token embedding: Y[t] = scale * E[id_t], and the table's gradient
+// dE[v] = scale * (sum of dY[t] over the tokens t with id_t = v).
+//
+// Lookup: a row's vectors are read and written once.
+//
+// Gradient: the tokens are sorted by (id, place) first, so that the rows of one
+// id stand in a run whose sum is taken in one fixed order, with no atomics on
+// values.
+//   1. Chunks of kChunk tokens are sorted by counting: a token's place is the
+//      number of tokens of its chunk that sort before it.  16 tokens to a block,
+//      64 comparisons to an instruction, counted as the bits of its mask.
+//   2. Up to 16 sorted lists are merged at a time: a token's place is its place
+//      in its own list plus the number of smaller ones in each other list, a
+//      binary search per lane.
+//   3. The sorted list is cut into pieces.  A wave sums the rows of one piece over
+//      512 columns, in fp32, and writes a run that lies inside its piece to the
+//      table; of a run that crosses a border it keeps the partial sum.  Other
+//      blocks of the same launch write the rows of ids without a token.
+//   4. The partial sums of every crossing run are added in order.
+#include "sl_rows.hpp"
+
+namespace sl {
+
+constexpr int kChunk = 2048;       // tokens sorted by counting
+constexpr int kRankTokens = 16;    // of them in one block
+constexpr int kLists = 16;         // sorted lists merged at a time
+constexpr int kSlice = 512;        // columns of a wave: 8 a lane
+constexpr int kEmptyRows = 16;     // table rows of a block that looks for ids without a token
+constexpr uint32_t kNoKey = 0xFFFFFFFEu;
+
+// ids outside the vocabulary are no tokens: they sort behind every id
+__device__ inline uint32_t token_key(int id, uint32_t V) { return (uint32_t)id < V ? (uint32_t)id : V; }
+
+template <typename T, int U>
+__global__ void __launch_bounds__(256) embed_fwd_kernel(const T* __restrict__ E, const int* __restrict__ ids, uint32_t V,
+                                                        int nvec, int ntok, int lanes_log2, float scale,
+                                                        T* __restrict__ Y) {
+  constexpr int W = 16 / sizeof(T);
+  using VT = Vec<T, W>;
+  const int lanes = 1 << lanes_log2, col = blockIdx.y * lanes + (threadIdx.x & (lanes - 1));
+  const int rows = 256 >> lanes_log2;
+  if (col >= nvec) return;
+  for (long long t0 = (long long)blockIdx.x * rows * U; t0 < ntok; t0 += (long long)gridDim.x * rows * U) {
+    VT v[U];
+    uint32_t id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long t = t0 + u * rows + (threadIdx.x >> lanes_log2);
+      id[u] = t < ntok ? token_key(ids[t], V) : V;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (id[u] < V) v[u] = reinterpret_cast<const VT*>(E)[(long long)id[u] * nvec + col];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long t = t0 + u * rows + (threadIdx.x >> lanes_log2);
+      VT o;
+#pragma unroll
+      for (int j = 0; j < W; ++j) o.v[j] = f2el<T>(id[u] < V ? el2f<T>(v[u].v[j]) * scale : 0.f);
+      if (t < ntok) reinterpret_cast<VT*>(Y)[t * nvec + col] = o;
+    }
+  }
+}
+
+// 1. sid, stok of every chunk in order of (id, token)
+__global__ void __launch_bounds__(256) embed_rank_kernel(const int* __restrict__ ids, uint32_t V, int ntok,
+                                                         uint32_t* __restrict__ sid, int* __restrict__ stok) {
+  constexpr int kGroups = kChunk / kRankTokens, N = kChunk / 256;
+  __shared__ int part[4][kRankTokens];
+  const int base = (int)(blockIdx.x / kGroups) * kChunk, g0 = (int)(blockIdx.x % kGroups) * kRankTokens;
+  const int n = ntok - base < kChunk ? ntok - base : kChunk;
+  if (g0 >= n) return;
+  const int tid = threadIdx.x, own = g0 / 256;   // the tokens of the block stand in this 256
+  // a key at a place behind the block's tokens counts where it is smaller, one
+  // before where it is not larger: key + 1 or key, against the token's key + 1
+  uint32_t key[N], kown = kNoKey;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int p = i * 256 + tid;
+    uint32_t k = p < n ? token_key(ids[base + p], V) : kNoKey;
+    if (i == own) {
+      kown = k;
+      k = kNoKey;
+    }
+    key[i] = i > own ? k + 1 : k;
+  }
+#pragma unroll
+  for (int g = 0; g < kRankTokens; ++g) {
+    const int p = g0 + g;
+    const uint32_t above = (p < n ? token_key(ids[base + p], V) : 0) + 1;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) c += __popcll(__ballot(key[i] < above));
+    c += __popcll(__ballot(kown + (own * 256 + tid >= p) < above));
+    if ((tid & 63) == 0) part[tid >> 6][g] = c;
+  }
+  __syncthreads();
+  if (tid < kRankTokens && g0 + tid < n) {
+    const int at = base + part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+    sid[at] = token_key(ids[base + g0 + tid], V);
+    stok[at] = base + g0 + tid;
+  }
+}
+
+// 2. lists of `len` sorted tokens -> lists of kLists * len
+__global__ void __launch_bounds__(256) embed_merge_kernel(const uint32_t* __restrict__ sid, const int* __restrict__ stok,
+                                                          int ntok, int len, uint32_t* __restrict__ osid,
+                                                          int* __restrict__ ostok) {
+  const int l = threadIdx.x & (kLists - 1);
+  const long long i = (long long)blockIdx.x * (256 / kLists) + threadIdx.x / kLists;
+  const bool on = i < ntok;
+  const int list = on ? (int)(i / len) : 0, mine = list % kLists;
+  const long long first = (long long)(list - mine) * len, start = first + (long long)l * len;
+  const uint32_t id = on ? sid[i] : 0;
+  long long count = 0;
+  if (on && l == mine) {
+    count = i - start;
+  } else if (on && start < ntok) {
+    const uint32_t above = id + (l < mine);   // tokens of an earlier list go first
+    int lo = 0, hi = (int)(ntok - start < len ? ntok - start : len);
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sid[start + mid] < above) lo = mid + 1;
+      else hi = mid;
+    }
+    count = lo;
+  }
+  int c = (int)count;
+#pragma unroll
+  for (int o = kLists / 2; o; o >>= 1) c += __shfl_xor(c, o);
+  if (on && l == 0) {
+    osid[first + c] = id;
+    ostok[first + c] = stok[i];
+  }
+}
+
+struct EmbedGradArgs {
+  const void* dY;
+  void* dE;
+  const uint32_t* sid;   // sorted ids, V behind the last token
+  const int* stok;       // their rows
+  float* part;           // [pieces][2][D]: the sums of a piece's first and last run that cross its borders
+  uint32_t V;
+  int ntok, D, piece, pieces, slices;
+  int sum_blocks;        // blocks that sum pieces; the others write empty rows
+  float scale;
+};
+
+// 8 columns of a table row
+template <typename GT> __device__ inline void store_grad(void* dE, long long at, const float* acc, float scale) {
+  constexpr int W = 16 / sizeof(GT);
+#pragma unroll
+  for (int e = 0; e < 8 / W; ++e) {
+    Vec<GT, W> o;
+#pragma unroll
+    for (int j = 0; j < W; ++j) o.v[j] = f2el<GT>(acc[e * W + j] * scale);
+    *reinterpret_cast<Vec<GT, W>*>(reinterpret_cast<GT*>(dE) + at + e * W) = o;
+  }
+}
+
+// 3.
+template <typename T, typename GT>
+__global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedGradArgs a) {
+  __shared__ int lower[kEmptyRows + 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  if ((int)blockIdx.x >= a.sum_blocks) {
+    constexpr int W = 16 / sizeof(GT);
+    const int nvec = a.D / W;
+    Vec<GT, W> zero;
+#pragma unroll
+    for (int j = 0; j < W; ++j) zero.v[j] = f2el<GT>(0.f);
+    const long long step = (long long)(gridDim.x - a.sum_blocks) * kEmptyRows;
+    for (long long r0 = (long long)(blockIdx.x - a.sum_blocks) * kEmptyRows; r0 < a.V; r0 += step) {
+      __syncthreads();
+      if (tid <= kEmptyRows) {   // tokens with a smaller id
+        int lo = 0, hi = a.ntok;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if ((long long)a.sid[mid] < r0 + tid) lo = mid + 1;
+          else hi = mid;
+        }
+        lower[tid] = lo;
+      }
+      __syncthreads();
+      for (int r = 0; r < kEmptyRows && r0 + r < a.V; ++r)
+        if (lower[r] == lower[r + 1])
+          for (int c = tid; c < nvec; c += 256) reinterpret_cast<Vec<GT, W>*>(a.dE)[(r0 + r) * nvec + c] = zero;
+    }
+    return;
+  }
+  constexpr int U = 8, W = 16 / sizeof(T), NV = 8 / W;   // rows in flight, vectors of a lane's 8 columns
+  using VT = Vec<T, W>;
+  const long long units = (long long)a.pieces * a.slices;
+  for (long long unit = (long long)blockIdx.x * 4 + (tid >> 6); unit < units; unit += (long long)a.sum_blocks * 4) {
+    const int piece = (int)(unit / a.slices), col = (int)(unit % a.slices) * kSlice + lane * 8;
+    const bool on = col < a.D;
+    const int p0 = piece * a.piece, n = a.ntok - p0 < a.piece ? a.ntok - p0 : a.piece;
+    const uint32_t kid = lane < n ? a.sid[p0 + lane] : a.V;
+    const int tok = lane < n ? a.stok[p0 + lane] : 0;
+    const uint32_t before = p0 > 0 ? a.sid[p0 - 1] : a.V + 1, behind = p0 + n < a.ntok ? a.sid[p0 + n] : a.V + 1;
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    bool crosses = (uint32_t)__builtin_amdgcn_readfirstlane(kid) == before;   // the run began in an earlier piece
+    for (int i0 = 0; i0 < n; i0 += U) {
+      VT v[U][NV];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u < n ? i0 + u : n - 1;
+        const long long row = __builtin_amdgcn_readlane(tok, i);
+        if (on && (uint32_t)__builtin_amdgcn_readlane(kid, i) < a.V) {
+#pragma unroll
+          for (int e = 0; e < NV; ++e)
+            v[u][e] = *reinterpret_cast<const VT*>(reinterpret_cast<const T*>(a.dY) + row * a.D + col + e * W);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u;
+        if (i >= n) break;
+        const uint32_t id = __builtin_amdgcn_readlane(kid, i);
+        if (id >= a.V) break;   // no tokens behind
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += el2f<T>(v[u][j / W].v[j % W]);
+        const bool last = i + 1 == n;
+        const uint32_t next = last ? behind : (uint32_t)__builtin_amdgcn_readlane(kid, i + 1);
+        if (next != id || last) {
+          if (on) {
+            if (next != id && !crosses)
+              store_grad<GT>(a.dE, (long long)id * a.D + col, acc, a.scale);
+            else
+              store_grad<float>(a.part, ((long long)piece * 2 + !crosses) * a.D + col, acc, 1.f);
+          }
+          crosses = false;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+        }
+      }
+    }
+  }
+}
+
+// 4. the runs that begin in a piece and go on behind it
+template <typename GT>
+__global__ void __launch_bounds__(256) embed_join_kernel(const EmbedGradArgs a) {
+  __shared__ float sum[3][64][8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const long long units = (long long)(a.pieces - 1) * a.slices;
+  for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int piece = (int)(unit / a.slices), col = (int)(unit % a.slices) * kSlice + lane * 8;
+    const int p0 = piece * a.piece, p1 = p0 + a.piece;
+    const uint32_t id = a.sid[p1 - 1];
+    if (id >= a.V || a.sid[p1] != id || (p0 > 0 && a.sid[p0] == id && a.sid[p0 - 1] == id)) continue;
+    int end = piece + 1;                     // the piece in which the run ends
+    for (;;) {
+      const long long q = (long long)(end + lane + 1) * a.piece;   // the lane's piece goes on behind its end?
+      const unsigned long long over = __ballot(q < a.ntok && a.sid[q < a.ntok ? q : 0] == id);
+      if (~over) {
+        end += __builtin_ctzll(~over);
+        break;
+      }
+      end += 64;
+    }
+    const bool on = col < a.D;
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    auto add = [&](long long slot) __attribute__((always_inline)) {
+      const float* s = a.part + slot * a.D + col;
+      const Vec<float, 4> x = *reinterpret_cast<const Vec<float, 4>*>(s);
+      const Vec<float, 4> y = *reinterpret_cast<const Vec<float, 4>*>(s + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[j] += x.v[j];
+        acc[j + 4] += y.v[j];
+      }
+    };
+    if (on) {
+      if (wave == 0) add(2LL * piece + 1);
+#pragma unroll 4
+      for (int p = piece + 1 + wave; p <= end; p += 4) add(2LL * p);
+    }
+    __syncthreads();                         // the last unit's sums have been read
+    if (wave > 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[wave - 1][lane][j] = acc[j];
+    __syncthreads();
+    if (wave == 0 && on) {
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += sum[w][lane][j];
+      store_grad<GT>(a.dE, (long long)id * a.D + col, acc, a.scale);
+    }
+  }
+}
+
+// Tokens of a piece.
+inline int embed_piece(int T) { return T >= 8192 ? 64 : 32; }
+
+struct EmbedWs {
+  size_t sid[2], stok[2], part, bytes;
+  EmbedWs(int T, long long D) {
+    Bump b;
+    for (int i = 0; i < (T > kChunk ? 2 : 1); ++i) {
+      sid[i] = b.take((size_t)T * 4);
+      stok[i] = b.take((size_t)T * 4);
+    }
+    part = b.take((size_t)ceil_div(T, embed_piece(T)) * 2 * D * 4);
+    bytes = b.off;
+  }
+};
+
+static sl_status check_embed(const sl_layout* lay, int64_t D) {
+  sl_status st = check_tokens(lay);
+  if (st != SL_OK) return st;
+  if (lay->batch * (long long)lay->seq_len > (1LL << 26)) SL_FAIL(SL_ERR_RANGE, "more than 2^26 tokens");
+  if (D < 8 || D % 8 || D > 65536) SL_FAIL(SL_ERR_SHAPE, "d_model %lld must be a multiple of 8 in [8, 65536]", (long long)D);
+  return SL_OK;
+}
+
+static sl_status check_embed_call(sl_dtype dt, const sl_layout* lay, int64_t V, int64_t D, float scale) {
+  sl_status st = check_dtype(dt);
+  if (st == SL_OK) st = check_embed(lay, D);
+  if (st != SL_OK) return st;
+  if (V < 1 || V > (1LL << 30)) SL_FAIL(SL_ERR_RANGE, "vocabulary of %lld outside [1, 2^30]", (long long)V);
+  if (!(scale - scale == 0.f)) SL_FAIL(SL_ERR_RANGE, "scale is not finite");
+  return SL_OK;
+}
+
+template <typename T>
+static void launch_fwd(const void* E, const int32_t* ids, int64_t V, int64_t D, int ntok, float scale, void* Y,
+                       hipStream_t s) {
+  const int nvec = (int)(D * sizeof(T) / 16);
+  int lg = 0;
+  while (lg < 8 && (1 << lg) < nvec) ++lg;
+  const int cols = ceil_div(nvec, 1 << lg), rows = 256 >> lg;
+  // four rows in flight a thread where that leaves four blocks to a CU
+  if ((long long)ceil_div(ntok, rows * 4) * cols >= 1024)
+    hipLaunchKernelGGL((embed_fwd_kernel<T, 4>), dim3(walk_grid(ceil_div(ntok, rows * 4), (1 << 23) / cols).x, cols), dim3(256), 0, s,
+                       (const T*)E, ids, (uint32_t)V, nvec, ntok, lg, scale, (T*)Y);
+  else
+    hipLaunchKernelGGL((embed_fwd_kernel<T, 1>), dim3(walk_grid(ceil_div(ntok, rows), (1 << 23) / cols).x, cols), dim3(256), 0, s,
+                       (const T*)E, ids, (uint32_t)V, nvec, ntok, lg, scale, (T*)Y);
+}
+
+template <typename T, typename GT>
+static void launch_grad(const EmbedGradArgs& a, hipStream_t s) {
+  const unsigned empty = walk_grid(ceil_div(a.V, kEmptyRows), 1 << 18).x;
+  hipLaunchKernelGGL((embed_grad_kernel<T, GT>), dim3(a.sum_blocks + empty), dim3(256), 0, s, a);
+  if (a.pieces > 1)
+    hipLaunchKernelGGL(embed_join_kernel<GT>, walk_grid((long long)(a.pieces - 1) * a.slices), dim3(256), 0, s, a);
+}
+
+}  // namespace sl
+
+using namespace sl;
+
+extern "C" sl_status sl_embed_fwd(sl_dtype dt, const sl_layout* lay, int64_t vocab, int64_t d_model, float scale,
+                                  const void* E, const int32_t* ids, void* Y, void* stream) {
+  if (!E || !ids || !Y) SL_FAIL(SL_ERR_NULL, "E, ids and Y required");
+  sl_status st = check_embed_call(dt, lay, vocab, d_model, scale);
+  if (st != SL_OK) return st;
+  if (!aligned16(E) || !aligned16(ids) || !aligned16(Y)) SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
+  st = check_arch();
+  if (st != SL_OK) return st;
+  const int T = lay->batch * lay->seq_len;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dt == SL_BF16) launch_fwd<bf16>(E, ids, vocab, d_model, T, scale, Y, s);
+  else launch_fwd<float>(E, ids, vocab, d_model, T, scale, Y, s);
+  SL_HIP(hipGetLastError());
+  return SL_OK;
+}
+
+extern "C" size_t sl_embed_workspace_bytes(const sl_layout* lay, int64_t d_model) {
+  if (check_embed(lay, d_model) != SL_OK) return 0;
+  return EmbedWs(lay->batch * lay->seq_len, d_model).bytes;
+}
+
+extern "C" sl_status sl_embed_bwd(sl_dtype dt, const sl_layout* lay, int64_t vocab, int64_t d_model, float scale,
+                                  const int32_t* ids, const void* dY, sl_dtype grad_dt, void* dE, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  if (!ids || !dY || !dE) SL_FAIL(SL_ERR_NULL, "ids, dY and dE required");
+  sl_status st = check_embed_call(dt, lay, vocab, d_model, scale);
+  if (st == SL_OK) st = check_dtype(grad_dt);
+  if (st != SL_OK) return st;
+  if (!aligned16(ids) || !aligned16(dY) || !aligned16(dE) || !aligned16(ws))
+    SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
+  const int T = lay->batch * lay->seq_len;
+  const EmbedWs at(T, d_model);
+  if (!ws || ws_bytes < at.bytes)
+    SL_FAIL(SL_ERR_WORKSPACE, "embedding workspace too small (%zu bytes, %zu needed)", ws_bytes, at.bytes);
+  st = check_arch();
+  if (st != SL_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* const w = reinterpret_cast<char*>(ws);
+  auto sid = [&](int i) { return reinterpret_cast<uint32_t*>(w + at.sid[i]); };
+  auto stok = [&](int i) { return reinterpret_cast<int*>(w + at.stok[i]); };
+  const uint32_t V = (uint32_t)vocab;
+  hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)ceil_div(T, kRankTokens)), dim3(256), 0, s, ids, V, T, sid(0),
+                     stok(0));
+  int cur = 0;
+  for (long long len = kChunk; len < T; len *= kLists, cur ^= 1)
+    hipLaunchKernelGGL(embed_merge_kernel, dim3((unsigned)ceil_div(T, 256 / kLists)), dim3(256), 0, s, sid(cur), stok(cur),
+                       T, (int)len, sid(cur ^ 1), stok(cur ^ 1));
+  EmbedGradArgs a{};
+  a.dY = dY; a.dE = dE; a.sid = sid(cur); a.stok = stok(cur);
+  a.part = reinterpret_cast<float*>(w + at.part);
+  a.V = V; a.ntok = T; a.D = (int)d_model; a.scale = scale;
+  a.piece = embed_piece(T);
+  a.pieces = ceil_div(T, a.piece);
+  a.slices = ceil_div(d_model, kSlice);
+  a.sum_blocks = (int)walk_grid(((long long)a.pieces * a.slices + 3) / 4, 1 << 20).x;
+  if (dt == SL_BF16 && grad_dt == SL_BF16) launch_grad<bf16, bf16>(a, s);
+  else if (dt == SL_BF16) launch_grad<bf16, float>(a, s);
+  else if (grad_dt == SL_BF16) launch_grad<float, bf16>(a, s);
+  else launch_grad<float, float>(a, s);
+  SL_HIP(hipGetLastError());
+  return SL_OK;
+}

@@ -27,8 +27,7 @@
 // 64 MiB at 6.8.
 #include <cmath>
 
-#include "sl_common.hpp"
-#include "sl_host.hpp"
+#include "sl_rows.hpp"
 
 namespace sl {
 
@@ -50,16 +49,6 @@ struct RotArgs {
 };
 
 constexpr int kTokens = 4;   // most tokens a block takes at a time
-
-// V values, moved as one
-template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
-
-template <typename T> __device__ inline float el2f(T x);
-template <> __device__ inline float el2f<float>(float x) { return x; }
-template <> __device__ inline float el2f<bf16>(bf16 x) { return bf2f(x.v); }
-template <typename T> __device__ inline T f2el(float x);
-template <> __device__ inline float f2el<float>(float x) { return x; }
-template <> __device__ inline bf16 f2el<bf16>(float x) { return __builtin_bit_cast(bf16, (__bf16)x); }   // to nearest even
 
 // cos and sin of 2 pi * phase / 2^32
 __device__ inline void cos_sin_turn(uint32_t phase, float& c, float& s) {
@@ -365,13 +354,9 @@ static sl_status check_heads(const sl_heads* h, bool has_k) {
 // Fill the arguments shared by every mode; rot may be NULL for the norms.
 static sl_status rot_args(RotArgs& a, sl_dtype dt, const sl_layout* lay, const sl_heads* heads,
                           const sl_rotary* rot, bool has_k, float sign, int* inter) {
-  if (dt != SL_BF16 && dt != SL_F32) SL_FAIL(SL_ERR_DTYPE, "dtype must be SL_F32 or SL_BF16");
-  if (!lay) SL_FAIL(SL_ERR_NULL, "layout is NULL");
-  if (lay->batch < 1 || lay->batch > SL_MAX_SEQS)
-    SL_FAIL(SL_ERR_RANGE, "batch %d outside [1, %d]", lay->batch, SL_MAX_SEQS);
-  if (lay->seq_len < 1) SL_FAIL(SL_ERR_RANGE, "seq_len %d < 1", lay->seq_len);
-  if ((long long)lay->batch * lay->seq_len > (1LL << 30)) SL_FAIL(SL_ERR_RANGE, "too many tokens");
-  sl_status st = check_heads(heads, has_k);
+  sl_status st = check_dtype(dt);
+  if (st == SL_OK) st = check_tokens(lay);
+  if (st == SL_OK) st = check_heads(heads, has_k);
   if (st != SL_OK) return st;
   a = RotArgs{};
   a.T = lay->batch * lay->seq_len;

@@ -27,7 +27,8 @@ from torch.autograd.function import once_differentiable
 
 from . import api as sl
 
-__all__ = ["LayerRatios", "SparsitySchedule", "SparseLoRAFFN", "SparseLoRAQKVO", "DiffAttention"]
+__all__ = ["LayerRatios", "SparsitySchedule", "SparseLoRAFFN", "SparseLoRAQKVO", "DiffAttention", "TokenEmbedding", "LayerNorm",
+           "DistillLoss"]
 
 
 @dataclass(frozen=True)
@@ -462,3 +463,119 @@ class DiffAttention(torch.nn.Module):
             return self(q, k, v, layout, lens, pos)
         attention.projection_heads = self.projection_heads
         return attention
+
+
+class _EmbedStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, weight, ids, layout, scale):
+        ctx.args = (layout, scale, weight.shape[0], weight.dtype)
+        ctx.save_for_backward(ids)
+        return sl.embed_fwd(weight.detach(), ids, layout, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        layout, scale, vocab, dtype = ctx.args
+        (ids,) = ctx.saved_tensors
+        return sl.embed_bwd(ids, dY.contiguous(), layout, vocab, scale, dtype), None, None, None
+
+
+class TokenEmbedding(torch.nn.Module):
+    """The rows of a trained table ``weight`` [vocab, d_model] (bf16 or fp32) at the
+    tokens ``ids`` [T] (int32), times ``scale``; an id outside the vocabulary is no
+    token (a row of zeros, no gradient).  The table's gradient has its type; the
+    sums are fp32 and in a fixed order."""
+
+    def __init__(self, weight: torch.Tensor, scale: float = 1.0):
+        super().__init__()
+        self.weight, self.scale = torch.nn.Parameter(weight.detach().contiguous()), float(scale)
+
+    def forward(self, ids: torch.Tensor, layout: sl.Layout):
+        return _EmbedStep.apply(self.weight, ids, layout, self.scale)
+
+
+class _LayerNormStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, w, b, layout, eps, centered):
+        x, r = x.detach().contiguous(), None if r is None else r.detach().contiguous()
+        y, h, stats = sl.layer_norm_fwd(x, w.detach(), None if b is None else b.detach(), layout, eps, centered, r)
+        ctx.set_materialize_grads(False)
+        ctx.args = (layout, centered, r is not None, b is not None)
+        ctx.save_for_backward(h, w, stats)
+        return y if r is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        layout, centered, added, bias = ctx.args
+        if dy is None and dh is None:
+            return (None,) * 7
+        h, w, stats = ctx.saved_tensors
+        dy = torch.zeros_like(h) if dy is None else dy.contiguous()
+        g = sl.layer_norm_bwd(h, w.detach(), stats, layout, dy, None if dh is None else dh.contiguous(), centered, bias)
+        return g["dx"], g["dx"] if added else None, g["dw"], g.get("db"), None, None, None
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm of token rows, or (not ``centered``) their root-mean-square norm,
+    with fp32 parameters ``weight`` and, where centred and with ``bias``, ``bias``:
+
+        y = norm(x, layout)
+        y, h = norm(x, layout, residual)      # h = x + residual, the next residual
+
+    One pass forms the sum and its norm, one the gradient of both.  Gradients are
+    first derivatives: a second one is refused."""
+
+    def __init__(self, width: int, eps: float = 1e-5, centered: bool = True, bias: bool = True, device="cuda"):
+        super().__init__()
+        self.eps, self.centered = float(eps), bool(centered)
+        self.weight = torch.nn.Parameter(torch.ones(width, device=device))
+        self.bias = torch.nn.Parameter(torch.zeros(width, device=device)) if centered and bias else None
+
+    def forward(self, x: torch.Tensor, layout: sl.Layout, residual: Optional[torch.Tensor] = None):
+        return _LayerNormStep.apply(x, residual, self.weight, self.bias, layout, self.eps, self.centered)
+
+
+class _DistillStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, p, layout):
+        z = logits.detach()
+        loss, stats = sl.distill_fwd(p, z, layout)
+        ctx.args = (p.temperature, p.hard, layout)
+        ctx.save_for_backward(z, stats, p.top_ids, p.top_logits, p.labels)
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss):
+        temperature, hard, layout = ctx.args
+        z, stats, top_ids, top_logits, labels = ctx.saved_tensors
+        p = sl.DistillTargets(top_ids, top_logits, labels, temperature, hard)
+        return sl.distill_bwd(p, z, stats, layout, dloss.contiguous()), None, None
+
+
+class DistillLoss(torch.nn.Module):
+    """Each output row's distance from a teacher's top logits at ``temperature``,
+    mixed with the cross entropy of hard labels by the weight ``hard``; 0 for
+    context rows.  ``forward`` returns the rows' losses [T] (fp32), differentiable
+    in the logits.  Where the rows' weights in the loss are known beforehand,
+    ``step`` forms losses and gradient in one pass:
+
+        losses, dlogits = crit.step(logits, layout, top_ids, top_logits, weights=w)
+        logits.backward(dlogits)"""
+
+    def __init__(self, temperature: float = 1.0, hard: float = 0.0):
+        super().__init__()
+        self.temperature, self.hard = float(temperature), float(hard)
+
+    def _targets(self, top_ids, top_logits, labels):
+        return sl.DistillTargets(top_ids, top_logits, labels, self.temperature, self.hard)
+
+    def forward(self, logits: torch.Tensor, layout: sl.Layout, top_ids: Optional[torch.Tensor] = None,
+                top_logits: Optional[torch.Tensor] = None, labels: Optional[torch.Tensor] = None):
+        return _DistillStep.apply(logits, self._targets(top_ids, top_logits, labels), layout)
+
+    def step(self, logits: torch.Tensor, layout: sl.Layout, top_ids: Optional[torch.Tensor] = None,
+             top_logits: Optional[torch.Tensor] = None, labels: Optional[torch.Tensor] = None,
+             weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+        return sl.distill_step(self._targets(top_ids, top_logits, labels), logits.detach(), layout, weights, out)

@@ -434,6 +434,101 @@ sl_status sl_diff_attn_bwd(sl_dtype dt, const sl_layout* lay, const sl_diff_attn
                            void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Around the layers: from tokens to rows, between two layers, from logits to a
+ * loss.  Of the layout batch and seq_len are read, and ctx_len by the loss alone.
+ * Every call is stream-ordered on `stream` alone, never synchronises, launches
+ * nothing on error, and may be captured into a graph.  Sums are fp32 and run in a
+ * fixed order.  Offsets are 64-bit.
+ *
+ * Token embedding.
+ *   E    [vocab, d_model]   ids [T] int32   Y, dY [T, d_model]
+ *   fwd: Y[t] = scale * E[ids[t]]; an id outside 0..vocab-1 is no token: its row
+ *        is 0 and it has no gradient (its row of dY is not read).
+ *   bwd: dE [vocab, d_model] in grad_dt (fp32, or bf16: the fp32 sum rounded
+ *        once), overwritten: scale * the sum of the token's rows of dY, 0 for
+ *        an id without one.
+ * d_model a multiple of 8, at most 65536; vocab at most 2^30, T at most 2^26.
+ * No output may overlap an input or the workspace.
+ * ------------------------------------------------------------------------- */
+sl_status sl_embed_fwd(sl_dtype dt, const sl_layout* lay, int64_t vocab, int64_t d_model, float scale, const void* E,
+                       const int32_t* ids, void* Y, void* stream);
+size_t sl_embed_workspace_bytes(const sl_layout* lay, int64_t d_model);
+sl_status sl_embed_bwd(sl_dtype dt, const sl_layout* lay, int64_t vocab, int64_t d_model, float scale,
+                       const int32_t* ids, const void* dY, sl_dtype grad_dt, void* dE, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norm of whole rows with the residual sum in the same pass.
+ *   h = x + r (rounded to the call's type; without r, h is x and not written)
+ *   y = (h - m) s w + b,  m = mean h,  s = (mean (h - m)^2 + eps)^(-1/2)
+ *   not centered: m = 0 and b = 0
+ *   w, b [d_model] fp32; b may be NULL (0)
+ *   fwd: x, r -> h, y [T, d_model] and stats [T, 3] fp32 (m, what m rounded away,
+ *        s; NULL: not written).  r and h both or neither.  h or y may be x, or r.
+ *   bwd: h, stats (the forward's), dy and optionally dh, the gradient that reaches
+ *        h by its other way -> dx, the gradient of x and of r alike, and the fp32
+ *        gradients dw and db [d_model], overwritten (db NULL: not written).  dx
+ *        may be dy, dh or h.
+ * Otherwise no output may overlap an input, the workspace or another output.
+ * d_model a multiple of 8, at most 16384; eps >= 0.  A row whose variance (mean
+ * square) and eps are both 0 has no norm: its outputs are NaN.
+ * ------------------------------------------------------------------------- */
+typedef struct sl_layer_norm {
+  int64_t d_model;
+  int32_t centered;
+  float eps;
+  const float *w, *b;
+} sl_layer_norm;
+sl_status sl_layer_norm_fwd(sl_dtype dt, const sl_layout* lay, const sl_layer_norm* p, const void* x, const void* r,
+                            void* h, void* y, float* stats, void* stream);
+size_t sl_layer_norm_workspace_bytes(const sl_layout* lay, int64_t d_model);
+sl_status sl_layer_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_layer_norm* p, const void* h,
+                            const float* stats, const void* dy, const void* dh, void* dx, float* dw, float* db,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Distillation from a teacher's top logits, mixed with hard labels.  Row t of the
+ * logits [T, ld] holds z over the vocabulary, in its first `vocab` elements:
+ *   p = softmax(top_logits[t] / temperature) over its `top` entries; an id
+ *       outside 0..vocab-1 is no entry, the same id twice counts twice
+ *   q = softmax(z / temperature),  o = softmax(z)
+ *   loss = (1 - hard) temperature^2 sum_k p_k (log p_k - log q_{i_k}) - hard log o_label
+ *   dlogits = dloss * the loss's gradient
+ * A row without entries has no first term, one whose label is outside 0..vocab-1
+ * no second.  Context rows (the first ctx_len[b] of each sequence) have neither:
+ * loss 0, dlogits 0, and like every row without a term they are not read.
+ *   top_ids [T, top] int32, top_logits [T, top] fp32   (hard = 1: may be NULL)
+ *   labels  [T] int32                                  (hard = 0: may be NULL)
+ *   fwd:  logits -> loss [T] fp32 and stats [T, 4] fp32 for the backward
+ *   bwd:  logits, stats, dloss [T] fp32 (NULL: ones) -> dlogits [T, ld_out]; a row
+ *         whose dloss is 0 gets zeros
+ *   step: logits, dloss -> loss and dlogits in one call, which reads logits from
+ *         memory once; for a loss whose weights are known beforehand
+ * dlogits may be logits (with ld_out = ld); otherwise no output may overlap an
+ * input or another output.  Elements of a row behind the vocabulary are neither
+ * read nor written.  ld, ld_out >= vocab, any number.
+ * Logits of -inf have probability 0.  A row of -inf alone, or with +inf or NaN,
+ * has no distribution: its loss and its gradient are NaN; so is the loss of a
+ * teacher's entry of +inf or NaN, and the gradient there.
+ * 0 <= hard <= 1, temperature > 0, 1 <= top <= SL_DISTILL_MAX_TOP, vocab <= 2^30.
+ * ------------------------------------------------------------------------- */
+#define SL_DISTILL_MAX_TOP 256
+typedef struct sl_distill {
+  int64_t vocab;
+  int32_t top;
+  float temperature, hard;
+  const int32_t* top_ids;
+  const float* top_logits;
+  const int32_t* labels;
+} sl_distill;
+sl_status sl_distill_fwd(sl_dtype dt, const sl_layout* lay, const sl_distill* p, const void* logits, int64_t ld,
+                         float* loss, float* stats, void* stream);
+sl_status sl_distill_bwd(sl_dtype dt, const sl_layout* lay, const sl_distill* p, const void* logits, int64_t ld,
+                         const float* stats, const float* dloss, void* dlogits, int64_t ld_out, void* stream);
+sl_status sl_distill_step(sl_dtype dt, const sl_layout* lay, const sl_distill* p, const void* logits, int64_t ld,
+                          const float* dloss, float* loss, void* dlogits, int64_t ld_out, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Offline quantization of a frozen weight to the 4-bit base of sl_ffn_weights
  * (SparseLoRA article §六: SparseLoRA over a QLoRA-style quantized base; the
  * pages name no format, this is the plainest 4-bit one).  W [rows, cols] in dt

@@ -9,5 +9,7 @@ from .quant4 import *  # noqa: F401,F403
 from .quant4 import __all__ as _quant_all
 from .attention import *  # noqa: F401,F403
 from .attention import __all__ as _attn_all
+from .around import *  # noqa: F401,F403
+from .around import __all__ as _around_all
 
-__all__ = list(_core_all) + list(_quant_all) + list(_attn_all)
+__all__ = list(_core_all) + list(_quant_all) + list(_attn_all) + list(_around_all)
