@@ -5,14 +5,17 @@
 //   dx = s (g - mean g - u mean(g u)) + dres,  dw = sum over rows of dy u,  db = sum over rows of dy.
 //
 // A row belongs to a group of lanes, 8 to 64 of one wave or several whole waves,
-// and stays in registers from its loads to its stores; its sums are added over
-// the lanes, and over the waves through LDS.  The variance is formed from
-// h - m, not from mean h^2 - m^2, and the mean's own rounding error is taken out
-// of both with the same sums.  A group walks over rows and loads the next row
-// before it works on this one.  The backward keeps the sums of dw and db of its
-// rows in registers; a block adds its groups' sums in LDS, and one more launch the
-// blocks' in a fixed order.
+// and stays in registers from its loads to its stores.  The variance is formed from
+// differences, never from mean h^2 - m^2: each wave takes the mean of its own
+// values and sums the squares of their distances from it, and the waves' means and
+// sums are joined (the squares about the row's mean are those about the wave's and
+// n (m_wave - m)^2), with one exchange through LDS a row.  The rounding error of the
+// mean comes out of the same sums and is kept beside it.  A group walks over
+// rows and loads the next row before it works on this one.  The backward keeps the
+// sums of dw and db of its rows in registers; a block adds its groups' sums in LDS,
+// and one more launch the blocks' in a fixed order.
 #include <cmath>
+#include <type_traits>
 
 #include "sl_rows.hpp"
 
@@ -30,46 +33,50 @@ struct RowNormArgs {
   float eps, inv_d;
 };
 
-constexpr int kNormThreads = 1024;   // most threads of a block
+constexpr int kNormWaves = 16;   // most waves of a block
 
-// Sums over a row's lanes.  Groups of whole waves go through LDS: calls take the
-// two halves of `red` in turn, so one barrier a call is enough (a half is written
-// again only behind the next call's barrier).
-template <int N>
-__device__ inline void row_add(float (&v)[N], const RowNormArgs& a, float (*red)[2][kNormThreads / 64], int& half) {
-  if (a.group < 64) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] += dpp<kXor1>(v[i]);
-      v[i] += dpp<kXor2>(v[i]);
-      v[i] += dpp<kMirror8>(v[i]);
-      if (a.group >= 16) v[i] += dpp<kMirror16>(v[i]);
-      if (a.group >= 32) v[i] += __shfl_xor(v[i], 16);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_add(v[i]);
-  if (a.group == 64) return;
-  const int wave = threadIdx.x >> 6, per = a.group >> 6, first = wave - wave % per;
-  if ((threadIdx.x & 63) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[half][i][wave] = v[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = red[half][i][first];
-  for (int k = 1; k < per; ++k)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += red[half][i][first + k];
-  half ^= 1;
+// Sum over a row's lanes where they are of one wave.
+__device__ inline float group_add(float x, int group) {
+  if (group == 64) return wave_add(x);
+  x += dpp<kXor1>(x);
+  x += dpp<kXor2>(x);
+  x += dpp<kMirror8>(x);
+  if (group >= 16) x += dpp<kMirror16>(x);
+  if (group >= 32) x += __shfl_xor(x, 16);
+  return x;
 }
 
+// x as it is rounded: the compiler may not take it as the product that it comes
+// from, fused into a difference (which would be to another mean than the kept one).
+__device__ inline float rounded(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
+// Lanes of a wave that hold values in place e of their vectors.
+__device__ inline int live_lanes(const RowNormArgs& a, int wave, int e) {
+  const int n = a.nvec - e * a.group - wave * 64;
+  return n < 0 ? 0 : n < 64 ? n : 64;
+}
+
+template <typename T, int N> __device__ inline void load_floats(const float* p, float (&v)[N], int at) {
+#pragma unroll
+  for (int j = 0; j < 16 / (int)sizeof(T); j += 4) {
+    const Vec<float, 4> x = *reinterpret_cast<const Vec<float, 4>*>(p + j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[at + j + i] = x.v[i];
+  }
+}
+
+// A row's exchange between waves takes the two halves of an LDS array in turn, so
+// one barrier a row is enough: a half is written again only behind the next row's.
 template <typename T, int NV, bool CENTERED>
-__global__ void __launch_bounds__(kNormThreads) row_norm_fwd_kernel(const RowNormArgs a) {
-  constexpr int W = 16 / sizeof(T), N = NV * W;
-  using VT = Vec<T, W>;
-  __shared__ float red[2][2][kNormThreads / 64];
-  const int groups = blockDim.x / a.group, group = threadIdx.x / a.group, lane = threadIdx.x % a.group;
+__global__ void __launch_bounds__(64 * kNormWaves) row_norm_fwd_kernel(const RowNormArgs a) {
+  using VT = Pack<T>;
+  constexpr int W = VT::W, N = NV * W;
+  __shared__ float red[2][3][kNormWaves];
+  const int groups = blockDim.x / a.group, group = threadIdx.x / a.group, lane = threadIdx.x - group * a.group;
+  const int wave = threadIdx.x >> 6, per = a.group >> 6;
   const long long step = (long long)gridDim.x * groups;
   long long row = (long long)blockIdx.x * groups + group;
   int half = 0;
@@ -77,15 +84,7 @@ __global__ void __launch_bounds__(kNormThreads) row_norm_fwd_kernel(const RowNor
   float w[N], b[N];
   VT vx[NV], vr[NV];
 #pragma unroll
-  for (int e = 0; e < NV; ++e) {
-    const int c = lane + e * a.group;
-    live[e] = c < a.nvec;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      w[e * W + j] = live[e] ? a.w[c * W + j] : 0.f;
-      b[e * W + j] = live[e] && a.b ? a.b[c * W + j] : 0.f;
-    }
-  }
+  for (int e = 0; e < NV; ++e) live[e] = lane + e * a.group < a.nvec;
   auto load = [&](long long t) __attribute__((always_inline)) {
     if (t >= a.T) return;
 #pragma unroll
@@ -97,72 +96,111 @@ __global__ void __launch_bounds__(kNormThreads) row_norm_fwd_kernel(const RowNor
       }
   };
   load(row);
+#pragma unroll
+  for (int e = 0; e < NV; ++e)
+    if (live[e]) {
+      load_floats<T>(a.w + (lane + e * a.group) * W, w, e * W);
+      if (CENTERED && a.b) load_floats<T>(a.b + (lane + e * a.group) * W, b, e * W);
+    }
   // the groups of a block go through the barriers together
   for (long long t0 = (long long)blockIdx.x * groups; t0 < a.T; t0 += step, row += step) {
     const bool on = row < a.T;
     float h[N];
-    VT vh[NV];
 #pragma unroll
-    for (int e = 0; e < NV; ++e)
+    for (int e = 0; e < NV; ++e) {
+      if (on && live[e] && a.r) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        float v = 0.f;
-        if (on && live[e]) {
-          v = el2f<T>(vx[e].v[j]);
-          if (a.r) v += el2f<T>(vr[e].v[j]);
-          vh[e].v[j] = f2el<T>(v);
-          v = el2f<T>(vh[e].v[j]);        // the norm is of the sum as it is kept
-        }
-        h[e * W + j] = v;
+        for (int j = 0; j < W; j += 2) vx[e].put(j, vx[e].get(j) + vr[e].get(j), vx[e].get(j + 1) + vr[e].get(j + 1));
+        reinterpret_cast<VT*>(a.h)[row * a.nvec + lane + e * a.group] = vx[e];
       }
-    if (on && a.h)
 #pragma unroll
-      for (int e = 0; e < NV; ++e)
-        if (live[e]) reinterpret_cast<VT*>(a.h)[row * a.nvec + lane + e * a.group] = vh[e];
+      for (int j = 0; j < W; ++j) h[e * W + j] = on && live[e] ? vx[e].get(j) : 0.f;   // the sum as it is kept
+    }
     load(row + step);
-    float m = 0.f, off = 0.f, ss;
+    // m + off: the mean and what its rounding lost; ss: the squares about it
+    float m = 0.f, off = 0.f, ss = 0.f;
     if constexpr (CENTERED) {
-      float s1[1] = {0.f};
+      int n = a.nvec * W;
+      if (a.group > 64) {
+        n = 0;
 #pragma unroll
-      for (int j = 0; j < N; ++j) s1[0] += h[j];
-      row_add(s1, a, red, half);
-      m = s1[0] * a.inv_d;
-      float s2[2] = {0.f, 0.f};
+        for (int e = 0; e < NV; ++e) n += live_lanes(a, wave - group * per, e) * W;
+      }
+      const float inv = n ? 1.f / n : 0.f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) m += h[j];
+      m = rounded(group_add(m, a.group < 64 ? a.group : 64) * inv);
 #pragma unroll
       for (int e = 0; e < NV; ++e)
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           const float d = live[e] ? h[e * W + j] - m : 0.f;
-          h[e * W + j] = d;
-          s2[0] += d;
-          s2[1] = fmaf(d, d, s2[1]);
+          off += d;
+          ss = fmaf(d, d, ss);
         }
-      row_add(s2, a, red, half);
-      off = s2[0] * a.inv_d;
-      ss = fmaxf(fmaf(-off, off, s2[1] * a.inv_d), 0.f);
-      if (!(s2[1] == s2[1])) ss = s2[1];   // (a row with a NaN stays one)
-    } else {
-      float s2[1] = {0.f};
+      off = group_add(off, a.group < 64 ? a.group : 64);
+      ss = group_add(ss, a.group < 64 ? a.group : 64);
+      if (a.group > 64) {
+        if ((threadIdx.x & 63) == 0) {
+          red[half][0][wave] = m;
+          red[half][1][wave] = off;
+          red[half][2][wave] = ss;
+        }
+        __syncthreads();
+        const int w0 = group * per;
+        m = 0.f;
+        for (int k = 0; k < per; ++k) {
+          int c = 0;
 #pragma unroll
-      for (int j = 0; j < N; ++j) s2[0] = fmaf(h[j], h[j], s2[0]);
-      row_add(s2, a, red, half);
-      ss = s2[0] * a.inv_d;
+          for (int e = 0; e < NV; ++e) c += live_lanes(a, k, e) * W;
+          m = fmaf((float)c, red[half][0][w0 + k], m);
+        }
+        m = rounded(m * a.inv_d);
+        off = ss = 0.f;
+        for (int k = 0; k < per; ++k) {
+          int c = 0;
+#pragma unroll
+          for (int e = 0; e < NV; ++e) c += live_lanes(a, k, e) * W;
+          // about the wave's mean: off_k, ss_k; about m: those moved by the distance
+          const float d = red[half][0][w0 + k] - m, o = red[half][1][w0 + k];
+          off += fmaf((float)c, d, o);
+          ss += fmaf(d, fmaf((float)c, d, 2.f * o), red[half][2][w0 + k]);
+        }
+        half ^= 1;
+      }
+      off *= a.inv_d;
+      const float var = fmaf(-off, off, ss * a.inv_d);
+      ss = var < 0.f ? 0.f : var;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) ss = fmaf(h[j], h[j], ss);
+      ss = group_add(ss, a.group < 64 ? a.group : 64);
+      if (a.group > 64) {
+        if ((threadIdx.x & 63) == 0) red[half][0][wave] = ss;
+        __syncthreads();
+        ss = 0.f;
+        for (int k = 0; k < per; ++k) ss += red[half][0][group * per + k];
+        half ^= 1;
+      }
+      ss *= a.inv_d;
     }
     const float s = 1.f / sqrtf(ss + a.eps);
     if (on) {
-      if (a.stats && lane == 0) {
-        a.stats[row * 3] = m;
-        a.stats[row * 3 + 1] = off;
-        a.stats[row * 3 + 2] = s;
-      }
+      if (a.stats && lane < 3) a.stats[row * 3 + lane] = lane == 0 ? m : lane == 1 ? off : s;
 #pragma unroll
       for (int e = 0; e < NV; ++e)
         if (live[e]) {
           VT o;
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const float u = (CENTERED ? h[e * W + j] - off : h[e * W + j]) * s;
-            o.v[j] = f2el<T>(fmaf(u, w[e * W + j], b[e * W + j]));
+          for (int j = 0; j < W; j += 2) {
+            float y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int n = e * W + j + i;
+              const float u = (CENTERED ? (h[n] - m) - off : h[n]) * s;
+              y[i] = CENTERED && a.b ? fmaf(u, w[n], b[n]) : u * w[n];
+            }
+            o.put(j, y[0], y[1]);
           }
           reinterpret_cast<VT*>(a.y)[row * a.nvec + lane + e * a.group] = o;
         }
@@ -171,12 +209,13 @@ __global__ void __launch_bounds__(kNormThreads) row_norm_fwd_kernel(const RowNor
 }
 
 template <typename T, int NV, bool CENTERED>
-__global__ void __launch_bounds__(kNormThreads) row_norm_bwd_kernel(const RowNormArgs a) {
-  constexpr int W = 16 / sizeof(T), N = NV * W;
-  using VT = Vec<T, W>;
-  __shared__ float red[2][2][kNormThreads / 64];
-  extern __shared__ float sums[];              // [2][D]
-  const int groups = blockDim.x / a.group, group = threadIdx.x / a.group, lane = threadIdx.x % a.group;
+__global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const RowNormArgs a) {
+  using VT = Pack<T>;
+  constexpr int W = VT::W, N = NV * W;
+  __shared__ float red[2][2][kNormWaves];
+  extern __shared__ float sums[];              // [2][D], where a block has several groups
+  const int groups = blockDim.x / a.group, group = threadIdx.x / a.group, lane = threadIdx.x - group * a.group;
+  const int wave = threadIdx.x >> 6, per = a.group >> 6;
   const long long step = (long long)gridDim.x * groups;
   long long row = (long long)blockIdx.x * groups + group;
   int half = 0;
@@ -185,15 +224,9 @@ __global__ void __launch_bounds__(kNormThreads) row_norm_bwd_kernel(const RowNor
   VT vh[NV], vg[NV], vd[NV];
   float st[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < NV; ++e) {
-    const int c = lane + e * a.group;
-    live[e] = c < a.nvec;
+  for (int e = 0; e < NV; ++e) live[e] = lane + e * a.group < a.nvec;
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      w[e * W + j] = live[e] ? a.w[c * W + j] : 0.f;
-      dw[e * W + j] = db[e * W + j] = 0.f;
-    }
-  }
+  for (int j = 0; j < N; ++j) w[j] = dw[j] = db[j] = 0.f;
   auto load = [&](long long t) __attribute__((always_inline)) {
     if (t >= a.T) return;
 #pragma unroll
@@ -208,40 +241,66 @@ __global__ void __launch_bounds__(kNormThreads) row_norm_bwd_kernel(const RowNor
       }
   };
   load(row);
+#pragma unroll
+  for (int e = 0; e < NV; ++e)
+    if (live[e]) load_floats<T>(a.w + (lane + e * a.group) * W, w, e * W);
   for (long long t0 = (long long)blockIdx.x * groups; t0 < a.T; t0 += step, row += step) {
     const bool on = row < a.T;
     const float m = st[0], off = st[1], s = st[2];
-    float u[N], g[N], other[N];
-    float c[2] = {0.f, 0.f};
+    float u[N], g[N];
+    VT other[NV];
+    float cu = 0.f, cg = 0.f;
 #pragma unroll
-    for (int e = 0; e < NV; ++e)
+    for (int e = 0; e < NV; ++e) {
+      other[e] = vd[e];
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const int n = e * W + j;
-        u[n] = g[n] = other[n] = 0.f;
+        u[n] = g[n] = 0.f;
         if (on && live[e]) {
-          const float h = el2f<T>(vh[e].v[j]), dy = el2f<T>(vg[e].v[j]);
-          u[n] = CENTERED ? ((h - m) - off) * s : h * s;
-          if (a.dres) other[n] = el2f<T>(vd[e].v[j]);
+          const float h = vh[e].get(j), dy = vg[e].get(j);
+          u[n] = (CENTERED ? (h - m) - off : h) * s;
           dw[n] = fmaf(dy, u[n], dw[n]);
           if (CENTERED) db[n] += dy;
           g[n] = dy * w[n];
-          c[0] = fmaf(g[n], u[n], c[0]);
-          if (CENTERED) c[1] += g[n];
+          cu = fmaf(g[n], u[n], cu);
+          if (CENTERED) cg += g[n];
         }
       }
+    }
     load(row + step);
-    row_add(c, a, red, half);
-    const float cu = c[0] * a.inv_d, cg = CENTERED ? c[1] * a.inv_d : 0.f;
+    cu = group_add(cu, a.group < 64 ? a.group : 64);
+    if (CENTERED) cg = group_add(cg, a.group < 64 ? a.group : 64);
+    if (a.group > 64) {
+      if ((threadIdx.x & 63) == 0) {
+        red[half][0][wave] = cu;
+        red[half][1][wave] = cg;
+      }
+      __syncthreads();
+      cu = cg = 0.f;
+      for (int k = 0; k < per; ++k) {
+        cu += red[half][0][group * per + k];
+        if (CENTERED) cg += red[half][1][group * per + k];
+      }
+      half ^= 1;
+    }
+    cu *= a.inv_d;
+    cg *= a.inv_d;
     if (on)
 #pragma unroll
       for (int e = 0; e < NV; ++e)
         if (live[e]) {
           VT o;
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const int n = e * W + j;
-            o.v[j] = f2el<T>(fmaf(s, (g[n] - cg) - u[n] * cu, other[n]));
+          for (int j = 0; j < W; j += 2) {
+            float y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int n = e * W + j + i;
+              const float d = (CENTERED ? g[n] - cg : g[n]) - u[n] * cu;
+              y[i] = a.dres ? fmaf(s, d, other[e].get(j + i)) : s * d;
+            }
+            o.put(j, y[0], y[1]);
           }
           reinterpret_cast<VT*>(a.y)[row * a.nvec + lane + e * a.group] = o;
         }
@@ -252,8 +311,12 @@ __global__ void __launch_bounds__(kNormThreads) row_norm_bwd_kernel(const RowNor
     for (int e = 0; e < NV; ++e)
       if (live[e]) {
         const int at = (lane + e * a.group) * W;
-        *reinterpret_cast<Vec<float, W>*>(out + at) = *reinterpret_cast<const Vec<float, W>*>(dw + e * W);
-        *reinterpret_cast<Vec<float, W>*>(out + a.D + at) = *reinterpret_cast<const Vec<float, W>*>(db + e * W);
+#pragma unroll
+        for (int j = 0; j < W; j += 4) {
+          *reinterpret_cast<Vec<float, 4>*>(out + at + j) = {{dw[e * W + j], dw[e * W + j + 1], dw[e * W + j + 2], dw[e * W + j + 3]}};
+          if (CENTERED)
+            *reinterpret_cast<Vec<float, 4>*>(out + a.D + at + j) = {{db[e * W + j], db[e * W + j + 1], db[e * W + j + 2], db[e * W + j + 3]}};
+        }
       }
     return;
   }
@@ -268,11 +331,11 @@ __global__ void __launch_bounds__(kNormThreads) row_norm_bwd_kernel(const RowNor
           for (int j = 0; j < W; ++j) {
             const int n = e * W + j, at = (lane + e * a.group) * W + j;
             sums[at] = dw[n] + (k ? sums[at] : 0.f);
-            sums[a.D + at] = db[n] + (k ? sums[a.D + at] : 0.f);
+            if (CENTERED) sums[a.D + at] = db[n] + (k ? sums[a.D + at] : 0.f);
           }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) out[i] = sums[i];
+  for (int i = threadIdx.x; i < (CENTERED ? 2 : 1) * a.D; i += blockDim.x) out[i] = sums[i];
 }
 
 // dw and db from the blocks' sums, in a fixed order: 64 row groups of 64 columns
@@ -307,16 +370,17 @@ __global__ void __launch_bounds__(1024) row_norm_sum_kernel(const float* __restr
 
 struct NormShape {
   int nv, group, block;   // vectors of a lane, lanes of a row, threads of a block
-  NormShape(sl_dtype dt, long long D, bool bwd) {
+  NormShape(sl_dtype dt, long long D) {
     const int nvec = (int)(D * (dt == SL_BF16 ? 2 : 4) / 16);
-    nv = nvec <= 64 ? 1 : nvec <= 2048 ? 2 : 4;
+    nv = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4;
     const int lanes = (nvec + nv - 1) / nv;
     if (lanes <= 64) for (group = 8; group < lanes;) group *= 2;
     else group = (lanes + 63) / 64 * 64;
-    const int want = bwd ? 512 : 256;
-    block = group >= want ? group : want / group * group;
+    block = group >= 512 ? group : 512 / group * group;
   }
 };
+
+constexpr int kFwdThreads = 256 * 2048;   // of a forward launch; past that its blocks walk on
 
 // Blocks of a backward launch, whose sums the last launch adds.
 inline int norm_bwd_blocks(int T, int rows) {
@@ -352,20 +416,27 @@ static sl_status norm_args(RowNormArgs& a, sl_dtype dt, const sl_layout* lay, co
   return SL_OK;
 }
 
-template <typename T, bool CENTERED>
-static void launch_fwd(int nv, const RowNormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
-  if (nv == 1) hipLaunchKernelGGL((row_norm_fwd_kernel<T, 1, CENTERED>), grid, block, 0, s, a);
-  else if (nv == 2) hipLaunchKernelGGL((row_norm_fwd_kernel<T, 2, CENTERED>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((row_norm_fwd_kernel<T, 4, CENTERED>), grid, block, 0, s, a);
+template <typename T, bool CENTERED, bool BWD>
+static void launch_norm(const NormShape& sh, const RowNormArgs& a, unsigned blocks, hipStream_t s) {
+  const dim3 grid(blocks), block(sh.block);
+  // (several groups to a block: rows of at most 256 lanes)
+  const size_t lds = !BWD || sh.block == sh.group ? 0 : (size_t)2 * a.D * sizeof(float);
+  auto launch = [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    if constexpr (BWD) hipLaunchKernelGGL((row_norm_bwd_kernel<T, NV, CENTERED>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((row_norm_fwd_kernel<T, NV, CENTERED>), grid, block, lds, s, a);
+  };
+  if (sh.nv == 1) launch(std::integral_constant<int, 1>());
+  else if (sizeof(T) == 2 || sh.nv == 2) launch(std::integral_constant<int, 2>());
+  else if constexpr (sizeof(T) == 4) launch(std::integral_constant<int, 4>());
 }
 
-template <typename T, bool CENTERED>
-static void launch_bwd(int nv, const RowNormArgs& a, dim3 grid, dim3 block, hipStream_t s) {
-  // (several groups to a block: rows of at most 256 lanes, two vectors each)
-  const size_t lds = (int)block.x == a.group ? 0 : (size_t)2 * a.D * sizeof(float);
-  if (nv == 1) hipLaunchKernelGGL((row_norm_bwd_kernel<T, 1, CENTERED>), grid, block, lds, s, a);
-  else if (nv == 2) hipLaunchKernelGGL((row_norm_bwd_kernel<T, 2, CENTERED>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((row_norm_bwd_kernel<T, 4, CENTERED>), grid, block, lds, s, a);
+template <bool BWD>
+static sl_status run_norm(sl_dtype dt, bool centered, const NormShape& sh, const RowNormArgs& a, int blocks, hipStream_t s) {
+  if (dt == SL_BF16) centered ? launch_norm<bf16, true, BWD>(sh, a, blocks, s) : launch_norm<bf16, false, BWD>(sh, a, blocks, s);
+  else centered ? launch_norm<float, true, BWD>(sh, a, blocks, s) : launch_norm<float, false, BWD>(sh, a, blocks, s);
+  SL_HIP(hipGetLastError());
+  return SL_OK;
 }
 
 }  // namespace sl
@@ -383,15 +454,11 @@ extern "C" sl_status sl_layer_norm_fwd(sl_dtype dt, const sl_layout* lay, const 
   st = check_arch();
   if (st != SL_OK) return st;
   a.x = x; a.r = r; a.h = h; a.y = y; a.stats = stats;
-  const NormShape sh(dt, a.D, false);
+  const NormShape sh(dt, a.D);
   a.group = sh.group;
   const int rows = sh.block / sh.group;
-  const dim3 grid = walk_grid(ceil_div(a.T, rows), 2048 * 256 / sh.block), block(sh.block);
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dt == SL_BF16) p->centered ? launch_fwd<bf16, true>(sh.nv, a, grid, block, s) : launch_fwd<bf16, false>(sh.nv, a, grid, block, s);
-  else p->centered ? launch_fwd<float, true>(sh.nv, a, grid, block, s) : launch_fwd<float, false>(sh.nv, a, grid, block, s);
-  SL_HIP(hipGetLastError());
-  return SL_OK;
+  return run_norm<false>(dt, p->centered != 0, sh, a, walk_grid(ceil_div(a.T, rows), kFwdThreads / sh.block).x,
+                         reinterpret_cast<hipStream_t>(stream));
 }
 
 extern "C" size_t sl_layer_norm_workspace_bytes(const sl_layout* lay, int64_t d_model) {
@@ -400,7 +467,7 @@ extern "C" size_t sl_layer_norm_workspace_bytes(const sl_layout* lay, int64_t d_
   const int T = lay->batch * lay->seq_len;
   int most = 0;
   for (sl_dtype dt : {SL_F32, SL_BF16}) {
-    const NormShape sh(dt, d_model, true);
+    const NormShape sh(dt, d_model);
     const int n = norm_bwd_blocks(T, sh.block / sh.group);
     most = n > most ? n : most;
   }
@@ -418,7 +485,7 @@ extern "C" sl_status sl_layer_norm_bwd(sl_dtype dt, const sl_layout* lay, const 
   if (!aligned16(h) || !aligned16(stats) || !aligned16(dy) || !aligned16(dh) || !aligned16(dx) || !aligned16(dw) ||
       !aligned16(db) || !aligned16(ws))
     SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
-  const NormShape sh(dt, a.D, true);
+  const NormShape sh(dt, a.D);
   const int blocks = norm_bwd_blocks(a.T, sh.block / sh.group);
   if (!ws || ws_bytes < (size_t)blocks * 2 * a.D * sizeof(float))
     SL_FAIL(SL_ERR_WORKSPACE, "layer norm workspace too small (%zu bytes)", ws_bytes);
@@ -428,9 +495,8 @@ extern "C" sl_status sl_layer_norm_bwd(sl_dtype dt, const sl_layout* lay, const 
   a.part = reinterpret_cast<float*>(ws);
   a.group = sh.group;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid(blocks), block(sh.block);
-  if (dt == SL_BF16) p->centered ? launch_bwd<bf16, true>(sh.nv, a, grid, block, s) : launch_bwd<bf16, false>(sh.nv, a, grid, block, s);
-  else p->centered ? launch_bwd<float, true>(sh.nv, a, grid, block, s) : launch_bwd<float, false>(sh.nv, a, grid, block, s);
+  st = run_norm<true>(dt, p->centered != 0, sh, a, blocks, s);
+  if (st != SL_OK) return st;
   hipLaunchKernelGGL(row_norm_sum_kernel, dim3((unsigned)ceil_div(2 * a.D, 64)), dim3(1024), 0, s, a.part, blocks, a.D, dw, db);
   SL_HIP(hipGetLastError());
   return SL_OK;

@@ -17,6 +17,30 @@ template <typename T> __device__ inline T f2el(float x);
 template <> __device__ inline float f2el<float>(float x) { return x; }
 template <> __device__ inline bf16 f2el<bf16>(float x) { return __builtin_bit_cast(bf16, (__bf16)x); }   // to nearest even
 
+// 16 bytes of row elements as the four registers they are loaded into; values are
+// taken out where they are used.
+template <typename T> struct Pack;
+template <> struct Pack<bf16> {
+  static constexpr int W = 8;
+  typedef uint32_t Raw __attribute__((ext_vector_type(4)));
+  Raw r;
+  __device__ float get(int j) const { return __builtin_bit_cast(float, j & 1 ? r[j / 2] & 0xFFFF0000u : r[j / 2] << 16); }
+  __device__ void put(int j, float lo, float hi) {   // values j and j + 1
+    typedef __bf16 Two __attribute__((ext_vector_type(2)));
+    r[j / 2] = __builtin_bit_cast(uint32_t, Two{(__bf16)lo, (__bf16)hi});
+  }
+};
+template <> struct Pack<float> {
+  static constexpr int W = 4;
+  typedef float Raw __attribute__((ext_vector_type(4)));
+  Raw r;
+  __device__ float get(int j) const { return r[j]; }
+  __device__ void put(int j, float lo, float hi) {
+    r[j] = lo;
+    r[j + 1] = hi;
+  }
+};
+
 // The value of the lane at a fixed place in the same 16 lanes (a DPP move).
 template <int CTRL> __device__ inline float dpp(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
