@@ -71,7 +71,7 @@ template <typename T, int N> __device__ inline void load_floats(const float* p, 
 // A row's exchange between waves takes the two halves of an LDS array in turn, so
 // one barrier a row is enough: a half is written again only behind the next row's.
 template <typename T, int NV, bool CENTERED>
-__global__ void __launch_bounds__(64 * kNormWaves) row_norm_fwd_kernel(const RowNormArgs a) {
+__global__ void __launch_bounds__(64 * kNormWaves, NV == 1 ? 8 : 4) row_norm_fwd_kernel(const RowNormArgs a) {
   using VT = Pack<T>;
   constexpr int W = VT::W, N = NV * W;
   __shared__ float red[2][3][kNormWaves];
@@ -213,20 +213,21 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
   using VT = Pack<T>;
   constexpr int W = VT::W, N = NV * W;
   __shared__ float red[2][2][kNormWaves];
-  extern __shared__ float sums[];              // [2][D], where a block has several groups
+  constexpr bool WLDS = NV > 1;                // wide rows: the weight in LDS, not in registers
+  extern __shared__ __attribute__((aligned(16))) float sums[];   // [2][D] where a block has several groups; the weight
   const int groups = blockDim.x / a.group, group = threadIdx.x / a.group, lane = threadIdx.x - group * a.group;
   const int wave = threadIdx.x >> 6, per = a.group >> 6;
   const long long step = (long long)gridDim.x * groups;
   long long row = (long long)blockIdx.x * groups + group;
   int half = 0;
   bool live[NV];
-  float w[N], dw[N], db[N];
+  float w[WLDS ? 1 : N], dw[N], db[N];
   VT vh[NV], vg[NV], vd[NV];
   float st[3] = {0.f, 0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < NV; ++e) live[e] = lane + e * a.group < a.nvec;
 #pragma unroll
-  for (int j = 0; j < N; ++j) w[j] = dw[j] = db[j] = 0.f;
+  for (int j = 0; j < N; ++j) dw[j] = db[j] = 0.f;
   auto load = [&](long long t) __attribute__((always_inline)) {
     if (t >= a.T) return;
 #pragma unroll
@@ -241,9 +242,13 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
       }
   };
   load(row);
-#pragma unroll
-  for (int e = 0; e < NV; ++e)
-    if (live[e]) load_floats<T>(a.w + (lane + e * a.group) * W, w, e * W);
+  if constexpr (WLDS) {
+    for (int i = threadIdx.x * 4; i < a.D; i += blockDim.x * 4)
+      *reinterpret_cast<Vec<float, 4>*>(sums + i) = *reinterpret_cast<const Vec<float, 4>*>(a.w + i);
+    __syncthreads();
+  } else if (live[0]) {
+    load_floats<T>(a.w + lane * W, w, 0);
+  }
   for (long long t0 = (long long)blockIdx.x * groups; t0 < a.T; t0 += step, row += step) {
     const bool on = row < a.T;
     const float m = st[0], off = st[1], s = st[2];
@@ -253,6 +258,13 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
       other[e] = vd[e];
+      float we[W];
+      if constexpr (WLDS) {
+        if (live[e]) load_floats<T>(sums + (lane + e * a.group) * W, we, 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) we[j] = w[j];
+      }
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const int n = e * W + j;
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
           u[n] = (CENTERED ? (h - m) - off : h) * s;
           dw[n] = fmaf(dy, u[n], dw[n]);
           if (CENTERED) db[n] += dy;
-          g[n] = dy * w[n];
+          g[n] = dy * we[j];
           cu = fmaf(g[n], u[n], cu);
           if (CENTERED) cg += g[n];
         }
@@ -380,12 +392,20 @@ struct NormShape {
   }
 };
 
-constexpr int kFwdThreads = 256 * 2048;   // of a forward launch; past that its blocks walk on
+// Blocks of a forward launch; past that they walk on.  A whole number to each of 256
+// CUs, as they all have the same work: three of up to 512 threads, two wider ones
+// (2 x 8192 rows of 5120 bf16 in blocks of 640: one to a CU 116 us, two 121, three 148; 1 x 2048
+// rows of 4096 in blocks of 512: one 19.3, two 15.3, three 14.0, four 14.7; 2048 of 8192: 37, 32, 33).
+inline unsigned norm_fwd_blocks(int T, const NormShape& sh) {
+  return walk_grid(ceil_div(T, sh.block / sh.group), 256 * (sh.block <= 512 ? 3 : 2)).x;
+}
 
-// Blocks of a backward launch, whose sums the last launch adds.
-inline int norm_bwd_blocks(int T, int rows) {
-  const int n = ceil_div(T, rows);
-  return n < 512 ? n : 512;
+// Blocks of a backward launch, whose sums the last launch adds: one to a CU (2048 rows
+// of 4096, with the last launch: 128 blocks 25.0 us, 256 19.3, 512 21.3, 1024 28.7), and
+// at least two rows to each (256 rows: 128 blocks 9.4 us, 256 11.9).
+inline int norm_bwd_blocks(int T, const NormShape& sh) {
+  const int n = ceil_div(T, 2 * (sh.block / sh.group));
+  return n < 256 ? n : 256;
 }
 
 static sl_status check_norm(const sl_layout* lay, int64_t D) {
@@ -420,7 +440,7 @@ template <typename T, bool CENTERED, bool BWD>
 static void launch_norm(const NormShape& sh, const RowNormArgs& a, unsigned blocks, hipStream_t s) {
   const dim3 grid(blocks), block(sh.block);
   // (several groups to a block: rows of at most 256 lanes)
-  const size_t lds = !BWD || sh.block == sh.group ? 0 : (size_t)2 * a.D * sizeof(float);
+  const size_t lds = !BWD ? 0 : sh.nv > 1 ? (size_t)a.D * sizeof(float) : sh.block == sh.group ? 0 : (size_t)2 * a.D * sizeof(float);
   auto launch = [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     if constexpr (BWD) hipLaunchKernelGGL((row_norm_bwd_kernel<T, NV, CENTERED>), grid, block, lds, s, a);
@@ -432,7 +452,7 @@ static void launch_norm(const NormShape& sh, const RowNormArgs& a, unsigned bloc
 }
 
 template <bool BWD>
-static sl_status run_norm(sl_dtype dt, bool centered, const NormShape& sh, const RowNormArgs& a, int blocks, hipStream_t s) {
+static sl_status run_norm(sl_dtype dt, bool centered, const NormShape& sh, const RowNormArgs& a, unsigned blocks, hipStream_t s) {
   if (dt == SL_BF16) centered ? launch_norm<bf16, true, BWD>(sh, a, blocks, s) : launch_norm<bf16, false, BWD>(sh, a, blocks, s);
   else centered ? launch_norm<float, true, BWD>(sh, a, blocks, s) : launch_norm<float, false, BWD>(sh, a, blocks, s);
   SL_HIP(hipGetLastError());
@@ -456,9 +476,7 @@ extern "C" sl_status sl_layer_norm_fwd(sl_dtype dt, const sl_layout* lay, const 
   a.x = x; a.r = r; a.h = h; a.y = y; a.stats = stats;
   const NormShape sh(dt, a.D);
   a.group = sh.group;
-  const int rows = sh.block / sh.group;
-  return run_norm<false>(dt, p->centered != 0, sh, a, walk_grid(ceil_div(a.T, rows), kFwdThreads / sh.block).x,
-                         reinterpret_cast<hipStream_t>(stream));
+  return run_norm<false>(dt, p->centered != 0, sh, a, norm_fwd_blocks(a.T, sh), reinterpret_cast<hipStream_t>(stream));
 }
 
 extern "C" size_t sl_layer_norm_workspace_bytes(const sl_layout* lay, int64_t d_model) {
@@ -468,7 +486,7 @@ extern "C" size_t sl_layer_norm_workspace_bytes(const sl_layout* lay, int64_t d_
   int most = 0;
   for (sl_dtype dt : {SL_F32, SL_BF16}) {
     const NormShape sh(dt, d_model);
-    const int n = norm_bwd_blocks(T, sh.block / sh.group);
+    const int n = norm_bwd_blocks(T, sh);
     most = n > most ? n : most;
   }
   return (size_t)most * 2 * d_model * sizeof(float);
@@ -486,7 +504,7 @@ extern "C" sl_status sl_layer_norm_bwd(sl_dtype dt, const sl_layout* lay, const 
       !aligned16(db) || !aligned16(ws))
     SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
   const NormShape sh(dt, a.D);
-  const int blocks = norm_bwd_blocks(a.T, sh.block / sh.group);
+  const int blocks = norm_bwd_blocks(a.T, sh);
   if (!ws || ws_bytes < (size_t)blocks * 2 * a.D * sizeof(float))
     SL_FAIL(SL_ERR_WORKSPACE, "layer norm workspace too small (%zu bytes)", ws_bytes);
   st = check_arch();
