@@ -7,13 +7,15 @@
 //   dz_v = dloss [(1 - hard) tau (q_v - sum_{k: i_k = v} p_k) + hard (o_v - [v = label])].
 // Rows of context have neither loss nor gradient and are not read.
 //
-// One block a row.  The first walk over the row keeps, per thread, the running
-// maximum and the running sums of exp((z - max) / tau) and exp(z - max), rescaled
-// where the maximum moves, and joins them over the block.  The second walk forms
-// the gradient; behind it the few ids of the teacher's entries and the label are
-// written again with their subtrahends.  A step (loss and gradient in one call)
-// does both walks in one launch, the second from the caches.  Rows need not be
-// aligned (an odd vocabulary): a vector is 16 bytes at any element.
+// One block a row, the rows with a loss first, so that the context rows' zeros fill the
+// time in which the last of them end.  The first walk over a row keeps, per thread, the
+// running maximum and the running sums of exp((z - max) / tau) and exp(z - max),
+// rescaled where the maximum moves, and joins them over the block.  The second walk
+// forms the gradient; behind it the few ids of the teacher's entries and the label are
+// written again with their subtrahends.  A step (loss and gradient in one call) does
+// both walks in one launch, the second from the caches.  Both load the next four
+// vectors of a thread before they work on these.  Rows need not be aligned (an odd
+// vocabulary): a vector is 16 bytes at any element.
 #include <cmath>
 
 #include "sl_rows.hpp"
@@ -21,7 +23,8 @@
 namespace sl {
 
 constexpr int kTop = SL_DISTILL_MAX_TOP;   // most entries of the teacher
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 512;           // most threads of a row
+constexpr int kVecs = 4;                   // vectors that a thread loads at a time
 
 enum DistillMode { DM_FWD, DM_BWD, DM_STEP };
 
@@ -35,12 +38,12 @@ struct DistillArgs {
   float* loss;
   float* stats;             // [T][4]: the maximum, the sums of exp((z - max) / tau) and of exp(z - max), 0
   long long ld, ld_out;     // elements from row to row
-  int V, top, L, rows;
+  int V, top, rows;
   float tau, inv_tau, hard;
-  int ctx[SL_MAX_SEQS];
+  SeqTab st;
 };
 
-constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // 16 bytes of row elements, at any element's address
 template <typename T> struct RowVec;
@@ -49,42 +52,79 @@ template <> struct RowVec<bf16> {
   static constexpr int W = 8;
   __device__ static inline float get(uint16_t x) { return bf2f(x); }
   __device__ static inline uint16_t put(float x) { return f2el<bf16>(x).v; }
+  __device__ static inline Raw none() { return (Raw)(uint16_t)0xFF80; }   // -inf
 };
 template <> struct RowVec<float> {
   typedef float Raw __attribute__((ext_vector_type(4), aligned(4)));
   static constexpr int W = 4;
   __device__ static inline float get(float x) { return x; }
   __device__ static inline float put(float x) { return x; }
+  __device__ static inline Raw none() { return (Raw)(-INFINITY); }
 };
 
-// e^((z - m) scale), z <= m; scale includes log2 e.  z - m first: lowest values and
-// infinities of a mask then behave (equal ones count 1, -inf below a finite maximum 0).
-__device__ inline float exp_below(float z, float m, float scale) { return __builtin_amdgcn_exp2f((z - m) * scale); }
-
-// Running maximum and the two sums relative to it; an empty one has m = -inf.
+// Running maximum m and the two sums of 2^(z scale - top), top = m scale rounded once
+// (then a number like any other: one rounding of the small difference is all an
+// exponent gets).  Past 2^20 that one rounding would reach the exponents' range: there,
+// and where m is infinite, the sums are of 2^((z - m) scale), so that equal lowest values
+// of a mask count 1 each.  An empty one has m = -inf.
 struct Sums {
-  float m, s[2];
+  float m, s[2], top[2];
+  bool near;                                    // |top| below 2^20
 };
-template <bool TWO> __device__ inline void rebase(Sums& a, float m, const float* scale) {
-  // (a row of -inf alone, or of NaN, keeps m = -inf: relative to 0 its sums stay what they are)
-  const float from = a.m == -INFINITY ? m : a.m;
-  a.s[0] *= m == -INFINITY ? 1.f : exp_below(from, m, scale[0]);
-  if (TWO) a.s[1] *= m == -INFINITY ? 1.f : exp_below(from, m, scale[1]);
+template <bool TWO> __device__ inline void set_top(Sums& a, float m, const float* scale) {
   a.m = m;
+  a.top[0] = rounded(m * scale[0]);
+  a.near = fabsf(a.top[0]) < 0x1p20f;
+  if (TWO) {
+    a.top[1] = rounded(m * scale[1]);
+    a.near = a.near && fabsf(a.top[1]) < 0x1p20f;
+  }
+}
+// 2^(z scale - top) of a value z <= m; m = -inf (nothing but -inf or NaN so far) counts as 0
+__device__ inline float term(const Sums& a, float z, float scale, int i) {
+  const float y = a.near ? fmaf(z, scale, -a.top[i]) : (z - (a.m == -INFINITY ? 0.f : a.m)) * scale;
+  return __builtin_amdgcn_exp2f(y);
+}
+// The sums relative to another maximum, at least the old one.
+template <bool TWO> __device__ inline void rebase(Sums& a, float m, const float* scale) {
+  const Sums old = a;
+  set_top<TWO>(a, m, scale);
+  if (old.m == -INFINITY) return;               // (the sums are 0, or NaN)
+#pragma unroll
+  for (int i = 0; i < 1 + TWO; ++i)
+    a.s[i] *= __builtin_amdgcn_exp2f(old.near && a.near ? old.top[i] - a.top[i] : (old.m - m) * scale[i]);
 }
 
-// The values of one vector into the running sums.
+// The values of some vectors into the running sums.
 template <bool TWO, int N> __device__ inline void absorb(Sums& a, const float (&x)[N], const float* scale) {
   float m = a.m;
 #pragma unroll
   for (int j = 0; j < N; ++j) m = fmaxf(m, x[j]);
   if (m > a.m) rebase<TWO>(a, m, scale);
-  const float at = a.m == -INFINITY ? 0.f : a.m;
+  if (a.near) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    a.s[0] += exp_below(x[j], at, scale[0]);
-    if (TWO) a.s[1] += exp_below(x[j], at, scale[1]);
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 1 + TWO; ++i) a.s[i] += __builtin_amdgcn_exp2f(fmaf(x[j], scale[i], -a.top[i]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 1 + TWO; ++i) a.s[i] += term(a, x[j], scale[i], i);
   }
+}
+
+__device__ inline float top_term(float t, float m, float scale) { return __builtin_amdgcn_exp2f((t - m) * scale); }
+
+// Token row of row i of the context rows.
+__device__ inline int context_token(const SeqTab& st, int i) {
+  int lo = 0, hi = st.nseq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (st.ctx_pre[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo * st.L + (i - st.ctx_pre[lo]);
 }
 
 // TWO: the teacher's term at tau and the label's at 1 need an exponential each.
@@ -93,164 +133,171 @@ template <typename T, int MODE, bool TWO>
 __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs a) {
   using RV = RowVec<T>;
   using Raw = typename RV::Raw;
-  constexpr int W = RV::W, U = 4, kWaves = kRowThreads / 64;
-  __shared__ float red[3][kWaves];
+  constexpr int W = RV::W, U = kVecs;
+  __shared__ float red[3][kRowThreads / 64];
   __shared__ int ids[kTop + 1];                 // the teacher's entries and, behind them, the label; -1: none
   __shared__ float ptop[kTop], ztop[kTop + 1];  // the entries' logits, the student's at these ids
-  __shared__ float teacher[2];                  // maximum and sum of the entries; sum 0: none
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ float dtop[MODE == DM_FWD ? 1 : kTop + 1];   // the gradient there
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
   const bool soft = a.hard < 1.f, hard = a.hard > 0.f;
   const int K = soft ? a.top : 0;
   const float scale[2] = {(soft ? a.inv_tau : 1.f) * kLog2e, kLog2e};
-  const int nvec = a.V / W;
+  const int nvec = a.V / W, ntail = a.V - nvec * W;
 
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  for (long long it = blockIdx.x; it < a.rows; it += gridDim.x) {
+    const bool out = it < a.st.T_out;
+    const long long row = out ? out_token(a.st, (int)it) : context_token(a.st, (int)it - a.st.T_out);
     const T* const z = reinterpret_cast<const T*>(a.z) + row * a.ld;
     T* const dz = reinterpret_cast<T*>(a.dz) + row * a.ld_out;
-    const int seq = (int)(row / a.L);
-    const float g = MODE == DM_FWD ? 0.f : a.dloss ? a.dloss[row] : 1.f;
-    bool read = (int)(row - (long long)seq * a.L) >= a.ctx[seq] && (MODE != DM_BWD || g != 0.f);
-    __syncthreads();                            // the last row's shared values have been read
-    if (read && tid <= K) {
-      int id = tid < K ? a.top_ids[row * a.top + tid] : hard ? a.labels[row] : -1;
-      if ((unsigned)id >= (unsigned)a.V) id = -1;
-      ids[tid] = id;
-      ztop[tid] = id >= 0 ? ldv<T>(z, id) : 0.f;
-      if (tid < K) ptop[tid] = id >= 0 ? a.top_logits[row * a.top + tid] : -INFINITY;
-    }
-    __syncthreads();
-    if (read && wave == 0) {
-      float m = -INFINITY, bad = 0.f, s = 0.f;
+    const float g = MODE == DM_FWD || !out ? 0.f : a.dloss ? a.dloss[row] : 1.f;
+    const bool live = out && (MODE != DM_BWD || g != 0.f);
+    auto fetch = [&](int c, Raw (&v)[U]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c + u * threads < nvec) v[u] = *reinterpret_cast<const Raw*>(z + (long long)(c + u * threads) * W);
+        else v[u] = RV::none();
+    };
+    Raw v[U], next[U];
+    bool taught = false, labelled = false;
+    float tmax = -INFINITY, tsum = 0.f;
+    if (live) {
+      __syncthreads();                          // the last row's shared values have been read
+      for (int k = tid; k <= K; k += threads) {
+        int id = k < K ? a.top_ids[row * a.top + k] : hard ? a.labels[row] : -1;
+        if ((unsigned)id >= (unsigned)a.V) id = -1;
+        ids[k] = id;
+        ztop[k] = id >= 0 ? ldv<T>(z, id) : 0.f;
+        if (k < K) ptop[k] = id >= 0 ? a.top_logits[row * a.top + k] : -INFINITY;
+      }
+      fetch(tid, v);
+      __syncthreads();
+      // every wave for itself
+      float bad = 0.f;
       for (int k = lane; k < K; k += 64) {
-        m = fmaxf(m, ptop[k]);
+        tmax = fmaxf(tmax, ptop[k]);
         if (!(ptop[k] < INFINITY)) bad = 1.f;   // infinite or NaN: no distribution
       }
-      m = wave_max(m);
-      bad = wave_add(bad);
-      if (m > -INFINITY)
-        for (int k = lane; k < K; k += 64) s += exp_below(ptop[k], m, scale[0]);
-      s = wave_add(s);
-      if (lane == 0) {
-        teacher[0] = m;
-        teacher[1] = bad > 0.f ? NAN : s;
-      }
+      tmax = wave_max(tmax);
+      if (tmax > -INFINITY)
+        for (int k = lane; k < K; k += 64) tsum += top_term(ptop[k], tmax, scale[0]);
+      tsum = wave_add(tsum);
+      if (wave_add(bad) > 0.f) tsum = NAN;
+      taught = !(tsum == 0.f);
+      labelled = ids[K] >= 0;
     }
-    __syncthreads();
-    const float tmax = teacher[0], tsum = teacher[1];
-    const bool taught = read && !(tsum == 0.f), labelled = read && ids[K] >= 0;
-    read = taught || labelled;                  // with neither the row has no loss
-    if (!read) {
+    if (!taught && !labelled) {                 // no loss
       if (MODE != DM_BWD && tid == 0) a.loss[row] = 0.f;
       if (MODE == DM_FWD && tid < 4) a.stats[row * 4 + tid] = 0.f;
       if (MODE != DM_FWD) {
         const Raw zero = {};
-        for (int c = tid; c < nvec; c += kRowThreads) *reinterpret_cast<Raw*>(dz + (long long)c * W) = zero;
-        if (tid < a.V - nvec * W) stv<T>(dz, nvec * W + tid, 0.f);
+        for (int c = tid; c < nvec; c += threads) *reinterpret_cast<Raw*>(dz + (long long)c * W) = zero;
+        if (tid < ntail) stv<T>(dz, nvec * W + tid, 0.f);
       }
       continue;
     }
 
-    Sums run = {-INFINITY, {0.f, 0.f}};
+    Sums run = {-INFINITY, {0.f, 0.f}, {0.f, 0.f}, false};
     if constexpr (MODE == DM_BWD) {
-      run = {a.stats[row * 4], {a.stats[row * 4 + 1], a.stats[row * 4 + 2]}};
+      set_top<TWO>(run, a.stats[row * 4], scale);
+      run.s[0] = a.stats[row * 4 + 1];
+      run.s[1] = a.stats[row * 4 + 2];
     } else {
-      int c = tid;
-      for (; c + (U - 1) * kRowThreads < nvec; c += kRowThreads * U) {
-        Raw v[U];
+      for (int c = tid; c - tid < nvec; c += threads * U) {
+        fetch(c + threads * U, next);
         float x[U * W];
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const Raw*>(z + (long long)(c + u * kRowThreads) * W);
 #pragma unroll
         for (int j = 0; j < U * W; ++j) x[j] = RV::get(v[j / W][j % W]);
         absorb<TWO>(run, x, scale);
-      }
-      for (; c < nvec; c += kRowThreads) {
-        const Raw v = *reinterpret_cast<const Raw*>(z + (long long)c * W);
-        float x[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) x[j] = RV::get(v[j]);
-        absorb<TWO>(run, x, scale);
+        for (int u = 0; u < U; ++u) v[u] = next[u];
       }
-      if (tid < a.V - nvec * W) {
+      if (tid < ntail) {
         const float x[1] = {ldv<T>(z, nvec * W + tid)};
         absorb<TWO>(run, x, scale);
       }
+      if (MODE == DM_STEP) fetch(tid, v);       // the second walk's first
       rebase<TWO>(run, wave_max(run.m), scale);
 #pragma unroll
       for (int i = 0; i < 1 + TWO; ++i) run.s[i] = wave_add(run.s[i]);
-      if (lane == 0) {
-        red[0][wave] = run.m;
-        red[1][wave] = run.s[0];
-        red[2][wave] = run.s[1];
+      if (threads > 64) {
+        if (lane == 0) {
+          red[0][wave] = run.m;
+          red[1][wave] = run.s[0];
+          red[2][wave] = run.s[1];
+        }
+        __syncthreads();
+        const int waves = threads >> 6;
+        float m = red[0][0];
+        for (int i = 1; i < waves; ++i) m = fmaxf(m, red[0][i]);
+        set_top<TWO>(run, m, scale);
+        run.s[0] = run.s[1] = 0.f;
+        for (int i = 0; i < waves; ++i) {
+          Sums p;
+          set_top<TWO>(p, red[0][i], scale);
+          p.s[0] = red[1][i];
+          p.s[1] = red[2][i];
+          rebase<TWO>(p, m, scale);
+          run.s[0] += p.s[0];
+          run.s[1] += p.s[1];
+        }
       }
-      __syncthreads();
-      float m = red[0][0];
-#pragma unroll
-      for (int i = 1; i < kWaves; ++i) m = fmaxf(m, red[0][i]);
-      run = {m, {0.f, 0.f}};
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        Sums p = {red[0][i], {red[1][i], red[2][i]}};
-        rebase<TWO>(p, m, scale);
-        run.s[0] += p.s[0];
-        run.s[1] += p.s[1];
-      }
-      if (m == -INFINITY) run.s[0] = run.s[1] = NAN;   // nothing to choose from: no distribution
+      if (run.m == -INFINITY) run.s[0] = run.s[1] = NAN;   // nothing to choose from: no distribution
       if (MODE == DM_FWD && tid < 4) a.stats[row * 4 + tid] = tid == 0 ? run.m : tid == 1 ? run.s[0] : tid == 2 ? run.s[1] : 0.f;
     }
     const float s_soft = run.s[0], s_hard = run.s[TWO];
 
     if (MODE != DM_BWD && wave == 0) {
+      // the natural logarithm of a term
+      auto below = [&](float x, int i) __attribute__((always_inline)) {
+        return kLn2 * (run.near ? fmaf(x, scale[i], -run.top[i]) : (x - run.m) * scale[i]);
+      };
       float kl = 0.f;
       const float lp = logf(tsum), lq = logf(s_soft);
       if (taught)
         for (int k = lane; k < K; k += 64) {
-          const float p = exp_below(ptop[k], tmax, scale[0]) / tsum;
-          if (!(p == 0.f)) kl += p * (((ptop[k] - tmax) * a.inv_tau - lp) - ((ztop[k] - run.m) * a.inv_tau - lq));
+          const float p = top_term(ptop[k], tmax, scale[0]) / tsum;
+          if (!(p == 0.f)) kl += p * (((ptop[k] - tmax) * a.inv_tau - lp) - (below(ztop[k], 0) - lq));
         }
       kl = wave_add(kl);
       if (lane == 0) {
         float l = taught ? (1.f - a.hard) * a.tau * a.tau * kl : 0.f;
-        if (labelled) l += a.hard * (logf(s_hard) - (ztop[K] - run.m));
+        if (labelled) l += a.hard * (logf(s_hard) - below(ztop[K], TWO));
         a.loss[row] = l;
       }
     }
     if constexpr (MODE != DM_FWD) {
       const float cs = taught ? g * (1.f - a.hard) * a.tau : 0.f, ch = labelled ? g * a.hard : 0.f;
-      const float as = (TWO ? cs : cs + ch) / s_soft, ah = ch / s_hard, at = run.m == -INFINITY ? 0.f : run.m;
+      const float as = (TWO ? cs : cs + ch) / s_soft, ah = ch / s_hard;
       auto grad = [&](float x) __attribute__((always_inline)) {
-        const float d = exp_below(x, at, scale[0]) * as;
-        return TWO ? fmaf(exp_below(x, at, scale[1]), ah, d) : d;
+        const float d = term(run, x, scale[0], 0) * as;
+        return TWO ? fmaf(term(run, x, scale[1], 1), ah, d) : d;
       };
-      auto vec = [&](const Raw& v) __attribute__((always_inline)) {
-        Raw o;
-#pragma unroll
-        for (int j = 0; j < W; ++j) o[j] = RV::put(grad(RV::get(v[j])));
-        return o;
-      };
-      int c = tid;
-      for (; c + (U - 1) * kRowThreads < nvec; c += kRowThreads * U) {
-        Raw v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const Raw*>(z + (long long)(c + u * kRowThreads) * W);
-#pragma unroll
-        for (int u = 0; u < U; ++u) *reinterpret_cast<Raw*>(dz + (long long)(c + u * kRowThreads) * W) = vec(v[u]);
-      }
-      for (; c < nvec; c += kRowThreads)
-        *reinterpret_cast<Raw*>(dz + (long long)c * W) = vec(*reinterpret_cast<const Raw*>(z + (long long)c * W));
-      if (tid < a.V - nvec * W) stv<T>(dz, nvec * W + tid, grad(ldv<T>(z, nvec * W + tid)));
-      __syncthreads();
-      // the entries and the label, their q and o from before dz may have been written
-      // over z; an id that comes twice gets the same value from each of its entries
-      if (tid <= K && ids[tid] >= 0) {
-        const int id = ids[tid];
-        float d = grad(ztop[tid]);
+      // at the entries' ids and the label; an id that comes twice gets the same value from
+      // each of its entries
+      for (int k = tid; k <= K; k += threads) {
+        const int id = ids[k];
+        float d = grad(ztop[k]);
         if (taught)
-          for (int k = 0; k < K; ++k)
-            if (ids[k] == id) d -= cs * (exp_below(ptop[k], tmax, scale[0]) / tsum);
+          for (int i = 0; i < K; ++i)
+            if (ids[i] == id) d -= cs * (top_term(ptop[i], tmax, scale[0]) / tsum);
         if (labelled && ids[K] == id) d -= ch;
-        stv<T>(dz, id, d);
+        dtop[k] = d;
       }
+      for (int c = tid; c - tid < nvec; c += threads * U) {
+        fetch(c + threads * U, next);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Raw o;
+#pragma unroll
+          for (int j = 0; j < W; ++j) o[j] = RV::put(grad(RV::get(v[u][j])));
+          if (c + u * threads < nvec) *reinterpret_cast<Raw*>(dz + (long long)(c + u * threads) * W) = o;
+          v[u] = next[u];
+        }
+      }
+      if (tid < ntail) stv<T>(dz, nvec * W + tid, grad(ldv<T>(z, nvec * W + tid)));
+      __syncthreads();                          // the row is written, and dtop
+      for (int k = tid; k <= K; k += threads)
+        if (ids[k] >= 0) stv<T>(dz, ids[k], dtop[k]);
     }
   }
 }
@@ -258,9 +305,8 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
 static sl_status distill_args(DistillArgs& a, sl_dtype dt, const sl_layout* lay, const sl_distill* p, const void* z,
                               int64_t ld, const void* dz, int64_t ld_out) {
   sl_status st = check_dtype(dt);
-  if (st == SL_OK) st = check_tokens(lay);
+  if (st == SL_OK) st = build_seqtab(lay, a.st);
   if (st != SL_OK) return st;
-  if (!lay->ctx_len) SL_FAIL(SL_ERR_NULL, "layout.ctx_len is NULL");
   if (!p || !z) SL_FAIL(SL_ERR_NULL, "the targets and logits required");
   if (p->vocab < 1 || p->vocab > (1LL << 30)) SL_FAIL(SL_ERR_RANGE, "vocabulary of %lld outside [1, 2^30]", (long long)p->vocab);
   if (!(p->hard >= 0.f && p->hard <= 1.f)) SL_FAIL(SL_ERR_RANGE, "hard must be in [0, 1]");
@@ -275,17 +321,11 @@ static sl_status distill_args(DistillArgs& a, sl_dtype dt, const sl_layout* lay,
     SL_FAIL(SL_ERR_SHAPE, "rows of %lld and %lld elements hold no %lld logits", (long long)ld, (long long)ld_out, (long long)p->vocab);
   if (!aligned16(z) || !aligned16(dz) || !aligned16(p->top_ids) || !aligned16(p->top_logits) || !aligned16(p->labels))
     SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
-  a = DistillArgs{};
   a.z = z; a.ld = ld; a.ld_out = ld_out;
   a.top_ids = p->top_ids; a.top_logits = p->top_logits; a.labels = p->labels;
   a.V = (int)p->vocab; a.top = p->top;
-  a.L = lay->seq_len; a.rows = lay->batch * lay->seq_len;
+  a.rows = lay->batch * lay->seq_len;
   a.tau = p->temperature; a.inv_tau = 1.f / p->temperature; a.hard = p->hard;
-  for (int b = 0; b < lay->batch; ++b) {
-    a.ctx[b] = lay->ctx_len[b];
-    if (a.ctx[b] < 0 || a.ctx[b] > lay->seq_len)
-      SL_FAIL(SL_ERR_RANGE, "ctx_len[%d] = %d outside [0, %d]", b, a.ctx[b], lay->seq_len);
-  }
   return SL_OK;
 }
 
@@ -293,7 +333,11 @@ template <int MODE> static sl_status run_distill(sl_dtype dt, const DistillArgs&
   sl_status st = check_arch();
   if (st != SL_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid = walk_grid(a.rows), block(kRowThreads);
+  // as few threads as load a row at once (8192 rows of 2000 bf16: 64 threads  us, 512  us)
+  const int nvec = a.V / (dt == SL_BF16 ? 8 : 4);
+  int threads = 64;
+  while (threads < kRowThreads && threads * kVecs < nvec) threads *= 2;
+  const dim3 grid = walk_grid(a.rows), block(threads);
   const bool two = a.hard > 0.f && a.hard < 1.f && a.tau != 1.f;
   if (dt == SL_BF16) {
     if (two) hipLaunchKernelGGL((distill_kernel<bf16, MODE, true>), grid, block, 0, s, a);
@@ -313,7 +357,7 @@ using namespace sl;
 extern "C" sl_status sl_distill_fwd(sl_dtype dt, const sl_layout* lay, const sl_distill* p, const void* logits,
                                     int64_t ld, float* loss, float* stats, void* stream) {
   if (!loss || !stats) SL_FAIL(SL_ERR_NULL, "loss and stats required");
-  DistillArgs a;
+  DistillArgs a{};
   sl_status st = distill_args(a, dt, lay, p, logits, ld, nullptr, 0);
   if (st != SL_OK) return st;
   if (!aligned16(loss) || !aligned16(stats)) SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
@@ -325,7 +369,7 @@ extern "C" sl_status sl_distill_bwd(sl_dtype dt, const sl_layout* lay, const sl_
                                     int64_t ld, const float* stats, const float* dloss, void* dlogits, int64_t ld_out,
                                     void* stream) {
   if (!stats || !dlogits) SL_FAIL(SL_ERR_NULL, "stats and dlogits required");
-  DistillArgs a;
+  DistillArgs a{};
   sl_status st = distill_args(a, dt, lay, p, logits, ld, dlogits, ld_out);
   if (st != SL_OK) return st;
   if (!aligned16(stats) || !aligned16(dloss)) SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
@@ -337,7 +381,7 @@ extern "C" sl_status sl_distill_step(sl_dtype dt, const sl_layout* lay, const sl
                                      int64_t ld, const float* dloss, float* loss, void* dlogits, int64_t ld_out,
                                      void* stream) {
   if (!loss || !dlogits) SL_FAIL(SL_ERR_NULL, "loss and dlogits required");
-  DistillArgs a;
+  DistillArgs a{};
   sl_status st = distill_args(a, dt, lay, p, logits, ld, dlogits, ld_out);
   if (st != SL_OK) return st;
   if (!aligned16(loss) || !aligned16(dloss)) SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");

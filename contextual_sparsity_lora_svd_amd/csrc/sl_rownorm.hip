@@ -46,13 +46,6 @@ __device__ inline float group_add(float x, int group) {
   return x;
 }
 
-// x as it is rounded: the compiler may not take it as the product that it comes
-// from, fused into a difference (which would be to another mean than the kept one).
-__device__ inline float rounded(float x) {
-  asm("" : "+v"(x));
-  return x;
-}
-
 // Lanes of a wave that hold values in place e of their vectors.
 __device__ inline int live_lanes(const RowNormArgs& a, int wave, int e) {
   const int n = a.nvec - e * a.group - wave * 64;
@@ -213,7 +206,10 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
   using VT = Pack<T>;
   constexpr int W = VT::W, N = NV * W;
   __shared__ float red[2][2][kNormWaves];
-  constexpr bool WLDS = NV > 1;                // wide rows: the weight in LDS, not in registers
+  // Rows of over 1024 vectors fill the registers of a block of 1024 threads: the weight is
+  // then kept in LDS and the next row is not loaded ahead (2048 rows of 16384 bf16: 71 us;
+  // loaded ahead 77, with the weight in registers too, 104: the compiler spills).
+  constexpr bool WLDS = NV > 1;
   extern __shared__ __attribute__((aligned(16))) float sums[];   // [2][D] where a block has several groups; the weight
   const int groups = blockDim.x / a.group, group = threadIdx.x / a.group, lane = threadIdx.x - group * a.group;
   const int wave = threadIdx.x >> 6, per = a.group >> 6;
@@ -241,7 +237,7 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
         if (a.dres) vd[e] = reinterpret_cast<const VT*>(a.dres)[at];
       }
   };
-  load(row);
+  if (!WLDS) load(row);
   if constexpr (WLDS) {
     for (int i = threadIdx.x * 4; i < a.D; i += blockDim.x * 4)
       *reinterpret_cast<Vec<float, 4>*>(sums + i) = *reinterpret_cast<const Vec<float, 4>*>(a.w + i);
@@ -251,6 +247,7 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
   }
   for (long long t0 = (long long)blockIdx.x * groups; t0 < a.T; t0 += step, row += step) {
     const bool on = row < a.T;
+    if (WLDS) load(row);
     const float m = st[0], off = st[1], s = st[2];
     float u[N], g[N];
     VT other[NV];
@@ -280,7 +277,7 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
         }
       }
     }
-    load(row + step);
+    if (!WLDS) load(row + step);
     cu = group_add(cu, a.group < 64 ? a.group : 64);
     if (CENTERED) cg = group_add(cg, a.group < 64 ? a.group : 64);
     if (a.group > 64) {

@@ -69,6 +69,13 @@ __device__ inline float wave_max(float x) {   // NaN only where every lane holds
   return fmaxf(fmaxf(lane_value(x, 0), lane_value(x, 16)), fmaxf(lane_value(x, 32), lane_value(x, 48)));
 }
 
+// A product as it is rounded: the compiler may not fuse it into the difference that
+// it goes into (which would be to another number than the one kept elsewhere).
+__device__ inline float rounded(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
 // batch and seq_len of a layout (ctx_len is not looked at)
 inline sl_status check_tokens(const sl_layout* lay) {
   if (!lay) SL_FAIL(SL_ERR_NULL, "layout is NULL");
