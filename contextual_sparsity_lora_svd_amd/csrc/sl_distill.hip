@@ -17,6 +17,7 @@
 // vectors of a thread before they work on these.  Rows need not be aligned (an odd
 // vocabulary): a vector is 16 bytes at any element.
 #include <cmath>
+#include <type_traits>
 
 #include "sl_rows.hpp"
 
@@ -81,8 +82,8 @@ template <bool TWO> __device__ inline void set_top(Sums& a, float m, const float
   }
 }
 // 2^(z scale - top) of a value z <= m; m = -inf (nothing but -inf or NaN so far) counts as 0
-__device__ inline float term(const Sums& a, float z, float scale, int i) {
-  const float y = a.near ? fmaf(z, scale, -a.top[i]) : (z - (a.m == -INFINITY ? 0.f : a.m)) * scale;
+template <bool NEAR> __device__ inline float term(const Sums& a, float z, float scale, int i) {
+  const float y = NEAR ? fmaf(z, scale, -a.top[i]) : (z - (a.m == -INFINITY ? 0.f : a.m)) * scale;
   return __builtin_amdgcn_exp2f(y);
 }
 // The sums relative to another maximum, at least the old one.
@@ -110,7 +111,7 @@ template <bool TWO, int N> __device__ inline void absorb(Sums& a, const float (&
 #pragma unroll
     for (int j = 0; j < N; ++j)
 #pragma unroll
-      for (int i = 0; i < 1 + TWO; ++i) a.s[i] += term(a, x[j], scale[i], i);
+      for (int i = 0; i < 1 + TWO; ++i) a.s[i] += term<false>(a, x[j], scale[i], i);
   }
 }
 
@@ -150,7 +151,6 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
     const T* const z = reinterpret_cast<const T*>(a.z) + row * a.ld;
     T* const dz = reinterpret_cast<T*>(a.dz) + row * a.ld_out;
     const float g = MODE == DM_FWD || !out ? 0.f : a.dloss ? a.dloss[row] : 1.f;
-    const bool live = out && (MODE != DM_BWD || g != 0.f);
     auto fetch = [&](int c, Raw (&v)[U]) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -158,18 +158,49 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
         else v[u] = RV::none();
     };
     Raw v[U], next[U];
+    Sums run = {-INFINITY, {0.f, 0.f}, {0.f, 0.f}, false};
     bool taught = false, labelled = false;
     float tmax = -INFINITY, tsum = 0.f;
-    if (live) {
+    if (out) {
       __syncthreads();                          // the last row's shared values have been read
+      if constexpr (MODE == DM_BWD) {
+        set_top<TWO>(run, a.stats[row * 4], scale);
+        run.s[0] = a.stats[row * 4 + 1];
+        run.s[1] = a.stats[row * 4 + 2];
+      }
+      fetch(tid, v);
       for (int k = tid; k <= K; k += threads) {
         int id = k < K ? a.top_ids[row * a.top + k] : hard ? a.labels[row] : -1;
         if ((unsigned)id >= (unsigned)a.V) id = -1;
+        const float t = k < K ? a.top_logits[row * a.top + k] : 0.f;
         ids[k] = id;
         ztop[k] = id >= 0 ? ldv<T>(z, id) : 0.f;
-        if (k < K) ptop[k] = id >= 0 ? a.top_logits[row * a.top + k] : -INFINITY;
+        if (k < K) ptop[k] = id >= 0 ? t : -INFINITY;
       }
-      fetch(tid, v);
+      if constexpr (MODE != DM_BWD) {
+        for (int c = tid; c - tid < nvec; c += threads * U) {
+          fetch(c + threads * U, next);
+          float x[U * W];
+#pragma unroll
+          for (int j = 0; j < U * W; ++j) x[j] = RV::get(v[j / W][j % W]);
+          absorb<TWO>(run, x, scale);
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[u] = next[u];
+        }
+        if (tid < ntail) {
+          const float x[1] = {ldv<T>(z, nvec * W + tid)};
+          absorb<TWO>(run, x, scale);
+        }
+        if (MODE == DM_STEP) fetch(tid, v);     // the second walk's first
+        rebase<TWO>(run, wave_max(run.m), scale);
+#pragma unroll
+        for (int i = 0; i < 1 + TWO; ++i) run.s[i] = wave_add(run.s[i]);
+        if (lane == 0) {
+          red[0][wave] = run.m;
+          red[1][wave] = run.s[0];
+          red[2][wave] = run.s[1];
+        }
+      }
       __syncthreads();
       // every wave for itself
       float bad = 0.f;
@@ -185,7 +216,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
       taught = !(tsum == 0.f);
       labelled = ids[K] >= 0;
     }
-    if (!taught && !labelled) {                 // no loss
+    if ((!taught && !labelled) || (MODE == DM_BWD && g == 0.f)) {   // no loss
       if (MODE != DM_BWD && tid == 0) a.loss[row] = 0.f;
       if (MODE == DM_FWD && tid < 4) a.stats[row * 4 + tid] = 0.f;
       if (MODE != DM_FWD) {
@@ -195,53 +226,22 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
       }
       continue;
     }
-
-    Sums run = {-INFINITY, {0.f, 0.f}, {0.f, 0.f}, false};
-    if constexpr (MODE == DM_BWD) {
-      set_top<TWO>(run, a.stats[row * 4], scale);
-      run.s[0] = a.stats[row * 4 + 1];
-      run.s[1] = a.stats[row * 4 + 2];
-    } else {
-      for (int c = tid; c - tid < nvec; c += threads * U) {
-        fetch(c + threads * U, next);
-        float x[U * W];
-#pragma unroll
-        for (int j = 0; j < U * W; ++j) x[j] = RV::get(v[j / W][j % W]);
-        absorb<TWO>(run, x, scale);
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = next[u];
+    if constexpr (MODE != DM_BWD) {
+      const int waves = threads >> 6;
+      float m = red[0][0];
+      for (int i = 1; i < waves; ++i) m = fmaxf(m, red[0][i]);
+      set_top<TWO>(run, m, scale);
+      run.s[0] = run.s[1] = 0.f;
+      for (int i = 0; i < waves; ++i) {
+        Sums p;
+        set_top<TWO>(p, red[0][i], scale);
+        p.s[0] = red[1][i];
+        p.s[1] = red[2][i];
+        rebase<TWO>(p, m, scale);
+        run.s[0] += p.s[0];
+        run.s[1] += p.s[1];
       }
-      if (tid < ntail) {
-        const float x[1] = {ldv<T>(z, nvec * W + tid)};
-        absorb<TWO>(run, x, scale);
-      }
-      if (MODE == DM_STEP) fetch(tid, v);       // the second walk's first
-      rebase<TWO>(run, wave_max(run.m), scale);
-#pragma unroll
-      for (int i = 0; i < 1 + TWO; ++i) run.s[i] = wave_add(run.s[i]);
-      if (threads > 64) {
-        if (lane == 0) {
-          red[0][wave] = run.m;
-          red[1][wave] = run.s[0];
-          red[2][wave] = run.s[1];
-        }
-        __syncthreads();
-        const int waves = threads >> 6;
-        float m = red[0][0];
-        for (int i = 1; i < waves; ++i) m = fmaxf(m, red[0][i]);
-        set_top<TWO>(run, m, scale);
-        run.s[0] = run.s[1] = 0.f;
-        for (int i = 0; i < waves; ++i) {
-          Sums p;
-          set_top<TWO>(p, red[0][i], scale);
-          p.s[0] = red[1][i];
-          p.s[1] = red[2][i];
-          rebase<TWO>(p, m, scale);
-          run.s[0] += p.s[0];
-          run.s[1] += p.s[1];
-        }
-      }
-      if (run.m == -INFINITY) run.s[0] = run.s[1] = NAN;   // nothing to choose from: no distribution
+      if (m == -INFINITY) run.s[0] = run.s[1] = NAN;   // nothing to choose from: no distribution
       if (MODE == DM_FWD && tid < 4) a.stats[row * 4 + tid] = tid == 0 ? run.m : tid == 1 ? run.s[0] : tid == 2 ? run.s[1] : 0.f;
     }
     const float s_soft = run.s[0], s_hard = run.s[TWO];
@@ -268,33 +268,38 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
     if constexpr (MODE != DM_FWD) {
       const float cs = taught ? g * (1.f - a.hard) * a.tau : 0.f, ch = labelled ? g * a.hard : 0.f;
       const float as = (TWO ? cs : cs + ch) / s_soft, ah = ch / s_hard;
-      auto grad = [&](float x) __attribute__((always_inline)) {
-        const float d = term(run, x, scale[0], 0) * as;
-        return TWO ? fmaf(term(run, x, scale[1], 1), ah, d) : d;
-      };
-      // at the entries' ids and the label; an id that comes twice gets the same value from
-      // each of its entries
-      for (int k = tid; k <= K; k += threads) {
-        const int id = ids[k];
-        float d = grad(ztop[k]);
-        if (taught)
-          for (int i = 0; i < K; ++i)
-            if (ids[i] == id) d -= cs * (top_term(ptop[i], tmax, scale[0]) / tsum);
-        if (labelled && ids[K] == id) d -= ch;
-        dtop[k] = d;
-      }
-      for (int c = tid; c - tid < nvec; c += threads * U) {
-        fetch(c + threads * U, next);
+      auto walk = [&](auto near) __attribute__((always_inline)) {
+        auto grad = [&](float x) __attribute__((always_inline)) {
+          const float d = term<decltype(near)::value>(run, x, scale[0], 0) * as;
+          return TWO ? fmaf(term<decltype(near)::value>(run, x, scale[1], 1), ah, d) : d;
+        };
+        for (int c = tid; c - tid < nvec; c += threads * U) {
+          fetch(c + threads * U, next);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          Raw o;
+          for (int u = 0; u < U; ++u) {
+            Raw o;
 #pragma unroll
-          for (int j = 0; j < W; ++j) o[j] = RV::put(grad(RV::get(v[u][j])));
-          if (c + u * threads < nvec) *reinterpret_cast<Raw*>(dz + (long long)(c + u * threads) * W) = o;
-          v[u] = next[u];
+            for (int j = 0; j < W; ++j) o[j] = RV::put(grad(RV::get(v[u][j])));
+            if (c + u * threads < nvec) *reinterpret_cast<Raw*>(dz + (long long)(c + u * threads) * W) = o;
+            v[u] = next[u];
+          }
         }
-      }
-      if (tid < ntail) stv<T>(dz, nvec * W + tid, grad(ldv<T>(z, nvec * W + tid)));
+        if (tid < ntail) stv<T>(dz, nvec * W + tid, grad(ldv<T>(z, nvec * W + tid)));
+        // at the entries' ids and the label; an id that comes twice gets the same value
+        // from each of its entries
+        for (int k = tid; k <= K; k += threads) {
+          const int id = ids[k];
+          float p = 0.f;
+#pragma unroll 8
+          for (int i = 0; i < K; ++i) p += ids[i] == id ? top_term(ptop[i], tmax, scale[0]) : 0.f;
+          float d = grad(ztop[k]);
+          if (taught) d -= cs * (p / tsum);
+          if (labelled && ids[K] == id) d -= ch;
+          dtop[k] = d;
+        }
+      };
+      if (run.near) walk(std::true_type());
+      else walk(std::false_type());
       __syncthreads();                          // the row is written, and dtop
       for (int k = tid; k <= K; k += threads)
         if (ids[k] >= 0) stv<T>(dz, ids[k], dtop[k]);
