@@ -26,6 +26,7 @@ namespace sl {
 constexpr int kTop = SL_DISTILL_MAX_TOP;   // most entries of the teacher
 constexpr int kRowThreads = 512;           // most threads of a row
 constexpr int kVecs = 4;                   // vectors that a thread loads at a time
+constexpr int kKept = 2;                   // such loads of a step that stay in LDS between the walks
 
 enum DistillMode { DM_FWD, DM_BWD, DM_STEP };
 
@@ -62,6 +63,10 @@ template <> struct RowVec<float> {
   __device__ static inline float put(float x) { return x; }
   __device__ static inline Raw none() { return (Raw)(-INFINITY); }
 };
+
+template <typename R, typename T> __device__ inline R* vec_at(T* row, int c) {
+  return reinterpret_cast<R*>(row) + c;
+}
 
 // Running maximum m and the two sums of 2^(z scale - top), top = m scale rounded once
 // (then a number like any other: one rounding of the small difference is all an
@@ -130,8 +135,9 @@ __device__ inline int context_token(const SeqTab& st, int i) {
 
 // TWO: the teacher's term at tau and the label's at 1 need an exponential each.
 // With one of the terms alone, or with tau = 1, one serves.
-template <typename T, int MODE, bool TWO>
-__global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs a) {
+// NT: past the caches, 1 the gradient's stores, 2 the loads of logits too.
+template <typename T, int MODE, bool TWO, int NT>
+__global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_kernel(const DistillArgs a) {
   using RV = RowVec<T>;
   using Raw = typename RV::Raw;
   constexpr int W = RV::W, U = kVecs;
@@ -139,11 +145,14 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
   __shared__ int ids[kTop + 1];                 // the teacher's entries and, behind them, the label; -1: none
   __shared__ float ptop[kTop], ztop[kTop + 1];  // the entries' logits, the student's at these ids
   __shared__ float dtop[MODE == DM_FWD ? 1 : kTop + 1];   // the gradient there
+  typedef uint32_t Line __attribute__((ext_vector_type(4)));
+  extern __shared__ Line kept[];                // step: the first loads of the row, a thread's where it left them
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
   const bool soft = a.hard < 1.f, hard = a.hard > 0.f;
   const int K = soft ? a.top : 0;
   const float scale[2] = {(soft ? a.inv_tau : 1.f) * kLog2e, kLog2e};
-  const int nvec = a.V / W, ntail = a.V - nvec * W;
+  const int nvec = a.V / W, ntail = a.V - nvec * W, batch = threads * U;
+  const int kept_end = MODE == DM_STEP ? kKept * batch < nvec ? kKept * batch : nvec : 0;   // vectors kept
 
   for (long long it = blockIdx.x; it < a.rows; it += gridDim.x) {
     const bool out = it < a.st.T_out;
@@ -154,8 +163,13 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
     auto fetch = [&](int c, Raw (&v)[U]) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (c + u * threads < nvec) v[u] = *reinterpret_cast<const Raw*>(z + (long long)(c + u * threads) * W);
-        else v[u] = RV::none();
+        if (c + u * threads >= nvec) v[u] = RV::none();
+        else if (NT == 2) v[u] = __builtin_nontemporal_load(vec_at<const Raw>(z, c + u * threads));
+        else v[u] = *vec_at<const Raw>(z, c + u * threads);
+    };
+    auto store = [&](int c, Raw o) __attribute__((always_inline)) {
+      if (NT) __builtin_nontemporal_store(o, vec_at<Raw>(dz, c));
+      else *vec_at<Raw>(dz, c) = o;
     };
     Raw v[U], next[U];
     Sums run = {-INFINITY, {0.f, 0.f}, {0.f, 0.f}, false};
@@ -168,21 +182,38 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
         run.s[0] = a.stats[row * 4 + 1];
         run.s[1] = a.stats[row * 4 + 2];
       }
-      fetch(tid, v);
-      for (int k = tid; k <= K; k += threads) {
-        int id = k < K ? a.top_ids[row * a.top + k] : hard ? a.labels[row] : -1;
+      // an entry a thread (more where the block is small): its id at once, the logit there
+      // behind the first vectors, both in LDS when the first walk is over
+      auto entry = [&](int k, int& id, float& t) __attribute__((always_inline)) {
+        id = k < K ? a.top_ids[row * a.top + k] : hard ? a.labels[row] : -1;
+        t = k < K ? a.top_logits[row * a.top + k] : 0.f;
+      };
+      auto share = [&](int k, int id, float t) __attribute__((always_inline)) {
         if ((unsigned)id >= (unsigned)a.V) id = -1;
-        const float t = k < K ? a.top_logits[row * a.top + k] : 0.f;
         ids[k] = id;
-        ztop[k] = id >= 0 ? ldv<T>(z, id) : 0.f;
         if (k < K) ptop[k] = id >= 0 ? t : -INFINITY;
+      };
+      int id0 = -1;
+      float t0 = 0.f, z0 = 0.f;
+      if (tid <= K) entry(tid, id0, t0);
+      fetch(tid, v);
+      if ((unsigned)id0 < (unsigned)a.V) z0 = ldv<T>(z, id0);
+      for (int k = tid + threads; k <= K; k += threads) {
+        int id;
+        float t;
+        entry(k, id, t);
+        share(k, id, t);
+        ztop[k] = ids[k] >= 0 ? ldv<T>(z, ids[k]) : 0.f;
       }
       if constexpr (MODE != DM_BWD) {
-        for (int c = tid; c - tid < nvec; c += threads * U) {
-          fetch(c + threads * U, next);
+        for (int c = tid; c - tid < nvec; c += batch) {
+          fetch(c + batch, next);
           float x[U * W];
 #pragma unroll
           for (int j = 0; j < U * W; ++j) x[j] = RV::get(v[j / W][j % W]);
+          if (c < kept_end)
+#pragma unroll
+            for (int u = 0; u < U; ++u) kept[c + u * threads] = __builtin_bit_cast(Line, v[u]);
           absorb<TWO>(run, x, scale);
 #pragma unroll
           for (int u = 0; u < U; ++u) v[u] = next[u];
@@ -191,7 +222,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
           const float x[1] = {ldv<T>(z, nvec * W + tid)};
           absorb<TWO>(run, x, scale);
         }
-        if (MODE == DM_STEP) fetch(tid, v);     // the second walk's first
+        if (MODE == DM_STEP) fetch(kKept * batch + tid, v);   // the second walk's first, behind what is kept
         rebase<TWO>(run, wave_max(run.m), scale);
 #pragma unroll
         for (int i = 0; i < 1 + TWO; ++i) run.s[i] = wave_add(run.s[i]);
@@ -200,6 +231,10 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
           red[1][wave] = run.s[0];
           red[2][wave] = run.s[1];
         }
+      }
+      if (tid <= K) {
+        share(tid, id0, t0);
+        ztop[tid] = z0;
       }
       __syncthreads();
       // every wave for itself
@@ -220,8 +255,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
       if (MODE != DM_BWD && tid == 0) a.loss[row] = 0.f;
       if (MODE == DM_FWD && tid < 4) a.stats[row * 4 + tid] = 0.f;
       if (MODE != DM_FWD) {
-        const Raw zero = {};
-        for (int c = tid; c < nvec; c += threads) *reinterpret_cast<Raw*>(dz + (long long)c * W) = zero;
+        for (int c = tid; c < nvec; c += threads) store(c, Raw{});
         if (tid < ntail) stv<T>(dz, nvec * W + tid, 0.f);
       }
       continue;
@@ -273,17 +307,21 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillArgs 
           const float d = term<decltype(near)::value>(run, x, scale[0], 0) * as;
           return TWO ? fmaf(term<decltype(near)::value>(run, x, scale[1], 1), ah, d) : d;
         };
-        for (int c = tid; c - tid < nvec; c += threads * U) {
-          fetch(c + threads * U, next);
+        auto put = [&](int c, Raw x) __attribute__((always_inline)) {
+          Raw o;
+#pragma unroll
+          for (int j = 0; j < W; ++j) o[j] = RV::put(grad(RV::get(x[j])));
+          if (c < nvec) store(c, o);
+        };
+        for (int c = (MODE == DM_STEP ? kKept * batch : 0) + tid; c - tid < nvec; c += batch) {
+          fetch(c + batch, next);
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            Raw o;
-#pragma unroll
-            for (int j = 0; j < W; ++j) o[j] = RV::put(grad(RV::get(v[u][j])));
-            if (c + u * threads < nvec) *reinterpret_cast<Raw*>(dz + (long long)(c + u * threads) * W) = o;
+            put(c + u * threads, v[u]);
             v[u] = next[u];
           }
         }
+        for (int c = tid; c < kept_end; c += threads) put(c, __builtin_bit_cast(Raw, kept[c]));
         if (tid < ntail) stv<T>(dz, nvec * W + tid, grad(ldv<T>(z, nvec * W + tid)));
         // at the entries' ids and the label; an id that comes twice gets the same value
         // from each of its entries
@@ -334,23 +372,31 @@ static sl_status distill_args(DistillArgs& a, sl_dtype dt, const sl_layout* lay,
   return SL_OK;
 }
 
+template <typename T, int MODE, bool TWO> static void launch_distill(const DistillArgs& a, hipStream_t s) {
+  // as few threads as load a row at once (8192 rows of 2000 bf16, loss: 64 threads 12 us, 512 72)
+  int threads = 64;
+  while (threads < kRowThreads && threads * kVecs < a.V / RowVec<T>::W) threads *= 2;
+  const dim3 grid = walk_grid(a.rows), block(threads);
+  const size_t lds = MODE == DM_STEP ? (size_t)kKept * threads * kVecs * 16 : 0;
+  // Logits of 2^27 bytes and more (half the last cache) go past the caches where they are
+  // used once: the gradient's stores (step of 4096 rows of 128256 bf16: 513 -> 457 us; with the
+  // product that reads the gradient next 2048 rows of 32000 278 -> 274, but 1024 rows 186 -> 193), and,
+  // in whole lines, the loads of loss and gradient in calls of their own (both, 4096 rows of 32000:
+  // 177 -> 170 us; 256 rows 20 -> 23).
+  const bool past = (long long)a.rows * a.V * (long long)sizeof(T) >= 1LL << 27;
+  const bool lines = a.ld * (long long)sizeof(T) % 16 == 0;
+  if (past && MODE != DM_STEP && lines) hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, MODE == DM_STEP ? 1 : 2>), grid, block, lds, s, a);
+  else if (past && MODE != DM_FWD) hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, MODE == DM_FWD ? 0 : 1>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, 0>), grid, block, lds, s, a);
+}
+
 template <int MODE> static sl_status run_distill(sl_dtype dt, const DistillArgs& a, void* stream) {
   sl_status st = check_arch();
   if (st != SL_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  // as few threads as load a row at once (8192 rows of 2000 bf16: 64 threads  us, 512  us)
-  const int nvec = a.V / (dt == SL_BF16 ? 8 : 4);
-  int threads = 64;
-  while (threads < kRowThreads && threads * kVecs < nvec) threads *= 2;
-  const dim3 grid = walk_grid(a.rows), block(threads);
   const bool two = a.hard > 0.f && a.hard < 1.f && a.tau != 1.f;
-  if (dt == SL_BF16) {
-    if (two) hipLaunchKernelGGL((distill_kernel<bf16, MODE, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((distill_kernel<bf16, MODE, false>), grid, block, 0, s, a);
-  } else {
-    if (two) hipLaunchKernelGGL((distill_kernel<float, MODE, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((distill_kernel<float, MODE, false>), grid, block, 0, s, a);
-  }
+  if (dt == SL_BF16) two ? launch_distill<bf16, MODE, true>(a, s) : launch_distill<bf16, MODE, false>(a, s);
+  else two ? launch_distill<float, MODE, true>(a, s) : launch_distill<float, MODE, false>(a, s);
   SL_HIP(hipGetLastError());
   return SL_OK;
 }
