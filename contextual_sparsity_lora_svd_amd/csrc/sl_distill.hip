@@ -135,7 +135,7 @@ __device__ inline int context_token(const SeqTab& st, int i) {
 
 // TWO: the teacher's term at tau and the label's at 1 need an exponential each.
 // With one of the terms alone, or with tau = 1, one serves.
-// NT: past the caches, 1 the gradient's stores, 2 the loads of logits too.
+// NT: past the caches, 1 the gradient's stores, 2 the logits' loads too.
 template <typename T, int MODE, bool TWO, int NT>
 __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_kernel(const DistillArgs a) {
   using RV = RowVec<T>;
@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
     Raw v[U], next[U];
     Sums run = {-INFINITY, {0.f, 0.f}, {0.f, 0.f}, false};
     bool taught = false, labelled = false;
-    float tmax = -INFINITY, tsum = 0.f;
+    float tmax = -INFINITY, tsum = 0.f, e[kTop / 64];
+    int eid[kTop / 64];
     if (out) {
       __syncthreads();                          // the last row's shared values have been read
       if constexpr (MODE == DM_BWD) {
@@ -237,15 +238,22 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
         ztop[tid] = z0;
       }
       __syncthreads();
-      // every wave for itself
+      // every wave for itself: lane l holds entries l, l + 64, ...
       float bad = 0.f;
-      for (int k = lane; k < K; k += 64) {
-        tmax = fmaxf(tmax, ptop[k]);
-        if (!(ptop[k] < INFINITY)) bad = 1.f;   // infinite or NaN: no distribution
+#pragma unroll
+      for (int j = 0; j < kTop / 64; ++j) {
+        const int k = lane + 64 * j;
+        eid[j] = k < K ? ids[k] : -1;
+        e[j] = k < K ? ptop[k] : -INFINITY;
+        tmax = fmaxf(tmax, e[j]);
+        if (!(e[j] < INFINITY)) bad = 1.f;      // infinite or NaN: no distribution
       }
       tmax = wave_max(tmax);
-      if (tmax > -INFINITY)
-        for (int k = lane; k < K; k += 64) tsum += top_term(ptop[k], tmax, scale[0]);
+#pragma unroll
+      for (int j = 0; j < kTop / 64; ++j) {
+        e[j] = tmax > -INFINITY ? top_term(e[j], tmax, scale[0]) : 0.f;
+        tsum += e[j];
+      }
       tsum = wave_add(tsum);
       if (wave_add(bad) > 0.f) tsum = NAN;
       taught = !(tsum == 0.f);
@@ -288,9 +296,11 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
       float kl = 0.f;
       const float lp = logf(tsum), lq = logf(s_soft);
       if (taught)
-        for (int k = lane; k < K; k += 64) {
-          const float p = top_term(ptop[k], tmax, scale[0]) / tsum;
-          if (!(p == 0.f)) kl += p * (((ptop[k] - tmax) * a.inv_tau - lp) - (below(ztop[k], 0) - lq));
+#pragma unroll
+        for (int j = 0; j < kTop / 64; ++j) {
+          const int k = lane + 64 * j;
+          const float p = e[j] / tsum;
+          if (k < K && !(p == 0.f)) kl += p * (((ptop[k] - tmax) * a.inv_tau - lp) - (below(ztop[k], 0) - lq));
         }
       kl = wave_add(kl);
       if (lane == 0) {
@@ -307,6 +317,20 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
           const float d = term<decltype(near)::value>(run, x, scale[0], 0) * as;
           return TWO ? fmaf(term<decltype(near)::value>(run, x, scale[1], 1), ah, d) : d;
         };
+        // at the entries' ids and the label; an id that comes twice gets the same value
+        // from each of its entries
+        for (int k = tid; k <= K; k += threads) {
+          const int id = ids[k];
+          float p = 0.f;
+#pragma unroll
+          for (int j = 0; j < kTop / 64; ++j)
+            for (int i = 0; i < 64 && i + 64 * j < K; ++i)
+              p += __builtin_amdgcn_readlane(eid[j], i) == id ? lane_value(e[j], i) : 0.f;
+          float d = grad(ztop[k]);
+          if (taught) d -= cs * (p / tsum);
+          if (labelled && ids[K] == id) d -= ch;
+          dtop[k] = d;
+        }
         auto put = [&](int c, Raw x) __attribute__((always_inline)) {
           Raw o;
 #pragma unroll
@@ -323,18 +347,6 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
         }
         for (int c = tid; c < kept_end; c += threads) put(c, __builtin_bit_cast(Raw, kept[c]));
         if (tid < ntail) stv<T>(dz, nvec * W + tid, grad(ldv<T>(z, nvec * W + tid)));
-        // at the entries' ids and the label; an id that comes twice gets the same value
-        // from each of its entries
-        for (int k = tid; k <= K; k += threads) {
-          const int id = ids[k];
-          float p = 0.f;
-#pragma unroll 8
-          for (int i = 0; i < K; ++i) p += ids[i] == id ? top_term(ptop[i], tmax, scale[0]) : 0.f;
-          float d = grad(ztop[k]);
-          if (taught) d -= cs * (p / tsum);
-          if (labelled && ids[K] == id) d -= ch;
-          dtop[k] = d;
-        }
       };
       if (run.near) walk(std::true_type());
       else walk(std::false_type());
@@ -378,15 +390,15 @@ template <typename T, int MODE, bool TWO> static void launch_distill(const Disti
   while (threads < kRowThreads && threads * kVecs < a.V / RowVec<T>::W) threads *= 2;
   const dim3 grid = walk_grid(a.rows), block(threads);
   const size_t lds = MODE == DM_STEP ? (size_t)kKept * threads * kVecs * 16 : 0;
-  // Logits of 2^27 bytes and more (half the last cache) go past the caches where they are
-  // used once: the gradient's stores (step of 4096 rows of 128256 bf16: 513 -> 457 us; with the
-  // product that reads the gradient next 2048 rows of 32000 278 -> 274, but 1024 rows 186 -> 193), and,
-  // in whole lines, the loads of loss and gradient in calls of their own (both, 4096 rows of 32000:
-  // 177 -> 170 us; 256 rows 20 -> 23).
-  const bool past = (long long)a.rows * a.V * (long long)sizeof(T) >= 1LL << 27;
-  const bool lines = a.ld * (long long)sizeof(T) % 16 == 0;
-  if (past && MODE != DM_STEP && lines) hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, MODE == DM_STEP ? 1 : 2>), grid, block, lds, s, a);
-  else if (past && MODE != DM_FWD) hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, MODE == DM_FWD ? 0 : 1>), grid, block, lds, s, a);
+  // Logits of 112 MiB and more (of the last cache's 256), in rows of whole vectors, go past
+  // the caches where they are used once: the gradient's stores, and in calls of loss or gradient
+  // alone the loads too.  Measured in us, through the caches and past them: step of 4096 rows of
+  // 128256 bf16 513, 456; step and then the product that reads the gradient, 1000 rows of
+  // 32000: 187, 193, 1500: 242, 245, 1750 (112 MB): 245, 244, 2500: 320, 318; the same with 1500 rows
+  // of 50021, which the product reads piecemeal: 490, 510; loss and gradient, 4096 rows of 32000: 182, 169.
+  const bool past = (long long)a.rows * a.V * (long long)sizeof(T) >= 112LL << 20 &&
+                    (a.ld | (MODE == DM_FWD ? 0 : a.ld_out)) * (long long)sizeof(T) % 16 == 0;
+  if (past) hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, MODE == DM_STEP ? 1 : 2>), grid, block, lds, s, a);
   else hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, 0>), grid, block, lds, s, a);
 }
 
