@@ -7,16 +7,16 @@
 // id stand in a run whose sum is taken in one fixed order, with no atomics on
 // values.
 //   1. Chunks of kChunk tokens are sorted by counting: a token's place is the
-//      number of tokens of its chunk that sort before it.  16 tokens to a block,
-//      64 comparisons to an instruction, counted as the bits of its mask.
+//      number of tokens of its chunk that sort before it, 16 tokens to a block.
 //   2. Up to 16 sorted lists are merged at a time: a token's place is its place
-//      in its own list plus the number of smaller ones in each other list, a
-//      binary search per lane.
+//      in its own list plus the number of smaller ones in each other list.
 //   3. The sorted list is cut into pieces.  A wave sums the rows of one piece over
 //      512 columns, in fp32, and writes a run that lies inside its piece to the
-//      table; of a run that crosses a border it keeps the partial sum.  Other
-//      blocks of the same launch write the rows of ids without a token.
+//      table; of a run that crosses a border it keeps the partial sum.
 //   4. The partial sums of every crossing run are added in order.
+// The table is zeroed beside step 1, every row of it: that needs no word of the ids, and
+// runs as fast as memory takes it where a block writes 4 KB, a vector a thread (524 MB: 77 us; in
+// 64 KB a block 98, which a search for the rows without a token needs to pay).
 #include "sl_rows.hpp"
 
 namespace sl {
@@ -24,8 +24,8 @@ namespace sl {
 constexpr int kChunk = 2048;       // tokens sorted by counting
 constexpr int kRankTokens = 16;    // of them in one block
 constexpr int kLists = 16;         // sorted lists merged at a time
+constexpr int kJoinWaves = 8;      // waves that add a run's partial sums
 constexpr int kSlice = 512;        // columns of a wave: 8 a lane
-constexpr int kEmptyRows = 16;     // table rows of a block that looks for ids without a token
 constexpr uint32_t kNoKey = 0xFFFFFFFEu;
 
 // ids outside the vocabulary are no tokens: they sort behind every id
@@ -62,11 +62,20 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const T* __restrict__ E,
   }
 }
 
-// 1. sid, stok of every chunk in order of (id, token)
+// 1. sid, stok of every chunk in order of (id, token); the blocks behind those zero the
+// table's vectors
 __global__ void __launch_bounds__(256) embed_rank_kernel(const int* __restrict__ ids, uint32_t V, int ntok,
-                                                         uint32_t* __restrict__ sid, int* __restrict__ stok) {
+                                                         uint32_t* __restrict__ sid, int* __restrict__ stok,
+                                                         uint4* __restrict__ table, long long nvec) {
   constexpr int kGroups = kChunk / kRankTokens, N = kChunk / 256;
   __shared__ int part[4][kRankTokens];
+  const unsigned rank_blocks = (unsigned)(ntok + kRankTokens - 1) / kRankTokens;
+  if (blockIdx.x >= rank_blocks) {
+    const long long step = (long long)(gridDim.x - rank_blocks) * 256;
+    for (long long i = (long long)(blockIdx.x - rank_blocks) * 256 + threadIdx.x; i < nvec; i += step)
+      table[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
   const int base = (int)(blockIdx.x / kGroups) * kChunk, g0 = (int)(blockIdx.x % kGroups) * kRankTokens;
   const int n = ntok - base < kChunk ? ntok - base : kChunk;
   if (g0 >= n) return;
@@ -84,15 +93,25 @@ __global__ void __launch_bounds__(256) embed_rank_kernel(const int* __restrict__
     }
     key[i] = i > own ? k + 1 : k;
   }
+  uint32_t above[kRankTokens];
+  int count[kRankTokens];
 #pragma unroll
   for (int g = 0; g < kRankTokens; ++g) {
     const int p = g0 + g;
-    const uint32_t above = (p < n ? token_key(ids[base + p], V) : 0) + 1;
-    int c = 0;
+    above[g] = (p < n ? token_key(ids[base + p], V) : 0) + 1;
+    count[g] = kown + (own * 256 + tid >= p) < above[g];
+  }
 #pragma unroll
-    for (int i = 0; i < N; ++i) c += __popcll(__ballot(key[i] < above));
-    c += __popcll(__ballot(kown + (own * 256 + tid >= p) < above));
-    if ((tid & 63) == 0) part[tid >> 6][g] = c;
+  for (int g = 0; g < kRankTokens; ++g)
+#pragma unroll
+    for (int i = 0; i < N; ++i) count[g] += key[i] < above[g];
+#pragma unroll
+  for (int g = 0; g < kRankTokens; g += 2) {      // two counts of at most kChunk / 4 in a register
+    const int c = wave_count(count[g] | count[g + 1] << 16);
+    if ((tid & 63) == 0) {
+      part[tid >> 6][g] = c & 0xFFFF;
+      part[tid >> 6][g + 1] = c >> 16;
+    }
   }
   __syncthreads();
   if (tid < kRankTokens && g0 + tid < n) {
@@ -102,35 +121,45 @@ __global__ void __launch_bounds__(256) embed_rank_kernel(const int* __restrict__
   }
 }
 
-// 2. lists of `len` sorted tokens -> lists of kLists * len
+// 2. lists of `len` sorted tokens -> lists of kLists * len.  A block takes 64 neighbours of
+// a list, one a lane, and each of its waves searches a quarter of the other lists, four at
+// once: the lanes' searches run side by side through the same few lines.
 __global__ void __launch_bounds__(256) embed_merge_kernel(const uint32_t* __restrict__ sid, const int* __restrict__ stok,
                                                           int ntok, int len, uint32_t* __restrict__ osid,
                                                           int* __restrict__ ostok) {
-  const int l = threadIdx.x & (kLists - 1);
-  const long long i = (long long)blockIdx.x * (256 / kLists) + threadIdx.x / kLists;
-  const bool on = i < ntok;
-  const int list = on ? (int)(i / len) : 0, mine = list % kLists;
-  const long long first = (long long)(list - mine) * len, start = first + (long long)l * len;
-  const uint32_t id = on ? sid[i] : 0;
-  long long count = 0;
-  if (on && l == mine) {
-    count = i - start;
-  } else if (on && start < ntok) {
-    const uint32_t above = id + (l < mine);   // tokens of an earlier list go first
-    int lo = 0, hi = (int)(ntok - start < len ? ntok - start : len);
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (sid[start + mid] < above) lo = mid + 1;
-      else hi = mid;
-    }
-    count = lo;
-  }
-  int c = (int)count;
+  constexpr int N = kLists / 4;
+  __shared__ int counts[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i0 = blockIdx.x * 64, i = i0 + lane, list = i0 / len, mine = list % kLists;
+  const long long first = (long long)(list - mine) * len;
+  const uint32_t id = i < ntok ? sid[i] : 0;
+  long long start[N];
+  int lo[N], hi[N];
 #pragma unroll
-  for (int o = kLists / 2; o; o >>= 1) c += __shfl_xor(c, o);
-  if (on && l == 0) {
-    osid[first + c] = id;
-    ostok[first + c] = stok[i];
+  for (int k = 0; k < N; ++k) {
+    const int l = wave * N + k;
+    start[k] = first + (long long)l * len;
+    lo[k] = 0;
+    hi[k] = l == mine || start[k] >= ntok ? 0 : (int)(ntok - start[k] < len ? ntok - start[k] : len);
+  }
+  for (int rest = len; rest; rest >>= 1) {
+    uint32_t at[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) at[k] = lo[k] < hi[k] ? sid[start[k] + ((lo[k] + hi[k]) >> 1)] : 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (lo[k] < hi[k]) {
+        const int mid = (lo[k] + hi[k]) >> 1;
+        if (at[k] < id + (wave * N + k < mine)) lo[k] = mid + 1;   // tokens of an earlier list go first
+        else hi[k] = mid;
+      }
+  }
+  counts[wave][lane] = (lo[0] + lo[1]) + (lo[2] + lo[3]);
+  __syncthreads();
+  if (wave == 0 && i < ntok) {
+    const long long at = first + (i - list * (long long)len) + ((counts[0][lane] + counts[1][lane]) + (counts[2][lane] + counts[3][lane]));
+    osid[at] = id;
+    ostok[at] = stok[i];
   }
 }
 
@@ -142,76 +171,48 @@ struct EmbedGradArgs {
   float* part;           // [pieces][2][D]: the sums of a piece's first and last run that cross its borders
   uint32_t V;
   int ntok, D, piece, pieces, slices;
-  int sum_blocks;        // blocks that sum pieces; the others write empty rows
   float scale;
 };
 
-// 8 columns of a table row
-template <typename GT> __device__ inline void store_grad(void* dE, long long at, const float* acc, float scale) {
+// 8 columns of a table row, or of a partial sum
+template <typename GT> __device__ inline void store_grad(GT* p, const float* acc, float scale) {
   constexpr int W = 16 / sizeof(GT);
 #pragma unroll
   for (int e = 0; e < 8 / W; ++e) {
-    Vec<GT, W> o;
+    Pack<GT> o;
 #pragma unroll
-    for (int j = 0; j < W; ++j) o.v[j] = f2el<GT>(acc[e * W + j] * scale);
-    *reinterpret_cast<Vec<GT, W>*>(reinterpret_cast<GT*>(dE) + at + e * W) = o;
+    for (int j = 0; j < W; j += 2) o.put(j, acc[e * W + j] * scale, acc[e * W + j + 1] * scale);
+    *reinterpret_cast<Pack<GT>*>(p + e * W) = o;
   }
 }
 
 // 3.
 template <typename T, typename GT>
 __global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedGradArgs a) {
-  __shared__ int lower[kEmptyRows + 1];
-  const int tid = threadIdx.x, lane = tid & 63;
-  if ((int)blockIdx.x >= a.sum_blocks) {
-    constexpr int W = 16 / sizeof(GT);
-    const int nvec = a.D / W;
-    Vec<GT, W> zero;
-#pragma unroll
-    for (int j = 0; j < W; ++j) zero.v[j] = f2el<GT>(0.f);
-    const long long step = (long long)(gridDim.x - a.sum_blocks) * kEmptyRows;
-    for (long long r0 = (long long)(blockIdx.x - a.sum_blocks) * kEmptyRows; r0 < a.V; r0 += step) {
-      __syncthreads();
-      if (tid <= kEmptyRows) {   // tokens with a smaller id
-        int lo = 0, hi = a.ntok;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if ((long long)a.sid[mid] < r0 + tid) lo = mid + 1;
-          else hi = mid;
-        }
-        lower[tid] = lo;
-      }
-      __syncthreads();
-      for (int r = 0; r < kEmptyRows && r0 + r < a.V; ++r)
-        if (lower[r] == lower[r + 1])
-          for (int c = tid; c < nvec; c += 256) reinterpret_cast<Vec<GT, W>*>(a.dE)[(r0 + r) * nvec + c] = zero;
-    }
-    return;
-  }
-  constexpr int U = 8, W = 16 / sizeof(T), NV = 8 / W;   // rows in flight, vectors of a lane's 8 columns
-  using VT = Vec<T, W>;
+  const int lane = threadIdx.x & 63;
+  constexpr int W = Pack<T>::W, NV = 8 / W, U = 8 / NV;   // vectors of a lane's 8 columns, rows in flight
   const long long units = (long long)a.pieces * a.slices;
-  for (long long unit = (long long)blockIdx.x * 4 + (tid >> 6); unit < units; unit += (long long)a.sum_blocks * 4) {
+  for (long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); unit < units; unit += (long long)gridDim.x * 4) {
     const int piece = (int)(unit / a.slices), col = (int)(unit % a.slices) * kSlice + lane * 8;
     const bool on = col < a.D;
     const int p0 = piece * a.piece, n = a.ntok - p0 < a.piece ? a.ntok - p0 : a.piece;
     const uint32_t kid = lane < n ? a.sid[p0 + lane] : a.V;
     const int tok = lane < n ? a.stok[p0 + lane] : 0;
     const uint32_t before = p0 > 0 ? a.sid[p0 - 1] : a.V + 1, behind = p0 + n < a.ntok ? a.sid[p0 + n] : a.V + 1;
+    const T* const dY = reinterpret_cast<const T*>(a.dY) + col;
     float acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     bool crosses = (uint32_t)__builtin_amdgcn_readfirstlane(kid) == before;   // the run began in an earlier piece
     for (int i0 = 0; i0 < n; i0 += U) {
-      VT v[U][NV];
+      Pack<T> v[U][NV];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u < n ? i0 + u : n - 1;
         const long long row = __builtin_amdgcn_readlane(tok, i);
         if (on && (uint32_t)__builtin_amdgcn_readlane(kid, i) < a.V) {
 #pragma unroll
-          for (int e = 0; e < NV; ++e)
-            v[u][e] = *reinterpret_cast<const VT*>(reinterpret_cast<const T*>(a.dY) + row * a.D + col + e * W);
+          for (int e = 0; e < NV; ++e) v[u][e] = *reinterpret_cast<const Pack<T>*>(dY + row * a.D + e * W);
         }
       }
 #pragma unroll
@@ -221,15 +222,15 @@ __global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedGradArgs a) 
         const uint32_t id = __builtin_amdgcn_readlane(kid, i);
         if (id >= a.V) break;   // no tokens behind
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += el2f<T>(v[u][j / W].v[j % W]);
+        for (int j = 0; j < 8; ++j) acc[j] += v[u][j / W].get(j % W);
         const bool last = i + 1 == n;
         const uint32_t next = last ? behind : (uint32_t)__builtin_amdgcn_readlane(kid, i + 1);
         if (next != id || last) {
           if (on) {
             if (next != id && !crosses)
-              store_grad<GT>(a.dE, (long long)id * a.D + col, acc, a.scale);
+              store_grad<GT>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
             else
-              store_grad<float>(a.part, ((long long)piece * 2 + !crosses) * a.D + col, acc, 1.f);
+              store_grad<float>(a.part + ((long long)piece * 2 + !crosses) * a.D + col, acc, 1.f);
           }
           crosses = false;
 #pragma unroll
@@ -242,8 +243,8 @@ __global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedGradArgs a) 
 
 // 4. the runs that begin in a piece and go on behind it
 template <typename GT>
-__global__ void __launch_bounds__(256) embed_join_kernel(const EmbedGradArgs a) {
-  __shared__ float sum[3][64][8];
+__global__ void __launch_bounds__(64 * kJoinWaves) embed_join_kernel(const EmbedGradArgs a) {
+  __shared__ float sum[kJoinWaves - 1][64][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const long long units = (long long)(a.pieces - 1) * a.slices;
   for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedGradArgs a) 
     if (on) {
       if (wave == 0) add(2LL * piece + 1);
 #pragma unroll 4
-      for (int p = piece + 1 + wave; p <= end; p += 4) add(2LL * p);
+      for (int p = piece + 1 + wave; p <= end; p += kJoinWaves) add(2LL * p);
     }
     __syncthreads();                         // the last unit's sums have been read
     if (wave > 0)
@@ -287,16 +288,23 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedGradArgs a) 
     __syncthreads();
     if (wave == 0 && on) {
 #pragma unroll
-      for (int w = 0; w < 3; ++w)
+      for (int w = 0; w < kJoinWaves - 1; ++w)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += sum[w][lane][j];
-      store_grad<GT>(a.dE, (long long)id * a.D + col, acc, a.scale);
+      store_grad<GT>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
     }
   }
 }
 
-// Tokens of a piece.
-inline int embed_piece(int T) { return T >= 8192 ? 64 : 32; }
+// Tokens of a piece: 8 to 64, as many as leave 4096 waves (2048 tokens of 4096 columns,
+// gradient of 32000 rows in us: 8 tokens 101, 16 105, 32 116, 64 138; 32768 tokens, 128256 rows in bf16:
+// 8 tokens 337, 16 307, 32 299, 64 292).
+inline int embed_piece(long long T, long long D) {
+  const long long waves = T * ceil_div(D, kSlice);
+  int piece = 8;
+  while (piece < 64 && waves >= 4096LL * 2 * piece) piece *= 2;
+  return piece;
+}
 
 struct EmbedWs {
   size_t sid[2], stok[2], part, bytes;
@@ -306,7 +314,7 @@ struct EmbedWs {
       sid[i] = b.take((size_t)T * 4);
       stok[i] = b.take((size_t)T * 4);
     }
-    part = b.take((size_t)ceil_div(T, embed_piece(T)) * 2 * D * 4);
+    part = b.take((size_t)ceil_div(T, embed_piece(T, D)) * 2 * D * 4);
     bytes = b.off;
   }
 };
@@ -346,10 +354,9 @@ static void launch_fwd(const void* E, const int32_t* ids, int64_t V, int64_t D, 
 
 template <typename T, typename GT>
 static void launch_grad(const EmbedGradArgs& a, hipStream_t s) {
-  const unsigned empty = walk_grid(ceil_div(a.V, kEmptyRows), 1 << 18).x;
-  hipLaunchKernelGGL((embed_grad_kernel<T, GT>), dim3(a.sum_blocks + empty), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((embed_grad_kernel<T, GT>), walk_grid(((long long)a.pieces * a.slices + 3) / 4), dim3(256), 0, s, a);
   if (a.pieces > 1)
-    hipLaunchKernelGGL(embed_join_kernel<GT>, walk_grid((long long)(a.pieces - 1) * a.slices), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(embed_join_kernel<GT>, walk_grid((long long)(a.pieces - 1) * a.slices), dim3(64 * kJoinWaves), 0, s, a);
 }
 
 }  // namespace sl
@@ -397,20 +404,20 @@ extern "C" sl_status sl_embed_bwd(sl_dtype dt, const sl_layout* lay, int64_t voc
   auto sid = [&](int i) { return reinterpret_cast<uint32_t*>(w + at.sid[i]); };
   auto stok = [&](int i) { return reinterpret_cast<int*>(w + at.stok[i]); };
   const uint32_t V = (uint32_t)vocab;
-  hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)ceil_div(T, kRankTokens)), dim3(256), 0, s, ids, V, T, sid(0),
-                     stok(0));
+  const long long nvec = vocab * d_model / (grad_dt == SL_BF16 ? 8 : 4);
+  hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)ceil_div(T, kRankTokens) + walk_grid((nvec + 255) / 256, 1 << 22).x),
+                     dim3(256), 0, s, ids, V, T, sid(0), stok(0), reinterpret_cast<uint4*>(dE), nvec);
   int cur = 0;
   for (long long len = kChunk; len < T; len *= kLists, cur ^= 1)
-    hipLaunchKernelGGL(embed_merge_kernel, dim3((unsigned)ceil_div(T, 256 / kLists)), dim3(256), 0, s, sid(cur), stok(cur),
+    hipLaunchKernelGGL(embed_merge_kernel, dim3((unsigned)ceil_div(T, 64)), dim3(256), 0, s, sid(cur), stok(cur),
                        T, (int)len, sid(cur ^ 1), stok(cur ^ 1));
   EmbedGradArgs a{};
   a.dY = dY; a.dE = dE; a.sid = sid(cur); a.stok = stok(cur);
   a.part = reinterpret_cast<float*>(w + at.part);
   a.V = V; a.ntok = T; a.D = (int)d_model; a.scale = scale;
-  a.piece = embed_piece(T);
+  a.piece = embed_piece(T, d_model);
   a.pieces = ceil_div(T, a.piece);
   a.slices = ceil_div(d_model, kSlice);
-  a.sum_blocks = (int)walk_grid(((long long)a.pieces * a.slices + 3) / 4, 1 << 20).x;
   if (dt == SL_BF16 && grad_dt == SL_BF16) launch_grad<bf16, bf16>(a, s);
   else if (dt == SL_BF16) launch_grad<bf16, float>(a, s);
   else if (grad_dt == SL_BF16) launch_grad<float, bf16>(a, s);

@@ -52,6 +52,16 @@ __device__ inline float lane_value(float x, int l) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
 }
 
+// Sum over the wave's 64 lanes of whole numbers.
+__device__ inline int wave_count(int x) {
+  x += __builtin_amdgcn_mov_dpp(x, kXor1, 0xf, 0xf, true);
+  x += __builtin_amdgcn_mov_dpp(x, kXor2, 0xf, 0xf, true);
+  x += __builtin_amdgcn_mov_dpp(x, kMirror8, 0xf, 0xf, true);
+  x += __builtin_amdgcn_mov_dpp(x, kMirror16, 0xf, 0xf, true);
+  return __builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16) + __builtin_amdgcn_readlane(x, 32) +
+         __builtin_amdgcn_readlane(x, 48);
+}
+
 // Sum and maximum over the wave's 64 lanes: over each 16 by DPP moves, then the
 // four 16s.  Every lane adds the same pairs, so all hold the same bits.
 __device__ inline float wave_add(float x) {
