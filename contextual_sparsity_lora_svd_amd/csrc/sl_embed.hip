@@ -10,9 +10,10 @@
 //      number of tokens of its chunk that sort before it, 16 tokens to a block.
 //   2. Up to 16 sorted lists are merged at a time: a token's place is its place
 //      in its own list plus the number of smaller ones in each other list.
-//   3. The sorted list is cut into pieces.  A wave sums the rows of one piece over
-//      512 columns, in fp32, and writes a run that lies inside its piece to the
-//      table; of a run that crosses a border it keeps the partial sum.
+//   3. The sorted list is cut into pieces of 64.  A block sums the rows of one piece over
+//      1 KB of columns, in fp32, eight rows to a wave, which loads them together; the
+//      waves' sums of one run are added through LDS.  A run that lies inside its
+//      piece goes to the table; of one that crosses a border the partial sum is kept.
 //   4. The partial sums of every crossing run are added in order.
 // The table is zeroed beside step 1, every row of it: that needs no word of the ids, and
 // runs as fast as memory takes it where a block writes 4 KB, a vector a thread (524 MB: 77 us; in
@@ -25,7 +26,8 @@ constexpr int kChunk = 2048;       // tokens sorted by counting
 constexpr int kRankTokens = 16;    // of them in one block
 constexpr int kLists = 16;         // sorted lists merged at a time
 constexpr int kJoinWaves = 8;      // waves that add a run's partial sums
-constexpr int kSlice = 512;        // columns of a wave: 8 a lane
+constexpr int kPieceWaves = 8, kWaveRows = 8, kPiece = kPieceWaves * kWaveRows;   // sorted tokens of a block
+constexpr int kJoinSlice = 512;    // and columns of them, 8 a lane
 constexpr uint32_t kNoKey = 0xFFFFFFFEu;
 
 // ids outside the vocabulary are no tokens: they sort behind every id
@@ -170,74 +172,106 @@ struct EmbedGradArgs {
   const int* stok;       // their rows
   float* part;           // [pieces][2][D]: the sums of a piece's first and last run that cross its borders
   uint32_t V;
-  int ntok, D, piece, pieces, slices;
+  int ntok, D, pieces, slices;
   float scale;
 };
 
-// 8 columns of a table row, or of a partial sum
-template <typename GT> __device__ inline void store_grad(GT* p, const float* acc, float scale) {
-  constexpr int W = 16 / sizeof(GT);
+// N columns of a table row, or of a partial sum
+template <int N, typename GT> __device__ inline void store_grad(GT* p, const float* acc, float scale) {
+  constexpr int W = N * sizeof(GT) < 16 ? N : 16 / sizeof(GT);
+  struct alignas(W * sizeof(GT)) Part { GT v[W]; };
 #pragma unroll
-  for (int e = 0; e < 8 / W; ++e) {
-    Pack<GT> o;
+  for (int e = 0; e < N / W; ++e) {
+    Part o;
 #pragma unroll
-    for (int j = 0; j < W; j += 2) o.put(j, acc[e * W + j] * scale, acc[e * W + j + 1] * scale);
-    *reinterpret_cast<Pack<GT>*>(p + e * W) = o;
+    for (int j = 0; j < W; ++j) o.v[j] = f2el<GT>(acc[e * W + j] * scale);
+    *reinterpret_cast<Part*>(p + e * W) = o;
   }
 }
 
-// 3.
-template <typename T, typename GT>
-__global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedGradArgs a) {
-  const int lane = threadIdx.x & 63;
-  constexpr int W = Pack<T>::W, NV = 8 / W, U = 8 / NV;   // vectors of a lane's 8 columns, rows in flight
+// 3.  PAST: rows of dY past the caches.
+template <typename T, typename GT, bool PAST>
+__global__ void __launch_bounds__(64 * kPieceWaves) embed_grad_kernel(const EmbedGradArgs a) {
+  constexpr int W = Pack<T>::W, R = kWaveRows;     // columns of a lane, rows of a wave
+  __shared__ float left[kPieceWaves][64][W], right[kPieceWaves][64][W];   // sums of a wave's run that crosses its ends
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const long long units = (long long)a.pieces * a.slices;
-  for (long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); unit < units; unit += (long long)gridDim.x * 4) {
-    const int piece = (int)(unit / a.slices), col = (int)(unit % a.slices) * kSlice + lane * 8;
+  for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int piece = (int)(unit / a.slices), col = ((int)(unit % a.slices) * 64 + lane) * W;
     const bool on = col < a.D;
-    const int p0 = piece * a.piece, n = a.ntok - p0 < a.piece ? a.ntok - p0 : a.piece;
+    const int p0 = piece * kPiece, n = a.ntok - p0 < kPiece ? a.ntok - p0 : kPiece;
     const uint32_t kid = lane < n ? a.sid[p0 + lane] : a.V;
-    const int tok = lane < n ? a.stok[p0 + lane] : 0;
+    // (a row of dY whatever a workspace holds that another stream has written over)
+    const int tok = lane < n ? (int)min((uint32_t)a.stok[p0 + lane], (uint32_t)(a.ntok - 1)) : 0;
     const uint32_t before = p0 > 0 ? a.sid[p0 - 1] : a.V + 1, behind = p0 + n < a.ntok ? a.sid[p0 + n] : a.V + 1;
-    const T* const dY = reinterpret_cast<const T*>(a.dY) + col;
-    float acc[8];
+    auto id_at = [&](int i) -> uint32_t {          // of the piece's places and the two beside it
+      return i < 0 ? before : i < n ? (uint32_t)__builtin_amdgcn_readlane(kid, i) : behind;
+    };
+    const int i0 = wave * R, i1 = i0 + R < n ? i0 + R : n;
+    Pack<T> v[R];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-    bool crosses = (uint32_t)__builtin_amdgcn_readfirstlane(kid) == before;   // the run began in an earlier piece
-    for (int i0 = 0; i0 < n; i0 += U) {
-      Pack<T> v[U][NV];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u < n ? i0 + u : n - 1;
-        const long long row = __builtin_amdgcn_readlane(tok, i);
-        if (on && (uint32_t)__builtin_amdgcn_readlane(kid, i) < a.V) {
-#pragma unroll
-          for (int e = 0; e < NV; ++e) v[u][e] = *reinterpret_cast<const Pack<T>*>(dY + row * a.D + e * W);
+    for (int u = 0; u < R; ++u)
+      if (i0 + u < i1) {
+        const long long row = __builtin_amdgcn_readlane(tok, i0 + u);
+        const Pack<T>* const p = reinterpret_cast<const Pack<T>*>(reinterpret_cast<const T*>(a.dY) + row * a.D + col);
+        if (on && id_at(i0 + u) < a.V) {
+          if constexpr (PAST) v[u].r = __builtin_nontemporal_load(&p->r);
+          else v[u] = *p;
         }
       }
+    float acc[W];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u;
-        if (i >= n) break;
-        const uint32_t id = __builtin_amdgcn_readlane(kid, i);
-        if (id >= a.V) break;   // no tokens behind
+    for (int j = 0; j < W; ++j) acc[j] = 0.f;
+    bool crosses = i0 < i1 && id_at(i0 - 1) == id_at(i0);   // the run began before this wave's rows
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += v[u][j / W].get(j % W);
-        const bool last = i + 1 == n;
-        const uint32_t next = last ? behind : (uint32_t)__builtin_amdgcn_readlane(kid, i + 1);
-        if (next != id || last) {
-          if (on) {
-            if (next != id && !crosses)
-              store_grad<GT>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
-            else
-              store_grad<float>(a.part + ((long long)piece * 2 + !crosses) * a.D + col, acc, 1.f);
-          }
-          crosses = false;
+    for (int u = 0; u < R; ++u) {
+      const int i = i0 + u;
+      if (i >= i1) break;
+      const uint32_t id = id_at(i);
+      if (id >= a.V) break;                        // no tokens behind
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+      for (int j = 0; j < W; ++j) acc[j] += v[u].get(j);
+      const bool ends = id_at(i + 1) != id;
+      if (ends || i + 1 == i1) {
+        if (ends && !crosses) {
+          if (on) store_grad<W>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
+        } else {
+          float* const to = crosses ? left[wave][lane] : right[wave][lane];
+#pragma unroll
+          for (int j = 0; j < W; ++j) to[j] = acc[j];
         }
+        crosses = false;
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j] = 0.f;
       }
     }
+    __syncthreads();
+    // The wave in whose rows a run begins adds it up, the first wave also the one that
+    // began in an earlier piece.
+    auto finish = [&](uint32_t id, bool inside, int w) __attribute__((always_inline)) {
+      const int end = 63 - __builtin_clzll(__ballot(kid == id));
+      for (; w * R <= end; ++w)
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j] += left[w][lane][j];
+      if (!on) return;
+      if (inside && id_at(end + 1) != id) store_grad<W>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
+      else store_grad<W>(a.part + ((long long)piece * 2 + inside) * a.D + col, acc, 1.f);
+    };
+    if (wave == 0 && id_at(0) == before && before < a.V) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[j] = 0.f;
+      finish(before, false, 0);
+    }
+    if (i0 < i1) {
+      const uint32_t id = id_at(i1 - 1);
+      // its last run goes on behind its rows and did not begin before them
+      if (id < a.V && id_at(i1) == id && !(id_at(i0) == id && id_at(i0 - 1) == id)) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j] = right[wave][lane][j];
+        finish(id, true, wave + 1);
+      }
+    }
+    __syncthreads();                               // the sums have been read
   }
 }
 
@@ -246,15 +280,16 @@ template <typename GT>
 __global__ void __launch_bounds__(64 * kJoinWaves) embed_join_kernel(const EmbedGradArgs a) {
   __shared__ float sum[kJoinWaves - 1][64][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const long long units = (long long)(a.pieces - 1) * a.slices;
+  const int slices = (a.D + kJoinSlice - 1) / kJoinSlice;
+  const long long units = (long long)(a.pieces - 1) * slices;
   for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int piece = (int)(unit / a.slices), col = (int)(unit % a.slices) * kSlice + lane * 8;
-    const int p0 = piece * a.piece, p1 = p0 + a.piece;
+    const int piece = (int)(unit / slices), col = (int)(unit % slices) * kJoinSlice + lane * 8;
+    const int p0 = piece * kPiece, p1 = p0 + kPiece;
     const uint32_t id = a.sid[p1 - 1];
     if (id >= a.V || a.sid[p1] != id || (p0 > 0 && a.sid[p0] == id && a.sid[p0 - 1] == id)) continue;
     int end = piece + 1;                     // the piece in which the run ends
     for (;;) {
-      const long long q = (long long)(end + lane + 1) * a.piece;   // the lane's piece goes on behind its end?
+      const long long q = (long long)(end + lane + 1) * kPiece;   // the lane's piece goes on behind its end?
       const unsigned long long over = __ballot(q < a.ntok && a.sid[q < a.ntok ? q : 0] == id);
       if (~over) {
         end += __builtin_ctzll(~over);
@@ -291,19 +326,9 @@ __global__ void __launch_bounds__(64 * kJoinWaves) embed_join_kernel(const Embed
       for (int w = 0; w < kJoinWaves - 1; ++w)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += sum[w][lane][j];
-      store_grad<GT>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
+      store_grad<8>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
     }
   }
-}
-
-// Tokens of a piece: 8 to 64, as many as leave 4096 waves (2048 tokens of 4096 columns,
-// gradient of 32000 rows in us: 8 tokens 101, 16 105, 32 116, 64 138; 32768 tokens, 128256 rows in bf16:
-// 8 tokens 337, 16 307, 32 299, 64 292).
-inline int embed_piece(long long T, long long D) {
-  const long long waves = T * ceil_div(D, kSlice);
-  int piece = 8;
-  while (piece < 64 && waves >= 4096LL * 2 * piece) piece *= 2;
-  return piece;
 }
 
 struct EmbedWs {
@@ -314,7 +339,7 @@ struct EmbedWs {
       sid[i] = b.take((size_t)T * 4);
       stok[i] = b.take((size_t)T * 4);
     }
-    part = b.take((size_t)ceil_div(T, embed_piece(T, D)) * 2 * D * 4);
+    part = b.take((size_t)ceil_div(T, kPiece) * 2 * D * 4);
     bytes = b.off;
   }
 };
@@ -354,9 +379,16 @@ static void launch_fwd(const void* E, const int32_t* ids, int64_t V, int64_t D, 
 
 template <typename T, typename GT>
 static void launch_grad(const EmbedGradArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((embed_grad_kernel<T, GT>), walk_grid(((long long)a.pieces * a.slices + 3) / 4), dim3(256), 0, s, a);
+  // Rows of 64 MiB and more go past the caches, each read once (32768 tokens of 4096 columns, with
+  // the fill of 128256 rows in bf16: 282 us through them, 266 past; 2048 tokens, 32000 rows: 99, 101).
+  const dim3 grid = walk_grid((long long)a.pieces * a.slices), block(64 * kPieceWaves);
+  if ((long long)a.ntok * a.D * (long long)sizeof(T) >= 64LL << 20)
+    hipLaunchKernelGGL((embed_grad_kernel<T, GT, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((embed_grad_kernel<T, GT, false>), grid, block, 0, s, a);
   if (a.pieces > 1)
-    hipLaunchKernelGGL(embed_join_kernel<GT>, walk_grid((long long)(a.pieces - 1) * a.slices), dim3(64 * kJoinWaves), 0, s, a);
+    hipLaunchKernelGGL(embed_join_kernel<GT>, walk_grid((long long)(a.pieces - 1) * ceil_div(a.D, kJoinSlice)),
+                       dim3(64 * kJoinWaves), 0, s, a);
 }
 
 }  // namespace sl
@@ -415,9 +447,8 @@ extern "C" sl_status sl_embed_bwd(sl_dtype dt, const sl_layout* lay, int64_t voc
   a.dY = dY; a.dE = dE; a.sid = sid(cur); a.stok = stok(cur);
   a.part = reinterpret_cast<float*>(w + at.part);
   a.V = V; a.ntok = T; a.D = (int)d_model; a.scale = scale;
-  a.piece = embed_piece(T, d_model);
-  a.pieces = ceil_div(T, a.piece);
-  a.slices = ceil_div(d_model, kSlice);
+  a.pieces = ceil_div(T, kPiece);
+  a.slices = ceil_div(d_model, dt == SL_BF16 ? 512 : 256);
   if (dt == SL_BF16 && grad_dt == SL_BF16) launch_grad<bf16, bf16>(a, s);
   else if (dt == SL_BF16) launch_grad<bf16, float>(a, s);
   else if (grad_dt == SL_BF16) launch_grad<float, bf16>(a, s);
