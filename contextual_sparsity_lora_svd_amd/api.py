@@ -232,6 +232,11 @@ def _stream() -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _stream_on(dev: int) -> int:
+    """_stream of a caller that has the current device at hand."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 class Layout:
     """Host-side sequence layout (batch, seq_len, ctx_len[b])."""
 
@@ -875,14 +880,16 @@ def embed_fwd(E: torch.Tensor, ids: torch.Tensor, layout: Layout, scale: float =
               out: Optional[torch.Tensor] = None):
     """Y [T, d_model]: scale * E[ids] (ids [T] int32; one outside E's rows is no
     token, its row of Y is 0)."""
+    if E.dim() != 2:
+        raise SparseLoraError(f"E: expected [vocab, d_model], got {tuple(E.shape)}")
     dt, T, dev = _dtype_code(E), layout.batch * layout.seq_len, _current(E)
     V, D = E.shape
     Ep, ip = _check_rows("E", E, (V, D), E.dtype, dev), _check_rows("ids", ids, (T,), torch.int32, dev)
-    Y = out if out is not None else torch.empty((T, D), dtype=E.dtype, device=E.device)
+    Y = out if out is not None else E.new_empty((T, D))
     Yp = _check_rows("Y", Y, (T, D), E.dtype, dev)
     if out is not None:
         _refuse_overlap((("Y", Y),), (("E", E), ("ids", ids)))
-    _check(lib().sl_embed_fwd(dt, layout.ref, V, D, scale, Ep, ip, Yp, _stream()), "sl_embed_fwd")
+    _check(lib().sl_embed_fwd(dt, layout.ref, V, D, scale, Ep, ip, Yp, _stream_on(dev)), "sl_embed_fwd")
     return Y
 
 
@@ -907,7 +914,7 @@ def embed_bwd(ids: torch.Tensor, dY: torch.Tensor, layout: Layout, vocab: int, s
     if out is not None:
         _refuse_overlap((("dE", dE),), (("ids", ids), ("dY", dY), ("ws", buf.ws)))
     _check(lib().sl_embed_bwd(dt, layout.ref, vocab, D, scale, ip, gp, _dtype_code(dE), dEp,
-                              _check_scratch("ws", buf.ws, dY), buf.ws.numel(), _stream()), "sl_embed_bwd")
+                              _check_scratch("ws", buf.ws, dY), buf.ws.numel(), _stream_on(dev)), "sl_embed_bwd")
     return dE
 
 
@@ -940,14 +947,14 @@ def layer_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor], 
     if residual is not None:
         h = h if h is not None else torch.empty_like(x)
         hp = _check_rows("h", h, (T, D), x.dtype, dev)
-    stats = torch.empty((T, 3), dtype=torch.float32, device=x.device) if want_stats else None
+    stats = w.new_empty((T, 3)) if want_stats else None
     if out is not None:
         _refuse_overlap((("y", y), ("h", None if residual is None else h)),
                         (("x", x), ("residual", residual), ("w", w), ("b", b)),
                         (("y", "x"), ("y", "residual"), ("h", "x"), ("h", "residual")))
     c = SlLayerNorm(D, int(centered), eps, wp, bp)
     _check(lib().sl_layer_norm_fwd(dt, layout.ref, ctypes.byref(c), xp, rp, hp, yp,
-                                   None if stats is None else stats.data_ptr(), _stream()), "sl_layer_norm_fwd")
+                                   None if stats is None else stats.data_ptr(), _stream_on(dev)), "sl_layer_norm_fwd")
     return y, x if residual is None else h, stats
 
 
@@ -981,7 +988,7 @@ def layer_norm_bwd(h: torch.Tensor, w: torch.Tensor, stats: torch.Tensor, layout
                         (("dx", "dy"), ("dx", "dh"), ("dx", "h")))
     c = SlLayerNorm(D, int(centered), 0.0, wp, None)
     _check(lib().sl_layer_norm_bwd(dt, layout.ref, ctypes.byref(c), hp, sp, gp, rp, dxp, dwp, dbp,
-                                   _check_scratch("ws", buf.ws, h), buf.ws.numel(), _stream()), "sl_layer_norm_bwd")
+                                   _check_scratch("ws", buf.ws, h), buf.ws.numel(), _stream_on(dev)), "sl_layer_norm_bwd")
     return out
 
 
@@ -1064,7 +1071,7 @@ def distill_fwd(p: DistillTargets, logits: torch.Tensor, layout: Layout):
     c = p._c(T, V, dev)
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
     stats = torch.empty((T, 4), dtype=torch.float32, device=logits.device)
-    _check(lib().sl_distill_fwd(dt, layout.ref, ctypes.byref(c), zp, ld, loss.data_ptr(), stats.data_ptr(), _stream()),
+    _check(lib().sl_distill_fwd(dt, layout.ref, ctypes.byref(c), zp, ld, loss.data_ptr(), stats.data_ptr(), _stream_on(dev)),
            "sl_distill_fwd")
     return loss, stats
 
@@ -1080,15 +1087,14 @@ def distill_bwd(p: DistillTargets, logits: torch.Tensor, stats: torch.Tensor, la
     sp = _check_rows("stats", stats, (T, 4), torch.float32, dev)
     gp = None if dloss is None else _check_rows("dloss", dloss, (T,), torch.float32, dev)
     dz, dzp, ldo = _distill_out(p, logits, out, T, V, (("stats", stats), ("dloss", dloss)))
-    _check(lib().sl_distill_bwd(dt, layout.ref, ctypes.byref(c), zp, ld, sp, gp, dzp, ldo, _stream()), "sl_distill_bwd")
+    _check(lib().sl_distill_bwd(dt, layout.ref, ctypes.byref(c), zp, ld, sp, gp, dzp, ldo, _stream_on(dev)), "sl_distill_bwd")
     return dz
 
 
 def distill_step(p: DistillTargets, logits: torch.Tensor, layout: Layout, dloss: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None):
-    """(loss [T], dlogits [T, vocab]) in one call that reads logits from memory once,
-    for a loss whose rows' weights ``dloss`` are known beforehand (None: ones).
-    ``out`` may be logits itself."""
+    """(loss [T], dlogits [T, vocab]) in one call, for a loss whose rows' weights
+    ``dloss`` are known beforehand (None: ones).  ``out`` may be logits itself."""
     dt, T, dev = _dtype_code(logits), layout.batch * layout.seq_len, _current(logits)
     V = logits.shape[-1]
     zp, ld = _logit_rows("logits", logits, T, V, logits.dtype)
@@ -1096,6 +1102,6 @@ def distill_step(p: DistillTargets, logits: torch.Tensor, layout: Layout, dloss:
     gp = None if dloss is None else _check_rows("dloss", dloss, (T,), torch.float32, dev)
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
     dz, dzp, ldo = _distill_out(p, logits, out, T, V, (("dloss", dloss),))
-    _check(lib().sl_distill_step(dt, layout.ref, ctypes.byref(c), zp, ld, gp, loss.data_ptr(), dzp, ldo, _stream()),
+    _check(lib().sl_distill_step(dt, layout.ref, ctypes.byref(c), zp, ld, gp, loss.data_ptr(), dzp, ldo, _stream_on(dev)),
            "sl_distill_step")
     return loss, dz

@@ -259,13 +259,14 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
       taught = !(tsum == 0.f);
       labelled = ids[K] >= 0;
     }
-    if ((!taught && !labelled) || (MODE == DM_BWD && g == 0.f)) {   // no loss
+    auto no_gradient = [&]() __attribute__((always_inline)) {
+      for (int c = tid; c < nvec; c += threads) store(c, Raw{});
+      if (tid < ntail) stv<T>(dz, nvec * W + tid, 0.f);
+    };
+    if ((!taught && !labelled) || (MODE == DM_BWD && g == 0.f)) {   // no loss, or none that counts
       if (MODE != DM_BWD && tid == 0) a.loss[row] = 0.f;
       if (MODE == DM_FWD && tid < 4) a.stats[row * 4 + tid] = 0.f;
-      if (MODE != DM_FWD) {
-        for (int c = tid; c < nvec; c += threads) store(c, Raw{});
-        if (tid < ntail) stv<T>(dz, nvec * W + tid, 0.f);
-      }
+      if (MODE != DM_FWD) no_gradient();
       continue;
     }
     if constexpr (MODE != DM_BWD) {
@@ -308,6 +309,10 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
         if (labelled) l += a.hard * (logf(s_hard) - below(ztop[K], TWO));
         a.loss[row] = l;
       }
+    }
+    if (MODE == DM_STEP && g == 0.f) {
+      no_gradient();
+      continue;
     }
     if constexpr (MODE != DM_FWD) {
       const float cs = taught ? g * (1.f - a.hard) * a.tau : 0.f, ch = labelled ? g * a.hard : 0.f;
@@ -365,8 +370,7 @@ static sl_status distill_args(DistillArgs& a, sl_dtype dt, const sl_layout* lay,
   if (!p || !z) SL_FAIL(SL_ERR_NULL, "the targets and logits required");
   if (p->vocab < 1 || p->vocab > (1LL << 30)) SL_FAIL(SL_ERR_RANGE, "vocabulary of %lld outside [1, 2^30]", (long long)p->vocab);
   if (!(p->hard >= 0.f && p->hard <= 1.f)) SL_FAIL(SL_ERR_RANGE, "hard must be in [0, 1]");
-  if (!(p->temperature > 0.f) || !std::isfinite(p->temperature) || !std::isfinite(1.f / p->temperature))
-    SL_FAIL(SL_ERR_RANGE, "temperature must be positive and finite");
+  if (!(p->temperature >= 1e-6f && p->temperature <= 1e6f)) SL_FAIL(SL_ERR_RANGE, "temperature must be in [1e-6, 1e6]");
   if (p->hard < 1.f) {
     if (p->top < 1 || p->top > kTop) SL_FAIL(SL_ERR_RANGE, "top = %d outside [1, %d]", p->top, kTop);
     if (!p->top_ids || !p->top_logits) SL_FAIL(SL_ERR_NULL, "top_ids and top_logits required");
@@ -374,7 +378,10 @@ static sl_status distill_args(DistillArgs& a, sl_dtype dt, const sl_layout* lay,
   if (p->hard > 0.f && !p->labels) SL_FAIL(SL_ERR_NULL, "labels required");
   if (ld < p->vocab || (dz && ld_out < p->vocab))
     SL_FAIL(SL_ERR_SHAPE, "rows of %lld and %lld elements hold no %lld logits", (long long)ld, (long long)ld_out, (long long)p->vocab);
-  if (!aligned16(z) || !aligned16(dz) || !aligned16(p->top_ids) || !aligned16(p->top_logits) || !aligned16(p->labels))
+  const uintptr_t es = dt == SL_BF16 ? 2 : 4;
+  if ((reinterpret_cast<uintptr_t>(z) | reinterpret_cast<uintptr_t>(dz)) % es)
+    SL_FAIL(SL_ERR_ALIGN, "logits and dlogits must be aligned to their elements");
+  if (!aligned16(p->top_ids) || !aligned16(p->top_logits) || !aligned16(p->labels))
     SL_FAIL(SL_ERR_ALIGN, "every pointer must be 16-byte aligned");
   a.z = z; a.ld = ld; a.ld_out = ld_out;
   a.top_ids = p->top_ids; a.top_logits = p->top_logits; a.labels = p->labels;
@@ -397,7 +404,7 @@ template <typename T, int MODE, bool TWO> static void launch_distill(const Disti
   // 32000: 187, 193, 1500: 242, 245, 1750 (112 MB): 245, 244, 2500: 320, 318; the same with 1500 rows
   // of 50021, which the product reads piecemeal: 490, 510; loss and gradient, 4096 rows of 32000: 182, 169.
   const bool past = (long long)a.rows * a.V * (long long)sizeof(T) >= 112LL << 20 &&
-                    (a.ld | (MODE == DM_FWD ? 0 : a.ld_out)) * (long long)sizeof(T) % 16 == 0;
+                    (a.ld | a.ld_out) * (long long)sizeof(T) % 16 == 0 && aligned16(a.z) && aligned16(a.dz);
   if (past) hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, MODE == DM_STEP ? 1 : 2>), grid, block, lds, s, a);
   else hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, 0>), grid, block, lds, s, a);
 }

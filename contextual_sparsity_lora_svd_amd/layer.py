@@ -484,7 +484,8 @@ class TokenEmbedding(torch.nn.Module):
     """The rows of a trained table ``weight`` [vocab, d_model] (bf16 or fp32) at the
     tokens ``ids`` [T] (int32), times ``scale``; an id outside the vocabulary is no
     token (a row of zeros, no gradient).  The table's gradient has its type; the
-    sums are fp32 and in a fixed order."""
+    sums are fp32 and in a fixed order.  A backward pass captured into a graph needs
+    every eager result of the same parameters dropped before, here and in LayerNorm."""
 
     def __init__(self, weight: torch.Tensor, scale: float = 1.0):
         super().__init__()

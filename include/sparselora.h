@@ -496,21 +496,22 @@ sl_status sl_layer_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_layer_no
  *   dlogits = dloss * the loss's gradient
  * A row without entries has no first term, one whose label is outside 0..vocab-1
  * no second.  Context rows (the first ctx_len[b] of each sequence) have neither:
- * loss 0, dlogits 0, and like every row without a term they are not read.
+ * loss 0, dlogits 0, whatever they hold; so has every row without a term.
  *   top_ids [T, top] int32, top_logits [T, top] fp32   (hard = 1: may be NULL)
  *   labels  [T] int32                                  (hard = 0: may be NULL)
  *   fwd:  logits -> loss [T] fp32 and stats [T, 4] fp32 for the backward
- *   bwd:  logits, stats, dloss [T] fp32 (NULL: ones) -> dlogits [T, ld_out]; a row
- *         whose dloss is 0 gets zeros
- *   step: logits, dloss -> loss and dlogits in one call, which reads logits from
- *         memory once; for a loss whose weights are known beforehand
+ *   bwd:  logits, stats, dloss [T] fp32 (NULL: ones) -> dlogits [T, ld_out]
+ *   step: logits, dloss -> loss and dlogits in one call, for a loss whose weights
+ *         are known beforehand: one launch, and most of logits read from memory once
+ *   A row whose dloss is 0 gets zeros.
  * dlogits may be logits (with ld_out = ld); otherwise no output may overlap an
  * input or another output.  Elements of a row behind the vocabulary are neither
- * read nor written.  ld, ld_out >= vocab, any number.
+ * read nor written.  ld, ld_out >= vocab, any number; logits and dlogits need no
+ * more than the alignment of their elements.
  * Logits of -inf have probability 0.  A row of -inf alone, or with +inf or NaN,
  * has no distribution: its loss and its gradient are NaN; so is the loss of a
  * teacher's entry of +inf or NaN, and the gradient there.
- * 0 <= hard <= 1, temperature > 0, 1 <= top <= SL_DISTILL_MAX_TOP, vocab <= 2^30.
+ * 0 <= hard <= 1, temperature in [1e-6, 1e6], 1 <= top <= SL_DISTILL_MAX_TOP, vocab <= 2^30.
  * ------------------------------------------------------------------------- */
 #define SL_DISTILL_MAX_TOP 256
 typedef struct sl_distill {

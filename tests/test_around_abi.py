@@ -109,14 +109,14 @@ def test_distillation_refusals(sl):
         assert f(p=_targets(sl, hard=1.0, top=0, ids=None, tl=None)) in (7, 8)
         assert f(p=_targets(sl, top=256)) in (7, 8) and f(p=_targets(sl, V=1)) in (7, 8)
         assert f(dt=3) == 4
-        assert f(z=None) == 1 and f(z=P + 2) == 2 and f(ld=99) == 3
+        assert f(z=None) == 1 and f(z=P + 1) == 2 and f(z=P + 2) in (7, 8) and f(dt=0, z=P + 2) == 2 and f(ld=99) == 3
         assert f(p=_targets(sl, ids=None)) == 1 and f(p=_targets(sl, tl=None)) == 1 and f(p=_targets(sl, labels=None)) == 1
         assert f(p=_targets(sl, ids=P + 4)) == 2 and f(p=_targets(sl, labels=P + 4)) == 2
         for top in (0, -1, 257):
             assert f(p=_targets(sl, top=top)) == 5, top
         for V in (0, (1 << 30) + 1):
             assert f(p=_targets(sl, V=V)) == 5, V
-        for tau in (0.0, -1.0, float("nan"), float("inf"), 1e-45):
+        for tau in (0.0, -1.0, float("nan"), float("inf"), 1e-45, 1e-7, 2e6):
             assert f(p=_targets(sl, tau=tau)) == 5, tau
         for hard in (-0.1, 1.1, float("nan")):
             assert f(p=_targets(sl, hard=hard)) == 5, hard
@@ -124,7 +124,7 @@ def test_distillation_refusals(sl):
             assert f(layout=sl.Layout(ctx, 4)) == 5
         assert f(layout=sl.Layout([0] * 65, 4)) == 5 and f(layout=sl.Layout([0], 0)) == 5
     assert fwd(loss=None) == 1 and fwd(stats=None) == 1 and fwd(stats=P + 4) == 2
-    assert bwd(stats=None) == 1 and bwd(dz=None) == 1 and bwd(ldo=99) == 3 and bwd(g=None) in (7, 8) and bwd(g=P + 4) == 2
+    assert bwd(stats=None) == 1 and bwd(dz=None) == 1 and bwd(dz=P + 1) == 2 and bwd(ldo=99) == 3 and bwd(g=None) in (7, 8) and bwd(g=P + 4) == 2
     assert step(loss=None) == 1 and step(dz=None) == 1 and step(ldo=99) == 3 and step(g=None) in (7, 8)
 
 
@@ -133,7 +133,7 @@ def test_binding_refusals(sl):
     torch = pytest.importorskip("torch")
     E, lay = sl.SparseLoraError, sl.Layout([0, 0], 4)
     x, ids, w = torch.zeros(8, 16), torch.zeros(8, dtype=torch.int32), torch.ones(16)
-    for bad in (dict(ids=ids.long()), dict(ids=ids[:7]), dict(E=x.half()), dict(E=x[:, ::2]), dict()):   # the last: no GPU
+    for bad in (dict(ids=ids.long()), dict(ids=ids[:7]), dict(E=x.half()), dict(E=x[:, ::2]), dict(E=x[0]), dict()):   # the last: no GPU
         with pytest.raises(E):
             sl.embed_fwd(**{"E": x, "ids": ids, **bad}, layout=lay)
     with pytest.raises(E):

@@ -125,6 +125,18 @@ def test_embedding_gradient_is_the_same_every_time():
         assert torch.equal(sl.embed_bwd(ids, dY, lay, V, buf=buf, out=out), first)
 
 
+def test_embedding_of_large_gradients():
+    """Past 64 MiB of rows: against sums in 64 bits, of exact terms."""
+    sl = _sl()
+    T, D, V, lay = 9000, 4096, 700, sl.Layout([0], 9000)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ids = (torch.rand(T, generator=g, device="cuda") ** 6 * V).int()
+    dY = torch.randint(-8, 9, (T, D), generator=g, device="cuda").bfloat16()
+    want = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dY.double())
+    assert torch.equal(sl.embed_bwd(ids, dY, lay, V).double(), want)            # whole numbers below 2^24
+    assert torch.equal(sl.embed_bwd(ids, dY.float(), lay, V).double(), want)
+
+
 def test_embedding_offsets_past_32_bits():
     """A table of more than 2^31 elements: its last rows."""
     sl = _sl()
@@ -276,6 +288,8 @@ DISTILL = [  # batch, seq, ctx, vocab, top
     (1, 4, [0], 32000, 64),
     (1, 3, [1], 50021, 5),
     (1, 2, [0], 128256, 128),
+    (3, 2, [0, 1, 0], 300, 256),         # more entries than threads
+    (2, 40, [3, 0], 513, 65),
 ]
 
 
@@ -408,6 +422,31 @@ def test_rows_without_a_loss_are_not_read():
     assert torch.equal(l2, loss) and torch.equal(d2, dz)
     z[3], g[3] = float("nan"), 0.0
     assert not sl.distill_bwd(p, z, stats, lay, g)[3].any()
+    l3, d3 = sl.distill_step(p, z, lay, g)
+    assert l3[3].isnan() and not d3[3].any() and torch.equal(d3[[2, 5]], dz[[2, 5]])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [32000, 32001])
+def test_large_logits_take_the_same_steps(dt, V):
+    """Past 112 MiB whole rows go past the caches: bit for bit what fewer rows give."""
+    sl = _sl()
+    T = 2400
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = (3 * torch.randn(T, V, generator=g, device="cuda")).to(DT[dt])
+    ids, labels = (torch.randint(0, V, s, generator=g, device="cuda").int() for s in ((T, 7), (T,)))
+    tl, w = torch.randn(T, 7, generator=g, device="cuda"), torch.rand(T, generator=g, device="cuda")
+    lay = sl.Layout([600, 0], T // 2)
+    p = sl.DistillTargets(ids, tl, labels, 1.5, 0.25)
+    loss, stats = sl.distill_fwd(p, z, lay)
+    dz = sl.distill_bwd(p, z, stats, lay, w)
+    l2, d2 = sl.distill_step(p, z, lay, w)
+    assert torch.equal(l2, loss) and torch.equal(d2, dz) and not loss[:600].any() and not dz[:600].any()
+    for a in (600, 1100, 1200, 2300):
+        s = slice(a, a + 100)
+        q = sl.DistillTargets(ids[s].clone(), tl[s].clone(), labels[s].clone(), 1.5, 0.25)
+        l3, d3 = sl.distill_step(q, z[s], sl.Layout([0], 100), w[s].clone())     # (z at any alignment of its rows)
+        assert torch.equal(l3, loss[s]) and torch.equal(d3, dz[s]), a
 
 
 def test_distillation_offsets_past_32_bits():
