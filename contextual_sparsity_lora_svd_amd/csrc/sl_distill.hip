@@ -14,8 +14,9 @@
 // forms the gradient; behind it the few ids of the teacher's entries and the label are
 // written again with their subtrahends.  A step (loss and gradient in one call) does
 // both walks in one launch, the second from the caches.  Both load the next four
-// vectors of a thread before they work on these.  Rows need not be aligned (an odd
-// vocabulary): a vector is 16 bytes at any element.
+// vectors of a thread before they work on these.  A row's vectors start at
+// its first 16-byte border (an odd vocabulary has it elsewhere in every row); in a
+// gradient whose rows stand otherwise they are stored where they fall.
 #include <cmath>
 #include <type_traits>
 
@@ -151,8 +152,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
   const bool soft = a.hard < 1.f, hard = a.hard > 0.f;
   const int K = soft ? a.top : 0;
   const float scale[2] = {(soft ? a.inv_tau : 1.f) * kLog2e, kLog2e};
-  const int nvec = a.V / W, ntail = a.V - nvec * W, batch = threads * U;
-  const int kept_end = MODE == DM_STEP ? kKept * batch < nvec ? kKept * batch : nvec : 0;   // vectors kept
+  const int batch = threads * U;
 
   for (long long it = blockIdx.x; it < a.rows; it += gridDim.x) {
     const bool out = it < a.st.T_out;
@@ -160,16 +160,26 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
     const T* const z = reinterpret_cast<const T*>(a.z) + row * a.ld;
     T* const dz = reinterpret_cast<T*>(a.dz) + row * a.ld_out;
     const float g = MODE == DM_FWD || !out ? 0.f : a.dloss ? a.dloss[row] : 1.f;
+    // the row: the elements up to a vector's border, the vectors, the elements behind
+    const int to_border = (int)(-reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
+    const int nhead = to_border < a.V ? to_border : a.V, nvec = (a.V - nhead) / W, ntail = a.V - nhead - nvec * W;
+    const T* const zv = z + nhead;
+    T* const dv = dz + nhead;
+    const int kept_end = MODE == DM_STEP ? kKept * batch < nvec ? kKept * batch : nvec : 0;   // vectors kept
+    auto odd_ones = [&](auto f) __attribute__((always_inline)) {
+      if (tid < nhead) f(tid);
+      if (tid < ntail) f(nhead + nvec * W + tid);
+    };
     auto fetch = [&](int c, Raw (&v)[U]) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (c + u * threads >= nvec) v[u] = RV::none();
-        else if (NT == 2) v[u] = __builtin_nontemporal_load(vec_at<const Raw>(z, c + u * threads));
-        else v[u] = *vec_at<const Raw>(z, c + u * threads);
+        else if (NT == 2) v[u] = __builtin_nontemporal_load(vec_at<const Raw>(zv, c + u * threads));
+        else v[u] = *vec_at<const Raw>(zv, c + u * threads);
     };
     auto store = [&](int c, Raw o) __attribute__((always_inline)) {
-      if (NT) __builtin_nontemporal_store(o, vec_at<Raw>(dz, c));
-      else *vec_at<Raw>(dz, c) = o;
+      if (NT) __builtin_nontemporal_store(o, vec_at<Raw>(dv, c));
+      else *vec_at<Raw>(dv, c) = o;
     };
     Raw v[U], next[U];
     Sums run = {-INFINITY, {0.f, 0.f}, {0.f, 0.f}, false};
@@ -219,10 +229,10 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
 #pragma unroll
           for (int u = 0; u < U; ++u) v[u] = next[u];
         }
-        if (tid < ntail) {
-          const float x[1] = {ldv<T>(z, nvec * W + tid)};
+        odd_ones([&](int i) __attribute__((always_inline)) {
+          const float x[1] = {ldv<T>(z, i)};
           absorb<TWO>(run, x, scale);
-        }
+        });
         if (MODE == DM_STEP) fetch(kKept * batch + tid, v);   // the second walk's first, behind what is kept
         rebase<TWO>(run, wave_max(run.m), scale);
 #pragma unroll
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
     }
     auto no_gradient = [&]() __attribute__((always_inline)) {
       for (int c = tid; c < nvec; c += threads) store(c, Raw{});
-      if (tid < ntail) stv<T>(dz, nvec * W + tid, 0.f);
+      odd_ones([&](int i) { stv<T>(dz, i, 0.f); });
     };
     if ((!taught && !labelled) || (MODE == DM_BWD && g == 0.f)) {   // no loss, or none that counts
       if (MODE != DM_BWD && tid == 0) a.loss[row] = 0.f;
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
           }
         }
         for (int c = tid; c < kept_end; c += threads) put(c, __builtin_bit_cast(Raw, kept[c]));
-        if (tid < ntail) stv<T>(dz, nvec * W + tid, grad(ldv<T>(z, nvec * W + tid)));
+        odd_ones([&](int i) __attribute__((always_inline)) { stv<T>(dz, i, grad(ldv<T>(z, i))); });
       };
       if (run.near) walk(std::true_type());
       else walk(std::false_type());

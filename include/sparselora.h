@@ -507,7 +507,8 @@ sl_status sl_layer_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_layer_no
  * dlogits may be logits (with ld_out = ld); otherwise no output may overlap an
  * input or another output.  Elements of a row behind the vocabulary are neither
  * read nor written.  ld, ld_out >= vocab, any number; logits and dlogits need no
- * more than the alignment of their elements.
+ * more than the alignment of their elements (by which, row by row, the order of the
+ * sums goes).
  * Logits of -inf have probability 0.  A row of -inf alone, or with +inf or NaN,
  * has no distribution: its loss and its gradient are NaN; so is the loss of a
  * teacher's entry of +inf or NaN, and the gradient there.

@@ -342,14 +342,20 @@ def test_distillation(case, dt, tau, hard):
     c = zt.clone()
     l3, _ = sl.distill_step(p, c, lay, gt, out=c)
     assert torch.equal(c, dz) and torch.equal(l3, loss)
-    for pad in (1, 13):
+    # (a row's vectors start at its first 16-byte border, so rows elsewhere are summed in another
+    # order: the bounds above hold for every order of additions of that length)
+    for pad in (1, 13, 16):
         wide, out = (torch.full((B * L, V + pad), float("nan"), dtype=DT[dt], device="cuda") for _ in range(2))
         wide[:, :V] = zt
         l4, s4 = sl.distill_fwd(p, wide[:, :V], lay)
-        assert torch.equal(l4, loss) and torch.equal(s4, stats)
-        sl.distill_bwd(p, wide[:, :V], stats, lay, gt, out=out[:, :V])
-        assert torch.equal(out[:, :V], dz) and out[:, V:].isnan().all()
-        assert torch.equal(sl.distill_step(p, wide[:, :V], lay, gt, out=wide[:, :V])[1], dz) and wide[:, V:].isnan().all()
+        _within(l4, rl, U32 * (bl(n) + np.abs(rl)), "loss of rows apart")
+        sl.distill_bwd(p, wide[:, :V], s4, lay, gt, out=out[:, :V])
+        _within(out[:, :V], rz, HALF[dt] * np.abs(rz) + U32 * bz(n) + TINY, "dz of rows apart")
+        assert out[:, V:].isnan().all()
+        d4 = out[:, :V].clone()
+        l5, d5 = sl.distill_step(p, wide[:, :V], lay, gt)          # rows of logits and gradient that stand differently
+        assert torch.equal(l5, l4) and torch.equal(d5, d4)
+        assert torch.equal(sl.distill_step(p, wide[:, :V], lay, gt, out=wide[:, :V])[1], d4) and wide[:, V:].isnan().all()
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
