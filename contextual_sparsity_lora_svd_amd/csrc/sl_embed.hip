@@ -1,7 +1,8 @@
 // Token embedding: Y[t] = scale * E[id_t], and the table's gradient
 // dE[v] = scale * (sum of dY[t] over the tokens t with id_t = v).
 //
-// Lookup: a row's vectors are read and written once.
+// Lookup: a row's vectors are read and written once (32768 rows of 4096 bf16 92 us, 5.8 TB/s;
+// 2048 rows 10 us, of which 5 are the chain from the id to the row to its store).
 //
 // Gradient: the tokens are sorted by (id, place) first, so that the rows of one
 // id stand in a run whose sum is taken in one fixed order, with no atomics on
@@ -18,6 +19,11 @@
 // The table is zeroed beside step 1, every row of it: that needs no word of the ids, and
 // runs as fast as memory takes it where a block writes 4 KB, a vector a thread (524 MB: 77 us; in
 // 64 KB a block 98, which a search for the rows without a token needs to pay).
+//
+// Measured: 2048 tokens, 32000 x 4096 fp32: sort and zeros 81 us, sums 14.5, join 4.8; 32768 tokens,
+// 128256 x 4096 bf16: 156, 8 for the merge, 76 (356 MB with what it writes: 4.7 TB/s) and 10.  What
+// bounds it: the table's writes; then the sums' chain from the sorted list to the rows to the
+// waves' exchange, two rounds of memory latency where there are few tokens.
 #include "sl_rows.hpp"
 
 namespace sl {
