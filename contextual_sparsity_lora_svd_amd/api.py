@@ -959,14 +959,14 @@ def layer_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor], 
 
 
 def layer_norm_bwd(h: torch.Tensor, w: torch.Tensor, stats: torch.Tensor, layout: Layout, dy: torch.Tensor,
-                   dh: Optional[torch.Tensor] = None, centered: bool = True, bias: bool = True,
+                   dh: Optional[torch.Tensor] = None, centered: bool = True, bias: Optional[bool] = None,
                    buf: Optional[LayerNormWorkspace] = None, out: Optional[Dict[str, torch.Tensor]] = None):
     """Gradients of layer_norm_fwd: dx (of x and of the residual alike) and dw, db
-    (fp32; db only with ``bias``).  h and stats are the forward's; ``dh`` is the
+    (fp32; db only with ``bias``, None: where centred).  h and stats are the forward's; ``dh`` is the
     gradient that reaches h by its other way.  ``out`` may hold results to write
     into: dx may be dy, dh or h."""
     dt, T, dev = _dtype_code(h), layout.batch * layout.seq_len, _current(h)
-    D = h.shape[-1]
+    D, bias = h.shape[-1], centered if bias is None else bias
     hp, wp = _check_rows("h", h, (T, D), h.dtype, dev), _check_rows("w", w, (D,), torch.float32, dev)
     sp = _check_rows("stats", stats, (T, 3), torch.float32, dev)
     gp = _check_rows("dy", dy, (T, D), h.dtype, dev)

@@ -340,17 +340,19 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_k
         };
         // at the entries' ids and the label; an id that comes twice gets the same value
         // from each of its entries
-        for (int k = tid; k <= K; k += threads) {
-          const int id = ids[k];
+        for (int k0 = wave * 64; k0 <= K; k0 += threads) {      // whole waves: lanes read each other's entries
+          const int k = k0 + lane, id = k <= K ? ids[k] : -1;
           float p = 0.f;
 #pragma unroll
           for (int j = 0; j < kTop / 64; ++j)
             for (int i = 0; i < 64 && i + 64 * j < K; ++i)
               p += __builtin_amdgcn_readlane(eid[j], i) == id ? lane_value(e[j], i) : 0.f;
-          float d = grad(ztop[k]);
-          if (taught) d -= cs * (p / tsum);
-          if (labelled && ids[K] == id) d -= ch;
-          dtop[k] = d;
+          if (k <= K) {
+            float d = grad(ztop[k]);
+            if (taught) d -= cs * (p / tsum);
+            if (labelled && ids[K] == id) d -= ch;
+            dtop[k] = d;
+          }
         }
         auto put = [&](int c, Raw x) __attribute__((always_inline)) {
           Raw o;

@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(64 * kPieceWaves) embed_grad_kernel(const Embe
       if (i0 + u < i1) {
         const long long row = __builtin_amdgcn_readlane(tok, i0 + u);
         const Pack<T>* const p = reinterpret_cast<const Pack<T>*>(reinterpret_cast<const T*>(a.dY) + row * a.D + col);
-        if (on && id_at(i0 + u) < a.V) {
+        const bool token = id_at(i0 + u) < a.V;
+        if (on && token) {
           if constexpr (PAST) v[u].r = __builtin_nontemporal_load(&p->r);
           else v[u] = *p;
         }
@@ -259,8 +260,9 @@ __global__ void __launch_bounds__(64 * kPieceWaves) embed_grad_kernel(const Embe
       for (; w * R <= end; ++w)
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[j] += left[w][lane][j];
+      const bool whole = inside && id_at(end + 1) != id;
       if (!on) return;
-      if (inside && id_at(end + 1) != id) store_grad<W>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
+      if (whole) store_grad<W>(reinterpret_cast<GT*>(a.dE) + (long long)id * a.D + col, acc, a.scale);
       else store_grad<W>(a.part + ((long long)piece * 2 + inside) * a.D + col, acc, 1.f);
     };
     if (wave == 0 && id_at(0) == before && before < a.V) {
