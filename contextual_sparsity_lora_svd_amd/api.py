@@ -932,7 +932,8 @@ def layer_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor], 
     weight w and bias b [d_model] (fp32, b may be None), or, not ``centered``, its
     root-mean-square norm (without a bias).  stats [T, 3] fp32 is what the backward
     reads (None unless ``want_stats``).  ``out``: tensors for y and h; either may be
-    x or the residual."""
+    x or the residual (y in the place of x without a residual: without ``want_stats``
+    only, as nothing is left for the backward, and the h returned is y then)."""
     y, h = out if out is not None else (None, None)
     if residual is None and h is not None and h is not x:
         raise SparseLoraError("h is x where nothing is added")
@@ -949,9 +950,10 @@ def layer_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor], 
         hp = _check_rows("h", h, (T, D), x.dtype, dev)
     stats = w.new_empty((T, 3)) if want_stats else None
     if out is not None:
+        over_x = () if residual is None and want_stats else (("y", "x"),)   # x is the h that the backward reads
         _refuse_overlap((("y", y), ("h", None if residual is None else h)),
                         (("x", x), ("residual", residual), ("w", w), ("b", b)),
-                        (("y", "x"), ("y", "residual"), ("h", "x"), ("h", "residual")))
+                        (*over_x, ("y", "residual"), ("h", "x"), ("h", "residual")))
     c = SlLayerNorm(D, int(centered), eps, wp, bp)
     _check(lib().sl_layer_norm_fwd(dt, layout.ref, ctypes.byref(c), xp, rp, hp, yp,
                                    None if stats is None else stats.data_ptr(), _stream_on(dev)), "sl_layer_norm_fwd")

@@ -563,7 +563,10 @@ class DistillLoss(torch.nn.Module):
     ``step`` forms losses and gradient in one pass:
 
         losses, dlogits = crit.step(logits, layout, top_ids, top_logits, weights=w)
-        logits.backward(dlogits)"""
+        logits.backward(dlogits)
+
+    (``out``: where the gradient goes; logits itself, unless what formed it or another
+    loss of it saved it for a backward pass, which then raises.)"""
 
     def __init__(self, temperature: float = 1.0, hard: float = 0.0):
         super().__init__()
@@ -579,4 +582,7 @@ class DistillLoss(torch.nn.Module):
     def step(self, logits: torch.Tensor, layout: sl.Layout, top_ids: Optional[torch.Tensor] = None,
              top_logits: Optional[torch.Tensor] = None, labels: Optional[torch.Tensor] = None,
              weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
-        return sl.distill_step(self._targets(top_ids, top_logits, labels), logits.detach(), layout, weights, out)
+        got = sl.distill_step(self._targets(top_ids, top_logits, labels), logits.detach(), layout, weights, out)
+        if out is not None and not out.is_inference():
+            torch.autograd.graph.increment_version(out)     # whoever saved these logits is told
+        return got

@@ -464,7 +464,8 @@ sl_status sl_embed_bwd(sl_dtype dt, const sl_layout* lay, int64_t vocab, int64_t
  *   not centered: m = 0 and b = 0
  *   w, b [d_model] fp32; b may be NULL (0)
  *   fwd: x, r -> h, y [T, d_model] and stats [T, 3] fp32 (m, what m rounded away,
- *        s; NULL: not written).  r and h both or neither.  h or y may be x, or r.
+ *        s; NULL: not written).  r and h both or neither.  h or y may be x, or r
+ *        (without r, y in x's place leaves no h for the backward).
  *   bwd: h, stats (the forward's), dy and optionally dh, the gradient that reaches
  *        h by its other way -> dx, the gradient of x and of r alike, and the fp32
  *        gradients dw and db [d_model], overwritten (db NULL: not written).  dx

@@ -100,3 +100,31 @@ def test_a_second_derivative_is_refused(mods, step):
     (g,) = torch.autograd.grad(x.sum() * y.sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.sum().backward()
+
+
+def test_a_gradient_over_saved_logits_is_noticed(mods, monkeypatch):
+    """step() may write the gradient over the logits; a backward pass that needs them raises."""
+    sl, _, lay = mods
+    from contextual_sparsity_lora_svd_amd import layer
+
+    def distill_step(p, z, layout, w, out):
+        out.data.fill_(0.5)
+        return torch.zeros(len(z)), out
+
+    monkeypatch.setattr(layer.sl, "distill_step", distill_step)
+    ids, top = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    x = torch.randn(3, 9, requires_grad=True)
+    z = torch.tanh(x)                                     # its backward reads its result
+    _, dz = sl.DistillLoss().step(z, lay, ids, top, out=z)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward(dz)
+    z = 2 * x
+    loss = sl.DistillLoss()(z, lay, ids, top)
+    _, dz = sl.DistillLoss().step(z, lay, ids, top, out=z)
+    z.backward(dz, retain_graph=True)                     # nothing of this product's backward is z
+    assert torch.equal(x.grad, torch.ones_like(x))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    with torch.inference_mode():
+        z = torch.randn(3, 9)
+        assert sl.DistillLoss().step(z, lay, ids, top, out=z)[1] is z

@@ -215,7 +215,12 @@ def test_layer_norm_in_place(dt):
         got = sl.layer_norm_bwd(c[0], w, stats, lay, c[1], c[2], out={"dx": c[n]})
         for k in g:
             assert torch.equal(got[k], g[k]), (n, k)
+    c = x.clone()                                         # without a residual: where no backward follows
+    y2, h2, s2 = sl.layer_norm_fwd(c, w, b, lay, want_stats=False, out=(c, None))
+    assert y2 is c and h2 is c and s2 is None and torch.equal(c, sl.layer_norm_fwd(x, w, b, lay)[0])
     E = sl.SparseLoraError
+    with pytest.raises(E, match="may not share"):
+        sl.layer_norm_fwd(x, w, b, lay, out=(x, None))
     with pytest.raises(E, match="may not share"):
         sl.layer_norm_fwd(x, w, b, lay, residual=r, out=(x, x))
     with pytest.raises(E, match="may not share"):
