@@ -98,14 +98,19 @@ template <bool NEAR> __device__ inline float term(const Sums& a, float z, float 
   const float y = NEAR ? fmaf(z, scale, -a.top[i]) : (z - (a.m == -INFINITY ? 0.f : a.m)) * scale;
   return __builtin_amdgcn_exp2f(y);
 }
-// The sums relative to another maximum, at least the old one.
+// The sums relative to another maximum, at least the old one.  Where one of the two is
+// within 2^20 and the other past it, the step is between a rounded product and one that is
+// not: the rounding, up to 2^-5 there, is part of it.
 template <bool TWO> __device__ inline void rebase(Sums& a, float m, const float* scale) {
   const Sums old = a;
   set_top<TWO>(a, m, scale);
   if (old.m == -INFINITY) return;               // (the sums are 0, or NaN)
 #pragma unroll
-  for (int i = 0; i < 1 + TWO; ++i)
-    a.s[i] *= __builtin_amdgcn_exp2f(old.near && a.near ? old.top[i] - a.top[i] : (old.m - m) * scale[i]);
+  for (int i = 0; i < 1 + TWO; ++i) {
+    const float within = old.near ? old.top[i] - a.top[i] : fmaf(old.m, scale[i], -a.top[i]);
+    const float past = old.near ? -fmaf(m, scale[i], -old.top[i]) : (old.m - m) * scale[i];
+    a.s[i] *= __builtin_amdgcn_exp2f(a.near ? within : past);
+  }
 }
 
 // The values of some vectors into the running sums.
@@ -143,8 +148,10 @@ __device__ inline int context_token(const SeqTab& st, int i) {
 // TWO: the teacher's term at tau and the label's at 1 need an exponential each.
 // With one of the terms alone, or with tau = 1, one serves.
 // NT: past the caches, 1 the gradient's stores, 2 the logits' loads too.
+// Loss or gradient alone: at most 80 registers, with which a CU takes three blocks (the
+// loss with two exponentials needs 85).
 template <typename T, int MODE, bool TWO, int NT>
-__global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD ? 6 : 4) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD || (MODE == DM_FWD && !TWO) ? 6 : 4) distill_kernel(const DistillArgs a) {
   using RV = RowVec<T>;
   using Raw = typename RV::Raw;
   constexpr int W = RV::W, U = kVecs;
