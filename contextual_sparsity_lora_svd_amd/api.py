@@ -576,6 +576,18 @@ def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, de
     raise SparseLoraError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
+def _check_values(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: Optional[int] = None):
+    """_check_rows of an input whose values kernels read one at a time (ids, labels,
+    positions, a number or three a row).  Callers have these as views that start anywhere
+    (``tokens[1:]``); the library takes pointers of 16 bytes, so such a view is copied.
+    Returns the pointer and its tensor, to be held until the launch."""
+    p = _check_rows(name, t, shape, dtype, dev)
+    if p % 16:
+        t = t.clone()
+        p = t.data_ptr()
+    return p, t
+
+
 def _refuse_overlap(outs, ins, in_place=()):
     """Refuse outputs ((name, tensor) pairs, None left out) that share memory with each
     other or with an input, but the ``in_place`` pairs (output, input) of the same rows.
@@ -625,9 +637,11 @@ class Rotary:
         self.turns = torch.tensor([ctypes.c_int64(x).value for x in table], dtype=torch.int64).to(device)
 
     def _c(self, pos: Optional[torch.Tensor], T: int, dev: Optional[int]) -> SlRotary:
-        pp = None if pos is None else _check_rows("pos", pos, (T,), torch.int32, dev)
+        pp, held = (None, None) if pos is None else _check_values("pos", pos, (T,), torch.int32, dev)
         tp = _check_rows("turns", self.turns, (self.rot_dim // 2,), torch.int64, dev)
-        return SlRotary(self.rot_dim, self.interleaved, self.amplitude, tp, pp)
+        c = SlRotary(self.rot_dim, self.interleaved, self.amplitude, tp, pp)
+        c.held = held
+        return c
 
 
 def _check_scratch(name: str, ws: torch.Tensor, like: torch.Tensor) -> int:
@@ -876,6 +890,8 @@ def diff_attn_bwd(p: DiffAttnParams, q: torch.Tensor, k: torch.Tensor, v: torch.
 
 # ---------------------------------------------------------------------------
 # Around the layers: token embedding, norm of whole rows, distillation.
+# Rows start at a 16-byte border (logits anywhere); ids, labels, teacher's entries, weights of
+# rows and statistics may be views that start anywhere.
 def embed_fwd(E: torch.Tensor, ids: torch.Tensor, layout: Layout, scale: float = 1.0,
               out: Optional[torch.Tensor] = None):
     """Y [T, d_model]: scale * E[ids] (ids [T] int32; one outside E's rows is no
@@ -884,7 +900,8 @@ def embed_fwd(E: torch.Tensor, ids: torch.Tensor, layout: Layout, scale: float =
         raise SparseLoraError(f"E: expected [vocab, d_model], got {tuple(E.shape)}")
     dt, T, dev = _dtype_code(E), layout.batch * layout.seq_len, _current(E)
     V, D = E.shape
-    Ep, ip = _check_rows("E", E, (V, D), E.dtype, dev), _check_rows("ids", ids, (T,), torch.int32, dev)
+    Ep = _check_rows("E", E, (V, D), E.dtype, dev)
+    ip, held = _check_values("ids", ids, (T,), torch.int32, dev)
     Y = out if out is not None else E.new_empty((T, D))
     Yp = _check_rows("Y", Y, (T, D), E.dtype, dev)
     if out is not None:
@@ -907,7 +924,8 @@ def embed_bwd(ids: torch.Tensor, dY: torch.Tensor, layout: Layout, vocab: int, s
     the fp32 sums rounded once); rows of ids without a token are 0."""
     dt, T, dev = _dtype_code(dY), layout.batch * layout.seq_len, _current(dY)
     D = dY.shape[-1]
-    ip, gp = _check_rows("ids", ids, (T,), torch.int32, dev), _check_rows("dY", dY, (T, D), dY.dtype, dev)
+    ip, held = _check_values("ids", ids, (T,), torch.int32, dev)
+    gp = _check_rows("dY", dY, (T, D), dY.dtype, dev)
     dE = out if out is not None else torch.empty((vocab, D), dtype=grad_dtype, device=dY.device)
     dEp = _check_rows("dE", dE, (vocab, D), grad_dtype, dev)
     buf = buf or EmbedWorkspace(layout, D, dY.device)
@@ -970,7 +988,7 @@ def layer_norm_bwd(h: torch.Tensor, w: torch.Tensor, stats: torch.Tensor, layout
     dt, T, dev = _dtype_code(h), layout.batch * layout.seq_len, _current(h)
     D, bias = h.shape[-1], centered if bias is None else bias
     hp, wp = _check_rows("h", h, (T, D), h.dtype, dev), _check_rows("w", w, (D,), torch.float32, dev)
-    sp = _check_rows("stats", stats, (T, 3), torch.float32, dev)
+    sp, held = _check_values("stats", stats, (T, 3), torch.float32, dev)
     gp = _check_rows("dy", dy, (T, D), h.dtype, dev)
     rp = None if dh is None else _check_rows("dh", dh, (T, D), h.dtype, dev)
     buf = buf or LayerNormWorkspace(layout, D, h.device)
@@ -1007,19 +1025,21 @@ class DistillTargets:
         self.temperature, self.hard = float(temperature), float(hard)
 
     def _c(self, T: int, V: int, dev: Optional[int]) -> SlDistill:
-        ip = tp = lp = None
+        (ip, ids), (tp, tops), (lp, labels) = ((None, None),) * 3
         top = 0
         if self.hard < 1.0:
             if self.top_ids is None or self.top_logits is None:
                 raise SparseLoraError("top_ids and top_logits are required where hard is below 1")
             top = self.top_ids.shape[-1]
-            ip = _check_rows("top_ids", self.top_ids, (T, top), torch.int32, dev)
-            tp = _check_rows("top_logits", self.top_logits, (T, top), torch.float32, dev)
+            ip, ids = _check_values("top_ids", self.top_ids, (T, top), torch.int32, dev)
+            tp, tops = _check_values("top_logits", self.top_logits, (T, top), torch.float32, dev)
         if self.hard > 0.0:
             if self.labels is None:
                 raise SparseLoraError("labels are required where hard is above 0")
-            lp = _check_rows("labels", self.labels, (T,), torch.int32, dev)
-        return SlDistill(V, top, self.temperature, self.hard, ip, tp, lp)
+            lp, labels = _check_values("labels", self.labels, (T,), torch.int32, dev)
+        c = SlDistill(V, top, self.temperature, self.hard, ip, tp, lp)
+        c.held = (ids, tops, labels)
+        return c
 
 
 def _logit_rows(name: str, z: torch.Tensor, T: int, V: int, dtype: torch.dtype):
@@ -1086,8 +1106,8 @@ def distill_bwd(p: DistillTargets, logits: torch.Tensor, stats: torch.Tensor, la
     V = logits.shape[-1]
     zp, ld = _logit_rows("logits", logits, T, V, logits.dtype)
     c = p._c(T, V, dev)
-    sp = _check_rows("stats", stats, (T, 4), torch.float32, dev)
-    gp = None if dloss is None else _check_rows("dloss", dloss, (T,), torch.float32, dev)
+    sp, held = _check_values("stats", stats, (T, 4), torch.float32, dev)
+    gp, weights = (None, None) if dloss is None else _check_values("dloss", dloss, (T,), torch.float32, dev)
     dz, dzp, ldo = _distill_out(p, logits, out, T, V, (("stats", stats), ("dloss", dloss)))
     _check(lib().sl_distill_bwd(dt, layout.ref, ctypes.byref(c), zp, ld, sp, gp, dzp, ldo, _stream_on(dev)), "sl_distill_bwd")
     return dz
@@ -1101,7 +1121,7 @@ def distill_step(p: DistillTargets, logits: torch.Tensor, layout: Layout, dloss:
     V = logits.shape[-1]
     zp, ld = _logit_rows("logits", logits, T, V, logits.dtype)
     c = p._c(T, V, dev)
-    gp = None if dloss is None else _check_rows("dloss", dloss, (T,), torch.float32, dev)
+    gp, weights = (None, None) if dloss is None else _check_values("dloss", dloss, (T,), torch.float32, dev)
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
     dz, dzp, ldo = _distill_out(p, logits, out, T, V, (("dloss", dloss),))
     _check(lib().sl_distill_step(dt, layout.ref, ctypes.byref(c), zp, ld, gp, loss.data_ptr(), dzp, ldo, _stream_on(dev)),

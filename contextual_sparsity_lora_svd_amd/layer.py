@@ -88,6 +88,13 @@ class SparsitySchedule:
         return n if pct == 0 else sl.k_from_ratio(n, pct)
 
 
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """t as the kernels take it: contiguous, from a 16-byte border on.  What arrives may
+    be a view that starts anywhere, as the gradient of one part of a cat does."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _all_channels(batch: int, n: int, device) -> torch.Tensor:
     return torch.arange(n, dtype=torch.int32, device=device).repeat(batch, 1).contiguous()
 
@@ -103,7 +110,7 @@ class _FFNStep(torch.autograd.Function):
         t = dict(mod.frozen)
         t.update(lora)
         w = sl.FFNWeights(t, mod.lora_scale)
-        Xc = X.detach().contiguous()
+        Xc = _packed(X.detach())
         Y, buf = sl.ffn_fwd(w, Xc, layout, k, idx, sl.FFNWorkspace(w, layout, k, X.device))
         ctx.state = (w, Xc, layout, k, idx, buf)
         return Y
@@ -111,7 +118,7 @@ class _FFNStep(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dY):
         w, Xc, layout, k, idx, buf = ctx.state
-        g = sl.ffn_bwd(w, Xc, layout, k, idx, buf, dY.contiguous())
+        g = sl.ffn_bwd(w, Xc, layout, k, idx, buf, _packed(dY))
         ctx.state = None
         return (g["dX"], g["dAg"], g["dBg"], g["dAu"], g["dBu"], g["dAd"], g["dBd"],
                 None, None, None, None)
@@ -188,7 +195,7 @@ class _QKVOState:
 class _QKVStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, Aq, Bq, Ak, Bk, Av, Bv, st):
-        Xc = X.detach().contiguous()
+        Xc = _packed(X.detach())
         o, _ = sl.qkvo_fwd(st.w, Xc, None, st.layout, st.k_qk, st.idx_qk, st.k_vo, st.idx_vo, st.buf)
         ctx.state = (st, Xc)
         return o["q"], o["k"], o["v"]
@@ -199,7 +206,7 @@ class _QKVStep(torch.autograd.Function):
         # an output the loss does not reach has no gradient: zeros stand in
         shapes = ((st.w.heads[0] * st.w.heads[2]), (st.w.heads[1] * st.w.heads[2]))
         T = Xc.shape[0]
-        z = lambda g, n: g.contiguous() if g is not None else torch.zeros(T, n, dtype=Xc.dtype,
+        z = lambda g, n: _packed(g) if g is not None else torch.zeros(T, n, dtype=Xc.dtype,
                                                                           device=Xc.device)
         g = sl.qkvo_bwd(st.w, Xc, None, st.layout, st.k_qk, st.idx_qk, st.k_vo, st.idx_vo, st.buf,
                         dq=z(dq, shapes[0]), dk=z(dk, shapes[1]), dv=z(dv, shapes[1]))
@@ -210,7 +217,7 @@ class _QKVStep(torch.autograd.Function):
 class _OStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, a, Ao, Bo, st):
-        ac = a.detach().contiguous()
+        ac = _packed(a.detach())
         o, _ = sl.qkvo_fwd(st.w, None, ac, st.layout, st.k_qk, st.idx_qk, st.k_vo, st.idx_vo, st.buf)
         ctx.state = (st, ac)
         return o["o"]
@@ -219,7 +226,7 @@ class _OStep(torch.autograd.Function):
     def backward(ctx, d_out):
         st, ac = ctx.state
         g = sl.qkvo_bwd(st.w, None, ac, st.layout, st.k_qk, st.idx_qk, st.k_vo, st.idx_vo, st.buf,
-                        d_out=d_out.contiguous())
+                        d_out=_packed(d_out))
         ctx.state = None
         return g["da"], g["dAo"], g["dBo"], None
 
@@ -337,21 +344,21 @@ class _RotaryStep(torch.autograd.Function):
     def forward(ctx, q, k, layout, heads, rot, pos):
         ctx.args = (layout, heads, rot)
         ctx.save_for_backward(pos)
-        return sl.rotary(q.detach().contiguous(), k.detach().contiguous(), layout, heads, rot, pos)
+        return sl.rotary(_packed(q.detach()), _packed(k.detach()), layout, heads, rot, pos)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
         layout, heads, rot = ctx.args
         (pos,) = ctx.saved_tensors
-        dq, dk = sl.rotary(dq.contiguous(), dk.contiguous(), layout, heads, rot, pos, inverse=True)
+        dq, dk = sl.rotary(_packed(dq), _packed(dk), layout, heads, rot, pos, inverse=True)
         return dq, dk, None, None, None, None
 
 
 class _HeadNormStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, wq, wk, layout, heads, rot, pos, eps):
-        q, k = q.detach().contiguous(), k.detach().contiguous()
+        q, k = _packed(q.detach()), _packed(k.detach())
         ctx.args = (layout, heads, rot, eps)
         ctx.save_for_backward(q, k, wq, wk, pos)
         return sl.head_norm_fwd(q, k, wq.detach(), wk.detach(), layout, heads, rot, pos, eps)
@@ -361,7 +368,7 @@ class _HeadNormStep(torch.autograd.Function):
     def backward(ctx, dq, dk):
         layout, heads, rot, eps = ctx.args
         q, k, wq, wk, pos = ctx.saved_tensors
-        g = sl.head_norm_bwd(q, k, wq.detach(), wk.detach(), layout, heads, dq.contiguous(), dk.contiguous(), rot,
+        g = sl.head_norm_bwd(q, k, wq.detach(), wk.detach(), layout, heads, _packed(dq), _packed(dk), rot,
                              pos, eps)
         return g["dq"], g["dk"], g["dwq"], g["dwk"], None, None, None, None, None
 
@@ -369,7 +376,7 @@ class _HeadNormStep(torch.autograd.Function):
 class _DiffAttnStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, lq1, lk1, lq2, lk2, mod, layout, lens):
-        q, k, v = (x.detach().contiguous() for x in (q, k, v))
+        q, k, v = (_packed(x.detach()) for x in (q, k, v))
         p = mod._params(lq1, lk1, lq2, lk2)
         buf = sl.DiffAttnWorkspace(p, layout, q.dtype, q.device, lens, scratch=False)
         a, _ = sl.diff_attn_fwd(p, q, k, v, layout, buf=buf)
@@ -387,7 +394,7 @@ class _DiffAttnStep(torch.autograd.Function):
         q, k, v, a, *_, saved = ctx.saved_tensors
         buf = copy.copy(buf)
         buf.saved = saved
-        g = sl.diff_attn_bwd(p, q, k, v, a, layout, buf, da.contiguous())
+        g = sl.diff_attn_bwd(p, q, k, v, a, layout, buf, _packed(da))
         return (g["dq"], g["dk"], g["dv"], g["dlq1"], g["dlk1"], g["dlq2"], g["dlk2"], None, None, None)
 
 
@@ -477,7 +484,7 @@ class _EmbedStep(torch.autograd.Function):
     def backward(ctx, dY):
         layout, scale, vocab, dtype = ctx.args
         (ids,) = ctx.saved_tensors
-        return sl.embed_bwd(ids, dY.contiguous(), layout, vocab, scale, dtype), None, None, None
+        return sl.embed_bwd(ids, _packed(dY), layout, vocab, scale, dtype), None, None, None
 
 
 class TokenEmbedding(torch.nn.Module):
@@ -498,7 +505,7 @@ class TokenEmbedding(torch.nn.Module):
 class _LayerNormStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, r, w, b, layout, eps, centered):
-        x, r = x.detach().contiguous(), None if r is None else r.detach().contiguous()
+        x, r = _packed(x.detach()), None if r is None else _packed(r.detach())
         y, h, stats = sl.layer_norm_fwd(x, w.detach(), None if b is None else b.detach(), layout, eps, centered, r)
         ctx.set_materialize_grads(False)
         ctx.args = (layout, centered, r is not None, b is not None)
@@ -512,8 +519,8 @@ class _LayerNormStep(torch.autograd.Function):
         if dy is None and dh is None:
             return (None,) * 7
         h, w, stats = ctx.saved_tensors
-        dy = torch.zeros_like(h) if dy is None else dy.contiguous()
-        g = sl.layer_norm_bwd(h, w.detach(), stats, layout, dy, None if dh is None else dh.contiguous(), centered, bias)
+        dy = torch.zeros_like(h) if dy is None else _packed(dy)
+        g = sl.layer_norm_bwd(h, w.detach(), stats, layout, dy, None if dh is None else _packed(dh), centered, bias)
         return g["dx"], g["dx"] if added else None, g["dw"], g.get("db"), None, None, None
 
 
