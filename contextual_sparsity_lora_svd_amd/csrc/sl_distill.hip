@@ -49,6 +49,7 @@ struct DistillArgs {
   long long ld, ld_out;     // elements from row to row
   int V, top, rows;
   float tau, inv_tau, hard;
+  float scale;              // log2(e) / tau rounded once (log2(e) where the label's term stands alone)
   SeqTab st;
 };
 
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD || (MODE == DM_FWD
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
   const bool soft = a.hard < 1.f, hard = a.hard > 0.f;
   const int K = soft ? a.top : 0;
-  const float scale[2] = {(soft ? a.inv_tau : 1.f) * kLog2e, kLog2e};
+  const float scale[2] = {a.scale, kLog2e};
   const int batch = threads * U;
 
   for (long long it = blockIdx.x; it < a.rows; it += gridDim.x) {
@@ -418,6 +419,7 @@ static sl_status distill_args(DistillArgs& a, sl_dtype dt, const sl_layout* lay,
   a.V = (int)p->vocab; a.top = p->top;
   a.rows = lay->batch * lay->seq_len;
   a.tau = p->temperature; a.inv_tau = 1.f / p->temperature; a.hard = p->hard;
+  a.scale = p->hard < 1.f ? (float)(1.4426950408889634 / (double)p->temperature) : kLog2e;
   return SL_OK;
 }
 

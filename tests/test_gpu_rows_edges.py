@@ -40,6 +40,29 @@ def test_maxima_on_both_sides_of_2_to_the_20th(tau, hard, border_of, sign):
     assert torch.equal(l2, loss) and torch.equal(d2, dz)
 
 
+@pytest.mark.parametrize("tau", [2.54, 5.54, 5.69])
+def test_the_scale_of_exponents_is_rounded_once(tau):
+    """Logits far below the maximum: their exponents y = z log2(e) / tau have the scale's rounding, half a step
+    relative to y, and their own, half a step of numbers from 64 on.  (At these temperatures log2(e) times a rounded
+    1 / tau is off by 1.7 half steps.)"""
+    sl = _sl()
+    V, lay, tau32 = 4096, sl.Layout([0], 2), float(np.float32(tau))
+    z = -np.random.default_rng(1).uniform(60.0 * tau32, 80.0 * tau32, (2, V)).astype(np.float32)
+    z[:, 0] = 0.0
+    p = sl.DistillTargets(_ints([[0], [0]]), torch.zeros(2, 1, device="cuda"), None, tau, 0.0)
+    below = z[:, 1:].astype(np.float64) / tau32
+    want = tau32 * np.exp(below)                           # the sum over the row is 1 to less than half a step
+    y = -below / np.log(2.0)
+    assert (y > 64).all() and (y < 128).all()
+    # the exponential's step and two products behind it
+    bound = want * (np.log(2.0) * (y * U32 + 2.0 ** -18) + 4 * U32)
+    z_ = _dev(z)
+    _, dz = sl.distill_step(p, z_, lay)
+    _within(dz[:, 1:], want, bound, "dz")
+    _, stats = sl.distill_fwd(p, z_, lay)
+    assert torch.equal(sl.distill_bwd(p, z_, stats, lay), dz)
+
+
 # ---- views that start at no 16-byte border -------------------------------------------
 def _apart(t):
     """The same values one element behind a 16-byte border."""
