@@ -106,12 +106,16 @@ template <bool TWO> __device__ inline void rebase(Sums& a, float m, const float*
   const Sums old = a;
   set_top<TWO>(a, m, scale);
   if (old.m == -INFINITY) return;               // (the sums are 0, or NaN)
+  float by[1 + TWO];
 #pragma unroll
-  for (int i = 0; i < 1 + TWO; ++i) {
-    const float within = old.near ? old.top[i] - a.top[i] : fmaf(old.m, scale[i], -a.top[i]);
-    const float past = old.near ? -fmaf(m, scale[i], -old.top[i]) : (old.m - m) * scale[i];
-    a.s[i] *= __builtin_amdgcn_exp2f(a.near ? within : past);
+  for (int i = 0; i < 1 + TWO; ++i) by[i] = old.near ? old.top[i] - a.top[i] : (old.m - m) * scale[i];
+  if (__builtin_expect(__ballot(old.near != a.near) != 0, 0)) {   // a branch, not two more operations in every step
+#pragma unroll
+    for (int i = 0; i < 1 + TWO; ++i)
+      if (old.near != a.near) by[i] = old.near ? -fmaf(m, scale[i], -old.top[i]) : fmaf(old.m, scale[i], -a.top[i]);
   }
+#pragma unroll
+  for (int i = 0; i < 1 + TWO; ++i) a.s[i] *= __builtin_amdgcn_exp2f(by[i]);
 }
 
 // The values of some vectors into the running sums.
@@ -149,8 +153,8 @@ __device__ inline int context_token(const SeqTab& st, int i) {
 // TWO: the teacher's term at tau and the label's at 1 need an exponential each.
 // With one of the terms alone, or with tau = 1, one serves.
 // NT: past the caches, 1 the gradient's stores, 2 the logits' loads too.
-// Loss or gradient alone: at most 80 registers, with which a CU takes three blocks (the
-// loss with two exponentials needs 85).
+// Loss or gradient alone: at most 80 registers, with which a CU takes three blocks (loss of 2048
+// rows of 32000 bf16: 32 us, with 83 registers 37); the loss with two exponentials needs 87.
 template <typename T, int MODE, bool TWO, int NT>
 __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD || (MODE == DM_FWD && !TWO) ? 6 : 4) distill_kernel(const DistillArgs a) {
   using RV = RowVec<T>;
