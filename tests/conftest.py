@@ -1,5 +1,7 @@
+import gc
 import os
 import sys
+import time
 
 import pytest
 
@@ -29,3 +31,30 @@ def pytest_collection_modifyitems(config, items):
     for it in items:
         if it.path.name in NEED_NO_GPU if have_gpu else "gpu" in it.keywords:
             it.add_marker(skip)
+
+
+def settle_readings(test, monkeypatch):
+    """Where a test reads how much memory is allocated: nothing that tests before it left
+    enters.  Garbage is collected and cached blocks given back first (a tensor that takes a cached
+    block counts with the block's size, up to 1 MiB more than its own); and each reading
+    waits for the work on the GPU and a moment more, as autograd's thread lets go of a pass's
+    results only after the call that waited for them has returned."""
+    if not {"memory_allocated", "max_memory_allocated"} & set(test.__code__.co_names):
+        return
+    import torch
+    gc.collect()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    reading = torch.cuda.memory_allocated
+
+    def settled(*args, **kwargs):
+        torch.cuda.synchronize()
+        time.sleep(0.02)
+        return reading(*args, **kwargs)
+    monkeypatch.setattr(torch.cuda, "memory_allocated", settled)
+
+
+@pytest.fixture(autouse=True)
+def _settled_readings(request, monkeypatch):
+    if "gpu" in request.keywords:
+        settle_readings(request.function, monkeypatch)

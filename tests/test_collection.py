@@ -1,6 +1,8 @@
-"""Which tests run where: conftest's rules, on machines with and without a GPU."""
+"""What conftest does for every test: which run where, on machines with and without a GPU, and
+readings of allocated memory."""
 import glob
 import os
+import threading
 from pathlib import Path
 
 import pytest
@@ -45,3 +47,32 @@ def test_every_module_with_such_calls_is_named():
         if "in (7" + ", 8)" in text and "mark.gpu" not in text:
             found.add(os.path.basename(path))
     assert found and found <= set(conftest.NEED_NO_GPU)
+
+
+def test_readings_of_memory_wait_for_what_is_let_go_late(monkeypatch):
+    """A stand-in for the allocator: a set of results that another thread lets go of a moment
+    after the call that made it has returned, cached blocks and work behind."""
+    import conftest
+    done, held = [], [6]
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda: done.append("synchronize"))
+    monkeypatch.setattr(torch.cuda, "empty_cache", lambda: done.append("empty_cache"))
+    monkeypatch.setattr(torch.cuda, "memory_allocated", lambda: sum(held))
+
+    def late():
+        threading.Timer(0.002, held.clear).start()
+
+    def reads():
+        late()
+        return torch.cuda.memory_allocated()
+
+    def reads_nothing():
+        return torch.cuda.synchronize
+
+    with monkeypatch.context() as m:
+        conftest.settle_readings(reads_nothing, m)
+        assert not done and torch.cuda.memory_allocated() == 6
+        conftest.settle_readings(reads, m)
+        assert done == ["synchronize", "empty_cache"]
+        assert reads() == 0
+    held.append(6)
+    assert torch.cuda.memory_allocated() == 6              # the reading itself is back
