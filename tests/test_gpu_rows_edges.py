@@ -4,10 +4,104 @@ import numpy as np
 import pytest
 
 import oracle as O
-from tests.test_gpu_rows import DT, HALF, TINY, U32, _dev, _ints, _sl, _within
+from tests.test_gpu_rows import DT, HALF, TINY, U32, _dev, _draw, _ints, _sl, _within
+from workloads import round_to_bf16
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
+
+
+# ---- token embedding -----------------------------------------------------------------
+# Sorted tokens are summed in pieces of 64, 512 columns of the joined sums to a block.
+PIECES = [  # rows of each id, one id behind the other, and the width
+    ([64], 520), ([65], 520), ([128], 4096), ([129], 4096),      # a run that ends at a border and one row behind it
+    ([1, 63, 64, 65], 520), ([30, 34, 1], 4096), ([63, 2, 63], 1032),
+    ([64 * 64], 1032), ([64 * 65 + 1], 1032),                    # as many pieces as a wave looks at once, and more
+    ([5, 64 * 131 + 7, 50], 1544),
+]
+
+
+@pytest.mark.parametrize("dt,gdt", [("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("counts,D", PIECES, ids=str)
+def test_embedding_gradient_of_runs_over_pieces(counts, D, dt, gdt):
+    sl = _sl()
+    rng, T, V = np.random.default_rng(sum(counts)), sum(counts), len(counts) + 2
+    ids = rng.permutation(np.repeat(np.arange(1, len(counts) + 1), counts))
+    dY = _draw(rng, (T, D), dt)
+    got = sl.embed_bwd(_ints(ids), _dev(dY, dt), sl.Layout([0], T), V, scale=1.5, grad_dtype=DT[gdt])
+    ref, mag, n = np.zeros((V, D)), np.zeros((V, D)), np.bincount(ids, minlength=V)
+    for v in range(V):
+        rows = dY[ids == v].astype(np.float64) * 1.5
+        ref[v], mag[v] = rows.sum(0), np.abs(rows).sum(0)
+    _within(got, ref, HALF[gdt] * np.abs(ref) + (n[:, None] + 8) * U32 * mag + TINY, "dE")
+    assert not got[0].any() and not got[V - 1].any()
+
+
+# ---- norm of whole rows ------------------------------------------------------------------
+# More rows than one round of the forward's blocks (768, 512 of them where a row takes over 512
+# lanes), the last round with rows for some of a block's groups only.
+WALKS = [  # rows, width
+    (1100, 16384),       # two and four vectors a lane
+    (1031, 8192),
+    (1601, 4104),        # 576 lanes a row in bf16
+    (3001, 1032),        # 192 lanes, two rows to a block
+    (3101, 1000),        # 128 lanes, four rows to a block
+    (7001, 520),
+    (25003, 72),         # 16 and 32 lanes of a wave
+    (50021, 8),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("centered", [True, False])
+@pytest.mark.parametrize("T,D", WALKS)
+def test_norm_forward_over_several_rounds_of_rows(T, D, centered, dt):
+    sl = _sl()
+    rng, lay = np.random.default_rng(T), sl.Layout([0], T)
+    x, r = _draw(rng, (T, D), dt), _draw(rng, (T, D), dt)
+    x += np.arange(T, dtype=np.float32)[:, None] % 5      # rows that tell each other apart
+    x = round_to_bf16(x) if dt == "bf16" else x
+    w, b = (1 + 0.3 * rng.standard_normal(D)).astype(np.float32), rng.standard_normal(D).astype(np.float32)
+    bt, bn = (_dev(b), b) if centered else (None, None)
+    xt, rt, wt = _dev(x, dt), _dev(r, dt), _dev(w)
+    y, h, stats = sl.layer_norm_fwd(xt, wt, bt, lay, 1e-5, centered, rt)
+    hn = (x + r).astype(np.float32)
+    hn = round_to_bf16(hn) if dt == "bf16" else hn
+    assert np.array_equal(h.float().cpu().numpy(), hn)
+    ref, u, s = O.layer_norm(hn, w, bn, 1e-5, centered)
+    # a lane's 16 values, 6 steps over a wave, 16 waves, the squares' halved by the root
+    own = (np.abs(u) + 1) * np.abs(w) + (0 if bn is None else np.abs(bn))
+    _within(y, ref, HALF[dt] * np.abs(ref) + 96 * U32 * own, "y")
+    _within(stats[:, 2], s[:, 0], 96 * U32 * s[:, 0], "s")
+    for swap in (False, True):                            # in place, over several rounds too
+        c = xt.clone(), rt.clone()
+        y2, h2, s2 = sl.layer_norm_fwd(c[0], wt, bt, lay, 1e-5, centered, c[1], out=c[::-1] if swap else c)
+        assert torch.equal(y2, y) and torch.equal(h2, h) and torch.equal(s2, stats)
+    y3, _, s3 = sl.layer_norm_fwd(h, wt, bt, lay, 1e-5, centered)          # no residual
+    assert torch.equal(y3, y) and torch.equal(s3, stats)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("centered", [True, False])
+@pytest.mark.parametrize("T,D", WALKS)
+def test_norm_backward_over_several_rounds_of_rows(T, D, centered, dt):
+    sl = _sl()
+    rng, lay = np.random.default_rng(T + 1), sl.Layout([0], T)
+    h, dy, dh = (_draw(rng, (T, D), dt) for _ in range(3))
+    w = (1 + 0.3 * rng.standard_normal(D)).astype(np.float32)
+    t = {n: _dev(v, dt) for n, v in (("h", h), ("dy", dy), ("dh", dh))}
+    _, _, stats = sl.layer_norm_fwd(t["h"], _dev(w), None, lay, 1e-5, centered)
+    g = sl.layer_norm_bwd(t["h"], _dev(w), stats, lay, t["dy"], t["dh"], centered)
+    dx, dw, db, mx, mw, mb = O.layer_norm_backward(h, w, dy, dh, 1e-5, centered)
+    _within(g["dx"], dx, HALF[dt] * np.abs(dx) + 128 * U32 * mx, "dx")
+    # rows of a group one after the other, the block's groups, the blocks by 64 and those
+    chain = T / 8 + 64 + 16 + 96
+    _within(g["dw"], dw, chain * U32 * mw, "dw")
+    if centered:
+        _within(g["db"], db, chain * U32 * mb, "db")
+    again = sl.layer_norm_bwd(t["h"], _dev(w), stats, lay, t["dy"], t["dh"], centered, out={"dx": t["dy"]})
+    for n in g:
+        assert torch.equal(again[n], g[n]), n
 
 
 # ---- distillation ------------------------------------------------------------------
