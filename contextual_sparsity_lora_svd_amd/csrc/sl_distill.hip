@@ -433,16 +433,25 @@ template <typename T, int MODE, bool TWO> static void launch_distill(const Disti
   while (threads < kRowThreads && threads * kVecs < a.V / RowVec<T>::W) threads *= 2;
   const dim3 grid = walk_grid(a.rows), block(threads);
   const size_t lds = MODE == DM_STEP ? (size_t)kKept * threads * kVecs * 16 : 0;
-  // Logits of 112 MiB and more (of the last cache's 256), in rows of whole vectors, go past
-  // the caches where they are used once: the gradient's stores, and in calls of loss or gradient
-  // alone the loads too.  Measured in us, through the caches and past them: step of 4096 rows of
-  // 128256 bf16 513, 456; step and then the product that reads the gradient, 1000 rows of
-  // 32000: 187, 193, 1500: 242, 245, 1750 (112 MB): 245, 244, 2500: 320, 318; the same with 1500 rows
-  // of 50021, which the product reads piecemeal: 490, 510; loss and gradient, 4096 rows of 32000: 182, 169.
-  const bool past = (long long)a.rows * a.V * (long long)sizeof(T) >= 112LL << 20 &&
-                    (a.ld | a.ld_out) * (long long)sizeof(T) % 16 == 0 && aligned16(a.z) && aligned16(a.dz);
-  if (past) hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, MODE == DM_STEP ? 1 : 2>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, 0>), grid, block, lds, s, a);
+  // What is used once goes past the caches, in rows of whole vectors, from 112 MiB (117 MB, of the last
+  // cache's 256 MiB) on: the gradient's stores by all rows, context rows' zeros among them, and in calls
+  // of loss or gradient alone the loads by the rows with a loss, which alone are read.  Measured in us,
+  // bf16, through the caches and past them.  Stores: step of 4096 rows of 128256 481, 438; with the products
+  // that make the logits and read the gradient, 1750 rows of 32000 (112 MB) 287, 296, 2000 (128 MB) 302, 302,
+  // 2500 364, 358, 4 x 1024 of 768 context rows each 398, 390; 4 x 512 of 384 (131 MB, 98 of them
+  // zeros) 240, 260, the step alone 41.5, 37.7.  Loads: loss and gradient with those products, 1750 rows
+  // 300, 313, 2000 311, 312, 2500 367, 372, 4096 490, 484, without them 2048 rows 88, 85; 4 x 512 of 384
+  // context rows (33 MB read) 45, 49.
+  const bool whole = (a.ld | a.ld_out) * (long long)sizeof(T) % 16 == 0 && aligned16(a.z) && aligned16(a.dz);
+  const long long row = a.V * (long long)sizeof(T);
+  const bool stores = whole && a.rows * row >= 112LL << 20, loads = whole && a.st.T_out * row >= 112LL << 20;
+  auto go = [&](auto nt) { hipLaunchKernelGGL((distill_kernel<T, MODE, TWO, decltype(nt)::value>), grid, block, lds, s, a); };
+  using None = std::integral_constant<int, 0>;
+  using Stores = std::integral_constant<int, 1>;
+  using Both = std::integral_constant<int, 2>;
+  if constexpr (MODE == DM_STEP) stores ? go(Stores()) : go(None());
+  else if constexpr (MODE == DM_BWD) loads ? go(Both()) : stores ? go(Stores()) : go(None());
+  else loads ? go(Both()) : go(None());
 }
 
 template <int MODE> static sl_status run_distill(sl_dtype dt, const DistillArgs& a, void* stream) {

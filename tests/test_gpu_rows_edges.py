@@ -270,3 +270,27 @@ def test_modules_take_gradients_that_start_anywhere(dt):
     alone = grads(lambda a, h: (a.reshape(-1) * weight[:T * D]).sum() + (h.reshape(-1) * weight[T * D:]).sum())
     for u, v in zip(behind, alone):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dt,T,V,ctx", [("bf16", 4000, 32000, 0), ("bf16", 4000, 32000, 3000), ("bf16", 2100, 32000, 500),
+                                        ("f32", 1000, 32000, 900), ("f32", 1900, 32000, 0)])
+def test_large_logits_of_few_rows_with_a_loss(dt, T, V, ctx):
+    """What goes past the caches depends on all rows and on those with a loss: bit for bit
+    what calls of a hundred rows give, zeros at context rows."""
+    sl = _sl()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = (3 * torch.randn(T, V, generator=g, device="cuda")).to(DT[dt])
+    tops, labels = (torch.randint(0, V, s, generator=g, device="cuda").int() for s in ((T, 8), (T,)))
+    tl, w = torch.randn(T, 8, generator=g, device="cuda"), torch.rand(T, generator=g, device="cuda")
+    lay, p = sl.Layout([ctx], T), sl.DistillTargets(tops, tl, labels, 1.5, 0.25)
+    loss, stats = sl.distill_fwd(p, z, lay)
+    dz = sl.distill_bwd(p, z, stats, lay, w)
+    l2, d2 = sl.distill_step(p, z, lay, w)
+    assert torch.equal(l2, loss) and torch.equal(d2, dz)
+    assert not loss[:ctx].any() and not dz[:ctx].any()
+    for a in {ctx, ctx + (T - ctx) // 2 // 100 * 100, T - 100}:
+        s = slice(a, a + 100)
+        q = sl.DistillTargets(tops[s], tl[s], labels[s], 1.5, 0.25)
+        l3, s3 = sl.distill_fwd(q, z[s], sl.Layout([0], 100))
+        assert torch.equal(l3, loss[s]) and torch.equal(s3, stats[s])
+        assert torch.equal(sl.distill_bwd(q, z[s], s3, sl.Layout([0], 100), w[s]), dz[s])
