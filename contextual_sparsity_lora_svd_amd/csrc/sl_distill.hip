@@ -154,7 +154,9 @@ __device__ inline int context_token(const SeqTab& st, int i) {
 // With one of the terms alone, or with tau = 1, one serves.
 // NT: past the caches, 1 the gradient's stores, 2 the logits' loads too.
 // Loss or gradient alone: at most 80 registers, with which a CU takes three blocks (loss of 2048
-// rows of 32000 bf16: 32 us, with 83 registers 37); the loss with two exponentials needs 87.
+// rows of 32000 bf16: 32 us, with 83 registers 37); the loss with two exponentials needs 87.  The
+// gradient's kernel spills up to 20 bytes a thread for it: with 90 registers and none, 2048 rows of
+// 32000 take 57.3 us in place of 55.3, 748 of 50021 41.5 for 40.1, 4096 of 128256 400 for 403.
 template <typename T, int MODE, bool TWO, int NT>
 __global__ void __launch_bounds__(kRowThreads, MODE == DM_BWD || (MODE == DM_FWD && !TWO) ? 6 : 4) distill_kernel(const DistillArgs a) {
   using RV = RowVec<T>;

@@ -376,8 +376,10 @@ static void launch_fwd(const void* E, const int32_t* ids, int64_t V, int64_t D, 
   int lg = 0;
   while (lg < 8 && (1 << lg) < nvec) ++lg;
   const int cols = ceil_div(nvec, 1 << lg), rows = 256 >> lg;
-  // four rows in flight a thread where that leaves four blocks to a CU
-  if ((long long)ceil_div(ntok, rows * 4) * cols >= 1024)
+  // four rows in flight a thread where that leaves 16 blocks to a CU (one row, four in us: 2048 rows of
+  // 4096 bf16 7.4, 8.2, 4096 13.5, 14.4, 8192, where they do, 27.3, 26.9; of 1000 fp32 4096 7.2, 7.9,
+  // 16384 28.3, 27.2)
+  if ((long long)ceil_div(ntok, rows * 4) * cols >= 4096)
     hipLaunchKernelGGL((embed_fwd_kernel<T, 4>), dim3(walk_grid(ceil_div(ntok, rows * 4), (1 << 23) / cols).x, cols), dim3(256), 0, s,
                        (const T*)E, ids, (uint32_t)V, nvec, ntok, lg, scale, (T*)Y);
   else
@@ -387,10 +389,11 @@ static void launch_fwd(const void* E, const int32_t* ids, int64_t V, int64_t D, 
 
 template <typename T, typename GT>
 static void launch_grad(const EmbedGradArgs& a, hipStream_t s) {
-  // Rows of 64 MiB and more go past the caches, each read once (32768 tokens of 4096 columns, with
-  // the fill of 128256 rows in bf16: 282 us through them, 266 past; 2048 tokens, 32000 rows: 99, 101).
+  // Rows of 32 MiB and more go past the caches, each read once (in us, through them and past, tokens of 4096
+  // columns in bf16: 2048 tokens and 32000 rows in fp32 99, 102, 4096 116, 114, 8192 142, 132; with the
+  // kernel before it that writes the rows 109, 109, 133, 128, 169, 163; 32768 tokens, 128256 rows in bf16 282, 266).
   const dim3 grid = walk_grid((long long)a.pieces * a.slices), block(64 * kPieceWaves);
-  if ((long long)a.ntok * a.D * (long long)sizeof(T) >= 64LL << 20)
+  if ((long long)a.ntok * a.D * (long long)sizeof(T) >= 32LL << 20)
     hipLaunchKernelGGL((embed_grad_kernel<T, GT, true>), grid, block, 0, s, a);
   else
     hipLaunchKernelGGL((embed_grad_kernel<T, GT, false>), grid, block, 0, s, a);

@@ -18,7 +18,11 @@
 // Measured (bf16, with the residual sum and its gradient): 2 x 8192 rows of 5120, not centred:
 // forward 113 us, 5.9 TB/s, backward 137 and 5 for the last launch, 4.7 TB/s, where a copy of 1 GiB
 // runs at 5.1; 2 x 1024 rows of 4096: 17, 17 and 4.  What bounds it: memory where there are rows enough
-// to fill it; below that the first loads and the last stores of two or three rows a block.
+// to fill it.  Below that, forward: the first loads and the last stores of two or three rows a
+// block, three blocks to a CU.  Backward: one block of 8 waves to a CU walks over eight rows with one
+// loaded ahead, some 24 KB in flight; more blocks cost more in partial sums than they bring, more waves
+// a block more in joining groups (figures at norm_bwd_blocks).  Narrow rows, many groups to a block:
+// that join, one group behind the other.
 #include <cmath>
 #include <type_traits>
 
@@ -404,7 +408,10 @@ inline unsigned norm_fwd_blocks(int T, const NormShape& sh) {
 
 // Blocks of a backward launch, whose sums the last launch adds: one to a CU (2048 rows
 // of 4096, with the last launch: 128 blocks 25.0 us, 256 19.3, 512 21.3, 1024 28.7), and
-// at least two rows to each (256 rows: 128 blocks 9.4 us, 256 11.9).
+// at least two rows to each (256 rows: 128 blocks 9.4 us, 256 11.9).  Other widths, with
+// 128, 256, 512 and 1024 blocks: 16384 rows of 5120 208, 133, 142, 150 us, of 1024 48, 33.5, 34.5, 40;
+// 131072 of 64 54, 49.5, 48.7, 84.  Blocks of 1024 threads in place of 512 (16 waves to a CU) lose
+// where groups have to join: 2048 rows of 4096 21.5 us, of 1024 12.4 to 15.2, of 64 39 to 73.
 inline int norm_bwd_blocks(int T, const NormShape& sh) {
   const int n = ceil_div(T, 2 * (sh.block / sh.group));
   return n < 256 ? n : 256;
