@@ -16,8 +16,8 @@
 // and one more launch the blocks' in a fixed order.
 //
 // Measured (bf16, with the residual sum and its gradient): 2 x 8192 rows of 5120, not centred:
-// forward 113 us, 5.9 TB/s, backward 137 and 5 for the last launch, 4.7 TB/s, where a copy of 1 GiB
-// runs at 5.1; 2 x 1024 rows of 4096: 17, 17 and 4.  What bounds it: memory where there are rows enough
+// forward 114 us, 5.9 TB/s, backward 137 and 5 for the last launch, 4.7 TB/s, where an elementwise
+// copy runs at 6.2; 2 x 1024 rows of 4096: 17, 17 and 4.  What bounds it: memory where there are rows enough
 // to fill it.  Below that, forward: the first loads and the last stores of two or three rows a
 // block, three blocks to a CU.  Backward: one block of 8 waves to a CU walks over eight rows with one
 // loaded ahead, some 24 KB in flight; more blocks cost more in partial sums than they bring, more waves
@@ -38,7 +38,7 @@ struct RowNormArgs {
   float* stats;              // [T][3]: m, what m rounded away, s
   float* part;               // backward: [blocks][2][D]
   int T, nvec, D;
-  int group, group_log2;     // lanes of a row; log2 below a wave
+  int group;                 // lanes of a row
   float eps, inv_d;
 };
 
@@ -217,7 +217,8 @@ __global__ void __launch_bounds__(64 * kNormWaves) row_norm_bwd_kernel(const Row
   __shared__ float red[2][2][kNormWaves];
   // Rows of over 1024 vectors fill the registers of a block of 1024 threads: the weight is
   // then kept in LDS and the next row is not loaded ahead (2048 rows of 16384 bf16: 71 us;
-  // loaded ahead 77, with the weight in registers too, 104: the compiler spills).
+  // loaded ahead 77, with the weight in registers too, 104: the compiler spills, as it still
+  // does with the four vectors of fp32 rows past 8192).
   constexpr bool WLDS = NV > 1;
   extern __shared__ __attribute__((aligned(16))) float sums[];   // [2][D] where a block has several groups; the weight
   const int groups = blockDim.x / a.group, group = threadIdx.x / a.group, lane = threadIdx.x - group * a.group;

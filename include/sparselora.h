@@ -472,7 +472,8 @@ sl_status sl_embed_bwd(sl_dtype dt, const sl_layout* lay, int64_t vocab, int64_t
  *        may be dy, dh or h.
  * Otherwise no output may overlap an input, the workspace or another output.
  * d_model a multiple of 8, at most 16384; eps >= 0.  A row whose variance (mean
- * square) and eps are both 0 has no norm: its outputs are NaN.
+ * square) and eps are both 0 has no norm: its outputs are NaN.  Squares are fp32:
+ * of rows whose values pass 10^17, s may be 0.
  * ------------------------------------------------------------------------- */
 typedef struct sl_layer_norm {
   int64_t d_model;
@@ -512,7 +513,9 @@ sl_status sl_layer_norm_bwd(sl_dtype dt, const sl_layout* lay, const sl_layer_no
  * sums goes).
  * Logits of -inf have probability 0.  A row of -inf alone, or with +inf or NaN,
  * has no distribution: its loss and its gradient are NaN; so is the loss of a
- * teacher's entry of +inf or NaN, and the gradient there.
+ * teacher's entry of +inf or NaN, and the gradient there.  The first term is
+ * temperature^2 times a difference of fp32 logarithms and has their rounding that
+ * many times.
  * 0 <= hard <= 1, temperature in [1e-6, 1e6], 1 <= top <= SL_DISTILL_MAX_TOP, vocab <= 2^30.
  * ------------------------------------------------------------------------- */
 #define SL_DISTILL_MAX_TOP 256
