@@ -37,6 +37,19 @@ def test_embedding_gradient_of_runs_over_pieces(counts, D, dt, gdt):
     assert not got[0].any() and not got[V - 1].any()
 
 
+@pytest.mark.parametrize("dt,T,D", [("bf16", 16387, 4096), ("f32", 16387, 1000), ("bf16", 8201, 4096), ("bf16", 600001, 64)])
+def test_lookup_of_many_rows(dt, T, D):
+    """Enough blocks that a thread holds four rows in flight, the last round of rows not full."""
+    sl = _sl()
+    g, V, s = torch.Generator(device="cuda").manual_seed(T), 777, 1.7
+    E = torch.randn(V, D, generator=g, device="cuda").to(DT[dt])
+    ids = torch.randint(-1, V + 1, (T,), generator=g, device="cuda").int()
+    ok = ((ids >= 0) & (ids < V))[:, None]
+    for scale in (1.0, s):
+        want = torch.where(ok, E[ids.long().clamp(0, V - 1)].float() * torch.tensor(scale, device="cuda"), 0.0).to(DT[dt])
+        assert torch.equal(sl.embed_fwd(E, ids, sl.Layout([0], T), scale=scale), want)
+
+
 # ---- norm of whole rows ------------------------------------------------------------------
 # More rows than one round of the forward's blocks (768, 512 of them where a row takes over 512
 # lanes), the last round with rows for some of a block's groups only.
@@ -294,3 +307,28 @@ def test_large_logits_of_few_rows_with_a_loss(dt, T, V, ctx):
         l3, s3 = sl.distill_fwd(q, z[s], sl.Layout([0], 100))
         assert torch.equal(l3, loss[s]) and torch.equal(s3, stats[s])
         assert torch.equal(sl.distill_bwd(q, z[s], s3, sl.Layout([0], 100), w[s]), dz[s])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_more_rows_than_blocks(dt):
+    """Past 2^20 rows a block takes several, rows with a loss and context rows."""
+    sl = _sl()
+    T, V, ctx = (1 << 20) + 70003, 5, 40000
+    g = torch.Generator(device="cuda").manual_seed(9)
+    z = (2 * torch.randn(T, V, generator=g, device="cuda")).to(DT[dt])
+    tops, labels = (torch.randint(-1, V, s, generator=g, device="cuda").int() for s in ((T, 2), (T,)))
+    tl, w = torch.randn(T, 2, generator=g, device="cuda"), torch.rand(T, generator=g, device="cuda")
+    lay, p = sl.Layout([ctx], T), sl.DistillTargets(tops, tl, labels, 2.0, 0.5)
+    loss, stats = sl.distill_fwd(p, z, lay)
+    dz = sl.distill_bwd(p, z, stats, lay, w)
+    l2, d2 = sl.distill_step(p, z, lay, w)
+    assert torch.equal(l2, loss) and torch.equal(d2, dz) and not loss[:ctx].any() and not dz[:ctx].any()
+    # a row's result is its own: the same rows in calls of fewer (V odd: at the same place to a 16-byte border)
+    for a in (ctx, ctx + 123456, 1 << 20, T - 5000):
+        a -= a % 8
+        a = max(a, ctx)
+        s = slice(a, min(a + 5000, T))
+        n = s.stop - s.start
+        q = sl.DistillTargets(tops[s], tl[s], labels[s], 2.0, 0.5)
+        l3, d3 = sl.distill_step(q, z[s], sl.Layout([0], n), w[s])
+        assert torch.equal(l3, loss[s]) and torch.equal(d3, dz[s]), a
